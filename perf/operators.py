@@ -125,7 +125,8 @@ def _paths(c, q_lens):
 def _quant(x, cache):
     """Codes and scales of rows x [..., D]."""
     amax = x.float().abs().amax(-1)
-    scale = torch.clamp_min(amax / _QMAX[cache], _MIN_SCALE)
+    # a tensor as the divisor: by a number, torch multiplies with its rounded reciprocal
+    scale = torch.clamp_min(amax / torch.full_like(amax, _QMAX[cache]), _MIN_SCALE)
     scale = torch.where(torch.isfinite(amax), scale, torch.full_like(scale, math.nan))
     inv = torch.where(torch.isfinite(amax), 1.0 / scale, torch.zeros_like(scale))[..., None]
     if cache == "int8":
