@@ -64,10 +64,12 @@ typedef enum {
   TA_ERR_ALIGNMENT = 3,   /* a pointer is not 16-byte aligned */
   TA_ERR_CUDA = 4,        /* a CUDA runtime/driver call or launch failed */
   TA_ERR_TIMEOUT = 5,     /* a kernel's bounded wait ran out (ta_sync_status) */
-  TA_ERR_GUARD = 6        /* guard build only: a device-side check failed (ta_sync_status) */
+  TA_ERR_GUARD = 6,       /* guard build only: a device-side check failed (ta_sync_status) */
+  TA_ERR_INDEX = 7        /* a length, page or token index outside the cache (ta_sync_status) */
 } ta_status;
 
-typedef enum { TA_F16 = 0, TA_BF16 = 1, TA_F32 = 2 } ta_dtype;
+/* TA_E4M3 and TA_I8 are element types of a key/value cache only. */
+typedef enum { TA_F16 = 0, TA_BF16 = 1, TA_F32 = 2, TA_E4M3 = 3, TA_I8 = 4 } ta_dtype;
 
 /* Forward: O = softmax(sm_scale * Q K^T) V with per-row LSE.
  * [FA-JVP] _attn_fwd (+ _attn_fwd_inner stages), [PW] _fwd_kernel.
@@ -237,8 +239,101 @@ ta_status attn_merge_fwd(const void* o1, const float* lse1, const void* o2, cons
 ta_status attn_merge_bwd(const void* o1, const float* lse1, const void* o2, const float* lse2, const void* dO,
                          const float* dlse, void* do1, float* dlse1, void* do2, float* dlse2, int B, int H,
                          int M, int D, ta_dtype dt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Key/value cache in pages, and attention over it (no counterpart on the
+ * pages; the definitions are those of attn_fwd with shared key heads).
+ *
+ * A cache holds k and v, each [num_pages, Hkv, page_size, D] contiguous, of
+ * type ct: TA_F16 or TA_BF16 (then the new tokens and the queries have that
+ * type), TA_E4M3 or TA_I8.  The 8-bit types have k_scale and v_scale,
+ * [num_pages, Hkv, page_size] fp32: a cached row stands for code * scale.  Any
+ * page_size >= 1; num_pages * Hkv * page_size < 2^31; D in {16, 32, 64, 128}.
+ *
+ * A sequence's tokens are found through three device arrays that every call
+ * takes:
+ *  - pages [B, max_pages] int32: position n of sequence b is row n % page_size
+ *    of page pages[b, n / page_size].  Entries behind a sequence's last
+ *    page are never read, and may be anything.
+ *  - kv_lens [B] int32: tokens of the sequence, the new ones included.
+ *  - q_lens [B] int32: new tokens, 0 <= q_lens[b] <= min(T, kv_lens[b]); the new
+ *    tokens are the last q_lens[b] positions.  NULL means T for every
+ *    sequence.  Rows t >= q_lens[b] of inputs are not read and of outputs
+ *    are left as they were.
+ * What these arrays hold is checked on the device.  Lengths that cannot be
+ * (also kv_lens[b] > max_pages * page_size) make the call treat that sequence
+ * as empty; a row of a page outside [0, num_pages) is not written, and reads
+ * as zeros.  Both make the next ta_sync_status return TA_ERR_INDEX.
+ * Sequences may share pages that no call writes (a common prompt).
+ *
+ * Tensors of tokens (k, v, q, o) are [B, heads, T, D] with element strides
+ * (b, head, t) given in an array of three; D is contiguous, rows are 16-byte
+ * aligned.  dt is TA_F16 or TA_BF16; TA_F32 is TA_ERR_UNSUPPORTED.  Calls allocate
+ * nothing and may be captured. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale; /* 8-bit types; NULL otherwise */
+  int num_pages, Hkv, page_size, D;
+  ta_dtype ct;
+} ta_kv_cache;
+
+/* Writes the new tokens' keys and values to their positions: row t of
+ * sequence b goes to position kv_lens[b] - q_lens[b] + t.  8-bit types, per
+ * row x of D elements:
+ *   scale = max(max |x| / Q, 2^-60) (Q = 448 for e4m3, 127 for int8) in fp32,
+ *   code  = x * (1 / scale) rounded to nearest even.
+ * A row with an infinity or a NaN gets codes 0 and a NaN scale, so that it
+ * reads back as NaN.  In: k, v [B, Hkv, T, D].  Two rows of one call must not
+ * share a position. */
+ta_status attn_cache_append(const ta_kv_cache* cache, const void* k, const int64_t* k_strides, const void* v,
+                            const int64_t* v_strides, const int* pages, int max_pages, const int* kv_lens,
+                            const int* q_lens, int B, int T, ta_dtype dt, void* stream);
+
+/* Reads positions 0 .. N - 1 of every sequence into contiguous k, v
+ * [B, Hkv, N, D] (16-byte aligned): code * scale rounded once to dt; zeros at
+ * and behind kv_lens[b].  A 16-bit cache has ct = dt. */
+ta_status attn_cache_read(const ta_kv_cache* cache, const int* pages, int max_pages, const int* kv_lens, void* k,
+                          void* v, int B, int N, ta_dtype dt, void* stream);
+
+/* Keeps keep_lens[b] of sequence b's new tokens and drops the others: token
+ * keep[b, i] (keep [B, T], strictly ascending in i, below q_lens[b]) moves to the
+ * place of new token i, codes and scales as they are.  Out: new_lens[b] =
+ * kv_lens[b] - q_lens[b] + keep_lens[b].  A list that is not ascending or leaves
+ * the draft moves nothing, gives new_lens[b] = kv_lens[b] - q_lens[b] and
+ * reports TA_ERR_INDEX.  new_lens must not overlap the other arrays
+ * (TA_ERR_INVALID_ARG). */
+ta_status attn_cache_keep(const ta_kv_cache* cache, const int* pages, int max_pages, const int* kv_lens,
+                          const int* q_lens, const int* keep, const int* keep_lens, int* new_lens, int B, int T,
+                          void* stream);
+
+/* Bytes of workspace attn_cache_fwd needs.  N: the largest kv_lens (at most
+ * max_pages * page_size). */
+size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, ta_dtype dt, ta_dtype ct);
+
+/* Attention of the new tokens over the cache, which holds their own keys and
+ * values already: O = softmax(sm_scale * q K^T) V with its LSE, as attn_fwd.
+ * Query head h reads key head h / (Hq / Hkv) (Hq a multiple of Hkv).  New token
+ * i of sequence b sees every position before the new tokens, and new token
+ * j iff tree[b * tree_strides[0] + i * tree_strides[1] + j] != 0 (bytes; a draft's
+ * tree, each token with its ancestors and itself); tree NULL: iff j <= i (a
+ * prompt's chunk; T = 1 is a generation step).  Rows that see nothing get O = 0,
+ * L = -inf.  Infinities and NaN in places that a row does not see do not
+ * reach it (16-bit caches, and rows that attn_cache_append wrote to 8-bit ones).
+ * In: q [B, Hq, T, D].  Out: o (strides o_strides), lse [B, Hq, T] fp32.
+ * ws: >= attn_cache_workspace_bytes(...) bytes, 16-byte aligned, contents need
+ * not be initialised; calls that may run at the same time need one each.
+ * 16-bit caches: scores in fp32 from products of the stored types, weights
+ * rounded to dt for the product with V.  8-bit caches: both products in fp16 on
+ * the bare codes (exact), scales in fp32; bf16 queries are scaled per row by a
+ * power of two. */
+ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_cache* cache, const int* pages,
+                         int max_pages, const int* kv_lens, const int* q_lens, const uint8_t* tree,
+                         const int64_t* tree_strides, void* o, const int64_t* o_strides, float* lse, void* ws,
+                         size_t ws_bytes, int B, int Hq, int T, ta_dtype dt, float sm_scale, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word that
- * the kernels set when a bounded wait runs out.  TA_OK, TA_ERR_TIMEOUT or
+ * the kernels set when a bounded wait runs out or an index leaves the cache.
+ * TA_OK, TA_ERR_TIMEOUT, TA_ERR_INDEX or
  * TA_ERR_CUDA (an asynchronous CUDA error); in the guard build also
  * TA_ERR_GUARD when a device-side check failed since the last call. */
 ta_status ta_sync_status(void* stream);

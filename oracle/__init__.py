@@ -57,6 +57,16 @@ Definitions, and the page passages they follow:
   ``dL2 = beta dL - alpha beta t``.  A row whose two parts both saw no key
   (L1 = L2 = -inf) merges to O = 0, L = -inf with zero gradients.
 
+* Key/value cache in pages (no counterpart on the pages): position n of a
+  sequence is row ``n % page`` of page ``pages[b, n // page]``; an 8-bit row is
+  ``code * scale`` with ``scale = max(max|x| / Q, 2^-60)`` stored in fp32 (Q = 448
+  for e4m3, 127 for int8) and ``code = x * fp32(1 / scale)`` rounded to the
+  nearest, ties to even; a row with an infinity or a NaN has codes 0 and a NaN
+  scale.  Attention of new tokens: the last ``q_len`` positions are the new
+  ones, token i sees every position before them and new token j where
+  ``tree[i, j]`` (without a tree ``j <= i``); query head h reads key head
+  ``h // (Hq // Hkv)``; softmax, L and empty rows as above.
+
 Every function here is pinned by the ``-m "not gpu"`` oracle tests (finite
 differences, closed forms, invariants, special cases); none is unpinned.
 """
@@ -71,6 +81,7 @@ __all__ = [
     "lse_merge_fwd", "lse_merge_bwd", "lse_merge_fwd_bhsd", "lse_merge_bwd_bhsd",
     "attention_jvp_tl", "attention_jvp_tl_bhsd", "attention_jvp_bwd", "attention_jvp_bwd_bhsd",
     "bwd_delta", "bwd_delta_bhsd",
+    "e4m3_grid", "cache_quantise", "cache_slot", "cache_attention",
 ]
 
 
@@ -395,3 +406,62 @@ def attention_rows(q, k, v, do, rows, causal: bool, sm_scale=None):
     delta = (dor * O).sum(axis=1)
     dS = P * (dor @ v.T - delta[:, None])
     return O, L, s * (dS @ k)
+
+
+# -------------------------------------------------------- key/value cache
+CACHE_QMAX = {"e4m3": 448.0, "int8": 127.0}
+CACHE_MIN_SCALE = 2.0 ** -60
+
+
+def e4m3_grid() -> np.ndarray:
+    """The finite non-negative e4m3 values in ascending order: (1 + m / 8)
+    2^(e - 7) for exponent fields e = 1 .. 15 (the last mantissa of the last one
+    is NaN) and m / 8 * 2^-6 for e = 0."""
+    v = [m / 8 * 2.0 ** -6 for m in range(8)]
+    v += [(1 + m / 8) * 2.0 ** (e - 7) for e in range(1, 16) for m in range(8) if not (e == 15 and m == 7)]
+    return np.array(v)
+
+
+def cache_quantise(x, kind: str):
+    """Rows x [..., D] -> (codes as float64 values, fp32 scales [...])."""
+    (x,) = _f64(x)
+    amax = np.abs(x).max(axis=-1)
+    ok = np.isfinite(amax)
+    q = np.float32(CACHE_QMAX[kind])
+    scale = np.maximum(np.where(ok, amax, 0.0).astype(np.float32) / q, np.float32(CACHE_MIN_SCALE))
+    inv = (np.float32(1.0) / scale).astype(np.float32)
+    x = np.where(ok[..., None], x, 0.0)
+    if kind == "int8":
+        code = np.rint(x * inv.astype(np.float64)[..., None])
+    else:
+        y = (x.astype(np.float32) * inv[..., None]).astype(np.float64)
+        g = e4m3_grid()
+        a = np.minimum(np.abs(y), g[-1])
+        hi = np.clip(np.searchsorted(g, a), 1, len(g) - 1)
+        lo = hi - 1
+        up = (a - g[lo] > g[hi] - a) | ((a - g[lo] == g[hi] - a) & (hi % 2 == 0))
+        code = np.copysign(np.where(up, g[hi], g[lo]), y)
+    return code, np.where(ok, scale, np.float32(np.nan)).astype(np.float32)
+
+
+def cache_slot(pages, page: int, n: int):
+    """(page id, row) of position n of the sequence with page list `pages`."""
+    return int(pages[n // page]), n % page
+
+
+def cache_attention(q, k, v, tree=None, sm_scale=None):
+    """One sequence and key head: q [G, T, D] (the G query heads that read it),
+    k, v [N, D] with the T new tokens' rows last -> (O [G, T, D], L [G, T])."""
+    q, k, v = _f64(q, k, v)
+    G, T, D = q.shape
+    N = k.shape[0]
+    keep = np.ones((T, N), dtype=bool)
+    keep[:, N - T:] = np.tril(np.ones((T, T), dtype=bool)) if tree is None else np.asarray(tree, dtype=bool)
+    O, L = np.zeros((G, T, D)), np.zeros((G, T))
+    for g in range(G):
+        with np.errstate(invalid="ignore"):
+            S = default_scale(D, sm_scale) * (q[g] @ k.T)
+        P, L[g] = _softmax(S, keep)
+        for i in range(T):
+            O[g, i] = P[i, keep[i]] @ v[keep[i]]
+    return O, L

@@ -15,7 +15,11 @@ Entry points (same names as the C ABI):
   piecewise_fwd(q1, k1, q2, k2, v, w, causal, sm_scale) -> (o, lse)
   piecewise_bwd(q1, k1, q2, k2, v, o, lse, do, w, causal, sm_scale)
                                                      -> (dq1, dk1, dq2, dk2, dv)
-Tensors are contiguous [B, H, S, D] float16/bfloat16 CUDA tensors; lse is
+  cache_append(cache, k, v, pages, kv_lens, q_lens)   new tokens into a KVCache's pages
+  cache_read(cache, pages, kv_lens, N)                -> (k, v)
+  cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens) -> new kv_lens
+  attn_cache_fwd(q, cache, pages, kv_lens, q_lens, tree, sm_scale) -> (o, lse)
+Except for the cache's calls (below), tensors are contiguous [B, H, S, D] float16/bfloat16 CUDA tensors; lse is
 float32 [B, H, M].  sm_scale None means 1/sqrt(D).
 """
 from __future__ import annotations
@@ -27,15 +31,19 @@ import torch
 
 __all__ = ["load", "lib_path", "attn_fwd", "attn_bwd", "attn_bwd_fused", "attn_fwd_jvp", "attn_bwd_jvp", "piecewise_fwd", "piecewise_bwd", "merge_fwd", "merge_bwd", "attn_fwd_fp8",
            "attn_bwd_workspace_bytes", "attn_bwd_fused_workspace_bytes", "sync_status", "selftest_wait_timeout", "profile_enable",
-           "profile_read", "set_wait_timeout_ms", "fwd_kv_split", "set_fwd_kv_split", "TAError", "STATUS"]
+           "profile_read", "set_wait_timeout_ms", "fwd_kv_split", "set_fwd_kv_split", "KVCache", "kv_cache", "cache_append", "cache_read", "cache_keep", "attn_cache_fwd",
+           "attn_cache_workspace_bytes", "TAError", "STATUS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libtattn.so")
 _lib = None
 
 STATUS = {0: "TA_OK", 1: "TA_ERR_INVALID_ARG", 2: "TA_ERR_UNSUPPORTED", 3: "TA_ERR_ALIGNMENT",
-          4: "TA_ERR_CUDA", 5: "TA_ERR_TIMEOUT", 6: "TA_ERR_GUARD"}
+          4: "TA_ERR_CUDA", 5: "TA_ERR_TIMEOUT", 6: "TA_ERR_GUARD", 7: "TA_ERR_INDEX"}
 _DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+# element types of a cache
+_CT = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 3, torch.int8: 4}
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _SIGS = {
@@ -53,6 +61,11 @@ _SIGS = {
     "attn_merge_fwd": ([_vp] * 6 + [_i] * 5 + [_vp], _i),
     "attn_fwd_fp8": ([_vp] * 5 + [_i] * 6 + [_f, _vp], _i),
     "attn_merge_bwd": ([_vp] * 10 + [_i] * 5 + [_vp], _i),
+    "attn_cache_append": ([_vp] * 6 + [_i] + [_vp] * 2 + [_i] * 3 + [_vp], _i),
+    "attn_cache_read": ([_vp] * 2 + [_i] + [_vp] * 3 + [_i] * 3 + [_vp], _i),
+    "attn_cache_keep": ([_vp] * 2 + [_i] + [_vp] * 5 + [_i] * 2 + [_vp], _i),
+    "attn_cache_workspace_bytes": ([_i] * 8, _sz),
+    "attn_cache_fwd": ([_vp] * 4 + [_i] + [_vp] * 8 + [_sz] + [_i] * 4 + [_f, _vp], _i),
     "ta_sync_status": ([_vp], _i),
     "ta_status_str": ([_i], ctypes.c_char_p),
     "ta_selftest_wait_timeout": ([_i, _vp], _i),
@@ -306,6 +319,271 @@ def merge_bwd(o1, lse1, o2, lse2, do, dlse=None, stream=None):
                                                 _ptr(do1), _ptr(dl1), _ptr(do2), _ptr(dl2), B, H, M, D, dt,
                                                 _stream(stream)))
     return do1, dl1, do2, dl2
+
+
+# ------------------------------------------------------- key/value cache
+class _CacheStruct(ctypes.Structure):
+    """ta_kv_cache of include/tattn.h."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i), ("Hkv", _i),
+                ("page_size", _i), ("D", _i), ("ct", _i)]
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+class KVCache:
+    """A key/value cache in pages: k, v contiguous CUDA tensors [num_pages,
+    Hkv, page_size, D] of float16, bfloat16, float8_e4m3fn or int8; the 8-bit
+    types with k_scale, v_scale float32 [num_pages, Hkv, page_size] (a row stands
+    for code * scale).  Holds the tensors; any page_size, D in {16, 32, 64, 128}.
+
+    Every call on it takes the sequences' page table and lengths, int32 CUDA
+    tensors: pages [B, max_pages] (position n of sequence b is row n % page_size
+    of page pages[b, n // page_size]), kv_lens [B] (tokens, the new ones
+    included) and q_lens [B] (new tokens, the last ones; None: T each).  Page ids
+    and lengths outside the cache are skipped on the device and make the next
+    sync_status() return TA_ERR_INDEX."""
+
+    __slots__ = ("_t", "_c", "_ref", "dtype", "device")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in _CT:
+            raise ValueError(f"unsupported cache dtype {k.dtype}")
+        if k.dim() != 4:
+            raise ValueError("k must be [num_pages, Hkv, page_size, D]")
+        scaled = k.dtype in (torch.float8_e4m3fn, torch.int8)
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("8-bit caches have k_scale and v_scale, 16-bit caches have none")
+        for name, t in (("k", k), ("v", v)):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            if t.dtype != k.dtype or t.shape != k.shape or t.device != k.device:
+                raise ValueError(f"{name} must have k's dtype, shape and device")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if scaled and (not t.is_cuda or t.device != k.device or t.dtype != torch.float32 or
+                           not t.is_contiguous() or t.shape != k.shape[:3]):
+                raise ValueError(f"{name} must be a contiguous float32 {tuple(k.shape[:3])} CUDA tensor")
+        self._t = (k, v, k_scale, v_scale)
+        P, Hkv, page, D = k.shape
+        p = [0 if t is None else t.data_ptr() for t in self._t]
+        self._c = _CacheStruct(*p, P, Hkv, page, D, _CT[k.dtype])
+        self._ref = ctypes.c_void_p(ctypes.addressof(self._c))
+        self.dtype, self.device = k.dtype, k.device
+
+    k = property(lambda self: self._t[0])
+    v = property(lambda self: self._t[1])
+    k_scale = property(lambda self: self._t[2])
+    v_scale = property(lambda self: self._t[3])
+    shape = property(lambda self: self._t[0].shape)
+
+
+def kv_cache(num_pages, Hkv, page_size, D, dtype=torch.bfloat16, device="cuda") -> KVCache:
+    """An empty KVCache (rows are whatever the memory holds until they are
+    written; no call reads rows behind a sequence's end)."""
+    k = torch.empty((num_pages, Hkv, page_size, D), dtype=dtype, device=device)
+    ks = vs = None
+    if dtype in (torch.float8_e4m3fn, torch.int8):
+        ks, vs = (torch.empty((num_pages, Hkv, page_size), dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, torch.empty_like(k), ks, vs)
+
+
+def _i32(name, t, shape, dev):
+    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} CUDA tensor on {dev}")
+
+
+def _cache_lists(cache, pages, kv_lens, q_lens):
+    """Checks the page table and the lengths; returns (B, max_pages)."""
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    if pages.dim() != 2:
+        raise ValueError("pages must be [B, max_pages]")
+    B, max_pages = pages.shape
+    dev = cache.device
+    _i32("pages", pages, (B, max_pages), dev)
+    _i32("kv_lens", kv_lens, (B,), dev)
+    if q_lens is not None:
+        _i32("q_lens", q_lens, (B,), dev)
+    return B, max_pages
+
+
+def _tokens(name, t, shape, dtype, dev, written=False):
+    """Checks a [B, heads, T, D] tensor with contiguous rows; returns its
+    strides (b, head, t)."""
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if written and not t.is_contiguous():
+        # no two elements share memory: each dimension steps over the ones inside it
+        end = 1
+        for s, n in sorted((s, n) for s, n in zip(st, shape) if n > 1):
+            if s < end:
+                raise ValueError(f"{name} overlaps itself")
+            end = s * (n - 1) + end
+    return _Strides(*st[:3])
+
+
+class _On:
+    """The stream a call runs on, with the cache's device made current: the
+    library launches on the current device.  Tensors that the call allocates
+    on one stream and uses on another are recorded there."""
+
+    __slots__ = ("stream", "foreign", "_guard")
+
+    def __init__(self, dev, stream):
+        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        current = torch.cuda.current_stream(dev)
+        if stream is None:
+            stream = current
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        self.foreign = stream.cuda_stream != current.cuda_stream
+        self.stream = stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self
+
+    def __exit__(self, *a):
+        if self._guard is not None:
+            self._guard.__exit__(*a)
+
+    def ptr(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def used(self, *ts):
+        if self.foreign:
+            for t in ts:
+                t.record_stream(self.stream)
+
+
+def cache_append(cache, k, v, pages, kv_lens, q_lens=None, stream=None):
+    """Writes new tokens' keys and values k, v [B, Hkv, T, D] (any strides with
+    contiguous rows) to their positions kv_lens - q_lens + t; 8-bit caches are
+    quantised with one scale per (token, head)."""
+    lib = load()
+    B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
+    P, Hkv, page, D = cache.shape
+    if k.dim() != 4 or k.dtype not in _DT:
+        raise ValueError("k must be a 4-D tensor of float16 or bfloat16")
+    T = k.shape[2]
+    ks = _tokens("k", k, (B, Hkv, T, D), k.dtype, cache.device)
+    vs = _tokens("v", v, (B, Hkv, T, D), k.dtype, cache.device)
+    with _On(cache.device, stream) as on:
+        _check("attn_cache_append", lib.attn_cache_append(
+            cache._ref, _ptr(k), ks, _ptr(v), vs, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), B, T,
+            _DT[k.dtype], on.ptr()))
+
+
+def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None):
+    """Positions 0 .. N - 1 of every sequence as (k, v) [B, Hkv, N, D] of dtype
+    (None: the cache's, bfloat16 for 8-bit caches); zeros at and behind
+    kv_lens.  k, v: tensors to write to."""
+    lib = load()
+    B, max_pages = _cache_lists(cache, pages, kv_lens, None)
+    P, Hkv, page, D = cache.shape
+    if dtype is None:
+        dtype = k.dtype if k is not None else cache.dtype if cache.dtype in _DT else torch.bfloat16
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    shape = (B, Hkv, int(N), D)
+    with _On(cache.device, stream) as on:
+        out = []
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=cache.device)
+                on.used(t)
+            else:
+                _tokens(name, t, shape, dtype, cache.device)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+            out.append(t)
+        _check("attn_cache_read", lib.attn_cache_read(
+            cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(out[0]), _ptr(out[1]), B, int(N), _DT[dtype],
+            on.ptr()))
+    return tuple(out)
+
+
+def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
+    """Keeps the accepted tokens of a draft: token keep[b, i] (keep int32 [B, T],
+    ascending, i < keep_lens[b]) moves to the place of new token i.  Returns the
+    sequences' new lengths, int32 [B]."""
+    lib = load()
+    B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
+    if keep.dim() != 2:
+        raise ValueError("keep must be [B, T]")
+    T = keep.shape[1]
+    _i32("keep", keep, (B, T), cache.device)
+    _i32("keep_lens", keep_lens, (B,), cache.device)
+    with _On(cache.device, stream) as on:
+        new = torch.empty((B,), dtype=torch.int32, device=cache.device)
+        on.used(new)
+        _check("attn_cache_keep", lib.attn_cache_keep(
+            cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), _ptr(keep), _ptr(keep_lens), _ptr(new),
+            B, T, on.ptr()))
+    return new
+
+
+def attn_cache_workspace_bytes(B, Hq, Hkv, T, N, D, dtype=torch.bfloat16, cache_dtype=None) -> int:
+    """Bytes of workspace attn_cache_fwd needs for sequences of at most N
+    tokens (N = max_pages * page_size covers every length)."""
+    ct = _CT[dtype if cache_dtype is None else cache_dtype]
+    return int(load().attn_cache_workspace_bytes(B, Hq, Hkv, T, min(int(N), 2 ** 31 - 1), D, _DT[dtype], ct))
+
+
+def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=None, o=None, lse=None, ws=None,
+                   stream=None):
+    """Attention of new tokens q [B, Hq, T, D] (any strides with contiguous
+    rows) over the cache, which holds their keys and values already; query head
+    h reads key head h // (Hq // Hkv).  tree: bool [B or 1, T, T], token i sees new token
+    j where tree[b, i, j] (None: where j <= i).  Returns (o, lse); rows
+    t >= q_lens[b] of given o, lse are left as they were."""
+    lib = load()
+    B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
+    P, Hkv, page, D = cache.shape
+    dev = cache.device
+    if q.dim() != 4 or q.dtype not in _DT:
+        raise ValueError("q must be a 4-D tensor of float16 or bfloat16")
+    _, Hq, T, _ = q.shape
+    shape = (B, Hq, T, D)
+    qs = _tokens("q", q, shape, q.dtype, dev)
+    ts = None
+    if tree is not None:
+        if tree.dtype not in (torch.bool, torch.uint8) or tree.device != dev or tree.dim() != 3 or \
+                tuple(tree.shape[1:]) != (T, T) or tree.shape[0] not in (1, B) or (T > 1 and tree.stride(2) != 1):
+            raise ValueError(f"tree must be a bool [B or 1, {T}, {T}] tensor on {dev} with contiguous rows")
+        ts = (ctypes.c_int64 * 2)(0 if tree.shape[0] == 1 else tree.stride(0), tree.stride(1))
+    with _On(dev, stream) as on:
+        if o is None:
+            o = torch.empty_like(q)
+            if q.stride() != o.stride():  # an expanded q has rows in common, o has not
+                o = torch.empty(shape, dtype=q.dtype, device=dev)
+            on.used(o)
+        os_ = _tokens("o", o, shape, q.dtype, dev, written=True)
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+            on.used(lse)
+        else:
+            _lse_of("lse", lse, B, Hq, T, dev)
+        if ws is None:
+            n = lib.attn_cache_workspace_bytes(B, Hq, Hkv, T, min(max_pages * page, 2 ** 31 - 1), D, _DT[q.dtype],
+                                               _CT[cache.dtype])
+            ws = torch.empty(max(int(n), 16), dtype=torch.uint8, device=dev)
+            on.used(ws)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous CUDA tensor on {dev}")
+        _check("attn_cache_fwd", lib.attn_cache_fwd(
+            _ptr(q), qs, cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), _ptr(tree), ts, _ptr(o), os_,
+            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), B, Hq, T, _DT[q.dtype],
+            _scale(sm_scale), on.ptr()))
+    return o, lse
 
 
 def sync_status(stream=None) -> str:

@@ -50,7 +50,8 @@ static ta_status guard_status() {
                                {"fwd_f8.cu", guard_take_fwd_f8}, {"bwd.cu", guard_take_bwd},
                                {"bwd_fused.cu", guard_take_bwd_fused}, {"bwd_jvp.cu", guard_take_bwd_jvp},
                                {"merge.cu", guard_take_merge},   {"fp32.cu", guard_take_fp32},
-                               {"bwd_pw_steps.cu", guard_take_bwd_pw_steps}};
+                               {"bwd_pw_steps.cu", guard_take_bwd_pw_steps},
+                               {"cache_io.cu", guard_take_cache_io}, {"attn_cache.cu", guard_take_attn_cache}};
   bool failed = false;
   for (const Unit& u : units) {
     uint32_t info[4] = {0u, 0u, 0u, 0u};  // line, rejected value, shared memory base, size
@@ -653,6 +654,86 @@ ta_status bwd_entry(bool allow_fused, const void* q, const void* k, const void* 
                  causal, 0, static_cast<cudaStream_t>(stream), allow_fused && bwd_fused_applies(D, dt));
 }
 
+// ------------------------------------------------------- key/value cache
+static bool head_dim_ok(int D) { return D == 16 || D == 32 || D == 64 || D == 128; }
+
+static int cache_type(ta_dtype ct) { return ct == TA_E4M3 ? kCacheE4m3 : ct == TA_I8 ? kCacheI8 : kCache16; }
+
+// Tokens of type dt with a cache of type ct: a 16-bit cache holds their type.
+static ta_status cache_dtype_status(ta_dtype dt, ta_dtype ct) {
+  if (dt != TA_F16 && dt != TA_BF16) return TA_ERR_UNSUPPORTED;
+  if (ct != TA_E4M3 && ct != TA_I8 && ct != TA_F16 && ct != TA_BF16) return TA_ERR_UNSUPPORTED;
+  if ((ct == TA_F16 || ct == TA_BF16) && ct != dt) return TA_ERR_UNSUPPORTED;
+  return TA_OK;
+}
+
+// 4-byte arrays (lengths, page tables, scales, lse).
+static ta_status check_ints(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p) return TA_ERR_INVALID_ARG;
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return TA_ERR_ALIGNMENT;
+  return TA_OK;
+}
+
+static ta_status check_cache(const ta_kv_cache* k, int B, int T, ta_dtype dt, CacheArgs* c) {
+  if (!k || B < 0 || T < 0) return TA_ERR_INVALID_ARG;
+  ta_status st = cache_dtype_status(dt, k->ct);
+  if (st != TA_OK) return st;
+  if (!head_dim_ok(k->D)) return TA_ERR_UNSUPPORTED;
+  if (k->num_pages < 1 || k->Hkv < 1 || k->page_size < 1) return TA_ERR_INVALID_ARG;
+  const __int128 rows = static_cast<__int128>(k->num_pages) * k->Hkv * k->page_size;
+  if (rows > 0x7fffffffll) return TA_ERR_UNSUPPORTED;
+  const bool scaled = cache_type(k->ct) != kCache16;
+  st = check_ptrs({k->k, k->v});
+  if (st == TA_OK && scaled) st = check_ints({k->k_scale, k->v_scale});
+  if (st != TA_OK) return st;
+  *c = CacheArgs{};
+  c->k = k->k;
+  c->v = k->v;
+  c->ks = k->k_scale;
+  c->vs = k->v_scale;
+  c->num_pages = k->num_pages;
+  c->Hkv = k->Hkv;
+  c->page = fast_div(k->page_size);
+  c->B = B;
+  c->T = T;
+  return TA_OK;
+}
+
+static ta_status set_cache_lists(CacheArgs* c, const int* pages, int max_pages, const int* kv_lens,
+                                 const int* q_lens) {
+  if (max_pages < 0) return TA_ERR_INVALID_ARG;
+  ta_status st = check_ints({kv_lens});
+  if (st == TA_OK && max_pages > 0) st = check_ints({pages});
+  if (st == TA_OK && q_lens) st = check_ints({q_lens});
+  if (st != TA_OK) return st;
+  c->table = pages;
+  c->max_pages = max_pages;
+  c->kv_lens = kv_lens;
+  c->q_lens = q_lens;
+  // positions stay below 2^31 with room for a last tile
+  c->capacity = static_cast<int>(
+      std::min<long long>(static_cast<long long>(max_pages) * c->page.d, 0x7fffffffll - 4096));
+  return TA_OK;
+}
+
+// Element strides (b, head, t) of 16-bit rows: 16-byte steps where a
+// dimension has more than one entry.
+static ta_status check_strides(const int64_t* st, int B, int H, int T) {
+  if (!st) return TA_ERR_INVALID_ARG;
+  if ((B > 1 && st[0] % 8 != 0) || (H > 1 && st[1] % 8 != 0) || (T > 1 && st[2] % 8 != 0)) return TA_ERR_ALIGNMENT;
+  return TA_OK;
+}
+
+// B * H * T rows, with room for a last block's.
+static bool row_count(int B, int H, int T, int* rows) {
+  const __int128 n = static_cast<__int128>(B) * H * T;
+  if (n > 0x7fffffffll - 65536) return false;
+  *rows = static_cast<int>(n);
+  return true;
+}
+
 }  // namespace ta
 
 using namespace ta;
@@ -676,6 +757,7 @@ const char* ta_status_str(ta_status s) {
     case TA_ERR_CUDA: return "TA_ERR_CUDA";
     case TA_ERR_TIMEOUT: return "TA_ERR_TIMEOUT";
     case TA_ERR_GUARD: return "TA_ERR_GUARD";
+    case TA_ERR_INDEX: return "TA_ERR_INDEX";
   }
   return "TA_ERR_UNKNOWN";
 }
@@ -880,6 +962,141 @@ ta_status piecewise_bwd(const void* q1, const void* k1, const void* q2, const vo
                  static_cast<cudaStream_t>(stream));
 }
 
+ta_status attn_cache_append(const ta_kv_cache* cache, const void* k, const int64_t* k_strides, const void* v,
+                            const int64_t* v_strides, const int* pages, int max_pages, const int* kv_lens,
+                            const int* q_lens, int B, int T, ta_dtype dt, void* stream) {
+  CacheArgs c;
+  ta_status st = check_cache(cache, B, T, dt, &c);
+  if (st != TA_OK) return st;
+  if (B == 0 || T == 0) return TA_OK;
+  st = set_cache_lists(&c, pages, max_pages, kv_lens, q_lens);
+  if (st == TA_OK) st = check_ptrs({k, v});
+  if (st == TA_OK) st = check_strides(k_strides, B, c.Hkv, T);
+  if (st == TA_OK) st = check_strides(v_strides, B, c.Hkv, T);
+  if (st != TA_OK) return st;
+  CacheAppendArgs a;
+  a.k = k;
+  a.v = v;
+  for (int i = 0; i < 3; ++i) {
+    a.ks[i] = k_strides[i];
+    a.vs[i] = v_strides[i];
+  }
+  if (!row_count(B, c.Hkv, T, &a.rows)) return TA_ERR_UNSUPPORTED;
+  a.t_div = fast_div(T);
+  a.h_div = fast_div(c.Hkv);
+  if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_cache_append", s);
+  cudaError_t e = launch_cache_append(dt == TA_BF16, cache_type(cache->ct), cache->D, c, a, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+ta_status attn_cache_read(const ta_kv_cache* cache, const int* pages, int max_pages, const int* kv_lens, void* k,
+                          void* v, int B, int N, ta_dtype dt, void* stream) {
+  CacheArgs c;
+  ta_status st = check_cache(cache, B, N, dt, &c);
+  if (st != TA_OK) return st;
+  if (B == 0 || N == 0) return TA_OK;
+  st = set_cache_lists(&c, pages, max_pages, kv_lens, nullptr);
+  if (st == TA_OK) st = check_ptrs({k, v});
+  if (st != TA_OK) return st;
+  CacheReadArgs a;
+  a.k = k;
+  a.v = v;
+  if (!row_count(B, c.Hkv, N, &a.rows)) return TA_ERR_UNSUPPORTED;
+  a.n_div = fast_div(N);
+  a.h_div = fast_div(c.Hkv);
+  if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_cache_read", s);
+  cudaError_t e = launch_cache_read(dt == TA_BF16, cache_type(cache->ct), cache->D, c, a, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+ta_status attn_cache_keep(const ta_kv_cache* cache, const int* pages, int max_pages, const int* kv_lens,
+                          const int* q_lens, const int* keep, const int* keep_lens, int* new_lens, int B, int T,
+                          void* stream) {
+  CacheArgs c;
+  ta_status st = check_cache(cache, B, T, cache && cache->ct == TA_F16 ? TA_F16 : TA_BF16, &c);
+  if (st != TA_OK) return st;
+  if (B == 0) return TA_OK;
+  st = set_cache_lists(&c, pages, max_pages, kv_lens, q_lens);
+  if (st == TA_OK) st = check_ints({keep_lens, new_lens});
+  if (st == TA_OK && T > 0) st = check_ints({keep});
+  if (st != TA_OK) return st;
+  const auto lo = reinterpret_cast<uintptr_t>(new_lens), hi = lo + static_cast<size_t>(B) * 4;
+  auto overlaps = [&](const int* p, size_t n) {
+    const auto x = reinterpret_cast<uintptr_t>(p);
+    return p && x < hi && x + n * 4 > lo;
+  };
+  if (overlaps(kv_lens, B) || overlaps(q_lens, B) || overlaps(keep_lens, B) ||
+      overlaps(keep, static_cast<size_t>(B) * T) || overlaps(pages, static_cast<size_t>(B) * max_pages))
+    return TA_ERR_INVALID_ARG;
+  int blocks;
+  if (!row_count(B, c.Hkv, 1, &blocks)) return TA_ERR_UNSUPPORTED;
+  CacheKeepArgs a;
+  a.keep = keep;
+  a.keep_lens = keep_lens;
+  a.new_lens = new_lens;
+  if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_cache_keep", s);
+  cudaError_t e = launch_cache_keep(cache_type(cache->ct), cache->D, c, a, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, ta_dtype dt, ta_dtype ct) {
+  if (B <= 0 || T <= 0 || N <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
+      cache_dtype_status(dt, ct) != TA_OK)
+    return 0;
+  return attn_cache_ws_bytes(D);
+}
+
+ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_cache* cache, const int* pages,
+                         int max_pages, const int* kv_lens, const int* q_lens, const uint8_t* tree,
+                         const int64_t* tree_strides, void* o, const int64_t* o_strides, float* lse, void* ws,
+                         size_t ws_bytes, int B, int Hq, int T, ta_dtype dt, float sm_scale, void* stream) {
+  CacheArgs c;
+  ta_status st = check_cache(cache, B, T, dt, &c);
+  if (st != TA_OK) return st;
+  if (Hq < 1 || Hq % c.Hkv != 0) return TA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return TA_OK;
+  st = set_cache_lists(&c, pages, max_pages, kv_lens, q_lens);
+  if (st == TA_OK) st = check_ptrs({q, o, ws});
+  if (st == TA_OK) st = check_ints({lse});
+  if (st == TA_OK) st = check_strides(q_strides, B, Hq, T);
+  if (st == TA_OK) st = check_strides(o_strides, B, Hq, T);
+  if (st != TA_OK) return st;
+  if (tree && !tree_strides) return TA_ERR_INVALID_ARG;
+  int rows;
+  if (!row_count(B, Hq, T, &rows)) return TA_ERR_UNSUPPORTED;
+  if (ws_bytes < attn_cache_ws_bytes(cache->D)) return TA_ERR_INVALID_ARG;
+  CacheAttnArgs a;
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = q_strides[i];
+    a.os[i] = o_strides[i];
+  }
+  a.tree = tree;
+  a.tree_b = tree ? tree_strides[0] : 0;
+  a.tree_t = tree ? tree_strides[1] : 0;
+  a.Hq = Hq;
+  a.G = Hq / c.Hkv;
+  a.g_div = fast_div(a.G);
+  a.scale_log2 =
+      ((std::isfinite(sm_scale) && sm_scale > 0.f) ? sm_scale : 1.0f / std::sqrt(static_cast<float>(cache->D))) *
+      kLog2e;
+  a.ws = static_cast<float*>(ws);
+  if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
+  return cuda_status(
+      launch_attn_cache(dt == TA_BF16, cache_type(cache->ct), cache->D, c, a, static_cast<cudaStream_t>(stream)));
+}
+
 ta_status ta_sync_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return TA_ERR_CUDA;
@@ -890,7 +1107,8 @@ ta_status ta_sync_status(void* stream) {
   if (h) {
     const uint32_t zero = 0;
     if (cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return TA_ERR_CUDA;
-    return TA_ERR_TIMEOUT;
+    // a wait that ran out outranks an index: what was computed is incomplete
+    return (h & ~ta::kErrIndex) ? TA_ERR_TIMEOUT : TA_ERR_INDEX;
   }
   return ta::guard_status();
 }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "tattn.h"
 
@@ -44,6 +45,8 @@ uint32_t guard_take_bwd_jvp(uint32_t* info);
 uint32_t guard_take_merge(uint32_t* info);
 uint32_t guard_take_fp32(uint32_t* info);
 uint32_t guard_take_bwd_pw_steps(uint32_t* info);
+uint32_t guard_take_cache_io(uint32_t* info);
+uint32_t guard_take_attn_cache(uint32_t* info);
 #endif
 cudaError_t launch_fwd(int mode, bool bf16, int D, const FwdMaps& maps, const FwdArgs& a, bool split,
                        cudaStream_t s);
@@ -125,6 +128,45 @@ struct MergePtrs {
   float *lse, *dl1, *dl2;
 };
 cudaError_t launch_merge(bool bwd, int dtype, int D, const MergePtrs& p, long long rows, cudaStream_t s);
+
+// ---------------------------------------------------- key/value cache
+// New tokens [B, Hkv, T, D] with element strides (b, h, t); rows = B Hkv T.
+struct CacheAppendArgs {
+  const void *k, *v;
+  long long ks[3], vs[3];
+  int rows;
+  FastDiv t_div, h_div;  // by T, by Hkv
+};
+// Contiguous outputs [B, Hkv, N, D]; rows = B Hkv N.
+struct CacheReadArgs {
+  void *k, *v;
+  int rows;
+  FastDiv n_div, h_div;  // by N, by Hkv
+};
+struct CacheKeepArgs {
+  const int *keep, *keep_lens;  // [B, T], [B]
+  int* new_lens;                // [B]
+};
+struct CacheAttnArgs {
+  const void* q;  // [B, Hq, T, D], element strides qs (b, h, t)
+  void* o;        // the same, strides os
+  float* lse;     // [B, Hq, T]
+  long long qs[3], os[3];
+  const uint8_t* tree;   // [B, T, T] or null; byte strides tree_b, tree_t (token i's row)
+  long long tree_b, tree_t;
+  int Hq, G;             // query heads, query heads per key head
+  FastDiv g_div;         // by G
+  float scale_log2;      // sm_scale * log2(e)
+  float* ws;
+};
+cudaError_t launch_cache_append(bool bf16, int ct, int D, const CacheArgs& c, const CacheAppendArgs& a,
+                                cudaStream_t s);
+cudaError_t launch_cache_read(bool bf16, int ct, int D, const CacheArgs& c, const CacheReadArgs& a, cudaStream_t s);
+cudaError_t launch_cache_keep(int ct, int D, const CacheArgs& c, const CacheKeepArgs& a, cudaStream_t s);
+// Workspace of the attention over the cache: the partial states of the
+// sequences that more than one block works on.
+size_t attn_cache_ws_bytes(int D);
+cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
 
 // Opts kernel `kern` into `bytes` of dynamic shared memory on the current
 // device, once per device (the attribute is per device, so a process that

@@ -18,6 +18,7 @@ enum : uint32_t {
   kErrTimeoutSoftmax = 1u << 2,  // a wait for softmax/producer output ran out
   kErrTimeoutOther = 1u << 3,
   kErrSmemLayout = 1u << 4,    // a kernel could not lay out its shared memory (did not run)
+  kErrIndex = 1u << 6,         // a length, page or token index outside the cache (bit 5: guard.cuh)
 };
 
 struct WaitCtl {
