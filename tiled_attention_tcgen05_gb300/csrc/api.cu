@@ -51,7 +51,9 @@ static ta_status guard_status() {
                                {"bwd_fused.cu", guard_take_bwd_fused}, {"bwd_jvp.cu", guard_take_bwd_jvp},
                                {"merge.cu", guard_take_merge},   {"fp32.cu", guard_take_fp32},
                                {"bwd_pw_steps.cu", guard_take_bwd_pw_steps},
-                               {"cache_io.cu", guard_take_cache_io}, {"attn_cache.cu", guard_take_attn_cache}};
+                               {"cache_io.cu", guard_take_cache_io}, {"attn_cache.cu", guard_take_attn_cache},
+                               {"attn_cache_tc.cu", guard_take_attn_cache_tc},
+                               {"attn_cache_tc8.cu", guard_take_attn_cache_tc8}};
   bool failed = false;
   for (const Unit& u : units) {
     uint32_t info[4] = {0u, 0u, 0u, 0u};  // line, rejected value, shared memory base, size
@@ -667,6 +669,17 @@ static ta_status cache_dtype_status(ta_dtype dt, ta_dtype ct) {
   return TA_OK;
 }
 
+// Query rows per key head up to which the kernel that reads each key once per
+// 16 rows is used.
+constexpr long long kFewRows = 16;
+
+static bool attn_cache_uses_tc(int G, int T) { return static_cast<long long>(G) * T > kFewRows; }
+
+static size_t attn_cache_bytes(int G, int T, int D, ta_dtype ct) {
+  if (!attn_cache_uses_tc(G, T)) return attn_cache_ws_bytes(D);
+  return cache_type(ct) == kCache16 ? attn_cache_tc16_ws_bytes(D) : attn_cache_tc8_ws_bytes(D);
+}
+
 // 4-byte arrays (lengths, page tables, scales, lse).
 static ta_status check_ints(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
@@ -1052,7 +1065,7 @@ size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, t
   if (B <= 0 || T <= 0 || N <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
       cache_dtype_status(dt, ct) != TA_OK)
     return 0;
-  return attn_cache_ws_bytes(D);
+  return attn_cache_bytes(Hq / Hkv, T, D, ct);
 }
 
 ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_cache* cache, const int* pages,
@@ -1073,7 +1086,7 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
   if (tree && !tree_strides) return TA_ERR_INVALID_ARG;
   int rows;
   if (!row_count(B, Hq, T, &rows)) return TA_ERR_UNSUPPORTED;
-  if (ws_bytes < attn_cache_ws_bytes(cache->D)) return TA_ERR_INVALID_ARG;
+  if (ws_bytes < attn_cache_bytes(Hq / c.Hkv, T, cache->D, cache->ct)) return TA_ERR_INVALID_ARG;
   CacheAttnArgs a;
   a.q = q;
   a.o = o;
@@ -1092,9 +1105,13 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
       ((std::isfinite(sm_scale) && sm_scale > 0.f) ? sm_scale : 1.0f / std::sqrt(static_cast<float>(cache->D))) *
       kLog2e;
   a.ws = static_cast<float*>(ws);
+  a.timeout_ns = g_timeout_ns;
   if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
-  return cuda_status(
-      launch_attn_cache(dt == TA_BF16, cache_type(cache->ct), cache->D, c, a, static_cast<cudaStream_t>(stream)));
+  const int ct = cache_type(cache->ct);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!attn_cache_uses_tc(a.G, T)) return cuda_status(launch_attn_cache(dt == TA_BF16, ct, cache->D, c, a, s));
+  if (ct == kCache16) return cuda_status(launch_attn_cache_tc16(dt == TA_BF16, cache->D, c, a, s));
+  return cuda_status(launch_attn_cache_tc8(dt == TA_BF16, ct, cache->D, c, a, s));
 }
 
 ta_status ta_sync_status(void* stream) {

@@ -20,15 +20,8 @@
 // memory (cp.async, swizzled), kStages tiles ahead.  The warps' states are
 // joined through shared memory at the end of a sequence.
 //
-// Work.  All (sequence, key head, row tile) units' key tiles form one line
-// that is cut into equal pieces, one per block, so that sequences of any mix
-// of lengths keep every SM busy to the end.  The cut depends on the lengths on
-// the device alone.  A unit inside one block is finished there; a unit cut by
-// block borders leaves one partial state per block in the workspace, and
-// the second kernel joins them in a fixed order (results do not depend on
-// timing).
-#include "cache.cuh"
-#include "launch.h"
+// Work is cut as attn_cache.cuh says, two blocks per SM.
+#include "attn_cache.cuh"
 
 namespace ta {
 
@@ -116,107 +109,6 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
   return v;
 }
 
-// ------------------------------------------------------------ work division
-// One sequence's part of the line: Hkv heads x row tiles x key tiles.
-struct SeqWork {
-  int kv, q, nrt, tiles;
-  long long all;
-};
-template <int TK>
-__device__ __forceinline__ SeqWork seq_work(const CacheArgs& c, const CacheAttnArgs& a, int b) {
-  const SeqLens s = cache_lens(c, b);
-  SeqWork w;
-  w.kv = s.kv;
-  w.q = s.q;
-  w.nrt = (s.q * a.G + kRows - 1) / kRows;
-  w.tiles = (s.kv + TK - 1) / TK;
-  w.all = static_cast<long long>(c.Hkv) * w.nrt * w.tiles;
-  return w;
-}
-
-// Place on the line: sequence b, head h, row tile rt, key tile t.
-struct Cursor {
-  int b, h, rt, t;
-  SeqWork w;
-};
-template <int TK>
-__device__ __forceinline__ void cursor_next(const CacheArgs& c, const CacheAttnArgs& a, Cursor& u) {
-  if (++u.t < u.w.tiles) return;
-  u.t = 0;
-  if (++u.rt < u.w.nrt) return;
-  u.rt = 0;
-  if (++u.h < c.Hkv) return;
-  u.h = 0;
-  while (++u.b < c.B) {
-    u.w = seq_work<TK>(c, a, u.b);
-    if (u.w.all > 0) return;
-  }
-}
-
-// Length of the line, and the sequence that holds place x (x < length; x the
-// same in all threads): every thread adds up a run of sequences, a scan over
-// the block gives the runs' starts.  Ends with a barrier.
-struct LineShared {
-  long long warp_sum[8];
-  int b;
-  long long start;  // first place of sequence b
-};
-template <int TK, int THREADS>
-__device__ __forceinline__ long long line_length(const CacheArgs& c, const CacheAttnArgs& a, LineShared& sh,
-                                                 long long* mine, long long* before) {
-  const int per = (c.B + THREADS - 1) / THREADS;
-  const int b0 = threadIdx.x * per, b1 = min(c.B, b0 + per);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_work<TK>(c, a, b).all;
-  long long inc = sum;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, s);
-    if ((threadIdx.x & 31) >= s) inc += o;
-  }
-  if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = inc;
-  __syncthreads();
-  long long total = 0, pre = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const long long v = sh.warp_sum[w];
-    if (w < static_cast<int>(threadIdx.x >> 5)) pre += v;
-    total += v;
-  }
-  *mine = sum;
-  *before = pre + inc - sum;
-  return total;
-}
-template <int TK, int THREADS>
-__device__ __forceinline__ void line_find(const CacheArgs& c, const CacheAttnArgs& a, LineShared& sh, long long x,
-                                          long long mine, long long before, Cursor& u) {
-  if (x >= before && x < before + mine) {
-    const int per = (c.B + THREADS - 1) / THREADS;
-    int b = threadIdx.x * per;
-    long long at = before;
-    while (true) {
-      const long long n = seq_work<TK>(c, a, b).all;
-      if (x < at + n) break;
-      at += n;
-      ++b;
-    }
-    sh.b = b;
-    sh.start = at;
-  }
-  __syncthreads();
-  u.b = sh.b;
-  u.w = seq_work<TK>(c, a, u.b);
-  const long long in = x - sh.start;
-  const long long per_head = static_cast<long long>(u.w.nrt) * u.w.tiles;
-  u.h = static_cast<int>(in / per_head);
-  const int rest = static_cast<int>(in - u.h * per_head);
-  u.rt = rest / u.w.tiles;
-  u.t = rest - u.rt * u.w.tiles;
-}
-
-// Block i's first place when the line of `len` is cut for `n` blocks.
-__device__ __forceinline__ long long cut(long long len, int n, int i) { return len * i / n; }
-
 // A partial state: 16 x D unnormalised accumulators, then m and l per row.
 template <int D>
 __host__ __device__ constexpr int part_floats() { return kRows * D + 2 * kRows; }
@@ -236,17 +128,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   constexpr int KW = F::KW, TK = F::TK, NT = KW / 8;
   constexpr int NK = D / 16;  // k-steps of Q K^T
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ LineShared line;
+  using Ln = Line<kRows, TK>;
+  __shared__ typename Ln::Shared line;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, cq = lane & 3;
 
   long long mine, before;
-  const long long len = line_length<TK, kWarps * 32>(c, a, line, &mine, &before);
+  const long long len = Ln::template length<kWarps * 32>(c, a, line, &mine, &before);
   const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
   if (x0 >= x1) return;
-  Cursor cc;
-  line_find<TK, kWarps * 32>(c, a, line, x0, mine, before, cc);
-  Cursor pc = cc;  // the next tile to copy
+  typename Ln::Cursor cc;
+  Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
+  typename Ln::Cursor pc = cc;  // the next tile to copy
 
   uint8_t* const ring = smem + warp * F::RING;
   float* const ml = reinterpret_cast<float*>(smem + kWarps * F::RING);  // [warps][16][2]
@@ -257,7 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   auto look_up = [&]() {
     const int n = pc.t * TK + warp * KW + (lane & (KW - 1));
     pid = -1;
-    if (n < pc.w.kv) pid = cache_page_id(c, pc.b, n, &prow);
+    if (n < pc.s.kv) pid = cache_page_id(c, pc.b, n, &prow);
     else prow = -1;
   };
   auto copy_tile = [&](int slot) {
@@ -284,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   for (int s = 0; s < kStages; ++s) {
     if (x0 + s < x1) {
       copy_tile(s);
-      cursor_next<TK>(c, a, pc);
+      Ln::next_tile(c, a, pc);
       if (x0 + s + 1 < x1) look_up();
     }
     cp_async_commit();
@@ -309,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
       for (int e = 0; e < 2; ++e) {
         const int r = cc.rt * kRows + g + 8 * e;
         const int t = static_cast<int>(a.g_div.div(r));
-        tok[e] = t < cc.w.q ? t : -1;
+        tok[e] = t < cc.s.q ? t : -1;
         fac[e] = a.scale_log2;
         const T* p = static_cast<const T*>(a.q);
         if (tok[e] >= 0)
@@ -363,8 +256,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
     __syncwarp();
     const uint32_t ks_a = ring_a + slot * (F::SLOT + F::SCALES), vs_a = ks_a + KW * F::RB, sc_a = ks_a + F::SLOT;
     const int n0 = cc.t * TK + warp * KW;          // this warp's first key
-    const int past = cc.w.kv - cc.w.q;             // keys every new token sees
-    if (n0 < cc.w.kv) {
+    const int past = cc.s.kv - cc.s.q;             // keys every new token sees
+    if (n0 < cc.s.kv) {
       float s[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
@@ -422,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
           }
         }
         if (lane < KW)  // the softmax sum's 1 / scale, read back below
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(1.f / vscale) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(vscale == vscale ? 1.f / vscale : 0.f) : "memory");
         __syncwarp();
       }
 
@@ -438,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
             for (int i = 0; i < 2; ++i) {
               const int n = n0 + j * 8 + 2 * cq + i;
               const int d = n - past;
-              bool see = tok[e] >= 0 && n < cc.w.kv;
+              bool see = tok[e] >= 0 && n < cc.s.kv;
               if (see && d >= 0)
                 see = a.tree ? __ldg(a.tree + cc.b * a.tree_b + tok[e] * a.tree_t + d) != 0 : d <= tok[e];
               if (!see) {
@@ -511,7 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
         // A new token's value may hold infinities or NaN that some rows must
         // not see, and 0 * NaN is NaN in the product: such elements are added
         // to the rows that do see them here and taken out of the tile.
-        if (masked && cc.w.kv > past) {
+        if (masked && cc.s.kv > past) {
           bool odd = false;
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;
 #pragma unroll
@@ -617,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
       }
     }
 
-    const bool last = cc.t + 1 == cc.w.tiles;
+    const bool last = cc.t + 1 == cc.ntiles;
     if (last || x + 1 == x1) {
       // ------------------------------------- end of the piece: join the warps
 #pragma unroll
@@ -671,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
         const bool whole = from_start && last;
         const int qr = cc.rt * kRows + r;
         const int t = static_cast<int>(a.g_div.div(qr)), hq = cc.h * a.G + (qr - t * a.G);
-        const bool real = t < cc.w.q;
+        const bool real = t < cc.s.q;
         float norm = 1.f;
         if (whole) norm = ll == 0.f ? 0.f : 1.f / ll;
         float* const part =
@@ -720,12 +613,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
     }
     if (x + kStages < x1) {
       copy_tile(slot);
-      cursor_next<TK>(c, a, pc);
+      Ln::next_tile(c, a, pc);
       if (x + kStages + 1 < x1) look_up();
     }
     cp_async_commit();
     slot = slot + 1 == kStages ? 0 : slot + 1;
-    cursor_next<TK>(c, a, cc);
+    Ln::next_tile(c, a, cc);
   }
 }
 
@@ -738,21 +631,21 @@ __global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, Cache
   constexpr bool BF = DT<T>::bf16;
   constexpr int TK = Cfg<CT, D>::TK;
   constexpr int VEC = D >= 128 ? 4 : (D >= 64 ? 2 : 1);  // elements per lane
-  __shared__ LineShared line;
+  using Ln = Line<kRows, TK>;
+  __shared__ typename Ln::Shared line;
   __shared__ float other[4][D + 2];
   long long mine, before;
-  const long long len = line_length<TK, 256>(c, a, line, &mine, &before);
+  const long long len = Ln::template length<256>(c, a, line, &mine, &before);
   const int i = blockIdx.x + 1;
   const long long x = cut(len, nblocks, i);
   if (x >= len) return;
-  Cursor u;
-  line_find<TK, 256>(c, a, line, x, mine, before, u);
-  const long long u0 = x - u.t, u1 = u0 + u.w.tiles;  // the unit's places
+  typename Ln::Cursor u;
+  Ln::template find<256>(c, a, line, x, mine, before, u);
+  const long long u0 = x - u.t, u1 = u0 + u.ntiles;  // the unit's places
   if (u.t == 0 || cut(len, nblocks, i - 1) > u0) return;
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 4 + wrow;
-  // the block that holds the unit's last place: cut(b) <= u1 - 1 < cut(b + 1)
-  const int b1 = static_cast<int>((u1 * nblocks - 1) / len);
+  const int b1 = block_of(len, nblocks, u1 - 1);  // holds the unit's last tile
   float mm = -INFINITY, ll = 0.f, v[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) v[k] = 0.f;
@@ -789,7 +682,7 @@ __global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, Cache
   ll = mn == -INFINITY ? ll + pl : ll * f0 + pl * f1;
   const int qr = u.rt * kRows + r;
   const int t = static_cast<int>(a.g_div.div(qr)), hq = u.h * a.G + (qr - t * a.G);
-  if (t >= u.w.q) return;
+  if (t >= u.s.q) return;
   const float norm = ll == 0.f ? 0.f : 1.f / ll;
   if (lane_on) {
     T* out = static_cast<T*>(a.o) + u.b * a.os[0] + hq * a.os[1] + t * a.os[2] + lane * VEC;

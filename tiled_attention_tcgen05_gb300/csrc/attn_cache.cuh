@@ -1,0 +1,149 @@
+// Work division of the attention over a cache, shared by its kernels.
+//
+// A unit is up to ROWS query rows of one sequence and key head: the G query
+// heads that share the key head, times the new tokens (row r is token r / G of
+// head r % G).  A unit needs the key tiles (TK keys) up to the last key its last
+// token can see.  All units' tiles, in the order sequence, key head, row tile,
+// make one line; block i of n takes the places cut(i) .. cut(i + 1), so that
+// sequences of any mix of lengths keep every SM busy to the end.  A unit inside
+// one block is finished there; a unit that block borders cut leaves one
+// partial state per block (the block's first piece in slot 0 of its two, a
+// later one in slot 1), and a second kernel joins them in a fixed order.  The
+// cut depends on the lengths alone, never on timing.
+#pragma once
+#include "cache.cuh"
+#include "launch.h"
+
+namespace ta {
+
+struct Seq {
+  int kv, q, nrt;
+  long long per_head, all;  // tiles of one key head, of the sequence
+};
+
+template <int ROWS, int TK>
+struct Line {
+  // key tiles of row tile rt
+  static __device__ __forceinline__ int tiles(const CacheAttnArgs& a, const Seq& s, int rt) {
+    int end = s.kv;
+    if (!a.tree) {
+      const int last = min(s.q - 1, static_cast<int>(a.g_div.div(min((rt + 1) * ROWS, s.q * a.G) - 1)));
+      end = s.kv - s.q + last + 1;
+    }
+    return (end + TK - 1) / TK;
+  }
+  static __device__ __forceinline__ Seq seq(const CacheArgs& c, const CacheAttnArgs& a, int b) {
+    const SeqLens n = cache_lens(c, b);
+    Seq s;
+    s.kv = n.kv;
+    s.q = n.q;
+    s.nrt = (n.q * a.G + ROWS - 1) / ROWS;
+    s.per_head = 0;
+    if (a.tree || s.nrt <= 1) {
+      if (s.nrt > 0) s.per_head = static_cast<long long>(s.nrt) * tiles(a, s, s.nrt - 1);
+    } else {
+      for (int rt = 0; rt < s.nrt; ++rt) s.per_head += tiles(a, s, rt);
+    }
+    s.all = s.per_head * c.Hkv;
+    return s;
+  }
+
+  struct Shared {
+    long long warp_sum[16];
+    int b;
+    long long start;  // first place of sequence b
+  };
+  // Length of the line: every thread adds up a run of sequences (mine, with
+  // `before` it on the line), a scan over the block joins the runs.
+  template <int THREADS>
+  static __device__ __forceinline__ long long length(const CacheArgs& c, const CacheAttnArgs& a, Shared& sh,
+                                                     long long* mine, long long* before) {
+    const int per = (c.B + THREADS - 1) / THREADS;
+    const int b0 = min(static_cast<long long>(c.B), static_cast<long long>(threadIdx.x) * per), b1 = min(c.B - b0, per) + b0;
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += seq(c, a, b).all;
+    long long inc = sum;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, s);
+      if ((threadIdx.x & 31) >= s) inc += o;
+    }
+    if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = inc;
+    __syncthreads();
+    long long total = 0, pre = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const long long v = sh.warp_sum[w];
+      if (w < static_cast<int>(threadIdx.x >> 5)) pre += v;
+      total += v;
+    }
+    *mine = sum;
+    *before = pre + inc - sum;
+    return total;
+  }
+
+  // Place on the line: sequence b, head h, row tile rt, key tile t.
+  struct Cursor {
+    int b, h, rt, t;
+    int ntiles;  // of this unit
+    Seq s;
+  };
+  // Cursor at place x (below the line's length, the same in all threads).
+  template <int THREADS>
+  static __device__ __forceinline__ void find(const CacheArgs& c, const CacheAttnArgs& a, Shared& sh, long long x,
+                                              long long mine, long long before, Cursor& u) {
+    if (x >= before && x < before + mine) {
+      const int per = (c.B + THREADS - 1) / THREADS;
+      int b = threadIdx.x * per;
+      long long at = before;
+      while (true) {
+        const long long n = seq(c, a, b).all;
+        if (x < at + n) break;
+        at += n;
+        ++b;
+      }
+      sh.b = b;
+      sh.start = at;
+    }
+    __syncthreads();
+    u.b = sh.b;
+    u.s = seq(c, a, u.b);
+    const long long in = x - sh.start;
+    u.h = static_cast<int>(in / u.s.per_head);
+    long long rest = in - u.h * u.s.per_head;
+    u.rt = 0;
+    u.ntiles = tiles(a, u.s, 0);
+    while (rest >= u.ntiles) {
+      rest -= u.ntiles;
+      u.ntiles = tiles(a, u.s, ++u.rt);
+    }
+    u.t = static_cast<int>(rest);
+  }
+  // To the first tile of the next unit (b == B behind the last).
+  static __device__ __forceinline__ void next_unit(const CacheArgs& c, const CacheAttnArgs& a, Cursor& u) {
+    u.t = 0;
+    if (++u.rt >= u.s.nrt) {
+      u.rt = 0;
+      if (++u.h >= c.Hkv) {
+        u.h = 0;
+        do {
+          if (++u.b >= c.B) return;
+          u.s = seq(c, a, u.b);
+        } while (u.s.all == 0);
+      }
+    }
+    u.ntiles = tiles(a, u.s, u.rt);
+  }
+  static __device__ __forceinline__ void next_tile(const CacheArgs& c, const CacheAttnArgs& a, Cursor& u) {
+    if (++u.t >= u.ntiles) next_unit(c, a, u);
+  }
+};
+
+// Block i's first place when the line of `len` is cut for `n` blocks, and the
+// block that holds place y: cut(b) <= y < cut(b + 1).
+__device__ __forceinline__ long long cut(long long len, int n, int i) { return len * i / n; }
+__device__ __forceinline__ int block_of(long long len, int n, long long y) {
+  return static_cast<int>(((y + 1) * n - 1) / len);
+}
+
+}  // namespace ta

@@ -47,6 +47,8 @@ uint32_t guard_take_fp32(uint32_t* info);
 uint32_t guard_take_bwd_pw_steps(uint32_t* info);
 uint32_t guard_take_cache_io(uint32_t* info);
 uint32_t guard_take_attn_cache(uint32_t* info);
+uint32_t guard_take_attn_cache_tc(uint32_t* info);
+uint32_t guard_take_attn_cache_tc8(uint32_t* info);
 #endif
 cudaError_t launch_fwd(int mode, bool bf16, int D, const FwdMaps& maps, const FwdArgs& a, bool split,
                        cudaStream_t s);
@@ -158,15 +160,22 @@ struct CacheAttnArgs {
   FastDiv g_div;         // by G
   float scale_log2;      // sm_scale * log2(e)
   float* ws;
+  uint64_t timeout_ns;
 };
 cudaError_t launch_cache_append(bool bf16, int ct, int D, const CacheArgs& c, const CacheAppendArgs& a,
                                 cudaStream_t s);
 cudaError_t launch_cache_read(bool bf16, int ct, int D, const CacheArgs& c, const CacheReadArgs& a, cudaStream_t s);
 cudaError_t launch_cache_keep(int ct, int D, const CacheArgs& c, const CacheKeepArgs& a, cudaStream_t s);
-// Workspace of the attention over the cache: the partial states of the
-// sequences that more than one block works on.
+// Attention over the cache: attn_cache for few query rows per key head, the
+// tc kernels for many (attn_cache_uses_tc).  Workspaces hold the partial states
+// of the units that more than one block works on.
 size_t attn_cache_ws_bytes(int D);
 cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
+size_t attn_cache_tc16_ws_bytes(int D);
+cudaError_t launch_attn_cache_tc16(bool bf16, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
+size_t attn_cache_tc8_ws_bytes(int D);
+cudaError_t launch_attn_cache_tc8(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a,
+                                  cudaStream_t s);
 
 // Opts kernel `kern` into `bytes` of dynamic shared memory on the current
 // device, once per device (the attribute is per device, so a process that
