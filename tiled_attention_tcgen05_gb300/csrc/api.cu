@@ -138,6 +138,24 @@ static bool make_map(CUtensorMap* map, const void* ptr, long long BH, long long 
   return r == CUDA_SUCCESS;
 }
 
+// A cache's k or v as [pages x Hkv, page, D] with boxes of box_rows rows: 16-bit
+// elements in 64-column, 128-byte-swizzled boxes (make_map's); 8-bit codes in
+// whole rows (64 columns where D is less, zeros past D), not swizzled.
+static bool make_page_map(CUtensorMap* map, const void* ptr, long long heads, int page, int D, int ct, bool bf16,
+                          int box_rows) {
+  if (ct == kCache16) return make_map(map, ptr, heads, page, D, bf16, box_rows);
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || !ensure_context()) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page) * D};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(D < 64 ? 64 : D), static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // [BH, rows, cols] 8-bit tensor as a 3-D map with box_cols x box_rows x 1
 // boxes and 128-byte swizzle (cols * 1 byte is the row stride; columns past
 // cols and rows past `rows` read as zeros).
@@ -673,14 +691,22 @@ static ta_status cache_dtype_status(ta_dtype dt, ta_dtype ct) {
 // 16 rows is used.
 constexpr long long kFewRows = 16;
 
-static bool attn_cache_uses_tc(int G, int T) { return static_cast<long long>(G) * T > kFewRows; }
+// Rows of a TMA box: the largest of 32, 16, 8 that divides a page, so that a
+// box never leaves its page and starts on a swizzle atom; 0: none does.
+static int page_box_rows(int page) { return page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : page % 8 == 0 ? 8 : 0; }
 
+static bool attn_cache_uses_tc(int G, int T, int page) {
+  return static_cast<long long>(G) * T > kFewRows && page_box_rows(page) > 0;
+}
+
+// The larger of the two kernels' needs: page_size is not among the arguments
+// of attn_cache_workspace_bytes.
 static size_t attn_cache_bytes(int G, int T, int D, ta_dtype ct) {
-  if (!attn_cache_uses_tc(G, T)) return attn_cache_ws_bytes(D);
+  if (static_cast<long long>(G) * T <= kFewRows) return attn_cache_ws_bytes(D);
   return cache_type(ct) == kCache16 ? attn_cache_tc16_ws_bytes(D) : attn_cache_tc8_ws_bytes(D);
 }
 
-// 4-byte arrays (lengths, page tables, scales, lse).
+// 4-byte arrays (lengths, page tables, lse).
 static ta_status check_ints(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (!p) return TA_ERR_INVALID_ARG;
@@ -699,7 +725,7 @@ static ta_status check_cache(const ta_kv_cache* k, int B, int T, ta_dtype dt, Ca
   if (rows > 0x7fffffffll) return TA_ERR_UNSUPPORTED;
   const bool scaled = cache_type(k->ct) != kCache16;
   st = check_ptrs({k->k, k->v});
-  if (st == TA_OK && scaled) st = check_ints({k->k_scale, k->v_scale});
+  if (st == TA_OK && scaled) st = check_ptrs({k->k_scale, k->v_scale});
   if (st != TA_OK) return st;
   *c = CacheArgs{};
   c->k = k->k;
@@ -1109,9 +1135,17 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
   if (!(c.err = error_word_ptr())) return TA_ERR_CUDA;
   const int ct = cache_type(cache->ct);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!attn_cache_uses_tc(a.G, T)) return cuda_status(launch_attn_cache(dt == TA_BF16, ct, cache->D, c, a, s));
-  if (ct == kCache16) return cuda_status(launch_attn_cache_tc16(dt == TA_BF16, cache->D, c, a, s));
-  return cuda_status(launch_attn_cache_tc8(dt == TA_BF16, ct, cache->D, c, a, s));
+  const bool bf16 = dt == TA_BF16;
+  if (!attn_cache_uses_tc(a.G, T, cache->page_size))
+    return cuda_status(launch_attn_cache(bf16, ct, cache->D, c, a, s));
+  PageMaps m;
+  const long long heads = static_cast<long long>(c.num_pages) * c.Hkv;
+  a.box_rows = page_box_rows(cache->page_size);
+  if (!make_page_map(&m.k, c.k, heads, cache->page_size, cache->D, ct, bf16, a.box_rows) ||
+      !make_page_map(&m.v, c.v, heads, cache->page_size, cache->D, ct, bf16, a.box_rows))
+    return TA_ERR_CUDA;
+  return cuda_status(ct == kCache16 ? launch_attn_cache_tc16(bf16, cache->D, m, c, a, s)
+                                    : launch_attn_cache_tc8(bf16, ct, cache->D, m, c, a, s));
 }
 
 ta_status ta_sync_status(void* stream) {

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   extern __shared__ __align__(128) uint8_t smem[];
   using Ln = Line<kRows, TK>;
   __shared__ typename Ln::Shared line;
+  let_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, cq = lane & 3;
 
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
           }
         }
         if (lane < KW)  // the softmax sum's 1 / scale, read back below
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(vscale == vscale ? 1.f / vscale : 0.f) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(vscale == vscale ? __fdividef(1.f, vscale) : 0.f) : "memory");
         __syncwarp();
       }
 
@@ -622,64 +623,75 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   }
 }
 
-// Joins the partial states of the units that block borders cut.  Block (i, y)
-// looks at border i of the line; where it is the first border inside its
-// unit, eight warps join rows 4 y .. 4 y + 3 (two warps per row, each half of
-// the unit's blocks).
+// Joins the partial states of the units that block borders cut: block (i, y)
+// joins rows 4 y .. 4 y + 3 of the unit that border i + 1 is the first to cut.
+// Two warps share a row.  A unit can have hundreds of parts (one long sequence
+// over all blocks), so that everything but the sum of the accumulators runs
+// over the parts in parallel, and that sum has eight loads in flight.
 template <typename T, int CT, int D>
-__global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, CacheAttnArgs a, int nblocks) {
+__global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, CacheAttnArgs a) {
   constexpr bool BF = DT<T>::bf16;
-  constexpr int TK = Cfg<CT, D>::TK;
   constexpr int VEC = D >= 128 ? 4 : (D >= 64 ? 2 : 1);  // elements per lane
-  using Ln = Line<kRows, TK>;
+  using Ln = Line<kRows, Cfg<CT, D>::TK>;
   __shared__ typename Ln::Shared line;
-  __shared__ float other[4][D + 2];
-  long long mine, before;
-  const long long len = Ln::template length<256>(c, a, line, &mine, &before);
-  const int i = blockIdx.x + 1;
-  const long long x = cut(len, nblocks, i);
-  if (x >= len) return;
+  __shared__ int slots[kBlocks];
+  __shared__ float fs[4][kBlocks];
+  __shared__ float other[4][D + 1];
   typename Ln::Cursor u;
-  Ln::template find<256>(c, a, line, x, mine, before, u);
-  const long long u0 = x - u.t, u1 = u0 + u.ntiles;  // the unit's places
-  if (u.t == 0 || cut(len, nblocks, i - 1) > u0) return;
+  const int parts = unit_parts<Ln, 256>(c, a, line, kBlocks, blockIdx.x + 1, slots, u);
+  wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
+  if (parts == 0 || static_cast<int>(blockIdx.y) * 4 + u.rt * kRows >= u.s.q * a.G) return;
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 4 + wrow;
-  const int b1 = block_of(len, nblocks, u1 - 1);  // holds the unit's last tile
-  float mm = -INFINITY, ll = 0.f, v[VEC];
+  auto part = [&](int i) { return a.ws + static_cast<size_t>(slots[i]) * part_floats<D>(); };
+  // both warps of a row: its maximum and sum, and the parts' factors
+  float mm = -INFINITY;
+  for (int i = lane; i < parts; i += 32)
+    if (slots[i] >= 0) mm = fmaxf(mm, __ldcg(part(i) + kRows * D + 2 * r));
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) v[k] = 0.f;
-  const bool lane_on = lane * VEC < D;
-  for (int b = i - 1 + half; b <= b1; b += 2) {
-    const long long s = cut(len, nblocks, b);
-    if (s == cut(len, nblocks, b + 1)) continue;  // an empty piece
-    const float* part = a.ws + (static_cast<size_t>(b) * 2 + (s < u0 ? 1 : 0)) * part_floats<D>();
-    const float pm = __ldcg(part + kRows * D + 2 * r), pl = __ldcg(part + kRows * D + 2 * r + 1);
-    const float mn = fmaxf(mm, pm);
-    const float f0 = mm == -INFINITY ? 0.f : ex2(mm - mn), f1 = pm == -INFINITY ? 0.f : ex2(pm - mn);
-    ll = mn == -INFINITY ? ll + pl : ll * f0 + pl * f1;
-    mm = mn;
-    if (lane_on) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[k] = v[k] * f0 + __ldcg(part + r * D + lane * VEC + k) * f1;
+  for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+  float ll = 0.f;
+  for (int i = lane; i < parts; i += 32) {
+    float f = 0.f;
+    if (slots[i] >= 0) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + kRows * D + 2 * r));
+      f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
+      ll += mm == -INFINITY ? ml.y : ml.y * f;  // a NaN sum stays one where no score was a number
     }
+    if (half == 0) fs[wrow][i] = f;
   }
-  if (half) {
-    if (lane_on) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
+  __syncthreads();
+  float v[VEC] = {};
+  const bool lane_on = lane * VEC < D;
+  if (lane_on) {
+#pragma unroll 8
+    for (int i = half; i < parts; i += 2) {
+      const float f = fs[wrow][i];
+      // (a block without a piece has factor 0; the first one listed always has a piece)
+      const float* p = part(slots[i] < 0 ? 0 : i) + r * D + lane * VEC;
+      if constexpr (VEC == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
+        v[0] = fmaf(y.x, f, v[0]);
+        v[1] = fmaf(y.y, f, v[1]);
+        v[2] = fmaf(y.z, f, v[2]);
+        v[3] = fmaf(y.w, f, v[3]);
+      } else if constexpr (VEC == 2) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
+        v[0] = fmaf(y.x, f, v[0]);
+        v[1] = fmaf(y.y, f, v[1]);
+      } else {
+        v[0] = fmaf(__ldcg(p), f, v[0]);
+      }
+    }
+    if (half) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) other[wrow][lane * VEC + k] = v[k];
-    }
-    if (lane == 0) {
-      other[wrow][D] = mm;
-      other[wrow][D + 1] = ll;
     }
   }
   __syncthreads();
   if (half) return;
-  const float pm = other[wrow][D], pl = other[wrow][D + 1];
-  const float mn = fmaxf(mm, pm);
-  const float f0 = mm == -INFINITY ? 0.f : ex2(mm - mn), f1 = pm == -INFINITY ? 0.f : ex2(pm - mn);
-  ll = mn == -INFINITY ? ll + pl : ll * f0 + pl * f1;
   const int qr = u.rt * kRows + r;
   const int t = static_cast<int>(a.g_div.div(qr)), hq = u.h * a.G + (qr - t * a.G);
   if (t >= u.s.q) return;
@@ -687,7 +699,7 @@ __global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, Cache
   if (lane_on) {
     T* out = static_cast<T*>(a.o) + u.b * a.os[0] + hq * a.os[1] + t * a.os[2] + lane * VEC;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = (v[k] * f0 + other[wrow][lane * VEC + k] * f1) * norm;
+    for (int k = 0; k < VEC; ++k) v[k] = (v[k] + other[wrow][lane * VEC + k]) * norm;
     if constexpr (VEC == 4) {
       uint2 w;
       w.x = pack2<BF>(v[0], v[1]);
@@ -702,7 +714,7 @@ __global__ void __launch_bounds__(256) attn_cache_join_kernel(CacheArgs c, Cache
   }
   if (lane == 0)
     a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + t] =
-        ll == 0.f ? -INFINITY : (mn == -INFINITY ? ll : (mn + lg2(ll)) * kLn2);
+        ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
 }
 
 template <typename T, int CT, int D>
@@ -718,9 +730,9 @@ cudaError_t run(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache_join", s);
-  attn_cache_join_kernel<T, CT, D><<<dim3(kBlocks - 1, kRows / 4), 256, 0, s>>>(c, a, kBlocks);
+  e = launch_join(attn_cache_join_kernel<T, CT, D>, dim3(kBlocks - 1, kRows / 4), 256, s, c, a);
   prof_end(s);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int CT>

@@ -146,4 +146,50 @@ __device__ __forceinline__ int block_of(long long len, int n, long long y) {
   return static_cast<int>(((y + 1) * n - 1) / len);
 }
 
+// ----------------------------------------------------------------- joining
+// The join kernel is launched while the main kernel runs (programmatic
+// dependent launch): it looks its units up meanwhile and waits before it reads
+// partial states.
+__device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_main_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Block `border - 1`'s look at border `border` of n: where it is the first
+// inside its unit, lists the partial states of the unit's blocks (slot: block
+// * 2 + which, -1 for a block without a piece) and returns their number;
+// else 0.  All threads, with a barrier.
+template <typename Ln, int THREADS>
+__device__ __forceinline__ int unit_parts(const CacheArgs& c, const CacheAttnArgs& a, typename Ln::Shared& sh, int n,
+                                          int border, int* slots, typename Ln::Cursor& u) {
+  long long mine, before;
+  const long long len = Ln::template length<THREADS>(c, a, sh, &mine, &before);
+  const long long x = cut(len, n, border);
+  if (x >= len) return 0;
+  Ln::template find<THREADS>(c, a, sh, x, mine, before, u);
+  const long long u0 = x - u.t, u1 = u0 + u.ntiles;  // the unit's places
+  if (u.t == 0 || cut(len, n, border - 1) > u0) return 0;
+  const int parts = block_of(len, n, u1 - 1) - (border - 1) + 1;
+  for (int i = threadIdx.x; i < parts; i += THREADS) {
+    const int b = border - 1 + i;
+    const long long s = cut(len, n, b);
+    slots[i] = s == cut(len, n, b + 1) ? -1 : b * 2 + (s < u0 ? 1 : 0);
+  }
+  __syncthreads();
+  return parts;
+}
+
+// Launches the join kernel behind the main one.
+template <typename K, typename... Args>
+inline cudaError_t launch_join(K kern, dim3 grid, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace ta

@@ -5,10 +5,10 @@ namespace ta {
 
 size_t attn_cache_tc16_ws_bytes(int D) { return tc_ws_bytes<kCache16>(D); }
 
-cudaError_t launch_attn_cache_tc16(bool bf16, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_cache_tc16(bool bf16, int D, const PageMaps& m, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   if (D <= 64)
-    return bf16 ? run_tc<__nv_bfloat16, kCache16, 64>(D, c, a, s) : run_tc<__half, kCache16, 64>(D, c, a, s);
-  return bf16 ? run_tc<__nv_bfloat16, kCache16, 128>(D, c, a, s) : run_tc<__half, kCache16, 128>(D, c, a, s);
+    return bf16 ? run_tc<__nv_bfloat16, kCache16, 64>(D, m, c, a, s) : run_tc<__half, kCache16, 64>(D, m, c, a, s);
+  return bf16 ? run_tc<__nv_bfloat16, kCache16, 128>(D, m, c, a, s) : run_tc<__half, kCache16, 128>(D, m, c, a, s);
 }
 
 }  // namespace ta

@@ -3,8 +3,10 @@
 //
 // A block works through its piece of the line (attn_cache.cuh) with the roles
 //   warps 0-3, 4-7  two softmax groups, a thread per query row (= TMEM lane);
-//   warps 8-11      copy Q and the key and value tiles into shared memory;
+//   warps 8-11      bring Q into shared memory, look through tiles with new
+//                   tokens, and turn 8-bit codes into fp16;
 //   warp 12         issues the MMAs: S = Q K^T, O += P V with P in TMEM;
+//   warps 13, 14    fetch keys and values (8-bit: 13 both) by TMA;
 // and the registers handed to the softmax groups (setmaxnreg).  The groups
 // alternate on the tensor core:  S0 S1 | PV0 S0' | PV1 S1' | ...  Units of more
 // than 128 rows give each group a row tile of its own and both the same keys;
@@ -12,16 +14,21 @@
 // key tile, and join the two states at the end: the softmax of one tile
 // then runs beside the other's MMAs in either case.
 //
-// Pages can have any size, so tiles are gathered row by row with 16-byte
-// cp.async into the 128-byte-swizzled layout that the MMA descriptors read.
-// 8-bit codes are gathered into a staging ring several tiles ahead and turned
-// into fp16 codes (exact) by the threads that copied them; scores take their
-// key's scale and the value's scale goes into the exponent as in
+// Tiles are gathered by TMA in boxes of 8, 16 or 32 rows (the largest that
+// divides a page), a lane per box.  Boxes behind the sequence's end or of pages
+// that do not exist are fetched from outside the map and so read as zeros.
+// 16-bit rows go straight into the 128-byte-swizzled layout that the MMA
+// descriptors read.  8-bit codes and their scales go into a staging ring
+// several tiles ahead; warps 8-11 turn the codes into fp16 codes (exact).  Scores
+// take their key's scale and the value's scale goes into the exponent as in
 // attn_cache.cu.
 //
-// Infinities and NaN among a draft's values would reach rows that must not
-// see them (0 * NaN): the copying warps take them out of the tile, and the
-// rows that do see them get them added to their result.
+// A box may bring rows behind the sequence's end, whose memory may hold
+// anything, and a draft's values may hold infinities and NaN that some rows
+// must not see: 0 * NaN would reach every row.  Tiles of values with new
+// tokens are looked through before they are handed on: dead rows are cleared
+// and non-finite values taken out; the rows that do see such a value get it
+// added to their result.
 #pragma once
 #include "attn_cache.cuh"
 #include "common.cuh"
@@ -32,10 +39,7 @@ namespace ta {
 namespace {
 
 constexpr int kTcBlocks = 152;    // one per SM
-constexpr int kTcThreads = 512;   // 16 warps; 13 to 15 only fill their register group
-constexpr int kTcRegsSoftmax = 184, kTcRegsCopy = 96, kTcRegsMma = 48;
-static_assert(256 * kTcRegsSoftmax + 128 * kTcRegsCopy + 128 * kTcRegsMma <= kTcThreads * 128,
-              "the groups' registers come out of the launch's");
+constexpr int kTcThreads = 512;   // 16 warps; the last one only fills its register group
 
 template <int CT, int DP>
 struct TcCfg {
@@ -50,8 +54,15 @@ struct TcCfg {
   static constexpr int SSLOT = OPB + 1024;               // and their scales (K tiles)
   static constexpr int SCS = KST + 2;                    // ring of scales for the softmax
   static constexpr int SCB = 128 * 12;                   // K scale, log2 and 1 / of the V scale
-  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * SSLOT + SCS * SCB : 0);
-  static constexpr int XCH = QT * TILE / 2048;           // float4 columns of 128 rows that fit over Q
+  static constexpr int REG_SOFTMAX = 192, REG_COPY = 64, REG_MMA = 64;
+  static_assert(256 * REG_SOFTMAX + 128 * REG_COPY + 128 * REG_MMA <= kTcThreads * 128,
+                "the groups' registers come out of the launch's");
+  // Where a one-tile unit's groups join: the second query tile (D = 128, 16
+  // bits), memory of its own (D = 64), or the query tile itself, which then
+  // is free for the next piece only after that.
+  static constexpr bool XOWN = DP == 64, XQ = DP == 128 && Q8;
+  static constexpr int XCH = DP == 64 ? 16 : TILE / 2048;  // float4 columns of 128 rows a round
+  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * SSLOT + SCS * SCB : 0) + (XOWN ? 32768 : 0);
   static_assert(SMEM + 2048 <= kSmemMax, "tiles do not fit in shared memory");
 };
 template <int CT, int DP>
@@ -59,14 +70,6 @@ constexpr int tc_part_floats() {
   return TcCfg<CT, DP>::ROWS * (DP + 2);
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
@@ -76,6 +79,18 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+// Global -> shared copy of a multiple of 16 bytes, both ends 16-byte aligned;
+// counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  if (!TA_CHECK_V((smem_u32(dst) & 15u) == 0u && guard_in_dyn_smem(smem_u32(dst)) &&
+                      (reinterpret_cast<uintptr_t>(src) & 15u) == 0u && (bytes & 15u) == 0u,
+                  smem_u32(dst)))
+    return;
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void sts_f32(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
@@ -111,7 +126,9 @@ __device__ __forceinline__ void add_non_finite(const CacheArgs& c, const CacheAt
 }
 
 template <typename T, int CT, int DP>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs c, CacheAttnArgs a, int dg) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs c,
+                         CacheAttnArgs a, int dg) {
   using F = TcCfg<CT, DP>;
   using Ln = Line<F::ROWS, kBN>;
   constexpr bool BF = DT<T>::bf16;
@@ -125,9 +142,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
   __shared__ int abort_flag;
   __shared__ int odd[4];  // piece + 1 (mod 4 slots) whose draft holds non-finite values
   __shared__ float xm[kBM], xl[kBM];
-  __shared__ float qfac[F::Q8 ? kBM : 1];
+  __shared__ float qfac[2][F::Q8 ? kBM : 1];  // of even and odd pieces
+  __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
+  __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_dependents_launch();
   long long mine, before;
   const long long len = Ln::template length<kTcThreads>(c, a, line, &mine, &before);
   const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
@@ -141,6 +161,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
   auto sV = [&](int st) { return sQ + (F::QT + KST + st) * F::TILE; };
   const uint32_t sStage = sQ + (F::QT + KST + VST) * F::TILE;
   const uint32_t sScale = sStage + F::SR * F::SSLOT;
+  const uint32_t sX = F::XOWN ? sScale + (F::Q8 ? F::SCS * F::SCB : 0) : F::XQ ? sQ : sQ + F::TILE;
 
   WaitCtl ctl{c.err, a.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
@@ -148,12 +169,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
     mbar_init(&bar_q, 4);
     mbar_init(&bar_qfree, 8);
     for (int s = 0; s < KST; ++s) {
-      mbar_init(&bar_k[s], 4);
+      mbar_init(&bar_k[s], F::Q8 ? 4 : 1);
       mbar_init(&bar_kempty[s], 1);
     }
     for (int s = 0; s < VST; ++s) {
       mbar_init(&bar_v[s], 4);
       mbar_init(&bar_vempty[s], 1);
+      mbar_init(&bar_scan[s], 1);
+    }
+    if constexpr (F::Q8) {
+      for (int s = 0; s < F::SR; ++s) {
+        mbar_init(&bar_stage[s], 1);
+        mbar_init(&bar_sempty[s], 4);
+      }
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar_s[w], 1);
@@ -185,17 +213,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
   auto piece_two = [&](const typename Ln::Cursor& p) { return !F::Q8 && p.s.q * a.G - p.rt * F::ROWS > kBM; };
 
   if (warp >= 8 && warp < 12) {
-    // ------------------------------------------------------------- copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsCopy));
+    // ------------------------------------------------------------- helpers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REG_COPY));
     const int pw = warp - 8, tid = threadIdx.x - 256;
-    // row of the cache that holds this lane's key of tile t (-1: none)
-    auto look_up = [&](const typename Ln::Cursor& p, int t) -> int {
-      const int n = t * kBN + pw * 32 + lane;
-      if (n >= p.s.kv) return -1;
-      int r;
-      const int id = cache_page_id(c, p.b, n, &r);
-      return cache_row(c, p.h, id, r);
-    };
     // query row i of tile w as an offset into q; false: no such row
     auto q_row = [&](const typename Ln::Cursor& p, int w, int i, long long* off) -> bool {
       const int rr = p.rt * F::ROWS + w * kBM + i;
@@ -204,255 +224,177 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
       *off = p.b * a.qs[0] + static_cast<long long>(p.h * a.G + (rr - t * a.G)) * a.qs[1] + t * a.qs[2];
       return true;
     };
-
-    if constexpr (!F::Q8) {
-      constexpr int CH = DP / 8;  // 16-byte chunks per row
-      const int dch = dg / 8;
-      // Copies in flight, oldest first: the barrier to signal and, for a
-      // tile with new tokens' values, the tile to look through.  At most
-      // three wait behind the one being issued.
-      uint64_t* fb0 = nullptr;
-      uint64_t* fb1 = nullptr;
-      uint64_t* fb2 = nullptr;
-      uint32_t fs0 = 0, fs1 = 0, fs2 = 0;
-      int fp0 = 0, fp1 = 0, fp2 = 0;
-      auto signal = [&](uint64_t* bar, uint32_t scan, int piece) {
-        if (scan) {
+    // the next piece's query rows towards L2, while this piece runs
+    auto prefetch_q = [&](const typename Ln::Cursor& p) {
+      for (int w = 0; w < F::QT; ++w) {
+        long long off = 0;
+        if (!q_row(p, w, tid, &off)) continue;
+        const char* at = reinterpret_cast<const char*>(static_cast<const T*>(a.q) + off);
+        for (int k = 0; k < dg * 2; k += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + k));
+      }
+    };
+    auto signal = [&](uint64_t* bar) {  // this warp's writes to shared memory, to the MMAs
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    int kt = 0;  // tiles before this piece
+    bool ok = true;
+    long long x = x0;
+    [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
+    for (int piece = 0; ok && x < x1; ++piece) {
+      const int nt = piece_tiles(u, x);
+      if constexpr (!F::Q8) {
+        constexpr int CH = DP / 8;  // 16-byte chunks per row
+        const int ntile = piece_two(u) ? 2 : 1, dch = dg / 8;
+        if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
+        for (int w = 0; w < ntile; ++w) {
+          long long off = 0;
+          const bool has = q_row(u, w, pw * 32 + lane, &off);
+#pragma unroll 4
+          for (int k = 0; k < CH; ++k) {
+            const int idx = k * 32 + lane, r = idx / CH, j = idx % CH;
+            const long long o = __shfl_sync(0xffffffffu, off, r);
+            const bool real = __shfl_sync(0xffffffffu, has, r) && j < dch;
+            cp_async16(tile_at(sQ + w * F::TILE, pw * 32 + r, j), static_cast<const T*>(a.q) + (real ? o + j * 8 : 0),
+                       real);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        signal(&bar_q);
+        if (x + nt < x1) {
+          typename Ln::Cursor n = u;
+          Ln::next_unit(c, a, n);
+          prefetch_q(n);
+        }
+        // tiles of values with new tokens
+        for (int i = max(0, (u.s.kv - u.s.q) / kBN - u.t); ok && i < nt; ++i) {
+          const int vs = (kt + i) % VST;
+          const uint32_t tile = sV(vs);
+          if (!(ok = warp_wait(&bar_scan[vs], (scan_par >> vs) & 1, ctl, kErrTimeoutTma))) break;
+          scan_par ^= 1u << vs;
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;
 #pragma unroll 4
-          for (int i = 0; i < CH; ++i) {  // the chunks this thread has copied
-            const int idx = i * 32 + lane;
-            const uint32_t at = tile_at(scan, pw * 32 + idx / CH, idx % CH);
+          for (int k = 0; k < CH; ++k) {
+            const int idx = k * 32 + lane, r = pw * 32 + idx / CH;
+            const uint32_t at = tile_at(tile, r, idx % CH);
             const uint4 v = lds_u4(at);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t wd[4] = {v.x, v.y, v.z, v.w};
             bool hit = false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & EXP) == EXP) hit = true, w[k] &= 0xffff0000u;
-              if (((w[k] >> 16) & EXP) == EXP) hit = true, w[k] &= 0x0000ffffu;
+            for (int e = 0; e < 4; ++e) {
+              if ((wd[e] & EXP) == EXP) hit = true, wd[e] &= 0xffff0000u;
+              if (((wd[e] >> 16) & EXP) == EXP) hit = true, wd[e] &= 0x0000ffffu;
             }
-            if (hit) {
-              sts_v4(at, w[0], w[1], w[2], w[3]);
+            if ((u.t + i) * kBN + r >= u.s.kv) {
+              sts_v4(at, 0u, 0u, 0u, 0u);
+            } else if (hit) {
+              sts_v4(at, wd[0], wd[1], wd[2], wd[3]);
               odd[piece & 3] = piece + 1;
             }
           }
+          signal(&bar_v[vs]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-      auto drain = [&]() {
-        cp_async_wait<0>();
-        if (fb0) signal(fb0, fs0, fp0);
-        if (fb1) signal(fb1, fs1, fp1);
-        if (fb2) signal(fb2, fs2, fp2);
-        fb0 = fb1 = fb2 = nullptr;
-      };
-      auto push = [&](uint64_t* bar, uint32_t scan, int piece) {
-        cp_async_commit();
-        if (fb2) {
-          cp_async_wait<3>();
-          signal(fb0, fs0, fp0);
-          fb0 = fb1, fs0 = fs1, fp0 = fp1;
-          fb1 = fb2, fs1 = fs2, fp1 = fp2;
-          fb2 = bar, fs2 = scan, fp2 = piece;
-        } else if (fb1) {
-          fb2 = bar, fs2 = scan, fp2 = piece;
-        } else if (fb0) {
-          fb1 = bar, fs1 = scan, fp1 = piece;
-        } else {
-          fb0 = bar, fs0 = scan, fp0 = piece;
-        }
-      };
-      // A wait that would block signals everything in flight first: what it
-      // waits for may depend on it.
-      auto acquire = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-        drain();
-        return warp_wait(bar, parity, ctl, kErrTimeoutMma);
-      };
-      auto copy = [&](const void* src, uint32_t tile, int rid) {
-        const uint8_t* p = static_cast<const uint8_t*>(src);
-#pragma unroll 4
-        for (int i = 0; i < CH; ++i) {
-          const int idx = i * 32 + lane, r = idx / CH, j = idx % CH;
-          const int row = __shfl_sync(0xffffffffu, rid, r);
-          const bool real = row >= 0 && j < dch;
-          const size_t off = real ? static_cast<size_t>(row) * (dg * 2) + j * 16 : 0;
-          cp_async16(tile_at(tile, pw * 32 + r, j), p + off, real);
-        }
-      };
-      int kt = 0;  // tiles so far
-      bool ok = true;
-      long long x = x0;
-      for (int piece = 0; ok && x < x1; ++piece) {
-        const int nt = piece_tiles(u, x);
-        const int past = u.s.kv - u.s.q;
-        int rid = look_up(u, u.t);
-        for (int i = 0; i < nt; ++i, ++kt) {
-          const int next = i + 1 < nt ? look_up(u, u.t + i + 1) : -1;
-          const int ks = kt % KST, vs = kt % VST;
-          if (kt >= KST && !(ok = acquire(&bar_kempty[ks], (kt / KST - 1) & 1))) break;
-          copy(c.k, sK(ks), rid);
-          push(&bar_k[ks], 0, piece);
-          if (kt >= VST && !(ok = acquire(&bar_vempty[vs], (kt / VST - 1) & 1))) break;
-          copy(c.v, sV(vs), rid);
-          push(&bar_v[vs], (u.t + i + 1) * kBN > past ? sV(vs) : 0u, piece);
-          rid = next;
-          if (i == 0) {  // the piece's queries, behind its first tile
-            if (piece > 0 && !(ok = acquire(&bar_qfree, (piece - 1) & 1))) break;
-            const int ntile = piece_two(u) ? 2 : 1;
-            for (int w = 0; w < ntile; ++w) {
-              long long off = 0;
-              const bool has = q_row(u, w, pw * 32 + lane, &off);
-#pragma unroll 4
-              for (int k = 0; k < CH; ++k) {
-                const int idx = k * 32 + lane, r = idx / CH, j = idx % CH;
-                const long long o = __shfl_sync(0xffffffffu, off, r);
-                const bool real = __shfl_sync(0xffffffffu, has, r) && j < dch;
-                cp_async16(tile_at(sQ + w * F::TILE, pw * 32 + r, j),
-                           static_cast<const T*>(a.q) + (real ? o + j * 8 : 0), real);
-              }
+      } else {
+        constexpr int CH = DP / 16;  // 16-byte chunks per row of codes
+        {  // the piece's queries, a row per thread, in fp16
+          long long off = 0;
+          const bool has = q_row(u, 0, tid, &off);
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + off);
+          uint32_t top = 0;
+          if constexpr (BF) {
+#pragma unroll 8
+            for (int j = 0; j < DP / 8; ++j) {
+              const uint4 v = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
             }
-            push(&bar_q, 0, piece);
           }
-        }
-        x += nt;
-        if (x < x1) Ln::next_unit(c, a, u);
-      }
-      drain();
-    } else {
-      constexpr int CH = DP / 16;  // 16-byte chunks per row of codes
-      const int dch = dg / 16;
-      // copy side: op n is K (even) or V (odd) of a tile, SR - 1 ahead of the
-      // conversions
-      typename Ln::Cursor q = u;
-      long long xq = x0;
-      int nq = 0, rid = -1;
-      auto copy_next = [&]() {
-        if (xq < x1) {
-          const uint32_t st = sStage + (nq % F::SR) * F::SSLOT;
-          const bool is_k = (nq & 1) == 0;
-          if (is_k) {
-            rid = look_up(q, q.t);
-            const size_t off = static_cast<size_t>(rid < 0 ? 0 : rid);
-            cp_async4(st + F::OPB + tid * 8, c.ks + off, rid >= 0);
-            cp_async4(st + F::OPB + tid * 8 + 4, c.vs + off, rid >= 0);
-          }
-          const uint8_t* p = static_cast<const uint8_t*>(is_k ? c.k : c.v);
+          uint4 first[8];  // half of the row (D = 128) is here before its place is free
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int idx = i * 32 + lane, r = idx / CH, j = idx % CH;
-            const int row = __shfl_sync(0xffffffffu, rid, r);
-            const bool real = row >= 0 && j < dch;
-            const size_t off = real ? static_cast<size_t>(row) * dg + j * 16 : 0;
-            cp_async16(st + (i * 128 + tid) * 16, p + off, real);
-          }
-          ++nq;
-          if (!is_k && ++xq < x1) Ln::next_tile(c, a, q);
-        }
-        cp_async_commit();
-      };
-      auto convert = [&](uint32_t st, uint32_t tile) {
+          for (int j = 0; j < 8; ++j) first[j] = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
+          if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
+          // bf16 rows: the largest magnitude to [1, 2) by a power of two
+          int ex = static_cast<int>(top >> 7);
+          ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
+          const float up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+          qfac[piece & 1][tid] = BF ? __uint_as_float(static_cast<uint32_t>(ex) << 23) : 1.f;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int idx = i * 32 + lane, r = idx / CH, j = idx % CH;
-          const uint4 v = lds_u4(st + (i * 128 + tid) * 16);
-          uint32_t h[8];
-          code4_to_f16<CT>(v.x, h[0], h[1]);
-          code4_to_f16<CT>(v.y, h[2], h[3]);
-          code4_to_f16<CT>(v.z, h[4], h[5]);
-          code4_to_f16<CT>(v.w, h[6], h[7]);
-          // the two halves in an order that spreads a quarter warp over the banks
-          const bool swap = DP == 128 && (j & 4);
-          const uint32_t a0 = tile_at(tile, pw * 32 + r, 2 * j), a1 = tile_at(tile, pw * 32 + r, 2 * j + 1);
-          if (swap) {
-            sts_v4(a1, h[4], h[5], h[6], h[7]);
-            sts_v4(a0, h[0], h[1], h[2], h[3]);
-          } else {
-            sts_v4(a0, h[0], h[1], h[2], h[3]);
-            sts_v4(a1, h[4], h[5], h[6], h[7]);
+          for (int j = 0; j < DP / 8; ++j) {
+            const uint4 v = j < 8 ? first[j & 7] : has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (BF) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<false>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+            }
+            sts_v4(tile_at(sQ, tid, j), w[0], w[1], w[2], w[3]);
           }
+          signal(&bar_q);
         }
-      };
-      auto signal = [&](uint64_t* bar) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-#pragma unroll 1
-      for (int i = 0; i < F::SR - 1; ++i) copy_next();
-      int kt = 0;
-      bool ok = true;
-      long long x = x0;
-      for (int piece = 0; ok && x < x1; ++piece) {
-        const int nt = piece_tiles(u, x);
-        for (int i = 0; i < nt; ++i, ++kt) {
-          const int ks = kt % KST, vs = kt % VST;
-          copy_next();
-          cp_async_wait<F::SR - 1>();
-          if (kt >= KST && !(ok = warp_wait(&bar_kempty[ks], (kt / KST - 1) & 1, ctl, kErrTimeoutMma))) break;
-          uint32_t st = sStage + (2 * kt % F::SR) * F::SSLOT;
-          convert(st, sK(ks));
-          {
+        if (x + nt < x1) {
+          typename Ln::Cursor n = u;
+          Ln::next_unit(c, a, n);
+          prefetch_q(n);
+        }
+        // op n's codes (K: n even, V: odd) -> fp16 codes in the tile; rows at
+        // and behind `end` are zeros
+        auto convert = [&](int n, uint32_t tile, int end, uint64_t* bar) -> bool {
+          const int slot = n % F::SR;
+          const uint32_t st = sStage + slot * F::SSLOT;
+          if (!warp_wait(&bar_stage[slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
+          if ((n & 1) == 0) {
             float ksc, vsc;
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ksc), "=f"(vsc) : "r"(st + F::OPB + tid * 8) : "memory");
-            // no scale (a row past the end or of a missing page): a value of zero
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(st + F::OPB + tid * 4) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vsc) : "r"(st + F::OPB + 512 + tid * 4) : "memory");
+            // no scale (a row of a missing page): a value of zero
             if (vsc == 0.f) vsc = kMinScale;
-            const uint32_t sc = sScale + (kt % F::SCS) * F::SCB + tid * 4;
+            const uint32_t sc = sScale + ((n >> 1) % F::SCS) * F::SCB + tid * 4;
             sts_f32(sc, ksc);
             sts_f32(sc + 512, lg2(vsc));
             // a NaN row's scores are NaN; its 1 / scale must not reach the sums of rows that do not see it
-            sts_f32(sc + 1024, vsc == vsc ? 1.f / vsc : 0.f);
+            sts_f32(sc + 1024, vsc == vsc ? __fdividef(1.f, vsc) : 0.f);
           }
-          signal(&bar_k[ks]);
-          copy_next();
-          cp_async_wait<F::SR - 1>();
-          if (kt >= VST && !(ok = warp_wait(&bar_vempty[vs], (kt / VST - 1) & 1, ctl, kErrTimeoutMma))) break;
-          st = sStage + ((2 * kt + 1) % F::SR) * F::SSLOT;
-          convert(st, sV(vs));
-          signal(&bar_v[vs]);
-          if (i == 0) {  // the piece's queries, a row per thread, in fp16
-            if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
-            long long off = 0;
-            const bool has = q_row(u, 0, tid, &off);
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + off);
-            uint32_t top = 0;
-            if constexpr (BF) {
-#pragma unroll 4
-              for (int j = 0; j < DP / 8; ++j) {
-                const uint4 v = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const bool all = end >= kBN;
+          uint4 codes[CH];  // all loads first: a load must not wait for the stores before it
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-              }
-            }
-            // bf16 rows: the largest magnitude to [1, 2) by a power of two
-            int ex = static_cast<int>(top >> 7);
-            ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
-            const float up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            qfac[tid] = BF ? __uint_as_float(static_cast<uint32_t>(ex) << 23) : 1.f;
-#pragma unroll 4
-            for (int j = 0; j < DP / 8; ++j) {
-              const uint4 v = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              if constexpr (BF) {
+          for (int i = 0; i < CH; ++i) codes[i] = lds_u4(st + pw * 32 * DP + (i * 32 + lane) * 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = pack2<false>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
-              }
-              sts_v4(tile_at(sQ, tid, j), w[0], w[1], w[2], w[3]);
-            }
-            signal(&bar_q);
+          for (int i = 0; i < CH; ++i) {
+            const int idx = i * 32 + lane, r = pw * 32 + idx / CH, j = idx % CH;
+            uint4 v = codes[i];
+            if (!all && r >= end) v = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t h[8];
+            code4_to_f16<CT>(v.x, h[0], h[1]);
+            code4_to_f16<CT>(v.y, h[2], h[3]);
+            code4_to_f16<CT>(v.z, h[4], h[5]);
+            code4_to_f16<CT>(v.w, h[6], h[7]);
+            // the two halves in an order that spreads a quarter warp over the banks
+            const bool swap = DP == 128 && (j & 4);
+            const uint32_t a0 = tile_at(tile, r, 2 * j), a1 = tile_at(tile, r, 2 * j + 1);
+            sts_v4(swap ? a1 : a0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+            sts_v4(swap ? a0 : a1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
           }
+          signal(bar);
+          if (lane == 0) mbar_arrive(&bar_sempty[slot]);
+          return true;
+        };
+        for (int i = 0; i < nt; ++i) {
+          const int t = kt + i, ks = t % KST, vs = t % VST, end = u.s.kv - (u.t + i) * kBN;
+          if (t >= KST && !(ok = warp_wait(&bar_kempty[ks], (t / KST - 1) & 1, ctl, kErrTimeoutMma))) break;
+          if (!(ok = convert(2 * t, sK(ks), end, &bar_k[ks]))) break;
+          if (t >= VST && !(ok = warp_wait(&bar_vempty[vs], (t / VST - 1) & 1, ctl, kErrTimeoutMma))) break;
+          if (!(ok = convert(2 * t + 1, sV(vs), end, &bar_v[vs]))) break;
         }
-        x += nt;
-        if (x < x1) Ln::next_unit(c, a, u);
       }
-      cp_async_wait<0>();
+      kt += nt;
+      x += nt;
+      if (x < x1) Ln::next_unit(c, a, u);
     }
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsMma));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REG_MMA));
     if (warp == 12) {
       // ------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_f16(kBM, kBN, MBF, false, false);
@@ -496,9 +438,105 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
         if (x < x1) Ln::next_unit(c, a, u);
       }
     }
+    if (warp == 13 || (warp == 14 && !F::Q8)) {
+      // ------------------------------------------------------- TMA fetches
+      const bool is_k = warp == 13;  // 8-bit: keys and values in turn
+      const int box = a.box_rows, nbox = kBN / box;
+      const int outside = c.num_pages * c.Hkv;  // past the maps: reads as zeros
+      // this lane's box of tile t: its page (-1: none) and first row
+      auto look_up = [&](const typename Ln::Cursor& p, int t, int* r) -> int {
+        const int n = t * kBN + lane * box;
+        *r = 0;
+        if (lane >= nbox || n >= p.s.kv) return -1;
+        const int id = cache_page_id(c, p.b, n, r);
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages)) return id;
+        cache_error(c.err);
+        *r = 0;
+        return -1;
+      };
+      if (lane == 0) tma_prefetch_desc(is_k ? &tm_k : &tm_v);
+      if (F::Q8 && lane == 1) tma_prefetch_desc(&tm_v);
+      int never = 0;
+      WaitCtl drain{c.err, a.timeout_ns, &never};  // for copies in flight, also after a time-out elsewhere
+      bool ok = true;
+      int kt = 0;
+      long long x = x0;
+      int r, id = look_up(u, u.t, &r);  // of the next tile
+      if constexpr (!F::Q8) {
+        const int depth = is_k ? KST : VST;
+        uint64_t* const full = is_k ? bar_k : bar_v;
+        uint64_t* const empty = is_k ? bar_kempty : bar_vempty;
+        uint32_t scanned = 0, scan_par = 0;  // stages whose last tile went to bar_scan; its phase
+        for (; ok && x < x1; ++x, ++kt) {
+          const int st = kt % depth;
+          const int row = r, head = id < 0 ? outside : id * c.Hkv + u.h;
+          const bool scan = !is_k && (u.t + 1) * kBN > u.s.kv - u.s.q;
+          if (x + 1 < x1) {
+            Ln::next_tile(c, a, u);
+            id = look_up(u, u.t, &r);
+          }
+          if (kt >= depth && !(ok = warp_wait(&empty[st], (kt / depth - 1) & 1, ctl, kErrTimeoutMma))) break;
+          uint64_t* const bar = scan ? &bar_scan[st] : &full[st];
+          scanned = scan ? scanned | (1u << st) : scanned & ~(1u << st);
+          scan_par ^= scan ? 1u << st : 0u;
+          if (lane == 0) mbar_expect_tx(bar, F::TILE);
+          else if (!is_k && !scan && lane < 4) mbar_arrive(bar);  // in place of the four helpers
+          __syncwarp();
+          if (lane < nbox) {
+            const uint32_t dst = (is_k ? sK(st) : sV(st)) + lane * box * 128;
+#pragma unroll
+            for (int kb = 0; kb < DP / 64; ++kb)
+              tma_load_3d(base + (dst - sQ) + kb * (kBM * 128), is_k ? &tm_k : &tm_v, bar, kb * 64, row, head);
+          }
+        }
+        if (lane == 0) {
+          for (int t = max(0, kt - depth); t < kt; ++t) {
+            const int st = t % depth;
+            if ((scanned >> st) & 1u) mbar_wait(&bar_scan[st], ~(scan_par >> st) & 1, drain, kErrTimeoutTma);
+            else mbar_wait(&full[st], (t / depth) & 1, drain, kErrTimeoutTma);
+          }
+        }
+      } else {
+        int n = 0;
+        for (; ok && x < x1; ++x) {
+          const int row = r, h = u.h, page = id;
+          if (x + 1 < x1) {
+            Ln::next_tile(c, a, u);
+            id = look_up(u, u.t, &r);
+          }
+          const bool real = page >= 0;
+          const int nreal = __popc(__ballot_sync(0xffffffffu, real));
+          for (int k = 0; k < 2; ++k, ++n) {
+            const int slot = n % F::SR;
+            if (n >= F::SR && !(ok = warp_wait(&bar_sempty[slot], (n / F::SR - 1) & 1, ctl, kErrTimeoutMma))) break;
+            const uint32_t st = sStage + slot * F::SSLOT;
+            if (k == 0 && !real && lane < nbox) {  // no scales: zeros
+              for (int e = 0; e < box; e += 4) {
+                sts_v4(st + F::OPB + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
+                sts_v4(st + F::OPB + 512 + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(&bar_stage[slot], F::OPB + (k == 0 ? nreal * box * 8 : 0));
+            __syncwarp();
+            if (lane < nbox)
+              tma_load_3d_any(base + (st - sQ) + lane * box * DP, k == 0 ? &tm_k : &tm_v, &bar_stage[slot], 0, row,
+                              real ? page * c.Hkv + h : outside);
+            if (k == 0 && real) {
+              const size_t at = static_cast<size_t>((page * c.Hkv + h) * static_cast<int>(c.page.d) + row);
+              bulk_load(base + (st - sQ) + F::OPB + lane * box * 4, c.ks + at, box * 4, &bar_stage[slot]);
+              bulk_load(base + (st - sQ) + F::OPB + 512 + lane * box * 4, c.vs + at, box * 4, &bar_stage[slot]);
+            }
+          }
+        }
+        if (lane == 0)
+          for (int t = max(0, n - F::SR); t < n; ++t)
+            mbar_wait(&bar_stage[t % F::SR], (t / F::SR) & 1, drain, kErrTimeoutTma);
+      }
+    }
   } else {
     // ---------------------------------- softmax, correction, epilogue (group w)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::REG_SOFTMAX));
     const int w = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -515,12 +553,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
       const int rr = u.rt * F::ROWS + (two ? w * kBM : 0) + r;
       const int tok = rr < u.s.q * a.G ? static_cast<int>(a.g_div.div(rr)) : -1;
       const int past = u.s.kv - u.s.q;
+      // Which of the keys k0 .. k0 + 127 the row sees (bit j of the 128: key
+      // k0 + j): those before the new tokens, and of these by the tree or, without
+      // one, those up to its own.
+      auto see_keys = [&](int k0, uint32_t (&vis)[4]) {
+        if (!a.tree) {
+          const int lim = min(u.s.kv - 1, past + tok) - k0;  // tok -1: rows that do not exist
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int bits = lim + 1 - 32 * k;
+            vis[k] = bits <= 0 ? 0u : bits >= 32 ? 0xffffffffu : (1u << bits) - 1u;
+          }
+          return;
+        }
+        // The warp's tokens, eight at a time: a load brings 32 keys' bytes of a
+        // token, all 32 loads are in flight together.
+        const int d0 = k0 - past;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) vis[k] = 0u;
+        const int lo = __shfl_sync(0xffffffffu, tok, 0);
+        const int hi = __reduce_max_sync(0xffffffffu, tok);
+        const uint8_t* const rows = a.tree + u.b * a.tree_b;
+#pragma unroll 1
+        for (int t0 = lo; t0 >= 0 && t0 <= hi; t0 += 8) {
+          uint32_t byte[4][8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int d = d0 + 32 * k + lane;
+            const bool in = d >= 0 && d < u.s.q;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              byte[k][e] = in ? __ldg(rows + min(t0 + e, hi) * a.tree_t + d) : d < 0 ? 1u : 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t word = __ballot_sync(0xffffffffu, byte[k][e] != 0u);
+              if (tok == t0 + e) vis[k] = word;
+            }
+          }
+        }
+      };
+      // The group's first tile with new tokens, looked up while the piece's
+      // first scores are under way.
+      uint32_t vis[4] = {0u, 0u, 0u, 0u};
+      int vis_t = max(0, past / kBN - u.t);
+      if (!two) vis_t = vis_t <= w ? 0 : (vis_t - w + 1) >> 1;
+      if (vis_t < n) see_keys((u.t + (two ? vis_t : 2 * vis_t + w)) * kBN, vis);
       float m_ref = -INFINITY, l = 0.f;
       for (int t = 0; t < n; ++t, ++ns) {
-        if (!(ok = warp_wait(&bar_s[w], ns & 1, ctl, kErrTimeoutMma))) break;
-        tc_fence_after();
         const int ti = two ? t : 2 * t + w;       // tile of the piece
         const int k0 = (u.t + ti) * kBN;
+        const bool masked = k0 + kBN > past;
+        if (masked && t != vis_t) see_keys(k0, vis);
+        if (!(ok = warp_wait(&bar_s[w], ns & 1, ctl, kErrTimeoutMma))) break;
+        tc_fence_after();
         const uint32_t sc = sScale + ((kt0 + ti) % F::SCS) * F::SCB;
         uint32_t s[128];
 #pragma unroll
@@ -531,7 +619,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
 #pragma unroll
         for (int j = 0; j < 128; ++j) y[j] = __uint_as_float(s[j]);
         if constexpr (F::Q8) {
-          const float f = a.scale_log2 * qfac[r];
+          const float f = a.scale_log2 * qfac[piece & 1][r];
           const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int j = 0; j < 128; j += 4) {
@@ -541,33 +629,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
             y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
           }
         }
-        if (k0 + kBN > past) {  // keys behind the end, and new tokens
-          if (!a.tree) {
-            const int lim = min(u.s.kv - 1, past + tok) - k0;  // tok -1: rows that do not exist
+        if (masked) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (j > lim) y[j] = -INFINITY;
-          } else {
-            // the warp's tokens one after the other: 32 keys' bytes a load
-            uint32_t vis[4] = {0u, 0u, 0u, 0u};
-            const int lo = __shfl_sync(0xffffffffu, tok, 0);
-            int hi = tok;
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, k));
-            for (int tt = lo; tt >= 0 && tt <= hi; ++tt) {
-              const uint8_t* row = a.tree + u.b * a.tree_b + tt * a.tree_t;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int d = k0 + 32 * k + lane - past;
-                const bool see = d < 0 || (d < u.s.q && __ldg(row + d) != 0);
-                const uint32_t word = __ballot_sync(0xffffffffu, see);
-                if (tok == tt) vis[k] = word;
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (!((vis[j >> 5] >> (j & 31)) & 1u)) y[j] = -INFINITY;
-          }
+          for (int j = 0; j < 128; ++j)
+            if (!((vis[j >> 5] >> (j & 31)) & 1u)) y[j] = -INFINITY;
         }
         float mx8[8];
 #pragma unroll
@@ -645,14 +710,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
       if (!ok) break;
       tc_fence_after();
       const bool odd_values = !F::Q8 && *const_cast<volatile int*>(&odd[piece & 3]) == piece + 1;
-      if (two) {
+      // Q's memory is free for the next piece now, or after the join where
+      // that piece may write what the join uses
+      const bool q_early = two || F::XOWN || (!F::XQ && u.s.q * a.G <= kBM && u.h + 1 < c.Hkv);
+      if (q_early) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_qfree);
       }
-      // one row tile: group 1 hands its state over through Q's memory, in
-      // rounds of as many columns as fit
+      // one row tile: group 1 hands its state over in rounds of XCH columns
       constexpr int NCH = DP / 4;                                  // float4 columns
-      constexpr int XCH = F::XCH < NCH ? F::XCH : NCH, XR = NCH / XCH;
+      constexpr int XCH = F::XCH, XR = NCH / XCH;
       float f0 = 1.f, f1 = 0.f;
       const bool whole = u.t == 0 && nt == u.ntiles;
       float* const part = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (x > x0 ? 1 : 0)) * tc_part_floats<CT, DP>();
@@ -680,7 +747,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              sts_v4(sQ + ((k + j) * kBM + r) * 16, ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+              sts_v4(sX + ((k + j) * kBM + r) * 16, ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_xfull);
@@ -712,7 +779,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
           if (!two) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 y = lds_f4(sQ + ((k + j) * kBM + r) * 16);
+              const float4 y = lds_f4(sX + ((k + j) * kBM + r) * 16);
               v[4 * j] = fmaf(v[4 * j], f0, y.x * f1);
               v[4 * j + 1] = fmaf(v[4 * j + 1], f0, y.y * f1);
               v[4 * j + 2] = fmaf(v[4 * j + 2], f0, y.z * f1);
@@ -761,7 +828,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
         }
       }
       tc_fence_before();
-      if (!two) {
+      if (!q_early) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_qfree);
       }
@@ -778,53 +845,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_cache_tc_kernel(CacheArgs 
 }
 
 // Joins the partial states of the units that block borders cut: block (i, y)
-// looks at border i + 1 and, where it is the first inside its unit, joins rows
-// 32 y .. 32 y + 31, a row per lane, every eighth group of four columns per warp.
+// joins rows 32 y .. 32 y + 31 of the unit that border i + 1 is the first to
+// cut, a row per lane, every eighth group of four columns per warp.
 template <typename T, int CT, int DP>
-__global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, CacheAttnArgs a, int dg, int nblocks) {
+__global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, CacheAttnArgs a, int dg) {
   using F = TcCfg<CT, DP>;
   using Ln = Line<F::ROWS, kBN>;
   constexpr bool BF = DT<T>::bf16;
   constexpr int NC = DP / 32;  // float4 columns per thread
   __shared__ typename Ln::Shared line;
-  long long mine, before;
-  const long long len = Ln::template length<256>(c, a, line, &mine, &before);
-  const int i = blockIdx.x + 1;
-  const long long x = cut(len, nblocks, i);
-  if (x >= len) return;
+  __shared__ int slots[kTcBlocks];
+  __shared__ float fs[kTcBlocks][32];
+  __shared__ float red[8][32];
   typename Ln::Cursor u;
-  Ln::template find<256>(c, a, line, x, mine, before, u);
-  const long long u0 = x - u.t, u1 = u0 + u.ntiles;
-  if (u.t == 0 || cut(len, nblocks, i - 1) > u0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int prow = blockIdx.y * 32 + lane, rr = u.rt * F::ROWS + prow;
+  const int parts = unit_parts<Ln, 256>(c, a, line, kTcBlocks, blockIdx.x + 1, slots, u);
+  wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
+  if (parts == 0) return;
   const int rows = u.s.q * a.G;
   if (u.rt * F::ROWS + static_cast<int>(blockIdx.y) * 32 >= rows) return;
-  const int b1 = block_of(len, nblocks, u1 - 1);
-  auto state = [&](int b) -> const float* {
-    const long long s = cut(len, nblocks, b);
-    if (s == cut(len, nblocks, b + 1)) return nullptr;  // an empty piece
-    return a.ws + (static_cast<size_t>(b) * 2 + (s < u0 ? 1 : 0)) * tc_part_floats<CT, DP>();
-  };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int prow = blockIdx.y * 32 + lane, rr = u.rt * F::ROWS + prow;
+  auto part = [&](int i) { return a.ws + static_cast<size_t>(slots[i]) * tc_part_floats<CT, DP>(); };
+  // every warp looks at every eighth part's maximum and sum
   float mm = -INFINITY;
-  for (int b = i - 1; b <= b1; ++b) {
-    const float* p = state(b);
-    if (p) mm = fmaxf(mm, __ldcg(p + F::ROWS * DP + prow));
-  }
+  for (int i = warp; i < parts; i += 8)
+    if (slots[i] >= 0) mm = fmaxf(mm, __ldcg(part(i) + F::ROWS * DP + prow));
+  red[warp][lane] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mm = fmaxf(mm, red[w][lane]);
+  __syncthreads();
   float ll = 0.f;
+  for (int i = warp; i < parts; i += 8) {
+    float f = 0.f;
+    if (slots[i] >= 0) {
+      const float pm = __ldcg(part(i) + F::ROWS * DP + prow), pl = __ldcg(part(i) + F::ROWS * (DP + 1) + prow);
+      f = pm == -INFINITY ? 0.f : ex2(pm - mm);
+      ll += mm == -INFINITY ? pl : pl * f;  // a NaN sum stays one where no score was a number
+    }
+    fs[i][lane] = f;
+  }
+  red[warp][lane] = ll;
+  __syncthreads();
+  ll = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) ll += red[w][lane];
   float v[NC][4] = {};
-#pragma unroll 2
-  for (int b = i - 1; b <= b1; ++b) {
-    const float* p = state(b);
-    if (!p) continue;
-    const float pm = __ldcg(p + F::ROWS * DP + prow), pl = __ldcg(p + F::ROWS * (DP + 1) + prow);
-    const float f = pm == -INFINITY ? 0.f : ex2(pm - mm);
-    ll += mm == -INFINITY ? pl : pl * f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float f = fs[i][lane];
+    // (a block without a piece has factor 0; the first one listed always has a piece)
+    const float4* p = reinterpret_cast<const float4*>(part(slots[i] < 0 ? 0 : i)) + prow;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int ch = warp + 8 * k;
       if (ch * 4 < dg) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + ch * F::ROWS + prow);
+        const float4 y = __ldcg(p + ch * F::ROWS);
         v[k][0] = fmaf(y.x, f, v[k][0]);
         v[k][1] = fmaf(y.y, f, v[k][1]);
         v[k][2] = fmaf(y.z, f, v[k][2]);
@@ -852,22 +928,21 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
 }
 
 template <typename T, int CT, int DP>
-cudaError_t run_tc(int dg, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
+cudaError_t run_tc(int dg, const PageMaps& m, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
   auto* kern = attn_cache_tc_kernel<T, CT, DP>;
   constexpr int smem = TcCfg<CT, DP>::SMEM;
   cudaError_t e = smem_attr_once(kern, smem, done);
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache_tc", s);
-  kern<<<kTcBlocks, kTcThreads, smem, s>>>(c, a, dg);
+  kern<<<kTcBlocks, kTcThreads, smem, s>>>(m.k, m.v, c, a, dg);
   prof_end(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache_tc_join", s);
-  attn_cache_tc_join_kernel<T, CT, DP>
-      <<<dim3(kTcBlocks - 1, TcCfg<CT, DP>::ROWS / 32), 256, 0, s>>>(c, a, dg, kTcBlocks);
+  e = launch_join(attn_cache_tc_join_kernel<T, CT, DP>, dim3(kTcBlocks - 1, TcCfg<CT, DP>::ROWS / 32), 256, s, c, a, dg);
   prof_end(s);
-  return cudaGetLastError();
+  return e;
 }
 template <int CT>
 size_t tc_ws_bytes(int D) {

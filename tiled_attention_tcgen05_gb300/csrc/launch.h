@@ -161,6 +161,11 @@ struct CacheAttnArgs {
   float scale_log2;      // sm_scale * log2(e)
   float* ws;
   uint64_t timeout_ns;
+  int box_rows;          // rows per box of the PageMaps
+};
+// k and v as [pages x Hkv, page_size, D] with boxes of box_rows rows.
+struct PageMaps {
+  CUtensorMap k, v;
 };
 cudaError_t launch_cache_append(bool bf16, int ct, int D, const CacheArgs& c, const CacheAppendArgs& a,
                                 cudaStream_t s);
@@ -172,10 +177,11 @@ cudaError_t launch_cache_keep(int ct, int D, const CacheArgs& c, const CacheKeep
 size_t attn_cache_ws_bytes(int D);
 cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
 size_t attn_cache_tc16_ws_bytes(int D);
-cudaError_t launch_attn_cache_tc16(bool bf16, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_cache_tc16(bool bf16, int D, const PageMaps& m, const CacheArgs& c, const CacheAttnArgs& a,
+                                   cudaStream_t s);
 size_t attn_cache_tc8_ws_bytes(int D);
-cudaError_t launch_attn_cache_tc8(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a,
-                                  cudaStream_t s);
+cudaError_t launch_attn_cache_tc8(bool bf16, int ct, int D, const PageMaps& m, const CacheArgs& c,
+                                  const CacheAttnArgs& a, cudaStream_t s);
 
 // Opts kernel `kern` into `bytes` of dynamic shared memory on the current
 // device, once per device (the attribute is per device, so a process that

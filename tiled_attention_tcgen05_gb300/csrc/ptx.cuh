@@ -127,6 +127,21 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// The same for maps without a swizzle: the destination needs 128 bytes of
+// alignment only.
+__device__ __forceinline__ void tma_load_3d_any(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                                int c2) {
+  if (!TA_CHECK_V((smem_u32(dst) & 127u) == 0u && guard_in_dyn_smem(smem_u32(dst)) && (c0 & 15) == 0 && c1 >= 0 &&
+                      c2 >= 0,
+                  smem_u32(dst)))
+    return;
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // 3-D tiled store of one box from shared memory (in the map's swizzled
 // layout) to global memory, tracked as a bulk async-group of this thread.
 // Parts of the box outside the tensor are not written.
