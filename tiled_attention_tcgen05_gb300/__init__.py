@@ -25,6 +25,7 @@ float32 [B, H, M].  sm_scale None means 1/sqrt(D).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -329,6 +330,7 @@ class _CacheStruct(ctypes.Structure):
 
 
 _Strides = ctypes.c_int64 * 3
+_TreeStrides = ctypes.c_int64 * 2
 
 
 class KVCache:
@@ -344,7 +346,7 @@ class KVCache:
     and lengths outside the cache are skipped on the device and make the next
     sync_status() return TA_ERR_INDEX."""
 
-    __slots__ = ("_t", "_c", "_ref", "dtype", "device")
+    __slots__ = ("_t", "_c", "_ref", "_index", "dtype", "device", "shape")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dtype not in _CT:
@@ -367,14 +369,14 @@ class KVCache:
         P, Hkv, page, D = k.shape
         p = [0 if t is None else t.data_ptr() for t in self._t]
         self._c = _CacheStruct(*p, P, Hkv, page, D, _CT[k.dtype])
-        self._ref = ctypes.c_void_p(ctypes.addressof(self._c))
-        self.dtype, self.device = k.dtype, k.device
+        self._ref = ctypes.addressof(self._c)
+        self._index = k.get_device()
+        self.dtype, self.device, self.shape = k.dtype, k.device, k.shape
 
     k = property(lambda self: self._t[0])
     v = property(lambda self: self._t[1])
     k_scale = property(lambda self: self._t[2])
     v_scale = property(lambda self: self._t[3])
-    shape = property(lambda self: self._t[0].shape)
 
 
 def kv_cache(num_pages, Hkv, page_size, D, dtype=torch.bfloat16, device="cuda") -> KVCache:
@@ -387,9 +389,9 @@ def kv_cache(num_pages, Hkv, page_size, D, dtype=torch.bfloat16, device="cuda") 
     return KVCache(k, torch.empty_like(k), ks, vs)
 
 
-def _i32(name, t, shape, dev):
-    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} CUDA tensor on {dev}")
+def _i32(name, t, shape, index):
+    if t.dtype is not torch.int32 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on CUDA device {index}")
 
 
 def _cache_lists(cache, pages, kv_lens, q_lens):
@@ -398,119 +400,118 @@ def _cache_lists(cache, pages, kv_lens, q_lens):
         raise ValueError("cache must be a KVCache")
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
-    B, max_pages = pages.shape
-    dev = cache.device
-    _i32("pages", pages, (B, max_pages), dev)
-    _i32("kv_lens", kv_lens, (B,), dev)
+    index, shape = cache._index, pages.shape
+    B = shape[0]
+    _i32("pages", pages, shape, index)
+    _i32("kv_lens", kv_lens, (B,), index)
     if q_lens is not None:
-        _i32("q_lens", q_lens, (B,), dev)
-    return B, max_pages
+        _i32("q_lens", q_lens, (B,), index)
+    return B, shape[1]
 
 
-def _tokens(name, t, shape, dtype, dev, written=False):
+def _tokens(name, t, shape, dtype, index, written=False):
     """Checks a [B, heads, T, D] tensor with contiguous rows; returns its
     strides (b, head, t)."""
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on CUDA device {index}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if written and not t.is_contiguous():
         # no two elements share memory: each dimension steps over the ones inside it
         end = 1
-        for s, n in sorted((s, n) for s, n in zip(st, shape) if n > 1):
-            if s < end:
+        for step, n in sorted((x, n) for x, n in zip(st, shape) if n > 1):
+            if step < end:
                 raise ValueError(f"{name} overlaps itself")
-            end = s * (n - 1) + end
-    return _Strides(*st[:3])
+            end = step * (n - 1) + end
+    return _Strides(st[0], st[1], st[2])
 
 
-class _On:
-    """The stream a call runs on, with the cache's device made current: the
-    library launches on the current device.  Tensors that the call allocates
-    on one stream and uses on another are recorded there."""
-
-    __slots__ = ("stream", "foreign", "_guard")
-
-    def __init__(self, dev, stream):
-        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        current = torch.cuda.current_stream(dev)
-        if stream is None:
-            stream = current
-        elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        self.foreign = stream.cuda_stream != current.cuda_stream
-        self.stream = stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *a):
-        if self._guard is not None:
-            self._guard.__exit__(*a)
-
-    def ptr(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def used(self, *ts):
-        if self.foreign:
-            for t in ts:
-                t.record_stream(self.stream)
+def _raw_stream(stream, *used):
+    """The handle of the stream a call runs on (None: the current one).  Tensors
+    that the call allocates on the current stream and uses on another are
+    recorded there."""
+    current = torch.cuda.current_stream()
+    if stream is None:
+        return current.cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream.cuda_stream != current.cuda_stream:
+        for t in used:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
+def _on_cache_device(fn):
+    """Runs fn with the cache's device current: the library launches there."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        for cache in args[:2]:
+            if isinstance(cache, KVCache):
+                if torch.cuda.current_device() != cache._index:
+                    with torch.cuda.device(cache._index):
+                        return fn(*args, **kw)
+                break
+        return fn(*args, **kw)
+    return call
+
+
+@_on_cache_device
 def cache_append(cache, k, v, pages, kv_lens, q_lens=None, stream=None):
     """Writes new tokens' keys and values k, v [B, Hkv, T, D] (any strides with
     contiguous rows) to their positions kv_lens - q_lens + t; 8-bit caches are
     quantised with one scale per (token, head)."""
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
-    P, Hkv, page, D = cache.shape
     if k.dim() != 4 or k.dtype not in _DT:
         raise ValueError("k must be a 4-D tensor of float16 or bfloat16")
+    _, Hkv, _, D = cache.shape
     T = k.shape[2]
-    ks = _tokens("k", k, (B, Hkv, T, D), k.dtype, cache.device)
-    vs = _tokens("v", v, (B, Hkv, T, D), k.dtype, cache.device)
-    with _On(cache.device, stream) as on:
-        _check("attn_cache_append", lib.attn_cache_append(
-            cache._ref, _ptr(k), ks, _ptr(v), vs, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), B, T,
-            _DT[k.dtype], on.ptr()))
+    shape = (B, Hkv, T, D)
+    ks = _tokens("k", k, shape, k.dtype, cache._index)
+    vs = _tokens("v", v, shape, k.dtype, cache._index)
+    _check("attn_cache_append", lib.attn_cache_append(
+        cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, pages.data_ptr(), max_pages, kv_lens.data_ptr(),
+        None if q_lens is None else q_lens.data_ptr(), B, T, _DT[k.dtype], _raw_stream(stream)))
 
 
+@_on_cache_device
 def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None):
     """Positions 0 .. N - 1 of every sequence as (k, v) [B, Hkv, N, D] of dtype
     (None: the cache's, bfloat16 for 8-bit caches); zeros at and behind
-    kv_lens.  k, v: tensors to write to."""
+    kv_lens.  k, v: contiguous tensors to write to."""
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, None)
-    P, Hkv, page, D = cache.shape
+    _, Hkv, _, D = cache.shape
     if dtype is None:
         dtype = k.dtype if k is not None else cache.dtype if cache.dtype in _DT else torch.bfloat16
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}")
-    shape = (B, Hkv, int(N), D)
-    with _On(cache.device, stream) as on:
-        out = []
-        for name, t in (("k", k), ("v", v)):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=cache.device)
-                on.used(t)
-            else:
-                _tokens(name, t, shape, dtype, cache.device)
-                if not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous")
-            out.append(t)
-        _check("attn_cache_read", lib.attn_cache_read(
-            cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(out[0]), _ptr(out[1]), B, int(N), _DT[dtype],
-            on.ptr()))
-    return tuple(out)
+    N = int(N)
+    shape = (B, Hkv, N, D)
+    made = []
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _tokens(name, t, shape, dtype, cache._index)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        made.append(k)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        made.append(v)
+    _check("attn_cache_read", lib.attn_cache_read(
+        cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, _DT[dtype],
+        _raw_stream(stream, *made)))
+    return k, v
 
 
+@_on_cache_device
 def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
     """Keeps the accepted tokens of a draft: token keep[b, i] (keep int32 [B, T],
     ascending, i < keep_lens[b]) moves to the place of new token i.  Returns the
@@ -520,14 +521,12 @@ def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
     if keep.dim() != 2:
         raise ValueError("keep must be [B, T]")
     T = keep.shape[1]
-    _i32("keep", keep, (B, T), cache.device)
-    _i32("keep_lens", keep_lens, (B,), cache.device)
-    with _On(cache.device, stream) as on:
-        new = torch.empty((B,), dtype=torch.int32, device=cache.device)
-        on.used(new)
-        _check("attn_cache_keep", lib.attn_cache_keep(
-            cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), _ptr(keep), _ptr(keep_lens), _ptr(new),
-            B, T, on.ptr()))
+    _i32("keep", keep, (B, T), cache._index)
+    _i32("keep_lens", keep_lens, (B,), cache._index)
+    new = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    _check("attn_cache_keep", lib.attn_cache_keep(
+        cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(),
+        keep.data_ptr(), keep_lens.data_ptr(), new.data_ptr(), B, T, _raw_stream(stream, new)))
     return new
 
 
@@ -538,6 +537,7 @@ def attn_cache_workspace_bytes(B, Hq, Hkv, T, N, D, dtype=torch.bfloat16, cache_
     return int(load().attn_cache_workspace_bytes(B, Hq, Hkv, T, min(int(N), 2 ** 31 - 1), D, _DT[dtype], ct))
 
 
+@_on_cache_device
 def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=None, o=None, lse=None, ws=None,
                    stream=None):
     """Attention of new tokens q [B, Hq, T, D] (any strides with contiguous
@@ -547,42 +547,45 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
     t >= q_lens[b] of given o, lse are left as they were."""
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
-    P, Hkv, page, D = cache.shape
-    dev = cache.device
-    if q.dim() != 4 or q.dtype not in _DT:
+    _, Hkv, page, D = cache.shape
+    index, dtype = cache._index, q.dtype
+    if q.dim() != 4 or dtype not in _DT:
         raise ValueError("q must be a 4-D tensor of float16 or bfloat16")
     _, Hq, T, _ = q.shape
     shape = (B, Hq, T, D)
-    qs = _tokens("q", q, shape, q.dtype, dev)
-    ts = None
+    qs = _tokens("q", q, shape, dtype, index)
+    tp = ts = None
     if tree is not None:
-        if tree.dtype not in (torch.bool, torch.uint8) or tree.device != dev or tree.dim() != 3 or \
-                tuple(tree.shape[1:]) != (T, T) or tree.shape[0] not in (1, B) or (T > 1 and tree.stride(2) != 1):
-            raise ValueError(f"tree must be a bool [B or 1, {T}, {T}] tensor on {dev} with contiguous rows")
-        ts = (ctypes.c_int64 * 2)(0 if tree.shape[0] == 1 else tree.stride(0), tree.stride(1))
-    with _On(dev, stream) as on:
-        if o is None:
-            o = torch.empty_like(q)
-            if q.stride() != o.stride():  # an expanded q has rows in common, o has not
-                o = torch.empty(shape, dtype=q.dtype, device=dev)
-            on.used(o)
-        os_ = _tokens("o", o, shape, q.dtype, dev, written=True)
-        if lse is None:
-            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-            on.used(lse)
-        else:
-            _lse_of("lse", lse, B, Hq, T, dev)
-        if ws is None:
-            n = lib.attn_cache_workspace_bytes(B, Hq, Hkv, T, min(max_pages * page, 2 ** 31 - 1), D, _DT[q.dtype],
-                                               _CT[cache.dtype])
-            ws = torch.empty(max(int(n), 16), dtype=torch.uint8, device=dev)
-            on.used(ws)
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be a contiguous CUDA tensor on {dev}")
-        _check("attn_cache_fwd", lib.attn_cache_fwd(
-            _ptr(q), qs, cache._ref, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(q_lens), _ptr(tree), ts, _ptr(o), os_,
-            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), B, Hq, T, _DT[q.dtype],
-            _scale(sm_scale), on.ptr()))
+        if tree.dtype not in (torch.bool, torch.uint8) or tree.get_device() != index or tree.dim() != 3 or \
+                tree.shape[1:] != (T, T) or tree.shape[0] not in (1, B) or (T > 1 and tree.stride(2) != 1):
+            raise ValueError(f"tree must be a bool [B or 1, {T}, {T}] tensor on CUDA device {index} with contiguous rows")
+        ts = _TreeStrides(0 if tree.shape[0] == 1 else tree.stride(0), tree.stride(1))
+        tp = tree.data_ptr()
+    made = []
+    if o is None:
+        o = torch.empty_like(q)
+        if o.stride() != q.stride():  # an expanded q has rows in common, o has not
+            o = torch.empty(shape, dtype=dtype, device=cache.device)
+        made.append(o)
+    os_ = _tokens("o", o, shape, dtype, index, written=True)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
+        made.append(lse)
+    elif lse.dtype is not torch.float32 or lse.shape != (B, Hq, T) or lse.get_device() != index or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on CUDA device {index}")
+    if ws is None:
+        n = lib.attn_cache_workspace_bytes(B, Hq, Hkv, T, min(max_pages * page, 2 ** 31 - 1), D, _DT[dtype],
+                                           _CT[cache.dtype])
+        ws = torch.empty(max(int(n), 16), dtype=torch.uint8, device=cache.device)
+        made.append(ws)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on CUDA device {index}")
+    _check("attn_cache_fwd", lib.attn_cache_fwd(
+        q.data_ptr(), qs, cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(),
+        None if q_lens is None else q_lens.data_ptr(), tp, ts, o.data_ptr(), os_, lse.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), B, Hq, T, _DT[dtype], -1.0 if sm_scale is None else float(sm_scale),
+        _raw_stream(stream, *made)))
     return o, lse
 
 

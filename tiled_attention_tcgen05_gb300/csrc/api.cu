@@ -52,6 +52,7 @@ static ta_status guard_status() {
                                {"merge.cu", guard_take_merge},   {"fp32.cu", guard_take_fp32},
                                {"bwd_pw_steps.cu", guard_take_bwd_pw_steps},
                                {"cache_io.cu", guard_take_cache_io}, {"attn_cache.cu", guard_take_attn_cache},
+                               {"attn_cache8.cu", guard_take_attn_cache8},
                                {"attn_cache_tc.cu", guard_take_attn_cache_tc},
                                {"attn_cache_tc8.cu", guard_take_attn_cache_tc8}};
   bool failed = false;
@@ -687,23 +688,25 @@ static ta_status cache_dtype_status(ta_dtype dt, ta_dtype ct) {
   return TA_OK;
 }
 
-// Query rows per key head up to which the kernel that reads each key once per
-// 16 rows is used.
-constexpr long long kFewRows = 16;
-
 // Rows of a TMA box: the largest of 32, 16, 8 that divides a page, so that a
 // box never leaves its page and starts on a swizzle atom; 0: none does.
 static int page_box_rows(int page) { return page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : page % 8 == 0 ? 8 : 0; }
 
-static bool attn_cache_uses_tc(int G, int T, int page) {
-  return static_cast<long long>(G) * T > kFewRows && page_box_rows(page) > 0;
+// Query rows per key head up to which attn_cache (16 to 64 rows per unit, exact
+// row tiles) is used; beyond, the tcgen05 kernel, whose tile has 128 rows.
+static bool attn_cache_few_rows(int D, long long rows) { return rows <= (D <= 64 ? 64 : 32); }
+
+static bool attn_cache_uses_tc(int D, long long rows, int page) {
+  return !attn_cache_few_rows(D, rows) && page_box_rows(page) > 0;
 }
 
-// The larger of the two kernels' needs: page_size is not among the arguments
-// of attn_cache_workspace_bytes.
+// The larger of the two kernels' needs where page_size, which is not among the
+// arguments of attn_cache_workspace_bytes, decides.
 static size_t attn_cache_bytes(int G, int T, int D, ta_dtype ct) {
-  if (static_cast<long long>(G) * T <= kFewRows) return attn_cache_ws_bytes(D);
-  return cache_type(ct) == kCache16 ? attn_cache_tc16_ws_bytes(D) : attn_cache_tc8_ws_bytes(D);
+  const long long rows = static_cast<long long>(G) * T;
+  const size_t few = attn_cache_ws_bytes(D, rows);
+  if (attn_cache_few_rows(D, rows)) return few;
+  return std::max(few, cache_type(ct) == kCache16 ? attn_cache_tc16_ws_bytes(D) : attn_cache_tc8_ws_bytes(D));
 }
 
 // 4-byte arrays (lengths, page tables, lse).
@@ -1136,7 +1139,7 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
   const int ct = cache_type(cache->ct);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dt == TA_BF16;
-  if (!attn_cache_uses_tc(a.G, T, cache->page_size))
+  if (!attn_cache_uses_tc(cache->D, static_cast<long long>(a.G) * T, cache->page_size))
     return cuda_status(launch_attn_cache(bf16, ct, cache->D, c, a, s));
   PageMaps m;
   const long long heads = static_cast<long long>(c.num_pages) * c.Hkv;

@@ -1,9 +1,8 @@
 // Writing to, reading from and compacting a paged key/value cache.
 //
 // All three are bound by memory traffic (or, for a token a sequence, by
-// latency).  Rows are spread over groups of D / 8 lanes, 8 elements a lane: a
-// lane's 16-bit accesses are 16 bytes and a warp's accesses cover whole
-// 128-byte lines; consecutive groups take consecutive tokens of one head,
+// latency).  Rows are spread over groups of lanes, 8 or 16 elements a lane: a
+// lane's accesses are 16 bytes and a warp's cover whole 128-byte lines; consecutive groups take consecutive tokens of one head,
 // which lie side by side in a page.
 #include "cache.cuh"
 #include "launch.h"
@@ -12,62 +11,77 @@ namespace ta {
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(static_cast<const uint4*>(p)); }
 
+// Largest magnitudes of two packed pairs, NaN kept.
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const T* h = reinterpret_cast<const T*>(&u);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(h[i]);
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+  if constexpr (DT<T>::bf16) {
+    __nv_bfloat162 r = __hmax2_nan(__habs2(reinterpret_cast<const __nv_bfloat162&>(a)),
+                                   __habs2(reinterpret_cast<const __nv_bfloat162&>(b)));
+    return reinterpret_cast<uint32_t&>(r);
+  } else {
+    __half2 r = __hmax2_nan(__habs2(reinterpret_cast<const __half2&>(a)), __habs2(reinterpret_cast<const __half2&>(b)));
+    return reinterpret_cast<uint32_t&>(r);
+  }
 }
 
-// One lane's 8 elements of a row -> codes; the row's G lanes (a power of two,
+// One lane's 16 elements of a row -> codes; the row's G lanes (a power of two,
 // aligned) must all call it.  Writes the scale from the group's first lane.
 template <typename T, int CT, int G>
-__device__ __forceinline__ uint2 quantise8(const uint4& u, float* scale_out, bool write) {
-  float f[8];
-  unpack8<T>(u, f);
-  // the row's largest magnitude with NaN kept: on bit patterns without the
-  // sign, larger is larger, infinity above every number and NaN above it
-  uint32_t top = 0;
+__device__ __forceinline__ uint4 quantise16(const uint4 (&u)[2], float* scale_out, bool write) {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  uint32_t top = absmax2<T>(absmax2<T>(absmax2<T>(w[0], w[1]), absmax2<T>(w[2], w[3])),
+                            absmax2<T>(absmax2<T>(w[4], w[5]), absmax2<T>(w[6], w[7])));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int s = G / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-  const bool finite = top < 0x7f800000u;
-  const float scale = fmaxf(__fdiv_rn(__uint_as_float(top), kQmax<CT>), kMinScale);
+  for (int s = G / 2; s > 0; s >>= 1) top = absmax2<T>(top, __shfl_xor_sync(0xffffffffu, top, s));
+  top = absmax2<T>(top, __byte_perm(top, top, 0x1032));
+  const float amax = static_cast<float>(reinterpret_cast<const T*>(&top)[0]);
+  const bool finite = amax < INFINITY;  // false for NaN too
+  const float scale = fmaxf(__fdiv_rn(amax, kQmax<CT>), kMinScale);
   const float inv = __frcp_rn(scale);
-  uint2 r = make_uint2(0u, 0u);
-  if (finite) {
-    r.x = code4<CT>(f[0], f[1], f[2], f[3], inv);
-    r.y = code4<CT>(f[4], f[5], f[6], f[7], inv);
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T* h = reinterpret_cast<const T*>(&w[2 * i]);
+    r[i] = code4<CT>(static_cast<float>(h[0]), static_cast<float>(h[1]), static_cast<float>(h[2]),
+                     static_cast<float>(h[3]), inv);
+    if (!finite) r[i] = 0u;
   }
   if (write) *scale_out = finite ? scale : __uint_as_float(0x7fc00000u);
-  return r;
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// cache_append.  Row i of B * Hkv * T is (b, h, t), t fastest.
+// cache_append.  Row i of B * Hkv * T is (b, h, t), t fastest.  8-bit caches: 16
+// elements a lane, so that a row's maximum, division and reciprocal are
+// shared by twice as many (with 8 the instructions, not the memory, set the
+// time of a prompt's rows).
 template <typename T, int CT, int D>
 __global__ void __launch_bounds__(256) append_kernel(CacheArgs c, CacheAppendArgs a) {
-  constexpr int G = D / 8;
+  constexpr int E = CT == kCache16 ? 8 : 16;  // elements per lane
+  constexpr int G = D / E;
   constexpr int U = 2;  // rows of K and of V in flight per lane
   const int g = threadIdx.x % G;
   const int rpb = 256 / G;
   const int base = blockIdx.x * (rpb * U) + threadIdx.x / G;
   int row[U];
-  uint4 xk[U], xv[U];
+  uint4 xk[U][E / 8], xv[U][E / 8];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = base + u * rpb;
     row[u] = -1;
-    xk[u] = xv[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) xk[u][e] = xv[u][e] = make_uint4(0u, 0u, 0u, 0u);
     if (i < a.rows) {
       const int bh = static_cast<int>(a.t_div.div(i)), t = i - bh * c.T;
       const int b = static_cast<int>(a.h_div.div(bh)), h = bh - b * c.Hkv;
       const SeqLens s = cache_lens(c, b);
       if (t < s.q) {
-        const T* pk = static_cast<const T*>(a.k) + b * a.ks[0] + h * a.ks[1] + t * a.ks[2] + g * 8;
-        const T* pv = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + t * a.vs[2] + g * 8;
-        xk[u] = ldg_stream(pk);
-        xv[u] = ldg_stream(pv);
+        const T* pk = static_cast<const T*>(a.k) + b * a.ks[0] + h * a.ks[1] + t * a.ks[2] + g * E;
+        const T* pv = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + t * a.vs[2] + g * E;
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) {
+          xk[u][e] = ldg_stream(pk + 8 * e);
+          xv[u][e] = ldg_stream(pv + 8 * e);
+        }
         int r;
         const int id = cache_page_id(c, b, s.kv - s.q + t, &r);
         row[u] = cache_row(c, h, id, r);
@@ -80,15 +94,15 @@ __global__ void __launch_bounds__(256) append_kernel(CacheArgs c, CacheAppendArg
     const size_t at = static_cast<size_t>(act ? row[u] : 0);
     if constexpr (CT == kCache16) {
       if (act) {
-        *reinterpret_cast<uint4*>(static_cast<T*>(c.k) + at * D + g * 8) = xk[u];
-        *reinterpret_cast<uint4*>(static_cast<T*>(c.v) + at * D + g * 8) = xv[u];
+        *reinterpret_cast<uint4*>(static_cast<T*>(c.k) + at * D + g * 8) = xk[u][0];
+        *reinterpret_cast<uint4*>(static_cast<T*>(c.v) + at * D + g * 8) = xv[u][0];
       }
     } else {
-      const uint2 yk = quantise8<T, CT, G>(xk[u], c.ks + at, act && g == 0);
-      const uint2 yv = quantise8<T, CT, G>(xv[u], c.vs + at, act && g == 0);
+      const uint4 yk = quantise16<T, CT, G>(xk[u], c.ks + at, act && g == 0);
+      const uint4 yv = quantise16<T, CT, G>(xv[u], c.vs + at, act && g == 0);
       if (act) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.k) + at * D + g * 8) = yk;
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.v) + at * D + g * 8) = yv;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(c.k) + at * D + g * 16) = yk;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(c.v) + at * D + g * 16) = yv;
       }
     }
   }
@@ -189,10 +203,10 @@ __global__ void __launch_bounds__(256) read_kernel(CacheArgs c, CacheReadArgs a)
 // place of a later token: rows move in rounds, each read into registers whole
 // before it is written.
 template <int RB>  // bytes of a row
-__global__ void __launch_bounds__(256) keep_kernel(CacheArgs c, CacheKeepArgs a, bool scaled) {
+__global__ void __launch_bounds__(128) keep_kernel(CacheArgs c, CacheKeepArgs a, bool scaled) {
   constexpr int L = RB / 16;          // lanes per row and tensor
   constexpr int U = 4;                // rows in flight per lane
-  constexpr int RPR = 256 / (2 * L);  // rows of K and V per step
+  constexpr int RPR = 128 / (2 * L);  // rows of K and V per step
   const int b = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
   const SeqLens s = cache_lens(c, b);
   const int n = __ldg(a.keep_lens + b);
@@ -203,7 +217,7 @@ __global__ void __launch_bounds__(256) keep_kernel(CacheArgs c, CacheKeepArgs a,
   if (n < 0 || n > s.q) {
     bad = true;
   } else {
-    for (int i = threadIdx.x; i < n; i += 256) {
+    for (int i = threadIdx.x; i < n; i += 128) {
       const int j = __ldg(keep + i);
       const int before = i ? __ldg(keep + i - 1) : -1;
       if (j <= before || j >= s.q) bad = true;
@@ -255,7 +269,7 @@ __global__ void __launch_bounds__(256) keep_kernel(CacheArgs c, CacheKeepArgs a,
 
 template <typename T, int CT, int D>
 static cudaError_t append_t(const CacheArgs& c, const CacheAppendArgs& a, cudaStream_t s) {
-  constexpr int rows = 2 * (256 / (D / 8));
+  constexpr int rows = 2 * (256 / (D / (CT == kCache16 ? 8 : 16)));
   append_kernel<T, CT, D><<<(a.rows + rows - 1) / rows, 256, 0, s>>>(c, a);
   return cudaGetLastError();
 }
@@ -301,11 +315,11 @@ cudaError_t launch_cache_keep(int ct, int D, const CacheArgs& c, const CacheKeep
   const int blocks = c.B * c.Hkv;
   const bool scaled = ct != kCache16;
   switch (rb) {
-    case 16: keep_kernel<16><<<blocks, 256, 0, s>>>(c, a, scaled); break;
-    case 32: keep_kernel<32><<<blocks, 256, 0, s>>>(c, a, scaled); break;
-    case 64: keep_kernel<64><<<blocks, 256, 0, s>>>(c, a, scaled); break;
-    case 128: keep_kernel<128><<<blocks, 256, 0, s>>>(c, a, scaled); break;
-    case 256: keep_kernel<256><<<blocks, 256, 0, s>>>(c, a, scaled); break;
+    case 16: keep_kernel<16><<<blocks, 128, 0, s>>>(c, a, scaled); break;
+    case 32: keep_kernel<32><<<blocks, 128, 0, s>>>(c, a, scaled); break;
+    case 64: keep_kernel<64><<<blocks, 128, 0, s>>>(c, a, scaled); break;
+    case 128: keep_kernel<128><<<blocks, 128, 0, s>>>(c, a, scaled); break;
+    case 256: keep_kernel<256><<<blocks, 128, 0, s>>>(c, a, scaled); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

@@ -47,6 +47,7 @@ uint32_t guard_take_fp32(uint32_t* info);
 uint32_t guard_take_bwd_pw_steps(uint32_t* info);
 uint32_t guard_take_cache_io(uint32_t* info);
 uint32_t guard_take_attn_cache(uint32_t* info);
+uint32_t guard_take_attn_cache8(uint32_t* info);
 uint32_t guard_take_attn_cache_tc(uint32_t* info);
 uint32_t guard_take_attn_cache_tc8(uint32_t* info);
 #endif
@@ -174,7 +175,7 @@ cudaError_t launch_cache_keep(int ct, int D, const CacheArgs& c, const CacheKeep
 // Attention over the cache: attn_cache for few query rows per key head, the
 // tc kernels for many (attn_cache_uses_tc).  Workspaces hold the partial states
 // of the units that more than one block works on.
-size_t attn_cache_ws_bytes(int D);
+size_t attn_cache_ws_bytes(int D, long long rows);  // rows: G * T
 cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s);
 size_t attn_cache_tc16_ws_bytes(int D);
 cudaError_t launch_attn_cache_tc16(bool bf16, int D, const PageMaps& m, const CacheArgs& c, const CacheAttnArgs& a,
