@@ -148,33 +148,49 @@ __device__ __forceinline__ int block_of(long long len, int n, long long y) {
 
 // ----------------------------------------------------------------- joining
 // The join kernel is launched while the main kernel runs (programmatic
-// dependent launch): it looks its units up meanwhile and waits before it reads
-// partial states.
+// dependent launch) and waits for its end before it reads anything.
 __device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_main_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Block `border - 1`'s look at border `border` of n: where it is the first
-// inside its unit, lists the partial states of the unit's blocks (slot: block
-// * 2 + which, -1 for a block without a piece) and returns their number;
-// else 0.  All threads, with a barrier.
-template <typename Ln, int THREADS>
-__device__ __forceinline__ int unit_parts(const CacheArgs& c, const CacheAttnArgs& a, typename Ln::Shared& sh, int n,
-                                          int border, int* slots, typename Ln::Cursor& u) {
-  long long mine, before;
-  const long long len = Ln::template length<THREADS>(c, a, sh, &mine, &before);
-  const long long x = cut(len, n, border);
-  if (x >= len) return 0;
-  Ln::template find<THREADS>(c, a, sh, x, mine, before, u);
-  const long long u0 = x - u.t, u1 = u0 + u.ntiles;  // the unit's places
-  if (u.t == 0 || cut(len, n, border - 1) > u0) return 0;
-  const int parts = block_of(len, n, u1 - 1) - (border - 1) + 1;
-  for (int i = threadIdx.x; i < parts; i += THREADS) {
-    const int b = border - 1 + i;
-    const long long s = cut(len, n, b);
-    slots[i] = s == cut(len, n, b + 1) ? -1 : b * 2 + (s < u0 ? 1 : 0);
+// What the join needs to know about the unit that block i's first border cuts,
+// where this is the first border inside the unit; written by block i of the
+// main kernel in every call (parts = 0 otherwise), so that the join does not
+// look the unit up again.
+struct __align__(16) CutUnit {
+  int b, h, rt, parts;  // unit; blocks first .. first + parts - 1 hold its pieces
+  int first;
+  int first_slot;       // the first block's slot (the others': 0)
+  int q;                // the sequence's new tokens
+  int sparse;           // fewer tiles than blocks: some of the blocks are empty
+  long long len, pad2;
+};
+
+// Block i's record; `u` is its first place, len the line's length (0: none).
+template <typename Cursor>
+__device__ __forceinline__ void write_cut(CutUnit* out, long long len, int n, int i, long long x0, long long x1,
+                                          const Cursor* u) {
+  CutUnit r = {};
+  if (x0 < x1 && i > 0 && u->t > 0) {
+    // the block that holds the place before starts at or before the unit?
+    const long long u0 = x0 - u->t;
+    const int first = block_of(len, n, x0 - 1);
+    const long long before = cut(len, n, first);
+    if (before <= u0) {
+      r.b = u->b, r.h = u->h, r.rt = u->rt, r.q = u->s.q;
+      r.first = first;
+      r.parts = block_of(len, n, u0 + u->ntiles - 1) - first + 1;
+      r.first_slot = before < u0 ? 1 : 0;
+      r.sparse = len < n;
+      r.len = len;
+    }
   }
-  __syncthreads();
-  return parts;
+  out[i] = r;
+}
+// Slot of part k, -1 for a block without a piece.
+__device__ __forceinline__ int part_slot(const CutUnit& r, int n, int k) {
+  const int b = r.first + k;
+  if (r.sparse && cut(r.len, n, b) == cut(r.len, n, b + 1)) return -1;
+  return b * 2 + (k == 0 ? r.first_slot : 0);
 }
 
 // Launches the join kernel behind the main one.

@@ -136,9 +136,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
   long long mine, before;
   const long long len = Ln::template length<kWarps * 32>(c, a, line, &mine, &before);
   const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
-  if (x0 >= x1) return;
   typename Ln::Cursor cc;
-  Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
+  if (x0 < x1) Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
+  if (threadIdx.x == 0)
+    write_cut(reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(gridDim.x) * 2 * F::PART), len, gridDim.x, blockIdx.x,
+              x0, x1, &cc);
+  if (x0 >= x1) return;
   typename Ln::Cursor pc = cc;  // the next tile to copy
 
   uint8_t* const ring = smem + warp * F::RING;
@@ -704,15 +707,15 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   constexpr int VEC = D >= 128 ? 4 : (D >= 64 ? 2 : 1);  // elements per lane
   using F = Cfg<CT, D, MT>;
   constexpr int ROWS = F::ROWS;
-  using Ln = Line<ROWS, F::TK>;
-  __shared__ typename Ln::Shared line;
   __shared__ int slots[kBlocks];
   __shared__ float fs[8][kBlocks];
   __shared__ float other[8][D + 1];
-  typename Ln::Cursor u;
-  const int parts = unit_parts<Ln, 512>(c, a, line, kBlocks, blockIdx.x + 1, slots, u);
   wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
-  if (parts == 0 || static_cast<int>(blockIdx.y) * 8 + u.rt * ROWS >= u.s.q * a.G) return;
+  const CutUnit u = reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(kBlocks) * 2 * F::PART)[blockIdx.x + 1];
+  const int parts = u.parts;
+  if (parts == 0 || static_cast<int>(blockIdx.y) * 8 + u.rt * ROWS >= u.q * a.G) return;
+  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot(u, kBlocks, i);
+  __syncthreads();
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + wrow;
   auto part = [&](int i) { return a.ws + static_cast<size_t>(slots[i]) * F::PART; };
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   if (half) return;
   const int qr = u.rt * ROWS + r;
   const int t = static_cast<int>(a.g_div.div(qr)), hq = u.h * a.G + (qr - t * a.G);
-  if (t >= u.s.q) return;
+  if (t >= u.q) return;
   const float norm = ll == 0.f ? 0.f : 1.f / ll;
   if (lane_on) {
     T* out = static_cast<T*>(a.o) + u.b * a.os[0] + hq * a.os[1] + t * a.os[2] + lane * VEC;

@@ -151,9 +151,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   long long mine, before;
   const long long len = Ln::template length<kTcThreads>(c, a, line, &mine, &before);
   const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
-  if (x0 >= x1) return;
   typename Ln::Cursor u;
-  Ln::template find<kTcThreads>(c, a, line, x0, mine, before, u);
+  if (x0 < x1) Ln::template find<kTcThreads>(c, a, line, x0, mine, before, u);
+  if (threadIdx.x == 0)
+    write_cut(reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(gridDim.x) * 2 * tc_part_floats<CT, DP>()), len,
+              gridDim.x, blockIdx.x, x0, x1, &u);
+  if (x0 >= x1) return;
 
   uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(base);
@@ -850,19 +853,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <typename T, int CT, int DP>
 __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, CacheAttnArgs a, int dg) {
   using F = TcCfg<CT, DP>;
-  using Ln = Line<F::ROWS, kBN>;
   constexpr bool BF = DT<T>::bf16;
   constexpr int NC = DP / 32;  // float4 columns per thread
-  __shared__ typename Ln::Shared line;
   __shared__ int slots[kTcBlocks];
   __shared__ float fs[kTcBlocks][32];
   __shared__ float red[8][32];
-  typename Ln::Cursor u;
-  const int parts = unit_parts<Ln, 256>(c, a, line, kTcBlocks, blockIdx.x + 1, slots, u);
   wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
-  if (parts == 0) return;
-  const int rows = u.s.q * a.G;
-  if (u.rt * F::ROWS + static_cast<int>(blockIdx.y) * 32 >= rows) return;
+  const CutUnit u =
+      reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(kTcBlocks) * 2 * tc_part_floats<CT, DP>())[blockIdx.x + 1];
+  const int parts = u.parts, rows = u.q * a.G;
+  if (parts == 0 || u.rt * F::ROWS + static_cast<int>(blockIdx.y) * 32 >= rows) return;
+  for (int i = threadIdx.x; i < parts; i += 256) slots[i] = part_slot(u, kTcBlocks, i);
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int prow = blockIdx.y * 32 + lane, rr = u.rt * F::ROWS + prow;
   auto part = [&](int i) { return a.ws + static_cast<size_t>(slots[i]) * tc_part_floats<CT, DP>(); };
@@ -947,7 +949,7 @@ cudaError_t run_tc(int dg, const PageMaps& m, const CacheArgs& c, const CacheAtt
 template <int CT>
 size_t tc_ws_bytes(int D) {
   const int f = D <= 64 ? tc_part_floats<CT, 64>() : tc_part_floats<CT, 128>();
-  return static_cast<size_t>(kTcBlocks) * 2 * f * sizeof(float);
+  return static_cast<size_t>(kTcBlocks) * (2 * f * sizeof(float) + sizeof(CutUnit));
 }
 
 }  // namespace
