@@ -11,7 +11,9 @@ cudaError_t launch_attn_cache_rows8(bool bf16, int ct, int D, int mt, const Cach
 static int row_tiles(int D, long long rows) { return rows <= 16 ? 1 : rows <= 32 || D > 64 ? 2 : 4; }
 
 size_t attn_cache_ws_bytes(int D, long long rows) {
-  return static_cast<size_t>(kBlocks) * (2 * (16 * row_tiles(D, rows)) * (D + 2) * sizeof(float) + sizeof(CutUnit));
+  const int mt = row_tiles(D, rows);
+  const size_t blocks = mt == 1 ? Cfg<kCache16, 64, 1>::BLOCKS : Cfg<kCache16, 64, 2>::BLOCKS;
+  return blocks * (2 * (16 * mt) * (D + 2) * sizeof(float) + sizeof(CutUnit));
 }
 
 cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {

@@ -17,7 +17,7 @@
 // a key's fragment is loaded, or converted, once for all of them).  A block's
 // four warps take 16 or 32 keys of a tile each and keep their own running
 // maximum, sum and accumulators in registers: no barrier between tiles.  Every warp copies its keys and values into its own ring in shared
-// memory (cp.async, swizzled), kStages tiles ahead.  The warps' states are
+// memory (cp.async, swizzled).  The warps' states are
 // joined through shared memory at the end of a sequence.
 //
 // Work is cut as attn_cache.cuh says, two blocks per SM.
@@ -29,12 +29,17 @@ namespace ta {
 namespace {
 
 constexpr int kWarps = 4;      // warps per block, each with its own keys
-constexpr int kStages = 3;     // tiles in a warp's ring
-constexpr int kBlocks = 304;   // two per SM: 152 SMs
 
 template <int CT, int D, int MT>
 struct Cfg {
   static constexpr int ROWS = 16 * MT;                      // query rows per unit
+  // Two blocks per SM and two tiles in a warp's ring, for [64, 32/8, 1, 8192,
+  // 128] bf16 and [3, 32/4, 1, 131071, 128] e4m3: 204 and 73 us; three
+  // stages 214 and 76; three blocks (168 registers) of two stages 210 and 80;
+  // one block of six stages 268 and 111.
+  static constexpr int BPS = 2;
+  static constexpr int BLOCKS = 152 * BPS;
+  static constexpr int STAGES = 2;
   static constexpr int ES = CT == kCache16 ? 2 : 1;         // bytes per element
   static constexpr int RB = D * ES;                         // bytes per row
   static constexpr int KW = RB >= 256 ? 16 : 32;            // keys per warp and tile
@@ -42,7 +47,7 @@ struct Cfg {
   static constexpr int CPR = RB / 16;                       // 16-byte chunks per row
   static constexpr int SLOT = 2 * KW * RB;                  // K and V of one warp and stage
   static constexpr int SCALES = CT == kCache16 ? 0 : KW * 12;  // K scale, V scale (then its log2), 1 / V scale
-  static constexpr int RING = kStages * (SLOT + SCALES);    // one warp
+  static constexpr int RING = STAGES * (SLOT + SCALES);    // one warp
   static_assert(SLOT >= 16 * D * 4, "a slot holds a row tile of a warp's accumulators");
   static constexpr int QBYTES = MT > 1 ? MT * D * 32 : 0;   // Q fragments (one row tile's stay in registers)
   static constexpr int SMEM = kWarps * RING + kWarps * ROWS * 8 + QBYTES + ROWS * 4;
@@ -120,7 +125,7 @@ __device__ __forceinline__ int oswz(int r, int ch) {
 }
 
 template <typename T, int CT, int D, int MT>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c, CacheAttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_kernel(CacheArgs c, CacheAttnArgs a) {
   using F = Cfg<CT, D, MT>;
   constexpr bool BF = DT<T>::bf16;
   constexpr bool MBF = BF && CT == kCache16;  // matrix instructions in bf16
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
 
   look_up();
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
+  for (int s = 0; s < F::STAGES; ++s) {
     if (x0 + s < x1) {
       copy_tile(s);
       Ln::next_tile(c, a, pc);
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
       }
     };
 
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<F::STAGES - 1>();
     __syncwarp();
     const uint32_t ks_a = ring_a + slot * (F::SLOT + F::SCALES), vs_a = ks_a + KW * F::RB, sc_a = ks_a + F::SLOT;
     const int n0 = cc.t * TK + warp * KW;          // this warp's first key
@@ -685,13 +690,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_cache_kernel(CacheArgs c,
     } else {
       __syncwarp();
     }
-    if (x + kStages < x1) {
+    if (x + F::STAGES < x1) {
       copy_tile(slot);
       Ln::next_tile(c, a, pc);
-      if (x + kStages + 1 < x1) look_up();
+      if (x + F::STAGES + 1 < x1) look_up();
     }
     cp_async_commit();
-    slot = slot + 1 == kStages ? 0 : slot + 1;
+    slot = slot + 1 == F::STAGES ? 0 : slot + 1;
     Ln::next_tile(c, a, cc);
   }
 }
@@ -707,14 +712,14 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   constexpr int VEC = D >= 128 ? 4 : (D >= 64 ? 2 : 1);  // elements per lane
   using F = Cfg<CT, D, MT>;
   constexpr int ROWS = F::ROWS;
-  __shared__ int slots[kBlocks];
-  __shared__ float fs[8][kBlocks];
+  __shared__ int slots[F::BLOCKS];
+  __shared__ float fs[8][F::BLOCKS];
   __shared__ float other[8][D + 1];
   wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
-  const CutUnit u = reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(kBlocks) * 2 * F::PART)[blockIdx.x + 1];
+  const CutUnit u = reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART)[blockIdx.x + 1];
   const int parts = u.parts;
   if (parts == 0 || static_cast<int>(blockIdx.y) * 8 + u.rt * ROWS >= u.q * a.G) return;
-  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot(u, kBlocks, i);
+  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot(u, F::BLOCKS, i);
   __syncthreads();
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + wrow;
@@ -800,12 +805,12 @@ cudaError_t run_rows(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s)
   cudaError_t e = smem_attr_once(kern, F::SMEM, done);
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache", s);
-  kern<<<kBlocks, kWarps * 32, F::SMEM, s>>>(c, a);
+  kern<<<F::BLOCKS, kWarps * 32, F::SMEM, s>>>(c, a);
   prof_end(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache_join", s);
-  e = launch_join(attn_cache_join_kernel<T, CT, D, MT>, dim3(kBlocks - 1, F::ROWS / 8), 512, s, c, a);
+  e = launch_join(attn_cache_join_kernel<T, CT, D, MT>, dim3(F::BLOCKS - 1, (min(a.G * c.T, F::ROWS) + 7) / 8), 512, s, c, a);
   prof_end(s);
   return e;
 }
