@@ -1,5 +1,7 @@
 // attn_cache_rows.cuh's kernels for 16-bit caches, and the choice between the
 // kernels of the attention over a cache.
+#include <algorithm>
+
 #include "attn_cache_rows.cuh"
 
 namespace ta {
@@ -8,7 +10,10 @@ cudaError_t launch_attn_cache_rows8(bool bf16, int ct, int D, int mt, const Cach
                                     cudaStream_t s);
 
 // Row tiles (of 16) per unit.
-static int row_tiles(int D, long long rows) { return rows <= 16 ? 1 : rows <= 32 || D > 64 ? 2 : 4; }
+static int row_tiles(int D, long long rows) {
+  const long long most = D <= 64 ? 4 : 2;
+  return static_cast<int>(std::min((rows + 15) / 16, most));
+}
 
 size_t attn_cache_ws_bytes(int D, long long rows) {
   const int mt = row_tiles(D, rows);

@@ -323,17 +323,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             }
           }
         }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][j][i] *= a.scale_log2;
       } else {
         // this lane's key: its value scale's log2 and 1 / scale take its place
         {
           float vscale;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vscale) : "r"(sc_a + KW * 4 + lane * 4) : "memory");
+          if constexpr (!BF) {
+            float kscale;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kscale) : "r"(sc_a + lane * 4) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + lane * 4), "f"(kscale * a.scale_log2) : "memory");
+          }
           // a scale of zero (a row of a page that the cache does not have
           // reads as zeros) stands for a value of zero whatever its codes; a NaN
           // row's scores are NaN, its 1 / scale must not reach other rows' sums
@@ -375,11 +374,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float f;
-              if constexpr (MT == 1) f = f1[e];
-              else f = BF ? facs[mt * 16 + g + 8 * e] : a.scale_log2;
-              s[mt][j][2 * e] = fmaf(s[mt][j][2 * e], f * kx.x, vx.x);
-              s[mt][j][2 * e + 1] = fmaf(s[mt][j][2 * e + 1], f * kx.y, vx.y);
+              float2 k2 = kx;  // fp16 queries: the factor is in it already
+              if constexpr (BF) {
+                float f;
+                if constexpr (MT == 1) f = f1[e];
+                else f = facs[mt * 16 + g + 8 * e];
+                k2 = fmul2(make_float2(f, f), kx);
+              }
+              const float2 t = ffma2(make_float2(s[mt][j][2 * e], s[mt][j][2 * e + 1]), k2, vx);
+              s[mt][j][2 * e] = t.x, s[mt][j][2 * e + 1] = t.y;
             }
           }
         }
@@ -423,6 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
         }
+        if constexpr (CT == kCache16) mx[0] *= a.scale_log2, mx[1] *= a.scale_log2;
         if (__any_sync(0xffffffffu,
                        mx[0] > m[mt][0] + kRescaleThreshold || mx[1] > m[mt][1] + kRescaleThreshold)) {
           float al[2];
@@ -443,23 +447,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float ref = m[mt][e] == -INFINITY ? 0.f : m[mt][e];
+          const float ref = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
+          const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(a.scale_log2, a.scale_log2);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) s[mt][j][2 * e + i] = ex2(s[mt][j][2 * e + i] - ref);
+            float2 t = make_float2(s[mt][j][2 * e], s[mt][j][2 * e + 1]);
+            if constexpr (CT == kCache16) t = ffma2(t, sc2, ref2);
+            else t = fadd2(t, ref2);
+            t = make_float2(ex2(t.x), ex2(t.y));
+            s[mt][j][2 * e] = t.x, s[mt][j][2 * e + 1] = t.y;
+            if constexpr (CT == kCache16) sum = fadd2(sum, t);
+            else sum = ffma2(t, lds_f2(sc_a + KW * 8 + (j * 8 + 2 * cq) * 4), sum);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if constexpr (CT == kCache16) {
-            l[mt][0] += s[mt][j][0] + s[mt][j][1];
-            l[mt][1] += s[mt][j][2] + s[mt][j][3];
-          } else {
-            const float2 iv = lds_f2(sc_a + KW * 8 + (j * 8 + 2 * cq) * 4);
-            l[mt][0] = fmaf(s[mt][j][0], iv.x, fmaf(s[mt][j][1], iv.y, l[mt][0]));
-            l[mt][1] = fmaf(s[mt][j][2], iv.x, fmaf(s[mt][j][3], iv.y, l[mt][1]));
-          }
+          l[mt][e] += sum.x + sum.y;
         }
 #pragma unroll
         for (int p = 0; p < KW / 16; ++p) {
@@ -819,7 +820,10 @@ template <typename T, int CT, int D>
 cudaError_t run_mt(int mt, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   if (mt == 1) return run_rows<T, CT, D, 1>(c, a, s);
   if (mt == 2) return run_rows<T, CT, D, 2>(c, a, s);
-  if constexpr (D <= 64) return run_rows<T, CT, D, 4>(c, a, s);  // (D = 128: 256 accumulators a lane)
+  if constexpr (D <= 64) {  // (D = 128: 192 and 256 accumulators a lane)
+    if (mt == 3) return run_rows<T, CT, D, 3>(c, a, s);
+    return run_rows<T, CT, D, 4>(c, a, s);
+  }
   return cudaErrorInvalidValue;
 }
 template <typename T, int CT>
