@@ -146,7 +146,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
   __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle from lane 0: a value the compiler knows to be the same in the
+  // whole warp lives in uniform registers, which is where the MMAs take their
+  // operands from)
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   let_dependents_launch();
   long long mine, before;
   const long long len = Ln::template length<kTcThreads>(c, a, line, &mine, &before);
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = uniform(tmem_slot);
   const uint32_t col_s[2] = {0u, 128u};
   const uint32_t col_o[2] = {256u, 256u + DP};
 
@@ -402,43 +406,70 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_f16(kBM, kBN, MBF, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(kBM, DP, MBF, false, true);
-      int kt0 = 0;                  // tiles before this piece
-      int np0 = 0, np1 = 0;         // products with V so far, per group
+      // The tiles' stages and phases are counted on, not divided out: this
+      // warp shares its issue slots with the softmax, and what it issues
+      // between two products is time the tensor core waits.
+      int ks = 0, vs = 0;                     // stages of the next tiles
+      uint32_t kp = 0, vp = 0, pp0 = 0, pp1 = 0;  // phases: of those stages, of the groups' P
       bool ok = true;
       long long x = x0;
-      for (int piece = 0; ok && x < x1; ++piece) {
-        const int nt = piece_tiles(u, x);
-        const bool two = piece_two(u);
-        // item i: group i & 1 with its (i >> 1)-th tile
-        const int ni = two ? 2 * nt : nt;
-        auto issue_s = [&](int i) -> bool {
-          const int kt = kt0 + (two ? i >> 1 : i), st = kt % KST, w = i & 1;
-          if ((!two || w == 0) && !warp_wait(&bar_k[st], (kt / KST) & 1, ctl, kErrTimeoutTma)) return false;
+      for (int piece = 0; ok; ++piece) {
+        const int nt = uniform(piece_tiles(u, x));
+        const bool two = uniform(piece_two(u)) != 0;
+        auto next_k = [&]() {
+          commit_el(&bar_kempty[ks]);
+          if (++ks == KST) ks = 0, kp ^= 1;
+        };
+        auto next_v = [&]() {
+          commit_el(&bar_vempty[vs]);
+          if (++vs == VST) vs = 0, vp ^= 1;
+        };
+        // S of group w with the next key tile, which `first` waits for and `last` releases
+        auto issue_s = [&](int w, bool first, bool last) -> bool {
+          if (first && !warp_wait(&bar_k[ks], kp, ctl, kErrTimeoutTma)) return false;
           tc_fence_after();
-          mma_qk<DP>(tmem + col_s[w], sQ + (two ? w * F::TILE : 0), sK(st), idesc_qk, false);
+          mma_qk<DP>(tmem + col_s[w], sQ + (two ? w * F::TILE : 0), sK(ks), idesc_qk, false);
           commit_el(&bar_s[w]);
-          if (!two || w == 1) commit_el(&bar_kempty[st]);
+          if (last) next_k();
+          return true;
+        };
+        auto issue_pv = [&](int w, bool first, bool last, bool add) -> bool {
+          if (first && !warp_wait(&bar_v[vs], vp, ctl, kErrTimeoutTma)) return false;
+          if (!warp_wait(&bar_p[w], w ? pp1 : pp0, ctl, kErrTimeoutSoftmax)) return false;
+          if (w) pp1 ^= 1;
+          else pp0 ^= 1;
+          tc_fence_after();
+          mma_pv<DP>(tmem + col_o[w], tmem + col_s[w], sV(vs), idesc_pv, add);
+          commit_el(&bar_o[w]);
+          if (last) next_v();
           return true;
         };
         ok = warp_wait(&bar_q, piece & 1, ctl, kErrTimeoutTma);
-        if (ok) ok = issue_s(0);
-        if (ok && ni > 1) ok = issue_s(1);
-        for (int i = 0; ok && i < ni; ++i) {
-          const int kt = kt0 + (two ? i >> 1 : i), st = kt % VST, w = i & 1;
-          if ((!two || w == 0) && !(ok = warp_wait(&bar_v[st], (kt / VST) & 1, ctl, kErrTimeoutTma))) break;
-          if (!(ok = warp_wait(&bar_p[w], (w ? np1 : np0) & 1, ctl, kErrTimeoutSoftmax))) break;
-          if (w) ++np1;
-          else ++np0;
-          tc_fence_after();
-          mma_pv<DP>(tmem + col_o[w], tmem + col_s[w], sV(st), idesc_pv, i > 1);
-          commit_el(&bar_o[w]);
-          if (!two || w == 1) commit_el(&bar_vempty[st]);
-          if (i + 2 < ni) ok = issue_s(i + 2);
+        if (two) {
+          ok = ok && issue_s(0, true, false) && issue_s(1, false, true);
+          for (int i = 0; ok && i < nt; ++i) {
+            const bool more = i + 1 < nt;
+            ok = issue_pv(0, true, false, i > 0);
+            if (ok && more) ok = issue_s(0, true, false);
+            ok = ok && issue_pv(1, false, true, i > 0);
+            if (ok && more) ok = issue_s(1, false, true);
+          }
+        } else {  // tile i with group i & 1
+          ok = ok && issue_s(0, true, true);
+          if (ok && nt > 1) ok = issue_s(1, true, true);
+          for (int i = 0; ok && i < nt; i += 2) {
+            ok = issue_pv(0, true, true, i > 0);
+            if (ok && i + 2 < nt) ok = issue_s(0, true, true);
+            if (ok && i + 1 < nt) {
+              ok = issue_pv(1, true, true, i > 0);
+              if (ok && i + 3 < nt) ok = issue_s(1, true, true);
+            }
+          }
         }
         if (ok) commit_el(&bar_ofinal);
-        kt0 += nt;
         x += nt;
-        if (x < x1) Ln::next_unit(c, a, u);
+        if (uniform(x >= x1)) break;
+        Ln::next_unit(c, a, u);
       }
     }
     if (warp == 13 || (warp == 14 && !F::Q8)) {
