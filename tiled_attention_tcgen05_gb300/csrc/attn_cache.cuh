@@ -109,7 +109,8 @@ struct Line {
     u.b = sh.b;
     u.s = seq(c, a, u.b);
     const long long in = x - sh.start;
-    u.h = static_cast<int>(in / u.s.per_head);
+    u.h = u.s.all <= 0xffffffffll ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(u.s.per_head))
+                                  : static_cast<int>(in / u.s.per_head);
     long long rest = in - u.h * u.s.per_head;
     u.rt = 0;
     u.ntiles = tiles(a, u.s, 0);
@@ -139,11 +140,16 @@ struct Line {
   }
 };
 
-// Block i's first place when the line of `len` is cut for `n` blocks, and the
-// block that holds place y: cut(b) <= y < cut(b + 1).
-__device__ __forceinline__ long long cut(long long len, int n, int i) { return len * i / n; }
-__device__ __forceinline__ int block_of(long long len, int n, long long y) {
-  return static_cast<int>(((y + 1) * n - 1) / len);
+// Block i's first place when the line of `len` is cut for N blocks (a constant:
+// a 64-bit division by a variable takes about as long as a load), and the block
+// that holds place y: cut(b) <= y < cut(b + 1).
+template <int N>
+__device__ __forceinline__ long long cut(long long len, int i) {
+  return static_cast<long long>(static_cast<unsigned long long>(len * i) / N);
+}
+template <int N>
+__device__ __forceinline__ int block_of(long long len, long long y) {
+  return static_cast<int>(((y + 1) * N - 1) / len);
 }
 
 // ----------------------------------------------------------------- joining
@@ -166,30 +172,31 @@ struct __align__(16) CutUnit {
 };
 
 // Block i's record; `u` is its first place, len the line's length (0: none).
-template <typename Cursor>
-__device__ __forceinline__ void write_cut(CutUnit* out, long long len, int n, int i, long long x0, long long x1,
+template <int N, typename Cursor>
+__device__ __forceinline__ void write_cut(CutUnit* out, long long len, int i, long long x0, long long x1,
                                           const Cursor* u) {
   CutUnit r = {};
   if (x0 < x1 && i > 0 && u->t > 0) {
     // the block that holds the place before starts at or before the unit?
     const long long u0 = x0 - u->t;
-    const int first = block_of(len, n, x0 - 1);
-    const long long before = cut(len, n, first);
+    const int first = block_of<N>(len, x0 - 1);
+    const long long before = cut<N>(len, first);
     if (before <= u0) {
       r.b = u->b, r.h = u->h, r.rt = u->rt, r.q = u->s.q;
       r.first = first;
-      r.parts = block_of(len, n, u0 + u->ntiles - 1) - first + 1;
+      r.parts = block_of<N>(len, u0 + u->ntiles - 1) - first + 1;
       r.first_slot = before < u0 ? 1 : 0;
-      r.sparse = len < n;
+      r.sparse = len < N;
       r.len = len;
     }
   }
   out[i] = r;
 }
 // Slot of part k, -1 for a block without a piece.
-__device__ __forceinline__ int part_slot(const CutUnit& r, int n, int k) {
+template <int N>
+__device__ __forceinline__ int part_slot(const CutUnit& r, int k) {
   const int b = r.first + k;
-  if (r.sparse && cut(r.len, n, b) == cut(r.len, n, b + 1)) return -1;
+  if (r.sparse && cut<N>(r.len, b) == cut<N>(r.len, b + 1)) return -1;
   return b * 2 + (k == 0 ? r.first_slot : 0);
 }
 

@@ -140,13 +140,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
 
   long long mine, before;
   const long long len = Ln::template length<kWarps * 32>(c, a, line, &mine, &before);
-  const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
+  const long long x0 = cut<F::BLOCKS>(len, blockIdx.x), x1 = cut<F::BLOCKS>(len, blockIdx.x + 1);
+  CutUnit* const cuts = reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART);
+  if (x0 >= x1) {
+    if (threadIdx.x == 0) write_cut<F::BLOCKS, typename Ln::Cursor>(cuts, len, blockIdx.x, x0, x1, nullptr);
+    return;
+  }
   typename Ln::Cursor cc;
-  if (x0 < x1) Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
-  if (threadIdx.x == 0)
-    write_cut(reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(gridDim.x) * 2 * F::PART), len, gridDim.x, blockIdx.x,
-              x0, x1, &cc);
-  if (x0 >= x1) return;
+  Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
   typename Ln::Cursor pc = cc;  // the next tile to copy
 
   uint8_t* const ring = smem + warp * F::RING;
@@ -248,6 +249,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
     }
     cp_async_commit();
   }
+
+  // (behind the first loads: its divisions take as long)
+  if (threadIdx.x == 32) write_cut<F::BLOCKS>(cuts, len, blockIdx.x, x0, x1, &cc);
 
   uint32_t qf[MT == 1 ? NK : 1][4];
   float f1[2];  // MT == 1: the rows' score factors
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   const CutUnit u = reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART)[blockIdx.x + 1];
   const int parts = u.parts;
   if (parts == 0 || static_cast<int>(blockIdx.y) * 8 + u.rt * ROWS >= u.q * a.G) return;
-  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot(u, F::BLOCKS, i);
+  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot<F::BLOCKS>(u, i);
   __syncthreads();
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + wrow;

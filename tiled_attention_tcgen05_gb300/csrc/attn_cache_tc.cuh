@@ -39,7 +39,7 @@ namespace ta {
 namespace {
 
 constexpr int kTcBlocks = 152;    // one per SM
-constexpr int kTcThreads = 512;   // 16 warps; the last one only fills its register group
+constexpr int kTcThreads = 512;   // 16 warps; the last one has the join's record to write only
 
 template <int CT, int DP>
 struct TcCfg {
@@ -54,7 +54,7 @@ struct TcCfg {
   static constexpr int SSLOT = OPB + 1024;               // and their scales (K tiles)
   static constexpr int SCS = KST + 2;                    // ring of scales for the softmax
   static constexpr int SCB = 128 * 12;                   // K scale, log2 and 1 / of the V scale
-  static constexpr int REG_SOFTMAX = 192, REG_COPY = 64, REG_MMA = 64;
+  static constexpr int REG_SOFTMAX = 176, REG_COPY = 80, REG_MMA = 80;
   static_assert(256 * REG_SOFTMAX + 128 * REG_COPY + 128 * REG_MMA <= kTcThreads * 128,
                 "the groups' registers come out of the launch's");
   // Where a one-tile unit's groups join: the second query tile (D = 128, 16
@@ -154,13 +154,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   let_dependents_launch();
   long long mine, before;
   const long long len = Ln::template length<kTcThreads>(c, a, line, &mine, &before);
-  const long long x0 = cut(len, gridDim.x, blockIdx.x), x1 = cut(len, gridDim.x, blockIdx.x + 1);
+  const long long x0 = cut<kTcBlocks>(len, blockIdx.x), x1 = cut<kTcBlocks>(len, blockIdx.x + 1);
+  CutUnit* const cuts =
+      reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(kTcBlocks) * 2 * tc_part_floats<CT, DP>());
+  if (x0 >= x1) {
+    if (threadIdx.x == 0) write_cut<kTcBlocks, typename Ln::Cursor>(cuts, len, blockIdx.x, x0, x1, nullptr);
+    return;
+  }
   typename Ln::Cursor u;
-  if (x0 < x1) Ln::template find<kTcThreads>(c, a, line, x0, mine, before, u);
-  if (threadIdx.x == 0)
-    write_cut(reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(gridDim.x) * 2 * tc_part_floats<CT, DP>()), len,
-              gridDim.x, blockIdx.x, x0, x1, &u);
-  if (x0 >= x1) return;
+  Ln::template find<kTcThreads>(c, a, line, x0, mine, before, u);
 
   uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(base);
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_slot);
+  if (warp == 15 && lane == 0) write_cut<kTcBlocks>(cuts, len, blockIdx.x, x0, x1, &u);
   const uint32_t col_s[2] = {0u, 128u};
   const uint32_t col_o[2] = {256u, 256u + DP};
 
@@ -254,11 +257,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (!F::Q8) {
         constexpr int CH = DP / 8;  // 16-byte chunks per row
         const int ntile = piece_two(u) ? 2 : 1, dch = dg / 8;
+        long long offs[2] = {0, 0};
+        bool rows[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) rows[w] = q_row(u, w, pw * 32 + lane, &offs[w]);
         if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
         for (int w = 0; w < ntile; ++w) {
-          long long off = 0;
-          const bool has = q_row(u, w, pw * 32 + lane, &off);
-#pragma unroll 4
+          const long long off = w ? offs[1] : offs[0];
+          const bool has = w ? rows[1] : rows[0];
+#pragma unroll 8
           for (int k = 0; k < CH; ++k) {
             const int idx = k * 32 + lane, r = idx / CH, j = idx % CH;
             const long long o = __shfl_sync(0xffffffffu, off, r);
@@ -894,7 +901,7 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
       reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(kTcBlocks) * 2 * tc_part_floats<CT, DP>())[blockIdx.x + 1];
   const int parts = u.parts, rows = u.q * a.G;
   if (parts == 0 || u.rt * F::ROWS + static_cast<int>(blockIdx.y) * 32 >= rows) return;
-  for (int i = threadIdx.x; i < parts; i += 256) slots[i] = part_slot(u, kTcBlocks, i);
+  for (int i = threadIdx.x; i < parts; i += 256) slots[i] = part_slot<kTcBlocks>(u, i);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int prow = blockIdx.y * 32 + lane, rr = u.rt * F::ROWS + prow;
