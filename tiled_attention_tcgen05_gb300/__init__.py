@@ -25,7 +25,6 @@ float32 [B, H, M].  sm_scale None means 1/sqrt(D).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -396,8 +395,6 @@ def _i32(name, t, shape, index):
 
 def _cache_lists(cache, pages, kv_lens, q_lens):
     """Checks the page table and the lengths; returns (B, max_pages)."""
-    if not isinstance(cache, KVCache):
-        raise ValueError("cache must be a KVCache")
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
     index, shape = cache._index, pages.shape
@@ -431,40 +428,44 @@ def _tokens(name, t, shape, dtype, index, written=False):
     return _Strides(st[0], st[1], st[2])
 
 
-def _raw_stream(stream, *used):
-    """The handle of the stream a call runs on (None: the current one).  Tensors
-    that the call allocates on the current stream and uses on another are
-    recorded there."""
-    current = torch.cuda.current_stream()
+# The current stream's handle without the Stream object around it, which costs
+# more host time than a small call's kernel takes; the public way where this
+# one is missing.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(index, stream, *used):
+    """The handle of the stream a call runs on (None: the device's current one).
+    Tensors that the call allocates on the current stream and uses on another
+    are recorded there."""
+    current = _current_raw_stream(index)
     if stream is None:
-        return current.cuda_stream
+        return current
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    if stream.cuda_stream != current.cuda_stream:
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    if stream.cuda_stream != current:
         for t in used:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _on_cache_device(fn):
-    """Runs fn with the cache's device current: the library launches there."""
-    @functools.wraps(fn)
-    def call(*args, **kw):
-        for cache in args[:2]:
-            if isinstance(cache, KVCache):
-                if torch.cuda.current_device() != cache._index:
-                    with torch.cuda.device(cache._index):
-                        return fn(*args, **kw)
-                break
-        return fn(*args, **kw)
-    return call
+def _elsewhere(cache):
+    """None, or a context that makes the cache's device current: the library
+    launches on the current device."""
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    return None if torch.cuda.current_device() == cache._index else torch.cuda.device(cache._index)
 
 
-@_on_cache_device
 def cache_append(cache, k, v, pages, kv_lens, q_lens=None, stream=None):
     """Writes new tokens' keys and values k, v [B, Hkv, T, D] (any strides with
     contiguous rows) to their positions kv_lens - q_lens + t; 8-bit caches are
     quantised with one scale per (token, head)."""
+    there = _elsewhere(cache)
+    if there is not None:
+        with there:
+            return cache_append(cache, k, v, pages, kv_lens, q_lens, stream)
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
     if k.dim() != 4 or k.dtype not in _DT:
@@ -476,14 +477,17 @@ def cache_append(cache, k, v, pages, kv_lens, q_lens=None, stream=None):
     vs = _tokens("v", v, shape, k.dtype, cache._index)
     _check("attn_cache_append", lib.attn_cache_append(
         cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, pages.data_ptr(), max_pages, kv_lens.data_ptr(),
-        None if q_lens is None else q_lens.data_ptr(), B, T, _DT[k.dtype], _raw_stream(stream)))
+        None if q_lens is None else q_lens.data_ptr(), B, T, _DT[k.dtype], _raw_stream(cache._index, stream)))
 
 
-@_on_cache_device
 def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None):
     """Positions 0 .. N - 1 of every sequence as (k, v) [B, Hkv, N, D] of dtype
     (None: the cache's, bfloat16 for 8-bit caches); zeros at and behind
     kv_lens.  k, v: contiguous tensors to write to."""
+    there = _elsewhere(cache)
+    if there is not None:
+        with there:
+            return cache_read(cache, pages, kv_lens, N, dtype, k, v, stream)
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, None)
     _, Hkv, _, D = cache.shape
@@ -507,15 +511,18 @@ def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None
         made.append(v)
     _check("attn_cache_read", lib.attn_cache_read(
         cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, _DT[dtype],
-        _raw_stream(stream, *made)))
+        _raw_stream(cache._index, stream, *made)))
     return k, v
 
 
-@_on_cache_device
 def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
     """Keeps the accepted tokens of a draft: token keep[b, i] (keep int32 [B, T],
     ascending, i < keep_lens[b]) moves to the place of new token i.  Returns the
     sequences' new lengths, int32 [B]."""
+    there = _elsewhere(cache)
+    if there is not None:
+        with there:
+            return cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream)
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
     if keep.dim() != 2:
@@ -526,7 +533,7 @@ def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
     new = torch.empty((B,), dtype=torch.int32, device=cache.device)
     _check("attn_cache_keep", lib.attn_cache_keep(
         cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(),
-        keep.data_ptr(), keep_lens.data_ptr(), new.data_ptr(), B, T, _raw_stream(stream, new)))
+        keep.data_ptr(), keep_lens.data_ptr(), new.data_ptr(), B, T, _raw_stream(cache._index, stream, new)))
     return new
 
 
@@ -537,7 +544,6 @@ def attn_cache_workspace_bytes(B, Hq, Hkv, T, N, D, dtype=torch.bfloat16, cache_
     return int(load().attn_cache_workspace_bytes(B, Hq, Hkv, T, min(int(N), 2 ** 31 - 1), D, _DT[dtype], ct))
 
 
-@_on_cache_device
 def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=None, o=None, lse=None, ws=None,
                    stream=None):
     """Attention of new tokens q [B, Hq, T, D] (any strides with contiguous
@@ -545,6 +551,10 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
     h reads key head h // (Hq // Hkv).  tree: bool [B or 1, T, T], token i sees new token
     j where tree[b, i, j] (None: where j <= i).  Returns (o, lse); rows
     t >= q_lens[b] of given o, lse are left as they were."""
+    there = _elsewhere(cache)
+    if there is not None:
+        with there:
+            return attn_cache_fwd(q, cache, pages, kv_lens, q_lens, tree, sm_scale, o, lse, ws, stream)
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
     _, Hkv, page, D = cache.shape
@@ -585,7 +595,7 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
         q.data_ptr(), qs, cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(),
         None if q_lens is None else q_lens.data_ptr(), tp, ts, o.data_ptr(), os_, lse.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size(), B, Hq, T, _DT[dtype], -1.0 if sm_scale is None else float(sm_scale),
-        _raw_stream(stream, *made)))
+        _raw_stream(cache._index, stream, *made)))
     return o, lse
 
 

@@ -718,56 +718,83 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   using F = Cfg<CT, D, MT>;
   constexpr int ROWS = F::ROWS;
   __shared__ int slots[F::BLOCKS];
-  __shared__ float fs[8][F::BLOCKS];
+  __shared__ float2 ml[8][2][F::BLOCKS];  // per row and warp: the parts' m and l, then their factors
   __shared__ float other[8][D + 1];
   wait_for_main_kernel();  // every block: the next kernel in the stream may start when this one has ended
   const CutUnit u = reinterpret_cast<const CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART)[blockIdx.x + 1];
   const int parts = u.parts;
   if (parts == 0 || static_cast<int>(blockIdx.y) * 8 + u.rt * ROWS >= u.q * a.G) return;
-  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot<F::BLOCKS>(u, i);
-  __syncthreads();
   const int wrow = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + wrow;
-  auto part = [&](int i) { return a.ws + static_cast<size_t>(slots[i]) * F::PART; };
-  // both warps of a row: its maximum and sum, and the parts' factors
+  auto part = [&](int slot) { return a.ws + static_cast<size_t>(slot) * F::PART; };
+  const bool lane_on = lane * VEC < D;
+  auto load = [&](int i, float (&y)[VEC]) {
+    if (slots[i] < 0) {  // a block without a piece
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) y[e] = 0.f;
+      return;
+    }
+    const float* p = part(slots[i]) + r * D + lane * VEC;
+    if constexpr (VEC == 4) {
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(p));
+      y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+    } else if constexpr (VEC == 2) {
+      const float2 w = __ldcg(reinterpret_cast<const float2*>(p));
+      y[0] = w.x, y[1] = w.y;
+    } else {
+      y[0] = __ldcg(p);
+    }
+  };
+  // Maxima and sums, a part per lane, by both warps of a row; kept in shared
+  // memory between the two passes.
+  for (int i = threadIdx.x; i < parts; i += 512) slots[i] = part_slot<F::BLOCKS>(u, i);
+  __syncthreads();
+  float2* const mls = ml[wrow][half];
   float mm = -INFINITY;
-  for (int i = lane; i < parts; i += 32)
-    if (slots[i] >= 0) mm = fmaxf(mm, __ldcg(part(i) + ROWS * D + 2 * r));
+  for (int i = lane; i < parts; i += 32) {
+    const float2 v = slots[i] < 0 ? make_float2(-INFINITY, 0.f)
+                                  : __ldcg(reinterpret_cast<const float2*>(part(slots[i]) + ROWS * D + 2 * r));
+    mls[i] = v;
+    mm = fmaxf(mm, v.x);
+  }
+  // the first parts' accumulators are on their way meanwhile
+  constexpr int AHEAD = 8;
+  float y[AHEAD][VEC] = {};
+  if (lane_on) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (half + 2 * k < parts) load(half + 2 * k, y[k]);
+  }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
   float ll = 0.f;
   for (int i = lane; i < parts; i += 32) {
-    float f = 0.f;
-    if (slots[i] >= 0) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + ROWS * D + 2 * r));
-      f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
-      ll += mm == -INFINITY ? ml.y : ml.y * f;  // a NaN sum stays one where no score was a number
-    }
-    if (half == 0) fs[wrow][i] = f;
+    const float2 v = mls[i];
+    const float f = v.x == -INFINITY ? 0.f : ex2(v.x - mm);
+    ll += mm == -INFINITY ? v.y : v.y * f;  // a NaN sum stays one where no score was a number
+    mls[i].x = f;
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
-  __syncthreads();
+  __syncwarp();
   float v[VEC] = {};
-  const bool lane_on = lane * VEC < D;
   if (lane_on) {
-#pragma unroll 8
-    for (int i = half; i < parts; i += 2) {
-      const float f = fs[wrow][i];
-      // (a block without a piece has factor 0; the first one listed always has a piece)
-      const float* p = part(slots[i] < 0 ? 0 : i) + r * D + lane * VEC;
-      if constexpr (VEC == 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
-        v[0] = fmaf(y.x, f, v[0]);
-        v[1] = fmaf(y.y, f, v[1]);
-        v[2] = fmaf(y.z, f, v[2]);
-        v[3] = fmaf(y.w, f, v[3]);
-      } else if constexpr (VEC == 2) {
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
-        v[0] = fmaf(y.x, f, v[0]);
-        v[1] = fmaf(y.y, f, v[1]);
-      } else {
-        v[0] = fmaf(__ldcg(p), f, v[0]);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float f = half + 2 * k < parts ? mls[half + 2 * k].x : 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = fmaf(y[k][e], f, v[e]);
+    }
+    for (int i0 = half + 2 * AHEAD; i0 < parts; i0 += 2 * AHEAD) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (i0 + 2 * k < parts) load(i0 + 2 * k, y[k]);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float f = i0 + 2 * k < parts ? mls[i0 + 2 * k].x : 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (i0 + 2 * k < parts) v[e] = fmaf(y[k][e], f, v[e]);
       }
     }
     if (half) {

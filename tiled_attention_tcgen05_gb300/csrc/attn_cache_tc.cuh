@@ -934,8 +934,8 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
     const float f = fs[i][lane];
-    // (a block without a piece has factor 0; the first one listed always has a piece)
-    const float4* p = reinterpret_cast<const float4*>(part(slots[i] < 0 ? 0 : i)) + prow;
+    if (slots[i] < 0) continue;  // a block without a piece
+    const float4* p = reinterpret_cast<const float4*>(part(i)) + prow;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int ch = warp + 8 * k;
