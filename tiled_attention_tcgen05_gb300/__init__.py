@@ -44,6 +44,7 @@ _DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 # element types of a cache
 _CT = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 3, torch.int8: 4}
+_T16 = {torch.float16: 0, torch.bfloat16: 1}  # of the tokens read from and written to it
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _SIGS = {
@@ -468,7 +469,7 @@ def cache_append(cache, k, v, pages, kv_lens, q_lens=None, stream=None):
             return cache_append(cache, k, v, pages, kv_lens, q_lens, stream)
     lib = load()
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
-    if k.dim() != 4 or k.dtype not in _DT:
+    if k.dim() != 4 or k.dtype not in _T16:
         raise ValueError("k must be a 4-D tensor of float16 or bfloat16")
     _, Hkv, _, D = cache.shape
     T = k.shape[2]
@@ -492,8 +493,8 @@ def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None
     B, max_pages = _cache_lists(cache, pages, kv_lens, None)
     _, Hkv, _, D = cache.shape
     if dtype is None:
-        dtype = k.dtype if k is not None else cache.dtype if cache.dtype in _DT else torch.bfloat16
-    if dtype not in _DT:
+        dtype = k.dtype if k is not None else cache.dtype if cache.dtype in _T16 else torch.bfloat16
+    if dtype not in _T16:
         raise ValueError(f"unsupported dtype {dtype}")
     N = int(N)
     shape = (B, Hkv, N, D)
@@ -559,7 +560,7 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
     B, max_pages = _cache_lists(cache, pages, kv_lens, q_lens)
     _, Hkv, page, D = cache.shape
     index, dtype = cache._index, q.dtype
-    if q.dim() != 4 or dtype not in _DT:
+    if q.dim() != 4 or dtype not in _T16:
         raise ValueError("q must be a 4-D tensor of float16 or bfloat16")
     _, Hq, T, _ = q.shape
     shape = (B, Hq, T, D)
