@@ -111,6 +111,32 @@ def test_one_long_sequence_over_every_block(gpu_lib, cache, dtype, T, G):
     check("L", lse[0], L, bL)
 
 
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("int8", "f16")])
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 8), (80, 2)])
+@pytest.mark.parametrize("junk", [0, 1, 0x7F, 0x80, 0xFF, 0x3C])
+def test_memory_behind_the_end_holds_anything(gpu_lib, cache, dtype, T, G, junk):
+    """Codes, values and scales of rows behind a sequence's end, in its last page
+    and in others: zeros, denormals, infinities, NaN, ordinary numbers."""
+    ta = gpu_lib
+    kv = [T + 5, T + 61, T + 133]
+    st = Setup(ta, kv, 1, 32, 64, dtype, cache, 3)
+    q = values(3, (3, G, T, 64), dtype)
+    o, lse = attend(ta, st, q)
+    compare_attention(st, q, o, lse, None, None)
+    owned = torch.zeros(st.cache.shape[0], 32, dtype=torch.bool)
+    for b, n in enumerate(kv):
+        for i in range(n):
+            owned[oracle.cache_slot(st.table[b], 32, i)] = True
+    free = (~owned).cuda()
+    for t in (st.cache.k, st.cache.v, st.cache.k_scale, st.cache.v_scale):
+        if t is not None:
+            raw = t.view(torch.uint8).view(t.shape[0], 32, -1)  # one head
+            raw[free] = junk
+    o2, lse2 = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_sequences_share_pages(gpu_lib):
     """A common prompt's pages in two page tables."""
     ta = gpu_lib

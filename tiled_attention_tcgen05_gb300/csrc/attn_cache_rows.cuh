@@ -337,10 +337,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kscale) : "r"(sc_a + lane * 4) : "memory");
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + lane * 4), "f"(kscale * a.scale_log2) : "memory");
           }
-          // a scale of zero (a row of a page that the cache does not have
-          // reads as zeros) stands for a value of zero whatever its codes; a NaN
-          // row's scores are NaN, its 1 / scale must not reach other rows' sums
-          if (vscale == 0.f) vscale = kMinScale;
+          // no scale (a row past the end, or of a page that the cache does not
+          // have) stands for a value of zero whatever its codes; a NaN row's
+          // scores are NaN, its 1 / scale must not reach other rows' sums
+          if (vscale < kMinScale) vscale = kMinScale;
           const float inv = vscale == vscale ? __fdividef(1.f, vscale) : 0.f;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(lg2(vscale)) : "memory");
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 8 + lane * 4), "f"(inv) : "memory");

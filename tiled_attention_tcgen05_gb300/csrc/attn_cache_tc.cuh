@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float ksc, vsc;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(st + F::OPB + tid * 4) : "memory");
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vsc) : "r"(st + F::OPB + 512 + tid * 4) : "memory");
-            // no scale (a row of a missing page): a value of zero
-            if (vsc == 0.f) vsc = kMinScale;
+            // No scale (a row of a missing page) stands for a value of zero; a row
+            // behind the end may hold any number, whose 1 / scale must be finite.
+            if (vsc < kMinScale) vsc = kMinScale;
             const uint32_t sc = sScale + ((n >> 1) % F::SCS) * F::SCB + tid * 4;
             sts_f32(sc, ksc);
             sts_f32(sc + 512, lg2(vsc));
