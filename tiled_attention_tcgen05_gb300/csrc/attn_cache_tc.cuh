@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ int abort_flag;
   __shared__ int odd[4];  // piece + 1 (mod 4 slots) whose draft holds non-finite values
   __shared__ float xm[kBM], xl[kBM];
-  __shared__ float qfac[2][F::Q8 ? kBM : 1];  // of even and odd pieces
+  __shared__ __align__(8) uint64_t bar_qtop;
+  __shared__ uint32_t qtop[2][4];  // largest query magnitudes, of even and odd pieces
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
   __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
 
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&bar_ofinal, 1);
     mbar_init(&bar_xfull, 4);
     mbar_init(&bar_xempty, 4);
+    mbar_init(&bar_qtop, 4);
     for (int i = 0; i < 4; ++i) odd[i] = 0;
     fence_mbar_init();
   }
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     long long x = x0;
     [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
+    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the keys' scales in this piece
     for (int piece = 0; ok && x < x1; ++piece) {
       const int nt = piece_tiles(u, x);
       if constexpr (!F::Q8) {
@@ -316,25 +319,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           long long off = 0;
           const bool has = q_row(u, 0, tid, &off);
           const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + off);
-          uint32_t top = 0;
+          // bf16 rows: the tile's largest finite magnitude to [1, 2) by a power of
+          // two.  An element is then off by at most 2^-25 of that, so a score
+          // by 2^-25 of what the largest query could give with the same key:
+          // one factor for all rows costs the scores of smaller ones nothing
+          // that the softmax could see, and goes into the keys' scales.
+          float up = 1.f;
+          kfac = a.scale_log2;
           if constexpr (BF) {
+            uint32_t top = 0;
 #pragma unroll 8
             for (int j = 0; j < DP / 8; ++j) {
               const uint4 v = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+                top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+              }
             }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) {
+              qtop[piece & 1][pw] = top;
+              mbar_arrive(&bar_qtop);
+            }
+            if (!(ok = warp_wait(&bar_qtop, piece & 1, ctl, kErrTimeoutOther))) break;
+            const uint32_t* t = qtop[piece & 1];
+            int ex = static_cast<int>(max(max(t[0], t[1]), max(t[2], t[3])) >> 7);  // biased exponent
+            ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
+            up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+            kfac *= __uint_as_float(static_cast<uint32_t>(ex) << 23);
           }
           uint4 first[8];  // half of the row (D = 128) is here before its place is free
 #pragma unroll
           for (int j = 0; j < 8; ++j) first[j] = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
           if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
-          // bf16 rows: the largest magnitude to [1, 2) by a power of two
-          int ex = static_cast<int>(top >> 7);
-          ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
-          const float up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-          qfac[piece & 1][tid] = BF ? __uint_as_float(static_cast<uint32_t>(ex) << 23) : 1.f;
 #pragma unroll
           for (int j = 0; j < DP / 8; ++j) {
             const uint4 v = j < 8 ? first[j & 7] : has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
@@ -367,30 +386,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // behind the end may hold any number, whose 1 / scale must be finite.
             if (vsc < kMinScale) vsc = kMinScale;
             const uint32_t sc = sScale + ((n >> 1) % F::SCS) * F::SCB + tid * 4;
-            sts_f32(sc, ksc);
+            sts_f32(sc, ksc * kfac);
             sts_f32(sc + 512, lg2(vsc));
             // a NaN row's scores are NaN; its 1 / scale must not reach the sums of rows that do not see it
             sts_f32(sc + 1024, vsc == vsc ? __fdividef(1.f, vsc) : 0.f);
           }
-          const bool all = end >= kBN;
+          // Chunk of 16 codes -> two of 8 fp16.  Eight neighbouring lanes take
+          // four chunks of a row and the other four of the next one (D = 128),
+          // or two rows (D = 64): their loads and their stores then cover all
+          // banks once.
+          auto place = [&](int i, int* r, int* j) {
+            if constexpr (CH == 8) {
+              *r = pw * 32 + 2 * ((i >> 1) * 4 + (lane >> 3)) + ((lane >> 2) & 1);
+              *j = (lane & 3) + 4 * (((lane >> 2) & 1) ^ (i & 1));
+            } else {
+              *r = pw * 32 + i * 8 + (lane >> 2);
+              *j = lane & 3;
+            }
+          };
           uint4 codes[CH];  // all loads first: a load must not wait for the stores before it
 #pragma unroll
-          for (int i = 0; i < CH; ++i) codes[i] = lds_u4(st + pw * 32 * DP + (i * 32 + lane) * 16);
+          for (int i = 0; i < CH; ++i) {
+            int r, j;
+            place(i, &r, &j);
+            codes[i] = lds_u4(st + r * DP + j * 16);
+          }
+          if (end < kBN) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              int r, j;
+              place(i, &r, &j);
+              if (r >= end) codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
-            const int idx = i * 32 + lane, r = pw * 32 + idx / CH, j = idx % CH;
-            uint4 v = codes[i];
-            if (!all && r >= end) v = make_uint4(0u, 0u, 0u, 0u);
+            int r, j;
+            place(i, &r, &j);
+            const uint4 v = codes[i];
             uint32_t h[8];
             code4_to_f16<CT>(v.x, h[0], h[1]);
             code4_to_f16<CT>(v.y, h[2], h[3]);
             code4_to_f16<CT>(v.z, h[4], h[5]);
             code4_to_f16<CT>(v.w, h[6], h[7]);
-            // the two halves in an order that spreads a quarter warp over the banks
-            const bool swap = DP == 128 && (j & 4);
-            const uint32_t a0 = tile_at(tile, r, 2 * j), a1 = tile_at(tile, r, 2 * j + 1);
-            sts_v4(swap ? a1 : a0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-            sts_v4(swap ? a0 : a1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+            sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
+            sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
           }
           signal(bar);
           if (lane == 0) mbar_arrive(&bar_sempty[slot]);
@@ -661,13 +701,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int j = 0; j < 128; ++j) y[j] = __uint_as_float(s[j]);
         if constexpr (F::Q8) {
-          const float f = a.scale_log2 * qfac[piece & 1][r];
-          const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int j = 0; j < 128; j += 4) {
             const float4 kx = lds_f4(sc + j * 4), vx = lds_f4(sc + 512 + j * 4);
-            const float2 p = ffma2(make_float2(y[j], y[j + 1]), fmul2(f2, make_float2(kx.x, kx.y)), make_float2(vx.x, vx.y));
-            const float2 q = ffma2(make_float2(y[j + 2], y[j + 3]), fmul2(f2, make_float2(kx.z, kx.w)), make_float2(vx.z, vx.w));
+            const float2 p = ffma2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y), make_float2(vx.x, vx.y));
+            const float2 q = ffma2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w), make_float2(vx.z, vx.w));
             y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
           }
         }
