@@ -87,8 +87,9 @@ def random_tree(rng, T, loose=0.1):
     return t
 
 
-def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=None):
+def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=None, rows=None):
     """Oracle O, L of one (sequence, key head) and the bounds |error| of O and L.
+    rows: query rows per key head of the call (longer sequences' among them).
 
     With u the unit roundoffs (output type; the weights' type: dt for 16-bit
     caches, fp16 for 8-bit ones) and P the exact weights:
@@ -103,7 +104,12 @@ def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=N
         2^-25 max_j(P_ij sv_j) sum_j |code_j|;
       * the product with V and the sum l: N fp32 adds, N 2^-23 (P |V|) each, and
         a few roundings of the joins: (N + 64) 2^-22 together;
-      * the result's rounding u |O|.
+      * the result's rounding u |O|;
+      * with more than 32 rows 8-bit rows may be multiplied out to fp16 (each
+        rounded to 2^-11, or half a step of 2^-24 of the largest scale, which is
+        at most max|k| / 127): s (2^-11 sum|q k| + 2^-25 max|k| / 127 sum|q|) in a
+        score, 2^-11 (P |V|) + 2^-25 max|v| / 127 in O; the weights' half steps then
+        count 2^-25 max_j P_ij sum_j |v_j|.
     """
     O, L = oracle.cache_attention(q, k, v, tree, sm_scale)
     qn, kn, vn = (np.asarray(x, dtype=np.float64) for x in (to_np(q), k, v))
@@ -120,6 +126,10 @@ def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=N
         e = s * D * 2.0 ** -23 * (np.abs(qn[g]) @ np.abs(kn).T) + 2.0 ** -22 * np.abs(S) + 2.0 ** -22
         if kind not in ("f16", "bf16"):
             e += s * 2.0 ** -24 * np.abs(qn[g]).max(1, keepdims=True) * np.abs(kn).sum(1)[None]
+        wide = kind not in ("f16", "bf16") and (rows or G * T) > 32
+        if wide and N:
+            e += s * (2.0 ** -11 * (np.abs(qn[g]) @ np.abs(kn).T)
+                      + 2.0 ** -25 * np.abs(kn).max() / 127 * np.abs(qn[g]).sum(1, keepdims=True))
         e = np.where(keep, e, 0.0).max(1)
         P = np.where(keep, np.exp(np.where(keep, S, -np.inf) - np.where(np.isfinite(L[g]), L[g], 0.0)[:, None]), 0.0)
         PV = P @ np.abs(vn)
@@ -127,6 +137,9 @@ def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=N
         if vscale_rows is not None:
             code = np.abs(vn) / vscale_rows[:, None]
             bO[g] += 2.0 ** -25 * (P * vscale_rows[None]).max(1)[:, None] * code.sum(0)[None]
+        if wide and N:
+            bO[g] += 2.0 ** -11 * PV + 2.0 ** -25 * np.abs(vn).max() / 127
+            bO[g] += 2.0 ** -25 * P.max(1)[:, None] * np.abs(vn).sum(0)[None]
         bL[g] = e + (N + 64) * 2.0 ** -22 + 2.0 ** -22 * np.where(np.isfinite(L[g]), np.abs(L[g]), 0.0)
     return O, L, bO, bL
 

@@ -193,7 +193,7 @@ def compare_attention(st, q, o, lse, ql, tree, seqs=None, sm_scale=None):
                 vs = np.array([st.scale["v"][pg, h, r] for pg, r in
                                (oracle.cache_slot(st.table[b], st.page, i) for i in range(st.kv[b]))], dtype=np.float64)
             O, L, bO, bL = attention_reference(q[b, h * G:(h + 1) * G, :n], st.rows["k"][b][h], st.rows["v"][b][h], tr,
-                                               st.kind, st.dtype, vs, sm_scale)
+                                               st.kind, st.dtype, vs, sm_scale, G * T)
             check(f"O[{b},{h}]", o[b, h * G:(h + 1) * G, :n], O, bO)
             check(f"L[{b},{h}]", lse[b, h * G:(h + 1) * G, :n], L, bL)
 
@@ -312,16 +312,21 @@ def test_scores_of_extreme_size(gpu_lib):
         compare_attention(st, q, o, lse, None, None)
 
 
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("order", [1, -1])
 @pytest.mark.parametrize("cache", ["e4m3", "int8"])
-def test_value_rows_of_very_different_size(gpu_lib, cache):
-    """Values from 2^-20 to 2^10 (and a row of zeros) beside each other: the
+def test_value_rows_of_very_different_size(gpu_lib, cache, order, T):
+    """Values from 2^-25 to 2^18 (and a row of zeros) beside each other: the
     scales' range does not cost the small ones their weight in the sum."""
     ta = gpu_lib
-    D, N = 64, 200
+    D, N = 64, 700
     st = Setup(ta, [N], 1, 16, D, "bf16", cache, 2)
     k = values(1, (1, 1, N, D), "bf16")
     v = values(2, (1, 1, N, D), "bf16")
-    v = v * torch.exp2(torch.arange(N) % 31 - 20.0)[None, None, :, None].to(v.dtype)
+    # tile by tile larger (or smaller), and every size inside each
+    steps = torch.arange(N) // 50
+    size = (steps if order > 0 else steps.flip(0)) + torch.arange(N) % 31 - 25.0
+    v = v * torch.exp2(size)[None, None, :, None].to(v.dtype)
     v[0, 0, 7] = 0
     k[0, 0, 7] = 3.0
     ta.cache_append(st.cache, k.cuda(), v.cuda(), st.pages, st.kv_lens)
@@ -331,7 +336,7 @@ def test_value_rows_of_very_different_size(gpu_lib, cache):
         for i in range(N):
             pg, r = oracle.cache_slot(st.table[0], 16, i)
             st.scale[name][pg, :, r] = torch.from_numpy(s)[:, i]
-    q = values(3, (1, 3, 1, D), "bf16", 2.0)
+    q = values(3, (1, 3, T, D), "bf16", 2.0)
     q[0, 0] = 2.0  # prefers the row of zeros
     o, lse = attend(ta, st, q)
     assert ta.sync_status() == "TA_OK"

@@ -49,7 +49,7 @@ struct Line {
   }
 
   struct Shared {
-    long long warp_sum[16];
+    long long warp_sum[32];
     int b;
     long long start;  // first place of sequence b
   };

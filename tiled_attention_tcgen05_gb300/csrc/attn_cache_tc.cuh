@@ -3,10 +3,11 @@
 //
 // A block works through its piece of the line (attn_cache.cuh) with the roles
 //   warps 0-3, 4-7  two softmax groups, a thread per query row (= TMEM lane);
-//   warps 8-11      bring Q into shared memory, look through tiles with new
-//                   tokens, and turn 8-bit codes into fp16;
-//   warp 12         issues the MMAs: S = Q K^T, O += P V with P in TMEM;
-//   warps 13, 14    fetch keys and values (8-bit: 13 both) by TMA;
+//   warps 8-11      bring Q into shared memory and look through tiles with new
+//                   tokens; 8 bits: turn the keys' codes into fp16, and four
+//                   warps more the values';
+//   a warp          issues the MMAs: S = Q K^T, O += P V with P in TMEM;
+//   two warps       fetch keys and values by TMA (8 bits: one fetches both);
 // and the registers handed to the softmax groups (setmaxnreg).  The groups
 // alternate on the tensor core:  S0 S1 | PV0 S0' | PV1 S1' | ...  Units of more
 // than 128 rows give each group a row tile of its own and both the same keys;
@@ -19,9 +20,15 @@
 // that do not exist are fetched from outside the map and so read as zeros.
 // 16-bit rows go straight into the 128-byte-swizzled layout that the MMA
 // descriptors read.  8-bit codes and their scales go into a staging ring
-// several tiles ahead; warps 8-11 turn the codes into fp16 codes (exact).  Scores
-// take their key's scale and the value's scale goes into the exponent as in
-// attn_cache.cu.
+// several tiles ahead; the eight helpers turn them into fp16 rows, code * scale with a
+// power of two taken out that all keys of the tile, and all values of the piece
+// so far, share.  (The scales as they are, one per column of S, would have to be
+// read by every row: 96 16-byte loads of shared memory a row and tile, which
+// took more of its bandwidth than the MMAs: 184 us where this takes @@ for 16
+// sequences of 8192, 8 key heads of 128 with 64 rows, e4m3.)  The rounding of a
+// row to 11 bits adds 2^-11 of sum |q k| to a score and of P |V| to the result
+// at most; attn_cache.cu, whose warps read a scale for many rows' scores, keeps
+// the codes exact.
 //
 // A box may bring rows behind the sequence's end, whose memory may hold
 // anything, and a draft's values may hold infinities and NaN that some rows
@@ -39,7 +46,6 @@ namespace ta {
 namespace {
 
 constexpr int kTcBlocks = 152;    // one per SM
-constexpr int kTcThreads = 512;   // 16 warps; the last one has the join's record to write only
 
 template <int CT, int DP>
 struct TcCfg {
@@ -52,17 +58,21 @@ struct TcCfg {
   static constexpr int OPB = Q8 ? 128 * DP : 0;          // codes of one tile
   static constexpr int SR = Q8 ? (DP == 128 ? 3 : 6) : 0;  // staging ring
   static constexpr int SSLOT = OPB + 1024;               // and their scales (K tiles)
-  static constexpr int SCS = KST + 2;                    // ring of scales for the softmax
-  static constexpr int SCB = 128 * 12;                   // K scale, log2 and 1 / of the V scale
-  static constexpr int REG_SOFTMAX = 176, REG_COPY = 80, REG_MMA = 80;
-  static_assert(256 * REG_SOFTMAX + 128 * REG_COPY + 128 * REG_MMA <= kTcThreads * 128,
+  static constexpr int SCS = KST + 2;                    // ring of the tiles' powers of two, for the softmax
+  static constexpr int MUL = Q8 ? 2 * 128 * 8 : 0;       // multipliers of a tile's rows
+  static constexpr int HELPERS = Q8 ? 8 : 4;             // warps 8 .. 8 + HELPERS - 1
+  static constexpr int MMA = 8 + HELPERS;                // warp; the fetching warps follow it
+  static constexpr int THREADS = 32 * (MMA + 4);         // whole register groups of four warps
+  static constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
+  static constexpr int REG_SOFTMAX = Q8 ? 152 : 176, REG_COPY = Q8 ? 64 : 80, REG_MMA = Q8 ? 48 : 80;
+  static_assert(256 * REG_SOFTMAX + 32 * HELPERS * REG_COPY + 128 * REG_MMA <= THREADS * REG_LAUNCH,
                 "the groups' registers come out of the launch's");
   // Where a one-tile unit's groups join: the second query tile (D = 128, 16
   // bits), memory of its own (D = 64), or the query tile itself, which then
   // is free for the next piece only after that.
   static constexpr bool XOWN = DP == 64, XQ = DP == 128 && Q8;
   static constexpr int XCH = DP == 64 ? 16 : TILE / 2048;  // float4 columns of 128 rows a round
-  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * SSLOT + SCS * SCB : 0) + (XOWN ? 32768 : 0);
+  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * SSLOT + MUL : 0) + (XOWN ? 32768 : 0);
   static_assert(SMEM + 2048 <= kSmemMax, "tiles do not fit in shared memory");
 };
 template <int CT, int DP>
@@ -126,7 +136,7 @@ __device__ __forceinline__ void add_non_finite(const CacheArgs& c, const CacheAt
 }
 
 template <typename T, int CT, int DP>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs c,
                          CacheAttnArgs a, int dg) {
   using F = TcCfg<CT, DP>;
@@ -144,6 +154,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ float xm[kBM], xl[kBM];
   __shared__ __align__(8) uint64_t bar_qtop;
   __shared__ uint32_t qtop[2][4];  // largest query magnitudes, of even and odd pieces
+  // 8 bits, per tile: factor of its scores; biased exponent taken out of its
+  // values (0: all of them are zero so far)
+  __shared__ float tile_f[F::SCS];
+  __shared__ int tile_e[F::SCS];
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
   __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
 
@@ -154,7 +168,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   let_dependents_launch();
   long long mine, before;
-  const long long len = Ln::template length<kTcThreads>(c, a, line, &mine, &before);
+  const long long len = Ln::template length<F::THREADS>(c, a, line, &mine, &before);
   const long long x0 = cut<kTcBlocks>(len, blockIdx.x), x1 = cut<kTcBlocks>(len, blockIdx.x + 1);
   CutUnit* const cuts =
       reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(kTcBlocks) * 2 * tc_part_floats<CT, DP>());
@@ -163,15 +177,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return;
   }
   typename Ln::Cursor u;
-  Ln::template find<kTcThreads>(c, a, line, x0, mine, before, u);
+  Ln::template find<F::THREADS>(c, a, line, x0, mine, before, u);
 
   uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(base);
   auto sK = [&](int st) { return sQ + (F::QT + st) * F::TILE; };
   auto sV = [&](int st) { return sQ + (F::QT + KST + st) * F::TILE; };
   const uint32_t sStage = sQ + (F::QT + KST + VST) * F::TILE;
-  const uint32_t sScale = sStage + F::SR * F::SSLOT;
-  const uint32_t sX = F::XOWN ? sScale + (F::Q8 ? F::SCS * F::SCB : 0) : F::XQ ? sQ : sQ + F::TILE;
+  const uint32_t sMul = sStage + F::SR * F::SSLOT;
+  const uint32_t sX = F::XOWN ? sMul + F::MUL : F::XQ ? sQ : sQ + F::TILE;
 
   WaitCtl ctl{c.err, a.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
@@ -205,7 +219,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 4; ++i) odd[i] = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == F::MMA) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_slot);
-  if (warp == 15 && lane == 0) write_cut<kTcBlocks>(cuts, len, blockIdx.x, x0, x1, &u);
+  if (warp == F::MMA + 3 && lane == 0) write_cut<kTcBlocks>(cuts, len, blockIdx.x, x0, x1, &u);
   const uint32_t col_s[2] = {0u, 128u};
   const uint32_t col_o[2] = {256u, 256u + DP};
 
@@ -224,10 +238,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   auto piece_two = [&](const typename Ln::Cursor& p) { return !F::Q8 && p.s.q * a.G - p.rt * F::ROWS > kBM; };
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8 && warp < F::MMA) {
     // ------------------------------------------------------------- helpers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REG_COPY));
-    const int pw = warp - 8, tid = threadIdx.x - 256;
+    const int pw = warp & 3, tid = threadIdx.x & 127;
+    const bool keys = warp < 12;  // 8 bits: warps 8-11 convert keys, 12-15 values
     // query row i of tile w as an offset into q; false: no such row
     auto q_row = [&](const typename Ln::Cursor& p, int w, int i, long long* off) -> bool {
       const int rr = p.rt * F::ROWS + w * kBM + i;
@@ -254,7 +269,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     long long x = x0;
     [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
-    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the keys' scales in this piece
+    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the scores in this piece
+    [[maybe_unused]] int vexp = 0;           // 8-bit: exponent taken out of the piece's values (tile_e)
     for (int piece = 0; ok && x < x1; ++piece) {
       const int nt = piece_tiles(u, x);
       if constexpr (!F::Q8) {
@@ -315,7 +331,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       } else {
         constexpr int CH = DP / 16;  // 16-byte chunks per row of codes
-        {  // the piece's queries, a row per thread, in fp16
+        vexp = 0;
+        if (keys) {  // the piece's queries, a row per thread, in fp16
           long long off = 0;
           const bool has = q_row(u, 0, tid, &off);
           const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + off);
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // two.  An element is then off by at most 2^-25 of that, so a score
           // by 2^-25 of what the largest query could give with the same key:
           // one factor for all rows costs the scores of smaller ones nothing
-          // that the softmax could see, and goes into the keys' scales.
+          // that the softmax could see, and goes into the tiles' factors.
           float up = 1.f;
           kfac = a.scale_log2;
           if constexpr (BF) {
@@ -367,7 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           signal(&bar_q);
         }
-        if (x + nt < x1) {
+        if (keys && x + nt < x1) {
           typename Ln::Cursor n = u;
           Ln::next_unit(c, a, n);
           prefetch_q(n);
@@ -378,18 +395,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int slot = n % F::SR;
           const uint32_t st = sStage + slot * F::SSLOT;
           if (!warp_wait(&bar_stage[slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
-          if ((n & 1) == 0) {
-            float ksc, vsc;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(st + F::OPB + tid * 4) : "memory");
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vsc) : "r"(st + F::OPB + 512 + tid * 4) : "memory");
-            // No scale (a row of a missing page) stands for a value of zero; a row
-            // behind the end may hold any number, whose 1 / scale must be finite.
-            if (vsc < kMinScale) vsc = kMinScale;
-            const uint32_t sc = sScale + ((n >> 1) % F::SCS) * F::SCB + tid * 4;
-            sts_f32(sc, ksc * kfac);
-            sts_f32(sc + 512, lg2(vsc));
-            // a NaN row's scores are NaN; its 1 / scale must not reach the sums of rows that do not see it
-            sts_f32(sc + 1024, vsc == vsc ? __fdividef(1.f, vsc) : 0.f);
+          const uint32_t mul = sMul + (keys ? 0 : 1024);
+          {
+            // The tile's largest scales, of four keys a lane; every warp for itself.
+            const uint32_t sc = st + F::OPB;
+            auto largest = [&](const float4& x) {
+              const float f[4] = {x.x, x.y, x.z, x.w};
+              uint32_t t = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t b = __float_as_uint(f[e]);
+                if (b < 0x7f800000u && lane * 4 + e < end) t = max(t, b);
+              }
+              return static_cast<int>(__reduce_max_sync(0xffffffffu, t) >> 23);  // biased exponent
+            };
+            const int ve = min(largest(lds_f4(sc + 512 + lane * 16)), 253);
+            // |code| 2^7 < 65504: values up to 2^7 times the power's size fit
+            if (vexp == 0 || ve > vexp + 6) vexp = ve;
+            float m;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + 512 + tid * 4) : "memory");
+            const bool number = m < INFINITY;
+            if (keys) {
+              const int ke = min(max(largest(lds_f4(sc + lane * 16)), 1), 253);
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + tid * 4) : "memory");
+              m *= __uint_as_float(static_cast<uint32_t>(254 - ke) << 23);
+              // A row whose values are not numbers: through its scores it makes
+              // the rows that see it NaN, and does not reach the others.
+              if (!number) m = __uint_as_float(0x7fc00000u);
+              if (tid == 0) {
+                tile_f[(n >> 1) % F::SCS] = kfac * __uint_as_float(static_cast<uint32_t>(ke) << 23);
+                tile_e[(n >> 1) % F::SCS] = vexp;
+              }
+            } else {
+              m = number ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
+            }
+            if (tid >= end) m = 0.f;  // whatever the memory holds there
+            // as the sum of two fp16, 22 bits
+            const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
+            const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mul + tid * 8), "r"(reinterpret_cast<const uint32_t&>(h2)),
+                         "r"(reinterpret_cast<const uint32_t&>(l2))
+                         : "memory");
+            __syncwarp();  // (a warp converts the rows whose multipliers it has stored)
           }
           // Chunk of 16 codes -> two of 8 fp16.  Eight neighbouring lanes take
           // four chunks of a row and the other four of the next one (D = 128),
@@ -404,33 +451,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               *j = lane & 3;
             }
           };
-          uint4 codes[CH];  // all loads first: a load must not wait for the stores before it
+          // four chunks at a time, their loads first (a load must not wait for
+          // the stores before it); not more: see the note on code size above
+#pragma unroll 1
+          for (int i0 = 0; i0 < CH; i0 += 4) {
+            uint4 codes[4];
+            uint32_t m[4][2];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            int r, j;
-            place(i, &r, &j);
-            codes[i] = lds_u4(st + r * DP + j * 16);
-          }
-          if (end < kBN) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
+            for (int i = 0; i < 4; ++i) {
               int r, j;
-              place(i, &r, &j);
-              if (r >= end) codes[i] = make_uint4(0u, 0u, 0u, 0u);
+              place(i0 + i, &r, &j);
+              codes[i] = lds_u4(st + r * DP + j * 16);
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(m[i][0]), "=r"(m[i][1]) : "r"(mul + r * 8) : "memory");
             }
-          }
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            int r, j;
-            place(i, &r, &j);
-            const uint4 v = codes[i];
-            uint32_t h[8];
-            code4_to_f16<CT>(v.x, h[0], h[1]);
-            code4_to_f16<CT>(v.y, h[2], h[3]);
-            code4_to_f16<CT>(v.z, h[4], h[5]);
-            code4_to_f16<CT>(v.w, h[6], h[7]);
-            sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
-            sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
+            for (int i = 0; i < 4; ++i) {
+              int r, j;
+              place(i0 + i, &r, &j);
+              uint4 v = codes[i];
+              if (r >= end) v = make_uint4(0u, 0u, 0u, 0u);
+              uint32_t h[8];
+              code4_to_f16<CT>(v.x, h[0], h[1]);
+              code4_to_f16<CT>(v.y, h[2], h[3]);
+              code4_to_f16<CT>(v.z, h[4], h[5]);
+              code4_to_f16<CT>(v.w, h[6], h[7]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
+                const __half2 x = reinterpret_cast<const __half2&>(h[e]);
+                const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
+                                          __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
+                h[e] = reinterpret_cast<const uint32_t&>(y);
+              }
+              sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
+              sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
+            }
           }
           signal(bar);
           if (lane == 0) mbar_arrive(&bar_sempty[slot]);
@@ -438,19 +492,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         for (int i = 0; i < nt; ++i) {
           const int t = kt + i, ks = t % KST, vs = t % VST, end = u.s.kv - (u.t + i) * kBN;
-          if (t >= KST && !(ok = warp_wait(&bar_kempty[ks], (t / KST - 1) & 1, ctl, kErrTimeoutMma))) break;
-          if (!(ok = convert(2 * t, sK(ks), end, &bar_k[ks]))) break;
-          if (t >= VST && !(ok = warp_wait(&bar_vempty[vs], (t / VST - 1) & 1, ctl, kErrTimeoutMma))) break;
-          if (!(ok = convert(2 * t + 1, sV(vs), end, &bar_v[vs]))) break;
+          uint64_t* const empty = keys ? &bar_kempty[ks] : &bar_vempty[vs];
+          static_assert(KST == VST, "one test for both rings");
+          if (t >= KST && !(ok = warp_wait(empty, (t / KST - 1) & 1, ctl, kErrTimeoutMma))) break;
+          if (!(ok = convert(2 * t + (keys ? 0 : 1), keys ? sK(ks) : sV(vs), end, keys ? &bar_k[ks] : &bar_v[vs]))) break;
         }
       }
       kt += nt;
       x += nt;
       if (x < x1) Ln::next_unit(c, a, u);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= F::MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REG_MMA));
-    if (warp == 12) {
+    if (warp == F::MMA) {
       // ------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_f16(kBM, kBN, MBF, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(kBM, DP, MBF, false, true);
@@ -520,9 +574,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Ln::next_unit(c, a, u);
       }
     }
-    if (warp == 13 || (warp == 14 && !F::Q8)) {
+    if (warp == F::MMA + 1 || (warp == F::MMA + 2 && !F::Q8)) {
       // ------------------------------------------------------- TMA fetches
-      const bool is_k = warp == 13;  // 8-bit: keys and values in turn
+      const bool is_k = warp == F::MMA + 1;  // 8-bit: keys and values in turn
       const int box = a.box_rows, nbox = kBN / box;
       const int outside = c.num_pages * c.Hkv;  // past the maps: reads as zeros
       // this lane's box of tile t: its page (-1: none) and first row
@@ -592,21 +646,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int slot = n % F::SR;
             if (n >= F::SR && !(ok = warp_wait(&bar_sempty[slot], (n / F::SR - 1) & 1, ctl, kErrTimeoutMma))) break;
             const uint32_t st = sStage + slot * F::SSLOT;
-            if (k == 0 && !real && lane < nbox) {  // no scales: zeros
+            // with the keys both scales, with the values theirs again
+            if (!real && lane < nbox) {  // none: zeros
               for (int e = 0; e < box; e += 4) {
-                sts_v4(st + F::OPB + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
+                if (k == 0) sts_v4(st + F::OPB + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
                 sts_v4(st + F::OPB + 512 + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
               }
             }
             __syncwarp();
-            if (lane == 0) mbar_expect_tx(&bar_stage[slot], F::OPB + (k == 0 ? nreal * box * 8 : 0));
+            if (lane == 0) mbar_expect_tx(&bar_stage[slot], F::OPB + nreal * box * (k == 0 ? 8 : 4));
             __syncwarp();
             if (lane < nbox)
               tma_load_3d_any(base + (st - sQ) + lane * box * DP, k == 0 ? &tm_k : &tm_v, &bar_stage[slot], 0, row,
                               real ? page * c.Hkv + h : outside);
-            if (k == 0 && real) {
+            if (real) {
               const size_t at = static_cast<size_t>((page * c.Hkv + h) * static_cast<int>(c.page.d) + row);
-              bulk_load(base + (st - sQ) + F::OPB + lane * box * 4, c.ks + at, box * 4, &bar_stage[slot]);
+              if (k == 0) bulk_load(base + (st - sQ) + F::OPB + lane * box * 4, c.ks + at, box * 4, &bar_stage[slot]);
               bulk_load(base + (st - sQ) + F::OPB + 512 + lane * box * 4, c.vs + at, box * 4, &bar_stage[slot]);
             }
           }
@@ -682,48 +737,70 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t vis[4] = {0u, 0u, 0u, 0u};
       int vis_t = max(0, past / kBN - u.t);
       if (!two) vis_t = vis_t <= w ? 0 : (vis_t - w + 1) >> 1;
-      if (vis_t < n) see_keys((u.t + (two ? vis_t : 2 * vis_t + w)) * kBN, vis);
       float m_ref = -INFINITY, l = 0.f;
+      [[maybe_unused]] int o_exp = 0;  // exponent taken out of the values that O has summed
       for (int t = 0; t < n; ++t, ++ns) {
         const int ti = two ? t : 2 * t + w;       // tile of the piece
         const int k0 = (u.t + ti) * kBN;
         const bool masked = k0 + kBN > past;
-        if (masked && t != vis_t) see_keys(k0, vis);
+        if (t == 0 ? vis_t < n : masked && t != vis_t)
+          see_keys(t == 0 ? (u.t + (two ? vis_t : 2 * vis_t + w)) * kBN : k0, vis);
         if (!(ok = warp_wait(&bar_s[w], ns & 1, ctl, kErrTimeoutMma))) break;
         tc_fence_after();
-        const uint32_t sc = sScale + ((kt0 + ti) % F::SCS) * F::SCB;
-        uint32_t s[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld_x32(s_addr + 32 * k, TA_CHUNK(s, k));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld_wait(TA_CHUNK(s, k));
-        float y[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j) y[j] = __uint_as_float(s[j]);
+        float f = a.scale_log2;  // of the scores
+        int e = 0;
         if constexpr (F::Q8) {
+          f = const_cast<volatile float*>(tile_f)[(kt0 + ti) % F::SCS];
+          e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
+        }
+        // 16 bits: the row's 128 scores in registers.  8 bits: two passes over S
+        // in tensor memory, XC columns at a time (maximum, weights): the loops
+        // of the softmax, the conversions and the MMA warp then stay in the
+        // instruction cache together (with the row in registers a third of all
+        // stalls were missing instructions: 212 us against 140 at the shape
+        // above; alone, beside idle helpers, one pass is faster: 377 us against
+        // 496 for the chunk).
+        constexpr int XC = F::Q8 ? 32 : 128;
+        float y[XC];
+        auto load = [&](int c0) {
+          uint32_t s[XC];
 #pragma unroll
-          for (int j = 0; j < 128; j += 4) {
-            const float4 kx = lds_f4(sc + j * 4), vx = lds_f4(sc + 512 + j * 4);
-            const float2 p = ffma2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y), make_float2(vx.x, vx.y));
-            const float2 q = ffma2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w), make_float2(vx.z, vx.w));
-            y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
+          for (int k = 0; k < XC / 32; ++k) tmem_ld_x32(s_addr + c0 + 32 * k, TA_CHUNK(s, k));
+#pragma unroll
+          for (int k = 0; k < XC / 32; ++k) tmem_ld_wait(TA_CHUNK(s, k));
+#pragma unroll
+          for (int j = 0; j < XC; ++j) y[j] = __uint_as_float(s[j]);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < XC / 32; ++k) {
+              uint32_t seen = vis[k];
+              if constexpr (XC < 128) {
+                const int at = c0 / 32 + k;
+                seen = at == 0 ? vis[0] : at == 1 ? vis[1] : at == 2 ? vis[2] : vis[3];
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((seen >> j) & 1u)) y[32 * k + j] = -INFINITY;
+            }
           }
-        }
-        if (masked) {
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += XC) {
+          load(c0);
+          constexpr int CHAINS = XC >= 64 ? 8 : 4;  // of three-input maxima
+          float mc[CHAINS];
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (!((vis[j >> 5] >> (j & 31)) & 1u)) y[j] = -INFINITY;
-        }
-        float mx8[8];
+          for (int k = 0; k < CHAINS; ++k) {
+            mc[k] = fmax3(y[k], y[CHAINS + k], y[2 * CHAINS + k]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          mx8[k] = fmax3(y[k], y[8 + k], y[16 + k]);
+            for (int j = 3 * CHAINS; j + CHAINS < XC; j += 2 * CHAINS) mc[k] = fmax3(mc[k], y[j + k], y[j + CHAINS + k]);
+            mc[k] = fmaxf(mc[k], y[XC - CHAINS + k]);
+          }
 #pragma unroll
-          for (int j = 24; j < 120; j += 16) mx8[k] = fmax3(mx8[k], y[j + k], y[j + 8 + k]);
-          mx8[k] = fmaxf(mx8[k], y[120 + k]);
+          for (int k = 0; k < CHAINS; k += 2) mx = fmax3(mx, mc[k], mc[k + 1]);
         }
-        const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-        const float m_new = fmaxf(m_ref, F::Q8 ? mx : mx * a.scale_log2);
+        const float m_new = fmaxf(m_ref, mx * f);
         bool resc = false;
         float alpha = 1.f;
         if (t == 0) {
@@ -733,37 +810,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           alpha = ex2(m_ref - m_new);
           m_ref = m_new;
         }
+        float o_alpha = alpha;
+        if constexpr (F::Q8) {  // values of a larger power of two from here on
+          if (t > 0 && e != o_exp) {
+            resc = true;
+            o_alpha *= o_exp ? ex2(static_cast<float>(o_exp - e)) : 0.f;
+          }
+          o_exp = e;
+        }
         const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        const float2 sc2 = make_float2(f, f);
         const float2 nm2 = make_float2(neg_m, neg_m);
         float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += XC) {
+          if constexpr (F::Q8) load(c0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t pk[8];
+          for (int k = 0; k < XC / 16; ++k) {
+            uint32_t pk[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int j = 16 * k + 2 * e;
-            float2 ya = make_float2(y[j], y[j + 1]), yb = make_float2(y[j + 2], y[j + 3]);
-            if constexpr (F::Q8) {
-              ya = fadd2(ya, nm2);
-              yb = fadd2(yb, nm2);
-            } else {
-              ya = ffma2(ya, sc2, nm2);
-              yb = ffma2(yb, sc2, nm2);
+            for (int e = 0; e < 8; ++e) {
+              const float2 t2 = ffma2(make_float2(y[16 * k + 2 * e], y[16 * k + 2 * e + 1]), sc2, nm2);
+              const float2 p2 = make_float2(ex2(t2.x), ex2(t2.y));
+              rs2[e & 3] = fadd2(rs2[e & 3], p2);
+              pk[e] = pack2<MBF>(p2.x, p2.y);
             }
-            const float2 pa = make_float2(ex2(ya.x), ex2(ya.y)), pb = make_float2(ex2(yb.x), ex2(yb.y));
-            if constexpr (F::Q8) {
-              const float4 iv = lds_f4(sc + 1024 + j * 4);
-              rs2[e & 2] = ffma2(pa, make_float2(iv.x, iv.y), rs2[e & 2]);
-              rs2[(e & 2) + 1] = ffma2(pb, make_float2(iv.z, iv.w), rs2[(e & 2) + 1]);
-            } else {
-              rs2[e & 2] = fadd2(rs2[e & 2], pa);
-              rs2[(e & 2) + 1] = fadd2(rs2[(e & 2) + 1], pb);
-            }
-            pk[e] = pack2<MBF>(pa.x, pa.y);
-            pk[e + 1] = pack2<MBF>(pb.x, pb.y);
+            tmem_st_x8(s_addr + c0 / 2 + 8 * k, pk);  // over columns that are read
           }
-          tmem_st_x8(s_addr + 8 * k, pk);
         }
         const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
         l = l * alpha + (rsa.x + rsa.y);
@@ -776,7 +849,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_ld_x32(o_addr + 32 * k, ov);
             tmem_ld_wait(ov);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * o_alpha);
             tmem_st_x32(o_addr + 32 * k, ov);
           }
         }
@@ -800,7 +873,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // one row tile: group 1 hands its state over in rounds of XCH columns
       constexpr int NCH = DP / 4;                                  // float4 columns
       constexpr int XCH = F::XCH, XR = NCH / XCH;
-      float f0 = 1.f, f1 = 0.f;
+      // O's power of two
+      const float o_pow = !F::Q8 ? 1.f : o_exp ? __uint_as_float(static_cast<uint32_t>(o_exp) << 23) : 0.f;
+      float f0 = o_pow, f1 = 0.f;
       const bool whole = u.t == 0 && nt == u.ntiles;
       float* const part = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (x > x0 ? 1 : 0)) * tc_part_floats<CT, DP>();
       const int prow = (two ? w * kBM : 0) + r;
@@ -821,6 +896,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (n > 0) {
               tmem_ld_x32(o_addr + (round * XCH + k) * 4, ov);
               tmem_ld_wait(ov);
+              if constexpr (F::Q8) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * o_pow);
+              }
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) ov[j] = 0u;
@@ -840,9 +919,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (round == 0) {
             const float m1 = xm[r], l1 = xl[r];
             const float mm = fmaxf(m_ref, m1);
-            f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - mm);
+            f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - mm) * o_pow;
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
-            l = mm == -INFINITY ? l + l1 : l * f0 + l1 * f1;
+            l = mm == -INFINITY ? l + l1 : l * (m_ref == -INFINITY ? 0.f : ex2(m_ref - mm)) + l1 * f1;  // NaN stays
             m_ref = mm;
           }
         }
@@ -921,7 +1000,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == F::MMA) tmem_dealloc(tmem, 512);
 }
 
 // Joins the partial states of the units that block borders cut: block (i, y)
@@ -1014,7 +1093,7 @@ cudaError_t run_tc(int dg, const PageMaps& m, const CacheArgs& c, const CacheAtt
   cudaError_t e = smem_attr_once(kern, smem, done);
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache_tc", s);
-  kern<<<kTcBlocks, kTcThreads, smem, s>>>(m.k, m.v, c, a, dg);
+  kern<<<kTcBlocks, TcCfg<CT, DP>::THREADS, smem, s>>>(m.k, m.v, c, a, dg);
   prof_end(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
