@@ -692,12 +692,21 @@ static ta_status cache_dtype_status(ta_dtype dt, ta_dtype ct) {
 // box never leaves its page and starts on a swizzle atom; 0: none does.
 static int page_box_rows(int page) { return page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : page % 8 == 0 ? 8 : 0; }
 
-// Query rows per key head up to which attn_cache (16 to 64 rows per unit, exact
-// row tiles) is used; beyond, the tcgen05 kernel, whose tile has 128 rows.
-static bool attn_cache_few_rows(int D, long long rows) { return rows <= (D <= 64 ? 64 : 32); }
+// Query rows per key head up to which attn_cache (exact tiles of 16 rows) is
+// used; beyond, the tcgen05 kernel, whose tile has 128 rows.  Measured on 16
+// sequences of 8192 tokens, 8 key heads, pages of 32; attn_cache / tcgen05 us:
+//           bf16: 24 rows    32         48         64      int8: 32         48         64
+//   D 128:  110 / 116   110 / 116  188 / 116  190 / 116   106 / 138  171 / 140  173 / 140
+//   D  64:   65 / 73     67 / 73    79 / 74   108 / 75     61 / 112   81 / 112  118 / 112
+//   D  32:   44 / 69     46 / 69    60 / 71    71 / 69     52 / 108   65 / 108   77 / 108
+static bool attn_cache_few_rows(int D, bool bits8, long long rows) {
+  if (D > 64) return rows <= 32;
+  if (D > 32) return rows <= (bits8 ? 48 : 32);
+  return rows <= (bits8 ? 64 : 48);
+}
 
-static bool attn_cache_uses_tc(int D, long long rows, int page) {
-  return !attn_cache_few_rows(D, rows) && page_box_rows(page) > 0;
+static bool attn_cache_uses_tc(int D, bool bits8, long long rows, int page) {
+  return !attn_cache_few_rows(D, bits8, rows) && page_box_rows(page) > 0;
 }
 
 // The larger of the two kernels' needs where page_size, which is not among the
@@ -705,7 +714,7 @@ static bool attn_cache_uses_tc(int D, long long rows, int page) {
 static size_t attn_cache_bytes(int G, int T, int D, ta_dtype ct) {
   const long long rows = static_cast<long long>(G) * T;
   const size_t few = attn_cache_ws_bytes(D, rows);
-  if (attn_cache_few_rows(D, rows)) return few;
+  if (attn_cache_few_rows(D, cache_type(ct) != kCache16, rows)) return few;
   return std::max(few, cache_type(ct) == kCache16 ? attn_cache_tc16_ws_bytes(D) : attn_cache_tc8_ws_bytes(D));
 }
 
@@ -1139,7 +1148,7 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
   const int ct = cache_type(cache->ct);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dt == TA_BF16;
-  if (!attn_cache_uses_tc(cache->D, static_cast<long long>(a.G) * T, cache->page_size))
+  if (!attn_cache_uses_tc(cache->D, ct != kCache16, static_cast<long long>(a.G) * T, cache->page_size))
     return cuda_status(launch_attn_cache(bf16, ct, cache->D, c, a, s));
   PageMaps m;
   const long long heads = static_cast<long long>(c.num_pages) * c.Hkv;

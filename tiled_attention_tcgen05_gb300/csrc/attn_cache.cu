@@ -9,9 +9,9 @@ namespace ta {
 cudaError_t launch_attn_cache_rows8(bool bf16, int ct, int D, int mt, const CacheArgs& c, const CacheAttnArgs& a,
                                     cudaStream_t s);
 
-// Row tiles (of 16) per unit.
+// Row tiles (of 16) per unit: as many as the accumulators leave registers for.
 static int row_tiles(int D, long long rows) {
-  const long long most = D <= 64 ? 4 : 2;
+  const long long most = D <= 32 ? 4 : D <= 64 ? 3 : 2;
   return static_cast<int>(std::min((rows + 15) / 16, most));
 }
 

@@ -851,9 +851,11 @@ template <typename T, int CT, int D>
 cudaError_t run_mt(int mt, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   if (mt == 1) return run_rows<T, CT, D, 1>(c, a, s);
   if (mt == 2) return run_rows<T, CT, D, 2>(c, a, s);
-  if constexpr (D <= 64) {  // (D = 128: 192 and 256 accumulators a lane)
+  if constexpr (D <= 64) {  // (MT x D / 2 accumulators a lane)
     if (mt == 3) return run_rows<T, CT, D, 3>(c, a, s);
-    return run_rows<T, CT, D, 4>(c, a, s);
+  }
+  if constexpr (D <= 32) {
+    if (mt == 4) return run_rows<T, CT, D, 4>(c, a, s);
   }
   return cudaErrorInvalidValue;
 }
