@@ -38,8 +38,8 @@
 // added to their result.
 #pragma once
 #include "attn_cache.cuh"
+#include "bwd_common.cuh"
 #include "common.cuh"
-#include "fwd_mma.cuh"
 #include "launch.h"
 
 namespace ta {
@@ -109,6 +109,35 @@ __device__ __forceinline__ void sts_f32(uint32_t a, float v) {
 // Address of 16-byte chunk j (8 elements) of row r in a tile.
 __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int j) {
   return tile + (j >> 3) * (kBM * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4);
+}
+
+// TMA load of a box of a map without a swizzle: the destination needs 128 bytes
+// of alignment only (tma_load_3d's check asks for a swizzle atom's).
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2) {
+  if (!TA_CHECK_V((smem_u32(dst) & 127u) == 0u && guard_in_dyn_smem(smem_u32(dst)) && c1 >= 0 && c2 >= 0,
+                  smem_u32(dst)))
+    return;
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// d (+)= P V: P 128 x 128 (16-bit, packed in tensor memory), V 128 rows of D,
+// read as an MN-major B operand.
+template <int D>
+__device__ __forceinline__ void mma_weights(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_smem, uint32_t idesc,
+                                            bool accumulate) {
+  const uint64_t dv = sdesc_sw128(v_smem, kBM * 128, 1024);
+  uint32_t a[kBN / 16];
+  uint64_t b[kBN / 16];
+#pragma unroll
+  for (int kk = 0; kk < kBN / 16; ++kk) {
+    a[kk] = p_tmem + kk * 8;
+    b[kk] = dv + static_cast<uint64_t>((kk * 16 * 128) >> 4);
+  }
+  mma_ts_n<kBN / 16>(d_tmem, a, b, idesc, accumulate ? 1u : 0u);
 }
 
 // Adds the infinities and NaN among the values of the draft's tokens that
@@ -530,7 +559,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         auto issue_s = [&](int w, bool first, bool last) -> bool {
           if (first && !warp_wait(&bar_k[ks], kp, ctl, kErrTimeoutTma)) return false;
           tc_fence_after();
-          mma_qk<DP>(tmem + col_s[w], sQ + (two ? w * F::TILE : 0), sK(ks), idesc_qk, false);
+          mma_abT<DP>(tmem + col_s[w], sQ + (two ? w * F::TILE : 0), sK(ks), idesc_qk);
           commit_el(&bar_s[w]);
           if (last) next_k();
           return true;
@@ -541,7 +570,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           if (w) pp1 ^= 1;
           else pp0 ^= 1;
           tc_fence_after();
-          mma_pv<DP>(tmem + col_o[w], tmem + col_s[w], sV(vs), idesc_pv, add);
+          mma_weights<DP>(tmem + col_o[w], tmem + col_s[w], sV(vs), idesc_pv, add);
           commit_el(&bar_o[w]);
           if (last) next_v();
           return true;
@@ -657,8 +686,8 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             if (lane == 0) mbar_expect_tx(&bar_stage[slot], F::OPB + nreal * box * (k == 0 ? 8 : 4));
             __syncwarp();
             if (lane < nbox)
-              tma_load_3d_any(base + (st - sQ) + lane * box * DP, k == 0 ? &tm_k : &tm_v, &bar_stage[slot], 0, row,
-                              real ? page * c.Hkv + h : outside);
+              tma_load_rows(base + (st - sQ) + lane * box * DP, k == 0 ? &tm_k : &tm_v, &bar_stage[slot], row,
+                            real ? page * c.Hkv + h : outside);
             if (real) {
               const size_t at = static_cast<size_t>((page * c.Hkv + h) * static_cast<int>(c.page.d) + row);
               if (k == 0) bulk_load(base + (st - sQ) + F::OPB + lane * box * 4, c.ks + at, box * 4, &bar_stage[slot]);
@@ -765,9 +794,9 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         auto load = [&](int c0) {
           uint32_t s[XC];
 #pragma unroll
-          for (int k = 0; k < XC / 32; ++k) tmem_ld_x32(s_addr + c0 + 32 * k, TA_CHUNK(s, k));
+          for (int k = 0; k < XC / 32; ++k) tmem_ld_x32(s_addr + c0 + 32 * k, TB_CHUNK(s, k));
 #pragma unroll
-          for (int k = 0; k < XC / 32; ++k) tmem_ld_wait(TA_CHUNK(s, k));
+          for (int k = 0; k < XC / 32; ++k) tmem_ld_wait(TB_CHUNK(s, k));
 #pragma unroll
           for (int j = 0; j < XC; ++j) y[j] = __uint_as_float(s[j]);
           if (masked) {

@@ -11,6 +11,10 @@
 
 namespace ta {
 
+// Bit of the device error word (ptx.cuh): a length, page or token index outside
+// the cache.
+constexpr uint32_t kErrIndex = 1u << 6;
+
 enum CacheType : int { kCache16 = 0, kCacheE4m3 = 1, kCacheI8 = 2 };
 
 // The scale of a row is amax / kQmax, at least this (a row of zeros, or of

@@ -18,7 +18,6 @@ enum : uint32_t {
   kErrTimeoutSoftmax = 1u << 2,  // a wait for softmax/producer output ran out
   kErrTimeoutOther = 1u << 3,
   kErrSmemLayout = 1u << 4,    // a kernel could not lay out its shared memory (did not run)
-  kErrIndex = 1u << 6,         // a length, page or token index outside the cache (bit 5: guard.cuh)
 };
 
 struct WaitCtl {
@@ -117,21 +116,6 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                                             int c2) {
   if (!TA_CHECK_V((smem_u32(dst) & 1023u) == 0u && guard_in_dyn_smem(smem_u32(dst)) && (c0 & 15) == 0 && c1 >= 0 &&
-                      c2 >= 0,
-                  smem_u32(dst)))
-    return;
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
-// The same for maps without a swizzle: the destination needs 128 bytes of
-// alignment only.
-__device__ __forceinline__ void tma_load_3d_any(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                                int c2) {
-  if (!TA_CHECK_V((smem_u32(dst) & 127u) == 0u && guard_in_dyn_smem(smem_u32(dst)) && (c0 & 15) == 0 && c1 >= 0 &&
                       c2 >= 0,
                   smem_u32(dst)))
     return;
