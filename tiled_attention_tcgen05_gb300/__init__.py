@@ -380,8 +380,8 @@ class KVCache:
 
 
 def kv_cache(num_pages, Hkv, page_size, D, dtype=torch.bfloat16, device="cuda") -> KVCache:
-    """An empty KVCache (rows are whatever the memory holds until they are
-    written; no call reads rows behind a sequence's end)."""
+    """An empty KVCache (its memory may hold anything: rows behind a sequence's
+    end have no effect)."""
     k = torch.empty((num_pages, Hkv, page_size, D), dtype=dtype, device=device)
     ks = vs = None
     if dtype in (torch.float8_e4m3fn, torch.int8):

@@ -52,7 +52,8 @@ static ta_status guard_status() {
                                {"merge.cu", guard_take_merge},   {"fp32.cu", guard_take_fp32},
                                {"bwd_pw_steps.cu", guard_take_bwd_pw_steps},
                                {"cache_io.cu", guard_take_cache_io}, {"attn_cache.cu", guard_take_attn_cache},
-                               {"attn_cache8.cu", guard_take_attn_cache8},
+                               {"attn_cache_e4m3.cu", guard_take_attn_cache_e4m3},
+                               {"attn_cache_i8.cu", guard_take_attn_cache_i8},
                                {"attn_cache_tc.cu", guard_take_attn_cache_tc},
                                {"attn_cache_tc8.cu", guard_take_attn_cache_tc8}};
   bool failed = false;

@@ -6,8 +6,10 @@
 
 namespace ta {
 
-cudaError_t launch_attn_cache_rows8(bool bf16, int ct, int D, int mt, const CacheArgs& c, const CacheAttnArgs& a,
-                                    cudaStream_t s);
+cudaError_t launch_attn_cache_rows_e4m3(bool bf16, int D, int mt, const CacheArgs& c, const CacheAttnArgs& a,
+                                        cudaStream_t s);
+cudaError_t launch_attn_cache_rows_i8(bool bf16, int D, int mt, const CacheArgs& c, const CacheAttnArgs& a,
+                                      cudaStream_t s);
 
 // Row tiles (of 16) per unit: as many as the accumulators leave registers for.
 static int row_tiles(int D, long long rows) {
@@ -23,7 +25,8 @@ size_t attn_cache_ws_bytes(int D, long long rows) {
 
 cudaError_t launch_attn_cache(bool bf16, int ct, int D, const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   const int mt = row_tiles(D, static_cast<long long>(a.G) * c.T);
-  if (ct != kCache16) return launch_attn_cache_rows8(bf16, ct, D, mt, c, a, s);
+  if (ct == kCacheE4m3) return launch_attn_cache_rows_e4m3(bf16, D, mt, c, a, s);
+  if (ct == kCacheI8) return launch_attn_cache_rows_i8(bf16, D, mt, c, a, s);
   return bf16 ? run_d<__nv_bfloat16, kCache16>(D, mt, c, a, s) : run_d<__half, kCache16>(D, mt, c, a, s);
 }
 

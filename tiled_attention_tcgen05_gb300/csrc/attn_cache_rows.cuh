@@ -20,9 +20,13 @@
 // memory (cp.async, swizzled).  The warps' states are
 // joined through shared memory at the end of a sequence.
 //
-// Work is cut as attn_cache.cuh says, two blocks per SM.
+// Work is cut as attn_cache.cuh says, two blocks per SM.  Few units of short
+// sequences are taken by a cluster of eight blocks each instead (CLUSTER): they
+// share the unit's keys and join their states over distributed shared memory,
+// which saves the look at all sequences' lengths and the second kernel.
 #pragma once
 #include "attn_cache.cuh"
+#include "cluster.cuh"
 
 namespace ta {
 
@@ -124,7 +128,9 @@ __device__ __forceinline__ int oswz(int r, int ch) {
   return ch ^ ((((r & 3) << 1) ^ (ch >> 3)) & (D / 4 - 1) & 7);
 }
 
-template <typename T, int CT, int D, int MT>
+constexpr int kCluster = 8;
+
+template <typename T, int CT, int D, int MT, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_kernel(CacheArgs c, CacheAttnArgs a) {
   using F = Cfg<CT, D, MT>;
   constexpr bool BF = DT<T>::bf16;
@@ -134,26 +140,44 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
   extern __shared__ __align__(128) uint8_t smem[];
   using Ln = Line<ROWS, TK>;
   __shared__ typename Ln::Shared line;
-  let_dependents_launch();
+  if constexpr (!CLUSTER) let_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, cq = lane & 3;
 
-  long long mine, before;
-  const long long len = Ln::template length<kWarps * 32>(c, a, line, &mine, &before);
-  const long long x0 = cut<F::BLOCKS>(len, blockIdx.x), x1 = cut<F::BLOCKS>(len, blockIdx.x + 1);
-  CutUnit* const cuts = reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART);
-  if (x0 >= x1) {
-    if (threadIdx.x == 0) write_cut<F::BLOCKS, typename Ln::Cursor>(cuts, len, blockIdx.x, x0, x1, nullptr);
-    return;
-  }
+  // This block's places x0 .. x1 of the line (CLUSTER: its tiles of the unit),
+  // and the first of them.
   typename Ln::Cursor cc;
-  Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
+  long long x0, x1;
+  [[maybe_unused]] long long len = 0;
+  CutUnit* const cuts = reinterpret_cast<CutUnit*>(a.ws + static_cast<size_t>(F::BLOCKS) * 2 * F::PART);
+  if constexpr (CLUSTER) {
+    const int unit = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+    cc.b = unit / c.Hkv;
+    cc.h = unit - cc.b * c.Hkv;
+    cc.rt = 0;
+    cc.s = Ln::seq(c, a, cc.b);
+    cc.ntiles = cc.s.nrt > 0 ? Ln::tiles(a, cc.s, 0) : 0;
+    x0 = cc.ntiles * rank / kCluster;
+    x1 = cc.ntiles * (rank + 1) / kCluster;
+    cc.t = static_cast<int>(x0);
+  } else {
+    long long mine, before;
+    len = Ln::template length<kWarps * 32>(c, a, line, &mine, &before);
+    x0 = cut<F::BLOCKS>(len, blockIdx.x);
+    x1 = cut<F::BLOCKS>(len, blockIdx.x + 1);
+    if (x0 >= x1) {
+      if (threadIdx.x == 0) write_cut<F::BLOCKS, typename Ln::Cursor>(cuts, len, blockIdx.x, x0, x1, nullptr);
+      return;
+    }
+    Ln::template find<kWarps * 32>(c, a, line, x0, mine, before, cc);
+  }
   typename Ln::Cursor pc = cc;  // the next tile to copy
 
   uint8_t* const ring = smem + warp * F::RING;
   float* const ml = reinterpret_cast<float*>(smem + kWarps * F::RING);      // [warps][ROWS][2]
   uint4* const qs = reinterpret_cast<uint4*>(ml + kWarps * ROWS * 2);       // [MT][NK][32], MT > 1
   float* const facs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(qs) + F::QBYTES);  // [ROWS]
+  float* const state = facs + ROWS;  // CLUSTER: this block's state, PART floats
   const uint32_t ring_a = smem_u32(ring);
 
   // Page entry of this lane's key of the next tile to copy, read a tile early.
@@ -239,7 +263,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
     }
   };
 
-  look_up();
+  if (x0 < x1) look_up();
 #pragma unroll
   for (int s = 0; s < F::STAGES; ++s) {
     if (x0 + s < x1) {
@@ -251,7 +275,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
   }
 
   // (behind the first loads: its divisions take as long)
-  if (threadIdx.x == 32) write_cut<F::BLOCKS>(cuts, len, blockIdx.x, x0, x1, &cc);
+  if constexpr (!CLUSTER) {
+    if (threadIdx.x == 32) write_cut<F::BLOCKS>(cuts, len, blockIdx.x, x0, x1, &cc);
+  }
 
   uint32_t qf[MT == 1 ? NK : 1][4];
   float f1[2];  // MT == 1: the rows' score factors
@@ -608,8 +634,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           }
         }
       }
-      const bool whole = from_start && last;
-      float* const part = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (x - x0 > cc.t ? 1 : 0)) * F::PART;
+      const bool whole = !CLUSTER && from_start && last;
+      float* const part =
+          CLUSTER ? state : a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (x - x0 > cc.t ? 1 : 0)) * F::PART;
       uint8_t* const st = ring + slot * (F::SLOT + F::SCALES);  // the tile this warp has just used
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -702,7 +729,59 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
     }
     cp_async_commit();
     slot = slot + 1 == F::STAGES ? 0 : slot + 1;
-    Ln::next_tile(c, a, cc);
+    if (!CLUSTER || x + 1 < x1) Ln::next_tile(c, a, cc);
+  }
+
+  if constexpr (CLUSTER) {
+    if (x0 >= x1) {  // no tiles: an empty state
+      for (int i = threadIdx.x; i < ROWS * D; i += kWarps * 32) state[i] = 0.f;
+      for (int i = threadIdx.x; i < ROWS; i += kWarps * 32) {
+        state[ROWS * D + 2 * i] = -INFINITY;
+        state[ROWS * D + 2 * i + 1] = 0.f;
+      }
+    }
+    cluster_sync_all();
+    // rows rank, rank + 8, ... of the unit, D / 4 threads a row
+    const int rank = static_cast<int>(cluster_ctarank());
+    constexpr int TPR = D / 4, RPP = kWarps * 32 / TPR;
+    const int ch = threadIdx.x % TPR;
+    for (int k = threadIdx.x / TPR; k < ROWS / kCluster; k += RPP) {
+      const int r = rank + kCluster * k;
+      const int t = static_cast<int>(a.g_div.div(r)), hq = cc.h * a.G + (r - t * a.G);
+      if (t >= cc.s.q) continue;
+      const uint32_t at = smem_u32(state);
+      float pm[kCluster], pl[kCluster];
+      float4 y[kCluster];
+#pragma unroll
+      for (int p = 0; p < kCluster; ++p) {
+        const uint32_t peer = mapa_shared(at, p);
+        pm[p] = ld_cluster_f32(peer + (ROWS * D + 2 * r) * 4);
+        pl[p] = ld_cluster_f32(peer + (ROWS * D + 2 * r + 1) * 4);
+        y[p] = ld_cluster_v4(peer + (r * D + ch * 4) * 4);
+      }
+      float mm = -INFINITY;
+#pragma unroll
+      for (int p = 0; p < kCluster; ++p) mm = fmaxf(mm, pm[p]);
+      float ll = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < kCluster; ++p) {
+        const float f = pm[p] == -INFINITY ? 0.f : ex2(pm[p] - mm);
+        ll += mm == -INFINITY ? pl[p] : pl[p] * f;  // a NaN sum stays one where no score was a number
+        v[0] = fmaf(y[p].x, f, v[0]);
+        v[1] = fmaf(y[p].y, f, v[1]);
+        v[2] = fmaf(y[p].z, f, v[2]);
+        v[3] = fmaf(y[p].w, f, v[3]);
+      }
+      const float norm = ll == 0.f ? 0.f : 1.f / ll;
+      uint2 o;
+      o.x = pack2<BF>(v[0] * norm, v[1] * norm);
+      o.y = pack2<BF>(v[2] * norm, v[3] * norm);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + cc.b * a.os[0] + hq * a.os[1] + t * a.os[2] + ch * 4) = o;
+      if (ch == 0)
+        a.lse[(static_cast<long long>(cc.b) * a.Hq + hq) * c.T + t] =
+            ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
+    }
+    cluster_sync_all();  // the peers have read this block's state
   }
 }
 
@@ -829,11 +908,53 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
         ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
 }
 
+// Whether each unit gets a cluster: few units, of sequences that cannot be long
+// as far as their page tables go (the lengths are on the device).  Measured, one
+// token a sequence, 4 query heads per key head of 128, us of a replayed graph, cut
+// line / clusters:
+//   tokens         1024          4096          8192          16384
+//   bf16,  1 unit  25.7 / 11.4   29.8 / 17.5   29.8 / 25.7   31.9 / 40.1
+//   bf16,  8       17.5 / 13.4   19.6 / 17.5   21.6 / 25.7   27.8 / 42.1
+//   bf16, 32       19.6 / 13.4   27.7 / 23.7   38.0 / 31.9   56.4 / 52.4
+//   int8,  8       19.6 / 13.4   19.6 / 17.5   21.7 / 21.6   25.8 / 29.8
+//   int8, 32       19.6 / 13.4   25.7 / 19.6   31.9 / 25.7   42.1 / 38.0
+// (where there are more units clusters would win longer, but only for
+// sequences of about one length).
+template <typename F>
+inline bool few_units(const CacheArgs& c, const CacheAttnArgs& a) {
+  return static_cast<long long>(a.G) * c.T <= F::ROWS && static_cast<long long>(c.B) * c.Hkv <= F::BLOCKS / kCluster &&
+         c.capacity <= 8192 && static_cast<long long>(c.capacity) * F::RB <= 4096 * 256;
+}
+
 template <typename T, int CT, int D, int MT>
 cudaError_t run_rows(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
   using F = Cfg<CT, D, MT>;
-  auto* kern = attn_cache_kernel<T, CT, D, MT>;
+  if constexpr (MT <= 2) {
+    if (few_units<F>(c, a)) {
+      static std::atomic<bool> cdone[kMaxDevices];
+      auto* kern = attn_cache_kernel<T, CT, D, MT, true>;
+      constexpr int smem = F::SMEM + F::PART * 4;
+      cudaError_t e = smem_attr_once(kern, smem, cdone);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c.B * c.Hkv * kCluster);
+      cfg.blockDim = dim3(kWarps * 32);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = s;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = kCluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      prof_begin("attn_cache_cluster", s);
+      e = cudaLaunchKernelEx(&cfg, kern, c, a);
+      prof_end(s);
+      return e;
+    }
+  }
+  auto* kern = attn_cache_kernel<T, CT, D, MT, false>;
   cudaError_t e = smem_attr_once(kern, F::SMEM, done);
   if (e != cudaSuccess) return e;
   prof_begin("attn_cache", s);

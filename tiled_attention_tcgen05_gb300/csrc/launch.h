@@ -47,7 +47,8 @@ uint32_t guard_take_fp32(uint32_t* info);
 uint32_t guard_take_bwd_pw_steps(uint32_t* info);
 uint32_t guard_take_cache_io(uint32_t* info);
 uint32_t guard_take_attn_cache(uint32_t* info);
-uint32_t guard_take_attn_cache8(uint32_t* info);
+uint32_t guard_take_attn_cache_e4m3(uint32_t* info);
+uint32_t guard_take_attn_cache_i8(uint32_t* info);
 uint32_t guard_take_attn_cache_tc(uint32_t* info);
 uint32_t guard_take_attn_cache_tc8(uint32_t* info);
 #endif
