@@ -105,11 +105,10 @@ def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=N
       * the product with V and the sum l: N fp32 adds, N 2^-23 (P |V|) each, and
         a few roundings of the joins: (N + 64) 2^-22 together;
       * the result's rounding u |O|;
-      * with more than 32 rows 8-bit rows may be multiplied out to fp16 (each
+      * with more than 32 rows 8-bit values may be multiplied out to fp16 (each
         rounded to 2^-11, or half a step of 2^-24 of the largest scale, which is
-        at most max|k| / 127): s (2^-11 sum|q k| + 2^-25 max|k| / 127 sum|q|) in a
-        score, 2^-11 (P |V|) + 2^-25 max|v| / 127 in O; the weights' half steps then
-        count 2^-25 max_j P_ij sum_j |v_j|.
+        at most max|v| / 127): 2^-11 (P |V|) + 2^-25 max|v| / 127 in O; the weights'
+        half steps then count 2^-25 max_j P_ij sum_j |v_j|.
     """
     O, L = oracle.cache_attention(q, k, v, tree, sm_scale)
     qn, kn, vn = (np.asarray(x, dtype=np.float64) for x in (to_np(q), k, v))
@@ -127,9 +126,6 @@ def attention_reference(q, k, v, tree, kind, dtype, vscale_rows=None, sm_scale=N
         if kind not in ("f16", "bf16"):
             e += s * 2.0 ** -24 * np.abs(qn[g]).max(1, keepdims=True) * np.abs(kn).sum(1)[None]
         wide = kind not in ("f16", "bf16") and (rows or G * T) > 32
-        if wide and N:
-            e += s * (2.0 ** -11 * (np.abs(qn[g]) @ np.abs(kn).T)
-                      + 2.0 ** -25 * np.abs(kn).max() / 127 * np.abs(qn[g]).sum(1, keepdims=True))
         e = np.where(keep, e, 0.0).max(1)
         P = np.where(keep, np.exp(np.where(keep, S, -np.inf) - np.where(np.isfinite(L[g]), L[g], 0.0)[:, None]), 0.0)
         PV = P @ np.abs(vn)

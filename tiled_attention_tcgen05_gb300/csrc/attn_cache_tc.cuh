@@ -20,15 +20,13 @@
 // that do not exist are fetched from outside the map and so read as zeros.
 // 16-bit rows go straight into the 128-byte-swizzled layout that the MMA
 // descriptors read.  8-bit codes and their scales go into a staging ring
-// several tiles ahead; the eight helpers turn them into fp16 rows, code * scale with a
-// power of two taken out that all keys of the tile, and all values of the piece
-// so far, share.  (The scales as they are, one per column of S, would have to be
-// read by every row: 96 16-byte loads of shared memory a row and tile, which
-// took more of its bandwidth than the MMAs: 184 us where this takes @@ for 16
-// sequences of 8192, 8 key heads of 128 with 64 rows, e4m3.)  The rounding of a
-// row to 11 bits adds 2^-11 of sum |q k| to a score and of P |V| to the result
-// at most; attn_cache.cu, whose warps read a scale for many rows' scores, keeps
-// the codes exact.
+// several tiles ahead; the eight helpers turn them into fp16: the keys' codes as
+// they are (exact; a key's scale multiplies its finished scores in fp32), the
+// values' rows multiplied out, with a power of two taken out that all values of
+// the piece so far share.  (A value's scale in the exponent, as in
+// attn_cache_rows.cuh, would have every row read two more numbers per key from
+// shared memory.)  That rounding, of a row to 11 bits, adds 2^-11 P |V| to the
+// result at most.
 //
 // A box may bring rows behind the sequence's end, whose memory may hold
 // anything, and a draft's values may hold infinities and NaN that some rows
@@ -58,8 +56,8 @@ struct TcCfg {
   static constexpr int OPB = Q8 ? 128 * DP : 0;          // codes of one tile
   static constexpr int SR = Q8 ? (DP == 128 ? 3 : 6) : 0;  // staging ring
   static constexpr int SSLOT = OPB + 1024;               // and their scales (K tiles)
-  static constexpr int SCS = KST + 2;                    // ring of the tiles' powers of two, for the softmax
-  static constexpr int MUL = Q8 ? 2 * 128 * 8 : 0;       // multipliers of a tile's rows
+  static constexpr int SCS = KST + 2;                    // tiles whose scales the softmax may need
+  static constexpr int MUL = Q8 ? 1024 + SCS * 512 : 0;  // values' multipliers; ring of keys' scales
   static constexpr int HELPERS = Q8 ? 8 : 4;             // warps 8 .. 8 + HELPERS - 1
   static constexpr int MMA = 8 + HELPERS;                // warp; the fetching warps follow it
   static constexpr int THREADS = 32 * (MMA + 4);         // whole register groups of four warps
@@ -183,9 +181,8 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   __shared__ float xm[kBM], xl[kBM];
   __shared__ __align__(8) uint64_t bar_qtop;
   __shared__ uint32_t qtop[2][4];  // largest query magnitudes, of even and odd pieces
-  // 8 bits, per tile: factor of its scores; biased exponent taken out of its
-  // values (0: all of them are zero so far)
-  __shared__ float tile_f[F::SCS];
+  // 8 bits, per tile: biased exponent taken out of its values (0: all of them
+  // are zero so far)
   __shared__ int tile_e[F::SCS];
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
   __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
@@ -298,7 +295,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     bool ok = true;
     long long x = x0;
     [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
-    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the scores in this piece
+    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the keys' scales in this piece
     [[maybe_unused]] int vexp = 0;           // 8-bit: exponent taken out of the piece's values (tile_e)
     for (int piece = 0; ok && x < x1; ++piece) {
       const int nt = piece_tiles(u, x);
@@ -369,7 +366,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           // two.  An element is then off by at most 2^-25 of that, so a score
           // by 2^-25 of what the largest query could give with the same key:
           // one factor for all rows costs the scores of smaller ones nothing
-          // that the softmax could see, and goes into the tiles' factors.
+          // that the softmax could see, and goes into the keys' scales.
           float up = 1.f;
           kfac = a.scale_log2;
           if constexpr (BF) {
@@ -424,48 +421,42 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           const int slot = n % F::SR;
           const uint32_t st = sStage + slot * F::SSLOT;
           if (!warp_wait(&bar_stage[slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
-          const uint32_t mul = sMul + (keys ? 0 : 1024);
           {
-            // The tile's largest scales, of four keys a lane; every warp for itself.
+            // The tile's largest value scale, of four keys a lane; every warp, of
+            // keys too, for itself.
             const uint32_t sc = st + F::OPB;
-            auto largest = [&](const float4& x) {
-              const float f[4] = {x.x, x.y, x.z, x.w};
-              uint32_t t = 0;
+            const float4 v4 = lds_f4(sc + 512 + lane * 16);
+            const float f4[4] = {v4.x, v4.y, v4.z, v4.w};
+            uint32_t top = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t b = __float_as_uint(f[e]);
-                if (b < 0x7f800000u && lane * 4 + e < end) t = max(t, b);
-              }
-              return static_cast<int>(__reduce_max_sync(0xffffffffu, t) >> 23);  // biased exponent
-            };
-            const int ve = min(largest(lds_f4(sc + 512 + lane * 16)), 253);
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t b = __float_as_uint(f4[e]);
+              if (b < 0x7f800000u && lane * 4 + e < end) top = max(top, b);
+            }
+            const int ve = min(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23), 253);  // biased exponent
             // |code| 2^7 < 65504: values up to 2^7 times the power's size fit
             if (vexp == 0 || ve > vexp + 6) vexp = ve;
             float m;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + 512 + tid * 4) : "memory");
             const bool number = m < INFINITY;
             if (keys) {
-              const int ke = min(max(largest(lds_f4(sc + lane * 16)), 1), 253);
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + tid * 4) : "memory");
-              m *= __uint_as_float(static_cast<uint32_t>(254 - ke) << 23);
               // A row whose values are not numbers: through its scores it makes
               // the rows that see it NaN, and does not reach the others.
-              if (!number) m = __uint_as_float(0x7fc00000u);
-              if (tid == 0) {
-                tile_f[(n >> 1) % F::SCS] = kfac * __uint_as_float(static_cast<uint32_t>(ke) << 23);
-                tile_e[(n >> 1) % F::SCS] = vexp;
-              }
+              m = number ? m * kfac : __uint_as_float(0x7fc00000u);
+              if (tid >= end) m = 0.f;  // whatever the memory holds there
+              sts_f32(sMul + 1024 + ((n >> 1) % F::SCS) * 512 + tid * 4, m);
+              if (tid == 0) tile_e[(n >> 1) % F::SCS] = vexp;
             } else {
-              m = number ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
+              m = number && tid < end ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
+              // as the sum of two fp16, 22 bits
+              const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
+              const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sMul + tid * 8),
+                           "r"(reinterpret_cast<const uint32_t&>(h2)), "r"(reinterpret_cast<const uint32_t&>(l2))
+                           : "memory");
+              __syncwarp();  // (a warp converts the rows whose multipliers it has stored)
             }
-            if (tid >= end) m = 0.f;  // whatever the memory holds there
-            // as the sum of two fp16, 22 bits
-            const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
-            const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mul + tid * 8), "r"(reinterpret_cast<const uint32_t&>(h2)),
-                         "r"(reinterpret_cast<const uint32_t&>(l2))
-                         : "memory");
-            __syncwarp();  // (a warp converts the rows whose multipliers it has stored)
           }
           // Chunk of 16 codes -> two of 8 fp16.  Eight neighbouring lanes take
           // four chunks of a row and the other four of the next one (D = 128),
@@ -485,13 +476,14 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
 #pragma unroll 1
           for (int i0 = 0; i0 < CH; i0 += 4) {
             uint4 codes[4];
-            uint32_t m[4][2];
+            uint32_t m[4][2] = {};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               int r, j;
               place(i0 + i, &r, &j);
               codes[i] = lds_u4(st + r * DP + j * 16);
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(m[i][0]), "=r"(m[i][1]) : "r"(mul + r * 8) : "memory");
+              if (!keys)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(m[i][0]), "=r"(m[i][1]) : "r"(sMul + r * 8) : "memory");
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -504,12 +496,14 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
               code4_to_f16<CT>(v.y, h[2], h[3]);
               code4_to_f16<CT>(v.z, h[4], h[5]);
               code4_to_f16<CT>(v.w, h[6], h[7]);
+              if (!keys) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
-                const __half2 x = reinterpret_cast<const __half2&>(h[e]);
-                const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
-                                          __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
-                h[e] = reinterpret_cast<const uint32_t&>(y);
+                for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
+                  const __half2 x = reinterpret_cast<const __half2&>(h[e]);
+                  const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
+                                            __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
+                  h[e] = reinterpret_cast<const uint32_t&>(y);
+                }
               }
               sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
               sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
@@ -776,14 +770,12 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           see_keys(t == 0 ? (u.t + (two ? vis_t : 2 * vis_t + w)) * kBN : k0, vis);
         if (!(ok = warp_wait(&bar_s[w], ns & 1, ctl, kErrTimeoutMma))) break;
         tc_fence_after();
-        float f = a.scale_log2;  // of the scores
+        const float f = F::Q8 ? 1.f : a.scale_log2;  // of the scores (8 bits: in the keys' scales)
         int e = 0;
-        if constexpr (F::Q8) {
-          f = const_cast<volatile float*>(tile_f)[(kt0 + ti) % F::SCS];
-          e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
-        }
+        if constexpr (F::Q8) e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
+        [[maybe_unused]] const uint32_t key_scales = sMul + 1024 + ((kt0 + ti) % F::SCS) * 512;
         // 16 bits: the row's 128 scores in registers.  8 bits: two passes over S
-        // in tensor memory, XC columns at a time (maximum, weights): the loops
+        // in tensor memory, XC columns at a time (scales, mask and maximum; weights): the loops
         // of the softmax, the conversions and the MMA warp then stay in the
         // instruction cache together (with the row in registers a third of all
         // stalls were missing instructions: 212 us against 140 at the shape
@@ -791,7 +783,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         // 496 for the chunk).
         constexpr int XC = F::Q8 ? 32 : 128;
         float y[XC];
-        auto load = [&](int c0) {
+        auto load = [&](int c0, bool first) {  // 8 bits: the first pass leaves what the second takes
           uint32_t s[XC];
 #pragma unroll
           for (int k = 0; k < XC / 32; ++k) tmem_ld_x32(s_addr + c0 + 32 * k, TB_CHUNK(s, k));
@@ -799,6 +791,16 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           for (int k = 0; k < XC / 32; ++k) tmem_ld_wait(TB_CHUNK(s, k));
 #pragma unroll
           for (int j = 0; j < XC; ++j) y[j] = __uint_as_float(s[j]);
+          if constexpr (F::Q8) {
+            if (!first) return;
+#pragma unroll
+            for (int j = 0; j < XC; j += 4) {
+              const float4 kx = lds_f4(key_scales + (c0 + j) * 4);
+              const float2 p = fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y));
+              const float2 q = fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w));
+              y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
+            }
+          }
           if (masked) {
 #pragma unroll
             for (int k = 0; k < XC / 32; ++k) {
@@ -812,11 +814,17 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
                 if (!((seen >> j) & 1u)) y[32 * k + j] = -INFINITY;
             }
           }
+          if constexpr (F::Q8) {
+#pragma unroll
+            for (int j = 0; j < XC; ++j) s[j] = __float_as_uint(y[j]);
+#pragma unroll
+            for (int k = 0; k < XC / 32; ++k) tmem_st_x32(s_addr + c0 + 32 * k, TB_CHUNK(s, k));
+          }
         };
         float mx = -INFINITY;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += XC) {
-          load(c0);
+          load(c0, true);
           constexpr int CHAINS = XC >= 64 ? 8 : 4;  // of three-input maxima
           float mc[CHAINS];
 #pragma unroll
@@ -829,6 +837,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < CHAINS; k += 2) mx = fmax3(mx, mc[k], mc[k + 1]);
         }
+        if constexpr (F::Q8) tmem_st_wait();
         const float m_new = fmaxf(m_ref, mx * f);
         bool resc = false;
         float alpha = 1.f;
@@ -853,13 +862,14 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += XC) {
-          if constexpr (F::Q8) load(c0);
+          if constexpr (F::Q8) load(c0, false);
 #pragma unroll
           for (int k = 0; k < XC / 16; ++k) {
             uint32_t pk[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 t2 = ffma2(make_float2(y[16 * k + 2 * e], y[16 * k + 2 * e + 1]), sc2, nm2);
+              const float2 y2 = make_float2(y[16 * k + 2 * e], y[16 * k + 2 * e + 1]);
+              const float2 t2 = F::Q8 ? fadd2(y2, nm2) : ffma2(y2, sc2, nm2);
               const float2 p2 = make_float2(ex2(t2.x), ex2(t2.y));
               rs2[e & 3] = fadd2(rs2[e & 3], p2);
               pk[e] = pack2<MBF>(p2.x, p2.y);
