@@ -53,9 +53,9 @@ struct TcCfg {
   static constexpr int ROWS = QT * kBM;                  // rows per unit
   static constexpr int KST = Q8 ? (DP == 128 ? 2 : 3) : (DP == 128 ? 3 : 4);
   static constexpr int VST = Q8 ? KST : (DP == 128 ? 2 : 4);
-  static constexpr int OPB = Q8 ? 128 * DP : 0;          // codes of one tile
-  static constexpr int SR = Q8 ? (DP == 128 ? 3 : 6) : 0;  // staging ring
-  static constexpr int SSLOT = OPB + 1024;               // and their scales (K tiles)
+  static constexpr int OPB = Q8 ? 64 * DP : 0;           // codes of half a tile
+  static constexpr int SR = Q8 ? (DP == 128 ? 3 : 6) : 0;  // staging rings, of keys and of values
+  static constexpr int SSLOT = OPB + 1024;               // and the whole tile's scales (keys': both)
   static constexpr int SCS = KST + 2;                    // tiles whose scales the softmax may need
   static constexpr int MUL = Q8 ? 1024 + SCS * 512 : 0;  // values' multipliers; ring of keys' scales
   static constexpr int HELPERS = Q8 ? 8 : 4;             // warps 8 .. 8 + HELPERS - 1
@@ -70,7 +70,7 @@ struct TcCfg {
   // is free for the next piece only after that.
   static constexpr bool XOWN = DP == 64, XQ = DP == 128 && Q8;
   static constexpr int XCH = DP == 64 ? 16 : TILE / 2048;  // float4 columns of 128 rows a round
-  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * SSLOT + MUL : 0) + (XOWN ? 32768 : 0);
+  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? 2 * SR * SSLOT + MUL : 0) + (XOWN ? 32768 : 0);
   static_assert(SMEM + 2048 <= kSmemMax, "tiles do not fit in shared memory");
 };
 template <int CT, int DP>
@@ -87,18 +87,6 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
-}
-// Global -> shared copy of a multiple of 16 bytes, both ends 16-byte aligned;
-// counted in bytes on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  if (!TA_CHECK_V((smem_u32(dst) & 15u) == 0u && guard_in_dyn_smem(smem_u32(dst)) &&
-                      (reinterpret_cast<uintptr_t>(src) & 15u) == 0u && (bytes & 15u) == 0u,
-                  smem_u32(dst)))
-    return;
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 __device__ __forceinline__ void sts_f32(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
@@ -120,6 +108,11 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2)
       : "memory");
+}
+
+// Arrives at bar when the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_signal(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // d (+)= P V: P 128 x 128 (16-bit, packed in tensor memory), V 128 rows of D,
@@ -185,7 +178,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   // are zero so far)
   __shared__ int tile_e[F::SCS];
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
-  __shared__ __align__(8) uint64_t bar_stage[F::Q8 ? F::SR : 1], bar_sempty[F::Q8 ? F::SR : 1];
+  __shared__ __align__(8) uint64_t bar_stage[2][F::Q8 ? F::SR : 1], bar_sempty[2][F::Q8 ? F::SR : 1];  // 8 bits: keys', values'
 
   // (a shuffle from lane 0: a value the compiler knows to be the same in the
   // whole warp lives in uniform registers, which is where the MMAs take their
@@ -210,7 +203,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   auto sK = [&](int st) { return sQ + (F::QT + st) * F::TILE; };
   auto sV = [&](int st) { return sQ + (F::QT + KST + st) * F::TILE; };
   const uint32_t sStage = sQ + (F::QT + KST + VST) * F::TILE;
-  const uint32_t sMul = sStage + F::SR * F::SSLOT;
+  const uint32_t sMul = sStage + 2 * F::SR * F::SSLOT;
   const uint32_t sX = F::XOWN ? sMul + F::MUL : F::XQ ? sQ : sQ + F::TILE;
 
   WaitCtl ctl{c.err, a.timeout_ns, &abort_flag};
@@ -228,9 +221,9 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
       mbar_init(&bar_scan[s], 1);
     }
     if constexpr (F::Q8) {
-      for (int s = 0; s < F::SR; ++s) {
-        mbar_init(&bar_stage[s], 1);
-        mbar_init(&bar_sempty[s], 4);
+      for (int s = 0; s < 2 * F::SR; ++s) {
+        mbar_init(&bar_stage[0][0] + s, 1 + 32);  // the codes' fetch, a warp's copies of scales
+        mbar_init(&bar_sempty[0][0] + s, 4);
       }
     }
     for (int w = 0; w < 2; ++w) {
@@ -415,14 +408,15 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           Ln::next_unit(c, a, n);
           prefetch_q(n);
         }
-        // op n's codes (K: n even, V: odd) -> fp16 codes in the tile; rows at
-        // and behind `end` are zeros
-        auto convert = [&](int n, uint32_t tile, int end, uint64_t* bar) -> bool {
+        // A tile's codes, of its half n & 1 -> fp16 in the tile; rows at and
+        // behind `end` are zeros.  A warp converts rows pw * 16 .. + 15 of a half.
+        const uint32_t ring = sStage + (keys ? 0 : F::SR * F::SSLOT);
+        auto convert = [&](int n, uint32_t tile, int end) -> bool {
           const int slot = n % F::SR;
-          const uint32_t st = sStage + slot * F::SSLOT;
-          if (!warp_wait(&bar_stage[slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
-          {
-            // The tile's largest value scale, of four keys a lane; every warp, of
+          const uint32_t st = ring + slot * F::SSLOT;
+          if (!warp_wait(&bar_stage[keys ? 0 : 1][slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
+          if (!(n & 1)) {  // the whole tile's scales have come with its first half
+            // The largest scale of the values, of four keys a lane; every warp, of
             // keys too, for itself.
             const uint32_t sc = st + F::OPB;
             const float4 v4 = lds_f4(sc + 512 + lane * 16);
@@ -436,81 +430,83 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             const int ve = min(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23), 253);  // biased exponent
             // |code| 2^7 < 65504: values up to 2^7 times the power's size fit
             if (vexp == 0 || ve > vexp + 6) vexp = ve;
+            const int key = (lane >> 4) * 64 + pw * 16 + (lane & 15);  // this lane's row of the warp's
             float m;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + 512 + tid * 4) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + 512 + key * 4) : "memory");
             const bool number = m < INFINITY;
             if (keys) {
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + tid * 4) : "memory");
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + key * 4) : "memory");
               // A row whose values are not numbers: through its scores it makes
               // the rows that see it NaN, and does not reach the others.
               m = number ? m * kfac : __uint_as_float(0x7fc00000u);
-              if (tid >= end) m = 0.f;  // whatever the memory holds there
-              sts_f32(sMul + 1024 + ((n >> 1) % F::SCS) * 512 + tid * 4, m);
+              if (key >= end) m = 0.f;  // whatever the memory holds there
+              sts_f32(sMul + 1024 + ((n >> 1) % F::SCS) * 512 + key * 4, m);
               if (tid == 0) tile_e[(n >> 1) % F::SCS] = vexp;
             } else {
-              m = number && tid < end ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
+              m = number && key < end ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
               // as the sum of two fp16, 22 bits
               const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
               const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sMul + tid * 8),
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sMul + key * 8),
                            "r"(reinterpret_cast<const uint32_t&>(h2)), "r"(reinterpret_cast<const uint32_t&>(l2))
                            : "memory");
-              __syncwarp();  // (a warp converts the rows whose multipliers it has stored)
+              __syncwarp();  // (the multipliers of the rows that this warp converts)
             }
           }
           // Chunk of 16 codes -> two of 8 fp16.  Eight neighbouring lanes take
           // four chunks of a row and the other four of the next one (D = 128),
           // or two rows (D = 64): their loads and their stores then cover all
           // banks once.
-          auto place = [&](int i, int* r, int* j) {
+          const int row0 = (n & 1) * 64;
+          auto place = [&](int i, int* r, int* j) {  // row of the half, chunk
             if constexpr (CH == 8) {
-              *r = pw * 32 + 2 * ((i >> 1) * 4 + (lane >> 3)) + ((lane >> 2) & 1);
+              *r = pw * 16 + 2 * ((i >> 1) * 4 + (lane >> 3)) + ((lane >> 2) & 1);
               *j = (lane & 3) + 4 * (((lane >> 2) & 1) ^ (i & 1));
             } else {
-              *r = pw * 32 + i * 8 + (lane >> 2);
+              *r = pw * 16 + i * 8 + (lane >> 2);
               *j = lane & 3;
             }
           };
-          // four chunks at a time, their loads first (a load must not wait for
-          // the stores before it); not more: see the note on code size above
-#pragma unroll 1
-          for (int i0 = 0; i0 < CH; i0 += 4) {
-            uint4 codes[4];
-            uint32_t m[4][2] = {};
+          // (all loads first: a load must not wait for the stores before it)
+          uint4 codes[CH / 2];
+          uint32_t m[CH / 2][2] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              int r, j;
-              place(i0 + i, &r, &j);
-              codes[i] = lds_u4(st + r * DP + j * 16);
-              if (!keys)
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(m[i][0]), "=r"(m[i][1]) : "r"(sMul + r * 8) : "memory");
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              int r, j;
-              place(i0 + i, &r, &j);
-              uint4 v = codes[i];
-              if (r >= end) v = make_uint4(0u, 0u, 0u, 0u);
-              uint32_t h[8];
-              code4_to_f16<CT>(v.x, h[0], h[1]);
-              code4_to_f16<CT>(v.y, h[2], h[3]);
-              code4_to_f16<CT>(v.z, h[4], h[5]);
-              code4_to_f16<CT>(v.w, h[6], h[7]);
-              if (!keys) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
-                  const __half2 x = reinterpret_cast<const __half2&>(h[e]);
-                  const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
-                                            __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
-                  h[e] = reinterpret_cast<const uint32_t&>(y);
-                }
-              }
-              sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
-              sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
-            }
+          for (int i = 0; i < CH / 2; ++i) {
+            int r, j;
+            place(i, &r, &j);
+            codes[i] = lds_u4(st + r * DP + j * 16);
+            if (!keys)
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                           : "=r"(m[i][0]), "=r"(m[i][1])
+                           : "r"(sMul + (row0 + r) * 8)
+                           : "memory");
           }
-          signal(bar);
-          if (lane == 0) mbar_arrive(&bar_sempty[slot]);
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) {
+            int r, j;
+            place(i, &r, &j);
+            r += row0;
+            uint4 v = codes[i];
+            if (r >= end) v = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t h[8];
+            code4_to_f16<CT>(v.x, h[0], h[1]);
+            code4_to_f16<CT>(v.y, h[2], h[3]);
+            code4_to_f16<CT>(v.z, h[4], h[5]);
+            code4_to_f16<CT>(v.w, h[6], h[7]);
+            if (!keys) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
+                const __half2 x = reinterpret_cast<const __half2&>(h[e]);
+                const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
+                                          __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
+                h[e] = reinterpret_cast<const uint32_t&>(y);
+              }
+            }
+            sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
+            sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_sempty[keys ? 0 : 1][slot]);
           return true;
         };
         for (int i = 0; i < nt; ++i) {
@@ -518,7 +514,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           uint64_t* const empty = keys ? &bar_kempty[ks] : &bar_vempty[vs];
           static_assert(KST == VST, "one test for both rings");
           if (t >= KST && !(ok = warp_wait(empty, (t / KST - 1) & 1, ctl, kErrTimeoutMma))) break;
-          if (!(ok = convert(2 * t + (keys ? 0 : 1), keys ? sK(ks) : sV(vs), end, keys ? &bar_k[ks] : &bar_v[vs]))) break;
+#pragma unroll 1
+          for (int half = 0; ok && half < 2; ++half) ok = convert(2 * t + half, keys ? sK(ks) : sV(vs), end);
+          if (!ok) break;
+          signal(keys ? &bar_k[ks] : &bar_v[vs]);
         }
       }
       kt += nt;
@@ -597,24 +596,27 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         Ln::next_unit(c, a, u);
       }
     }
-    if (warp == F::MMA + 1 || (warp == F::MMA + 2 && !F::Q8)) {
+    if (warp == F::MMA + 1 || warp == F::MMA + 2) {
       // ------------------------------------------------------- TMA fetches
-      const bool is_k = warp == F::MMA + 1;  // 8-bit: keys and values in turn
+      const bool is_k = warp == F::MMA + 1;
       const int box = a.box_rows, nbox = kBN / box;
       const int outside = c.num_pages * c.Hkv;  // past the maps: reads as zeros
-      // this lane's box of tile t: its page (-1: none) and first row
+      // this lane's box of tile t: the table's entry and the first row (-1: none)
       auto look_up = [&](const typename Ln::Cursor& p, int t, int* r) -> int {
         const int n = t * kBN + lane * box;
-        *r = 0;
-        if (lane >= nbox || n >= p.s.kv) return -1;
-        const int id = cache_page_id(c, p.b, n, r);
-        if (static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages)) return id;
-        cache_error(c.err);
-        *r = 0;
+        *r = -1;
+        return lane >= nbox || n >= p.s.kv ? 0 : cache_page_id(c, p.b, n, r);
+      };
+      // the same a tile later, when the entry is there: page (-1: none) and row
+      auto take = [&](int id, int* row) -> int {
+        if (*row >= 0) {
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages)) return id;
+          cache_error(c.err);
+        }
+        *row = 0;
         return -1;
       };
       if (lane == 0) tma_prefetch_desc(is_k ? &tm_k : &tm_v);
-      if (F::Q8 && lane == 1) tma_prefetch_desc(&tm_v);
       int never = 0;
       WaitCtl drain{c.err, a.timeout_ns, &never};  // for copies in flight, also after a time-out elsewhere
       bool ok = true;
@@ -628,7 +630,8 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         uint32_t scanned = 0, scan_par = 0;  // stages whose last tile went to bar_scan; its phase
         for (; ok && x < x1; ++x, ++kt) {
           const int st = kt % depth;
-          const int row = r, head = id < 0 ? outside : id * c.Hkv + u.h;
+          int row = r;
+          const int page = take(id, &row), head = page < 0 ? outside : page * c.Hkv + u.h;
           const bool scan = !is_k && (u.t + 1) * kBN > u.s.kv - u.s.q;
           if (x + 1 < x1) {
             Ln::next_tile(c, a, u);
@@ -656,42 +659,45 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           }
         }
       } else {
+        // A warp and a ring each for keys and values, in halves of a tile: the
+        // rings are short beside a fetch's 1.2 us.
+        const uint32_t ring = sStage + (is_k ? 0 : F::SR * F::SSLOT);
+        uint64_t* const full = bar_stage[is_k ? 0 : 1];
+        uint64_t* const empty = bar_sempty[is_k ? 0 : 1];
         int n = 0;
         for (; ok && x < x1; ++x) {
-          const int row = r, h = u.h, page = id;
+          int row = r;
+          const int h = u.h, page = take(id, &row);
           if (x + 1 < x1) {
             Ln::next_tile(c, a, u);
             id = look_up(u, u.t, &r);
           }
-          const bool real = page >= 0;
-          const int nreal = __popc(__ballot_sync(0xffffffffu, real));
-          for (int k = 0; k < 2; ++k, ++n) {
+          for (int half = 0; half < 2; ++half, ++n) {
             const int slot = n % F::SR;
-            if (n >= F::SR && !(ok = warp_wait(&bar_sempty[slot], (n / F::SR - 1) & 1, ctl, kErrTimeoutMma))) break;
-            const uint32_t st = sStage + slot * F::SSLOT;
-            // with the keys both scales, with the values theirs again
-            if (!real && lane < nbox) {  // none: zeros
-              for (int e = 0; e < box; e += 4) {
-                if (k == 0) sts_v4(st + F::OPB + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
-                sts_v4(st + F::OPB + 512 + (lane * box + e) * 4, 0u, 0u, 0u, 0u);
-              }
-            }
+            if (n >= F::SR && !(ok = warp_wait(&empty[slot], (n / F::SR - 1) & 1, ctl, kErrTimeoutMma))) break;
+            const uint32_t st = ring + slot * F::SSLOT;
+            if (lane == 0) mbar_expect_tx(&full[slot], F::OPB);
             __syncwarp();
-            if (lane == 0) mbar_expect_tx(&bar_stage[slot], F::OPB + nreal * box * (k == 0 ? 8 : 4));
-            __syncwarp();
-            if (lane < nbox)
-              tma_load_rows(base + (st - sQ) + lane * box * DP, k == 0 ? &tm_k : &tm_v, &bar_stage[slot], row,
-                            real ? page * c.Hkv + h : outside);
-            if (real) {
-              const size_t at = static_cast<size_t>((page * c.Hkv + h) * static_cast<int>(c.page.d) + row);
-              if (k == 0) bulk_load(base + (st - sQ) + F::OPB + lane * box * 4, c.ks + at, box * 4, &bar_stage[slot]);
-              bulk_load(base + (st - sQ) + F::OPB + 512 + lane * box * 4, c.vs + at, box * 4, &bar_stage[slot]);
+            const int first = half * (nbox >> 1);
+            if (lane >= first && lane < first + (nbox >> 1))
+              tma_load_rows(base + (st - sQ) + (lane - first) * box * DP, is_k ? &tm_k : &tm_v, &full[slot], row,
+                            page >= 0 ? page * c.Hkv + h : outside);
+            if (half == 0) {
+              // The tile's scales, four keys' a lane, zeros for none: with the
+              // keys both, with the values theirs again.
+              const int b = lane * 4 / box;
+              const int pg = __shfl_sync(0xffffffffu, page, b);
+              const int rw = __shfl_sync(0xffffffffu, row, b) + lane * 4 % box;
+              const size_t at = pg < 0 ? 0 : static_cast<size_t>((pg * c.Hkv + h) * static_cast<int>(c.page.d) + rw);
+              if (is_k) cp_async16(st + F::OPB + lane * 16, c.ks + at, pg >= 0);
+              cp_async16(st + F::OPB + 512 + lane * 16, c.vs + at, pg >= 0);
             }
+            cp_async_signal(&full[slot]);
           }
         }
         if (lane == 0)
           for (int t = max(0, n - F::SR); t < n; ++t)
-            mbar_wait(&bar_stage[t % F::SR], (t / F::SR) & 1, drain, kErrTimeoutTma);
+            mbar_wait(&full[t % F::SR], (t / F::SR) & 1, drain, kErrTimeoutTma);
       }
     }
   } else {
