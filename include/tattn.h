@@ -323,10 +323,11 @@ size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, t
  * ws: >= attn_cache_workspace_bytes(...) bytes, 16-byte aligned, contents need
  * not be initialised; calls that may run at the same time need one each.
  * Scores, softmax sums and accumulators are fp32.  16-bit caches: weights are
- * rounded to dt for the product with V.  8-bit caches: products in fp16; up to 32
- * to 64 query rows (Hq / Hkv * T) per key head on the bare codes (exact), the
- * scales applied in fp32, beyond on rows multiplied out and rounded to fp16; bf16
- * queries are scaled by a power of two into fp16's range. */
+ * rounded to dt for the product with V.  8-bit caches: products in fp16 on the
+ * bare codes (exact), the scales applied in fp32; beyond 32 to 64 query rows
+ * (Hq / Hkv * T) per key head the values are multiplied out and rounded to fp16;
+ * bf16 queries are scaled by a power of two into fp16's range.  A row that sees a
+ * value with a NaN scale gets NaN in O and L. */
 ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_cache* cache, const int* pages,
                          int max_pages, const int* kv_lens, const int* q_lens, const uint8_t* tree,
                          const int64_t* tree_strides, void* o, const int64_t* o_strides, float* lse, void* ws,

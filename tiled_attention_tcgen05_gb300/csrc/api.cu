@@ -697,9 +697,9 @@ static int page_box_rows(int page) { return page % 32 == 0 ? 32 : page % 16 == 0
 // used; beyond, the tcgen05 kernel, whose tile has 128 rows.  Measured on 16
 // sequences of 8192 tokens, 8 key heads, pages of 32; attn_cache / tcgen05 us:
 //           bf16: 24 rows    32         48         64      int8: 32         48         64
-//   D 128:  110 / 116   110 / 116  188 / 116  190 / 116   106 / 138  171 / 140  173 / 140
-//   D  64:   65 / 73     67 / 73    79 / 74   108 / 75     61 / 112   81 / 112  118 / 112
-//   D  32:   44 / 69     46 / 69    60 / 71    71 / 69     52 / 108   65 / 108   77 / 108
+//   D 128:  110 / 116   110 / 116  188 / 116  190 / 116   106 / 138  171 / 139  173 / 138
+//   D  64:   65 / 73     67 / 73    79 / 74   108 / 75     61 / 108   81 / 108  118 / 108
+//   D  32:   44 / 69     46 / 69    60 / 71    71 / 69     52 / 104   65 / 104   77 / 104
 static bool attn_cache_few_rows(int D, bool bits8, long long rows) {
   if (D > 64) return rows <= 32;
   if (D > 32) return rows <= (bits8 ? 48 : 32);

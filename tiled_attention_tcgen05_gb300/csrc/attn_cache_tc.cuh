@@ -19,14 +19,17 @@
 // divides a page), a lane per box.  Boxes behind the sequence's end or of pages
 // that do not exist are fetched from outside the map and so read as zeros.
 // 16-bit rows go straight into the 128-byte-swizzled layout that the MMA
-// descriptors read.  8-bit codes and their scales go into a staging ring
-// several tiles ahead; the eight helpers turn them into fp16: the keys' codes as
+// descriptors read.  8-bit codes and their scales go into staging rings, one of
+// keys and one of values; the eight helpers turn them into fp16: the keys' codes as
 // they are (exact; a key's scale multiplies its finished scores in fp32), the
 // values' rows multiplied out, with a power of two taken out that all values of
 // the piece so far share.  (A value's scale in the exponent, as in
 // attn_cache_rows.cuh, would have every row read two more numbers per key from
 // shared memory.)  That rounding, of a row to 11 bits, adds 2^-11 P |V| to the
-// result at most.
+// result at most.  16 sequences of 8192, 8 key heads of 128, 64 rows, e4m3: 132 us,
+// 31 % of the copy rate.  Fetch, conversion, softmax and MMA each take about
+// as long there (1.6 to 2 us a tile): a faster fetch or a pipelined softmax
+// alone gained nothing.
 //
 // A box may bring rows behind the sequence's end, whose memory may hold
 // anything, and a draft's values may hold infinities and NaN that some rows
@@ -781,12 +784,13 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         if constexpr (F::Q8) e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
         [[maybe_unused]] const uint32_t key_scales = sMul + 1024 + ((kt0 + ti) % F::SCS) * 512;
         // 16 bits: the row's 128 scores in registers.  8 bits: two passes over S
-        // in tensor memory, XC columns at a time (scales, mask and maximum; weights): the loops
-        // of the softmax, the conversions and the MMA warp then stay in the
-        // instruction cache together (with the row in registers a third of all
-        // stalls were missing instructions: 212 us against 140 at the shape
-        // above; alone, beside idle helpers, one pass is faster: 377 us against
-        // 496 for the chunk).
+        // in tensor memory, XC columns at a time (scales, mask and maximum;
+        // weights): the loops of the softmax, the conversions and the MMA warp
+        // then stay in the instruction cache together (with the row in registers
+        // a third of all stalls were missing instructions: 212 us against 140 at
+        // 128 rows of D = 128, e4m3, when that was changed; alone, beside idle
+        // helpers, one pass is faster: 377 us against 496 for 16 bits' chunk of
+        // 2048 over 16384).
         constexpr int XC = F::Q8 ? 32 : 128;
         float y[XC];
         auto load = [&](int c0, bool first) {  // 8 bits: the first pass leaves what the second takes
