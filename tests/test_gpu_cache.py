@@ -286,8 +286,10 @@ def test_rows_that_see_nothing_and_hidden_non_finite(gpu_lib, cache, dtype, T, G
     hit = torch.zeros(T, dtype=torch.bool)
     hit[3] = True
     assert torch.isfinite(o[:, :, ~hit].float()).all()
+    assert torch.isfinite(lse[:, :, ~hit & (torch.arange(T) > 0)]).all()
     if cache in ("e4m3", "int8"):
         assert torch.isnan(o[:, :, 3].float()).all()  # the row reads back as NaN whole
+        assert torch.isnan(lse[:, :, 3]).all()
     else:
         f = o[:, :, 3].float()
         assert torch.isinf(f[..., 3]).all()
