@@ -27,9 +27,10 @@
 // attn_cache_rows.cuh, would have every row read two more numbers per key from
 // shared memory.)  That rounding, of a row to 11 bits, adds 2^-11 P |V| to the
 // result at most.  16 sequences of 8192, 8 key heads of 128, 64 rows, e4m3: 132 us,
-// 31 % of the copy rate.  Fetch, conversion, softmax and MMA each take about
-// as long there (1.6 to 2 us a tile): a faster fetch or a pipelined softmax
-// alone gained nothing.
+// 31 % of the copy rate.  Most of that is hand-overs between the roles: over int8
+// (138 us) the conversions' arithmetic and the first pass of the softmax are 8 to 10 us
+// each, the exponentials and the fetched bytes 5 more, and 108 are left without
+// all of them.
 //
 // A box may bring rows behind the sequence's end, whose memory may hold
 // anything, and a draft's values may hold infinities and NaN that some rows
