@@ -1,0 +1,85 @@
+"""Attention over a cache whose keys and values lie far apart, or are no numbers:
+infinities and NaN among older tokens and the draft's, scales of very different
+size, queries of very different size, values that a row does not see."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from _cache import Setup, attention_reference, check, int32, values
+from _parity import to_np
+from test_gpu_cache import attend
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def put(ta, st, b, k, v):
+    """Writes sequence b of the setup anew: k, v [Hkv, n, D] on the host."""
+    n = st.kv[b]
+    ta.cache_append(st.cache, k[None].cuda(), v[None].cuda(), st.pages[b:b + 1], int32([n]))
+    for name, x in (("k", k), ("v", v)):
+        if st.scale[name] is None:
+            st.rows[name][b] = x.double().numpy()
+            continue
+        c, s = oracle.cache_quantise(x, st.kind)
+        st.rows[name][b] = c * s.astype(np.float64)[..., None]
+        slots = [oracle.cache_slot(st.table[b], st.page, i) for i in range(n)]
+        pg, r = (torch.tensor(z) for z in zip(*slots))
+        st.scale[name][pg, :, r] = torch.from_numpy(s).T
+
+
+def compare(st, q, o, lse, tree=None, heads=None, columns=None, rows=None, b=0):
+    """Rows (default: all) and columns of O against the oracle, and L.
+
+    The bounds are those of products on the bare codes whatever the number of
+    rows: nothing in them comes from a key that a row does not see, but for the
+    weights' half steps, which the row's largest contribution scales."""
+    G, n = q.shape[1] // st.Hkv, q.shape[2]
+    for h in range(st.Hkv) if heads is None else heads:
+        vs = None
+        if st.scale["v"] is not None:
+            vs = np.array([st.scale["v"][pg, h, r] for pg, r in
+                           (oracle.cache_slot(st.table[b], st.page, i) for i in range(st.kv[b]))], dtype=np.float64)
+        v = np.where(np.isfinite(st.rows["v"][b][h]), st.rows["v"][b][h], 0.0)
+        O, L, bO, bL = attention_reference(q[b, h * G:(h + 1) * G].cpu(), st.rows["k"][b][h], v, tree, st.kind, st.dtype,
+                                           vs, rows=1)
+        got, gl = to_np(o[b, h * G:(h + 1) * G]), to_np(lse[b, h * G:(h + 1) * G])
+        r = np.arange(n) if rows is None else np.asarray(rows)
+        c = np.arange(st.D) if columns is None else np.asarray(columns)
+        check(f"O[{b},{h}]", got[:, r][:, :, c], O[:, r][:, :, c], bO[:, r][:, :, c])
+        check(f"L[{b},{h}]", gl[:, r], L[:, r], bL[:, r])
+
+
+def place(st, b, n):
+    return oracle.cache_slot(st.table[b], st.page, n)
+
+
+# ------------------------------------------- infinities and NaN, 16-bit caches
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("T,G", [(3, 4), (12, 8), (40, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_non_finite_values_of_older_tokens(gpu_lib, D, dtype, T, G, tree):
+    """Every row sees the tokens before the new ones, those that share a key tile
+    with new ones among them."""
+    ta = gpu_lib
+    n = 333
+    st = Setup(ta, [n], 2, 16, D, dtype, dtype, 5)
+    q = values(3, (1, 2 * G, T, D), dtype, 0.7)
+    past = n - T
+    tr = np.tril(np.ones((T, T), dtype=bool)) if tree else None
+    for pos in (past - 1, past // 128 * 128, past - 129):
+        pg, r = place(st, 0, pos)
+        kept = st.cache.v[pg, :, r].clone()
+        st.cache.v[pg, 0, r, 3] = NAN
+        st.cache.v[pg, 1, r, 5] = INF
+        o, lse = attend(ta, st, q, None, None if tr is None else tr[None])
+        assert ta.sync_status() == "TA_OK"
+        f = o.float().cpu()
+        assert torch.isnan(f[0, :G, :, 3]).all(), pos
+        assert not torch.isfinite(f[0, G:, :, 5]).any(), pos  # (0 * inf where a weight rounds to nothing)
+        compare(st, q, o, lse, tr, heads=[0], columns=[c for c in range(D) if c != 3])
+        compare(st, q, o, lse, tr, heads=[1], columns=[c for c in range(D) if c != 5])
+        st.cache.v[pg, :, r] = kept

@@ -36,8 +36,9 @@
 // anything, and a draft's values may hold infinities and NaN that some rows
 // must not see: 0 * NaN would reach every row.  Tiles of values with new
 // tokens are looked through before they are handed on: dead rows are cleared
-// and non-finite values taken out; the rows that do see such a value get it
-// added to their result.
+// and the new tokens' non-finite values taken out; the rows that do see such a
+// value get it added to their result.  Older tokens' values stay: every row
+// sees them.
 #pragma once
 #include "attn_cache.cuh"
 #include "bwd_common.cuh"
@@ -343,9 +344,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
               if ((wd[e] & EXP) == EXP) hit = true, wd[e] &= 0xffff0000u;
               if (((wd[e] >> 16) & EXP) == EXP) hit = true, wd[e] &= 0x0000ffffu;
             }
-            if ((u.t + i) * kBN + r >= u.s.kv) {
+            const int n = (u.t + i) * kBN + r;
+            if (n >= u.s.kv) {
               sts_v4(at, 0u, 0u, 0u, 0u);
-            } else if (hit) {
+            } else if (hit && n >= u.s.kv - u.s.q) {  // a new token's
               sts_v4(at, wd[0], wd[1], wd[2], wd[3]);
               odd[piece & 3] = piece + 1;
             }
