@@ -319,6 +319,9 @@ size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, t
  * prompt's chunk; T = 1 is a generation step).  Rows that see nothing get O = 0,
  * L = -inf.  Infinities and NaN in places that a row does not see do not
  * reach it (16-bit caches, and rows that attn_cache_append wrote to 8-bit ones).
+ * One among the values that a row sees reaches that element of O (16-bit caches;
+ * an infinity of a token before the new ones as NaN where its weight rounds to
+ * zero).
  * In: q [B, Hq, T, D].  Out: o (strides o_strides), lse [B, Hq, T] fp32.
  * ws: >= attn_cache_workspace_bytes(...) bytes, 16-byte aligned, contents need
  * not be initialised; calls that may run at the same time need one each.

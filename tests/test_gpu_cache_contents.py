@@ -83,3 +83,69 @@ def test_non_finite_values_of_older_tokens(gpu_lib, D, dtype, T, G, tree):
         compare(st, q, o, lse, tr, heads=[0], columns=[c for c in range(D) if c != 3])
         compare(st, q, o, lse, tr, heads=[1], columns=[c for c in range(D) if c != 5])
         st.cache.v[pg, :, r] = kept
+
+
+@pytest.mark.parametrize("T,G", [(3, 2), (24, 1), (40, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_non_finite_values_of_new_tokens_with_tiny_weights(gpu_lib, dtype, T, G):
+    """A row that sees an infinity or a NaN gets it, however far below the row's
+    maximum its score lies."""
+    ta = gpu_lib
+    D, n = 64, 200
+    st = Setup(ta, [n], 1, 16, D, dtype, dtype, 6)
+    k, v = (torch.from_numpy(st.rows[x][0]).to(q16(dtype)) for x in "kv")
+    k[:, n - T + 1] = -20.0
+    v[:, n - T + 1, 2], v[:, n - T + 1, 7] = NAN, INF
+    put(ta, st, 0, k, v)
+    q = values(3, (1, G, T, D), dtype, 0.1) + 2.0
+    o, lse = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    f = o.float()
+    assert torch.isfinite(f[:, :, 0]).all()
+    assert torch.isnan(f[:, :, 1:, 2]).all() and (f[:, :, 1:, 7] == INF).all()
+    compare(st, q, o, lse, columns=[c for c in range(D) if c not in (2, 7)])
+
+
+def q16(dtype):
+    return {"bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hkv,G,T,n,high", [
+    (1, 1, 32, 140, 25),      # rows of one tile, keys over a cluster's blocks
+    (45, 1, 32, 140, 25),     # units cut by block borders
+    (400, 1, 32, 140, 25),    # whole units
+    (1, 1, 32, 19990, 25),    # one unit over all blocks
+    (1, 2, 64, 150, 50),      # 128 rows, cut
+    (200, 2, 64, 150, 50),    # 128 rows, whole
+    (1, 1, 300, 310, 295),    # a pair of row tiles and one alone
+])
+def test_infinities_outlive_a_larger_maximum(gpu_lib, dtype, Hkv, G, T, n, high):
+    """An infinity among the draft's first values, and a later key whose score
+    lies so far above that everything before it weighs nothing."""
+    ta = gpu_lib
+    D = 64
+    st = Setup(ta, [n], Hkv, 16, D, dtype, dtype, 6) if n < 1000 and Hkv < 100 else blank(ta, n, Hkv, D, dtype)
+    k, v = values(11, (Hkv, n, D), dtype), values(12, (Hkv, n, D), dtype)
+    v[:, n - T, 7] = INF
+    k[:, n - T + high] = 20.0
+    put(ta, st, 0, k, v)
+    q = values(3, (1, Hkv * G, T, D), dtype, 0.1) + 2.0
+    o, lse = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    f = o.float()
+    assert (f[..., 7] == INF).all()
+    compare(st, q, o, lse, columns=[c for c in range(D) if c != 7], heads=sorted({0, Hkv // 2, Hkv - 1}))
+
+
+def blank(ta, n, Hkv, D, dtype, cache=None):
+    """A setup whose one sequence put() fills (a long one's rows take the
+    setup's own loop too long)."""
+    st = Setup(ta, [0], Hkv, 16, D, dtype, cache or dtype, 6)
+    P = (n + 15) // 16
+    st.kv, st.table = [n], torch.arange(P, dtype=torch.int32).flip(0)[None].contiguous()
+    st.cache = ta.kv_cache(P, Hkv, 16, D, st.cache.dtype)
+    st.pages, st.kv_lens = st.table.cuda(), int32([n])
+    if st.scale["v"] is not None:
+        st.scale = {x: torch.zeros(P, Hkv, 16) for x in "kv"}
+    return st

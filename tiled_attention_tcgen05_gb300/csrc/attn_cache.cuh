@@ -152,6 +152,11 @@ __device__ __forceinline__ int block_of(long long len, long long y) {
   return static_cast<int>(((y + 1) * N - 1) / len);
 }
 
+// A factor <= 1 for accumulators whose row got a larger maximum, kept above
+// zero: an infinity that the row has seen stays one.  To finite accumulators
+// 2^-126 is what a weight that small, flushed to zero, is.
+__device__ __forceinline__ float keep_infinite(float f) { return fmaxf(f, 1.1754943508222875e-38f); }
+
 // ----------------------------------------------------------------- joining
 // The join kernel is launched while the main kernel runs (programmatic
 // dependent launch) and waits for its end before it reads anything.

@@ -420,6 +420,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
 
       // keys behind the end, and new tokens that a row must not see
       const bool masked = n0 + KW > past;
+      auto sees = [&](int t, int n) {  // new token t, key n
+        const int d = n - past;
+        if (t >= cc.s.q || n >= cc.s.kv) return false;
+        return d < 0 || (a.tree ? __ldg(a.tree + cc.b * a.tree_b + t * a.tree_t + d) != 0 : d <= t);
+      };
       if (masked) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -430,11 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const int n = n0 + j * 8 + 2 * cq + i;
-                const int d = n - past;
-                bool see = t < cc.s.q && n < cc.s.kv;
-                if (see && d >= 0) see = a.tree ? __ldg(a.tree + cc.b * a.tree_b + t * a.tree_t + d) != 0 : d <= t;
-                if (!see) s[mt][j][2 * e + i] = -INFINITY;
+                if (!sees(t, n0 + j * 8 + 2 * cq + i)) s[mt][j][2 * e + i] = -INFINITY;
               }
             }
           }
@@ -466,6 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             al[e] = mn == -INFINITY ? 1.f : ex2(m[mt][e] - mn);
             m[mt][e] = mn;
             l[mt][e] *= al[e];
+            al[e] = keep_infinite(al[e]);
           }
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
@@ -504,7 +506,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
       if constexpr (CT == kCache16) {
         // A new token's value may hold infinities or NaN that some rows must
         // not see, and 0 * NaN is NaN in the product: such elements are added
-        // to the rows that do see them here and taken out of the tile.
+        // to the rows that do see them here, however small their weight, and
+        // taken out of the tile.
         if (masked) {
           bool odd = false;
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;
@@ -518,26 +521,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           }
           if (__any_sync(0xffffffffu, odd)) {
             for (int r = 0; r < KW; ++r) {
-              // weights of key r for this thread's rows: held by the lane of the
-              // same quad at column (r % 8) / 2, rounded in its half of a pair
-              const int from = (lane & ~3) | ((r & 7) >> 1);
-              float w0[MT], w1[MT];
+              bool see[MT][2];
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                w0[mt] = w1[mt] = 0.f;
+              for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int p = 0; p < KW / 16; ++p) {
-#pragma unroll
-                  for (int hh = 0; hh < 2; ++hh) {
-                    if (r >> 3 == 2 * p + hh) {
-                      const uint32_t a0 = __shfl_sync(0xffffffffu, pf[mt][p][2 * hh], from);
-                      const uint32_t a1 = __shfl_sync(0xffffffffu, pf[mt][p][2 * hh + 1], from);
-                      w0[mt] = static_cast<float>(reinterpret_cast<const T*>(&a0)[r & 1]);
-                      w1[mt] = static_cast<float>(reinterpret_cast<const T*>(&a1)[r & 1]);
-                    }
-                  }
-                }
-              }
+                for (int e = 0; e < 2; ++e)
+                  see[mt][e] = sees(static_cast<int>(a.g_div.div(cc.rt * ROWS + mt * 16 + g + 8 * e)), n0 + r);
 #pragma unroll
               for (int j = 0; j < D / 8; ++j) {
                 uint32_t w[1];
@@ -549,8 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
                   if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                      if (w0[mt] != 0.f) oa[mt][j][i] = fmaf(w0[mt], v, oa[mt][j][i]);
-                      if (w1[mt] != 0.f) oa[mt][j][2 + i] = fmaf(w1[mt], v, oa[mt][j][2 + i]);
+                      if (see[mt][0]) oa[mt][j][i] += v;
+                      if (see[mt][1]) oa[mt][j][2 + i] += v;
                     }
                   }
                 }
@@ -674,6 +663,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           f[w] = mm == -INFINITY ? 0.f : ex2(ml[(w * ROWS + ur) * 2] - mm);
           // a NaN sum stays one where no score was a number
           ll += (mm == -INFINITY ? 1.f : f[w]) * ml[(w * ROWS + ur) * 2 + 1];
+          f[w] = keep_infinite(f[w]);
         }
         const int qr = cc.rt * ROWS + ur;
         const int t = static_cast<int>(a.g_div.div(qr)), hq = cc.h * a.G + (qr - t * a.G);
@@ -765,8 +755,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
       float ll = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < kCluster; ++p) {
-        const float f = pm[p] == -INFINITY ? 0.f : ex2(pm[p] - mm);
+        float f = pm[p] == -INFINITY ? 0.f : ex2(pm[p] - mm);
         ll += mm == -INFINITY ? pl[p] : pl[p] * f;  // a NaN sum stays one where no score was a number
+        f = keep_infinite(f);
         v[0] = fmaf(y[p].x, f, v[0]);
         v[1] = fmaf(y[p].y, f, v[1]);
         v[2] = fmaf(y[p].z, f, v[2]);
@@ -851,7 +842,7 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
     const float2 v = mls[i];
     const float f = v.x == -INFINITY ? 0.f : ex2(v.x - mm);
     ll += mm == -INFINITY ? v.y : v.y * f;  // a NaN sum stays one where no score was a number
-    mls[i].x = f;
+    mls[i].x = keep_infinite(f);
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);

@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           alpha = ex2(m_ref - m_new);
           m_ref = m_new;
         }
-        float o_alpha = alpha;
+        float o_alpha = keep_infinite(alpha);
         if constexpr (F::Q8) {  // values of a larger power of two from here on
           if (t > 0 && e != o_exp) {
             resc = true;
@@ -971,9 +971,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           if (round == 0) {
             const float m1 = xm[r], l1 = xl[r];
             const float mm = fmaxf(m_ref, m1);
-            f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - mm) * o_pow;
+            f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - mm);
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
-            l = mm == -INFINITY ? l + l1 : l * (m_ref == -INFINITY ? 0.f : ex2(m_ref - mm)) + l1 * f1;  // NaN stays
+            l = mm == -INFINITY ? l + l1 : l * f0 + l1 * f1;  // NaN stays
+            f0 = keep_infinite(f0) * o_pow, f1 = keep_infinite(f1);
             m_ref = mm;
           }
         }
@@ -1093,7 +1094,7 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
       f = pm == -INFINITY ? 0.f : ex2(pm - mm);
       ll += mm == -INFINITY ? pl : pl * f;  // a NaN sum stays one where no score was a number
     }
-    fs[i][lane] = f;
+    fs[i][lane] = keep_infinite(f);
   }
   red[warp][lane] = ll;
   __syncthreads();
