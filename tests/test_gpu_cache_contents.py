@@ -149,3 +149,25 @@ def blank(ta, n, Hkv, D, dtype, cache=None):
     if st.scale["v"] is not None:
         st.scale = {x: torch.zeros(P, Hkv, 16) for x in "kv"}
     return st
+
+
+# ---------------------------------------------------- scales of 8-bit caches
+@pytest.mark.parametrize("order", ["zeros first", "zeros last", "mixed"])
+@pytest.mark.parametrize("size", [2.0 ** 30, 2.0 ** 80, 2.0 ** 118])
+@pytest.mark.parametrize("Hkv,G,T", [(1, 1, 1), (1, 4, 3), (40, 1, 1), (400, 2, 1), (1, 4, 40), (200, 1, 70)])
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_rows_of_zeros_beside_large_values(gpu_lib, cache, Hkv, G, T, size, order):
+    """The softmax's sum does not depend on the values: keys whose values are
+    zeros (their scale is 2^-60) keep their weight in it."""
+    ta = gpu_lib
+    D, n = 64, 300
+    st = blank(ta, n, Hkv, D, "bf16", cache)
+    k, v = values(11, (Hkv, n, D), "bf16"), values(12, (Hkv, n, D), "bf16")
+    i = torch.arange(n)
+    zero = {"zeros first": i < 170, "zeros last": i >= 130, "mixed": i % 2 == 0}[order]
+    v = torch.where(zero[None, :, None], torch.zeros_like(v), v * size)
+    put(ta, st, 0, k, v)
+    q = values(3, (1, Hkv * G, T, D), "bf16")
+    o, lse = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    compare(st, q, o, lse, heads=sorted({0, Hkv // 2, Hkv - 1}))

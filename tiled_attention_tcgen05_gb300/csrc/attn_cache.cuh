@@ -157,6 +157,34 @@ __device__ __forceinline__ int block_of(long long len, long long y) {
 // 2^-126 is what a weight that small, flushed to zero, is.
 __device__ __forceinline__ float keep_infinite(float f) { return fmaxf(f, 1.1754943508222875e-38f); }
 
+// 8-bit caches.  A value's scale sv is part of the exponent of its weight,
+// p = 2^(t - m) with t = s + log2 sv, and the softmax sum is that of the bare
+// scores s, l = sum 2^(s - m + kSumUp).  p can be far too small for fp32 where
+// 2^(s - m) decides the sum (a row of zeros, of scale 2^-60, beside values of
+// 2^80), so that p / sv would not do: from h = 2^((t - m) / 2), p = h^2 and the
+// sum's part is (h 2^((kSumUp - log2 sv) / 2))^2, which vanishes only where it does not
+// count.  With kSumUp a part lies below 2^92 and those of keys with t near m
+// above 2^-98 (scales 2^-60 to 2^122): 2^31 of them fit.  Two packed products a
+// pair of keys more; a branch for such tiles alone cost more (48 rows of D = 64
+// over int8, 16 x 4096: 76.5 us; this 75.5; the plain quotient 70.7).
+constexpr float kSumUp = 24.f;
+// A sum whose reference rises by -by.  The sum may be far above 1, so that 2^by
+// alone would be zero where the product counts.
+__device__ __forceinline__ float lower_sum(float l, float by) {
+  const float h = ex2(0.5f * by);
+  return l * h * h;
+}
+// 1 / sum and L of a row with reference m (0 and -inf for a row that saw
+// nothing; a NaN sum stays one where no score was a number).
+template <int CT>
+__device__ __forceinline__ float sum_norm(float l) {
+  return l == 0.f ? 0.f : (CT == kCache16 ? 1.f : 16777216.f) / l;  // 2^kSumUp
+}
+template <int CT>
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + (CT == kCache16 ? lg2(l) : lg2(l) - kSumUp)) * kLn2);
+}
+
 // ----------------------------------------------------------------- joining
 // The join kernel is launched while the main kernel runs (programmatic
 // dependent launch) and waits for its end before it reads anything.

@@ -4,13 +4,13 @@
 //
 //   t_ij = log2(e) sm_scale <q_i, k_j> (+ log2 sv_j for 8-bit caches)
 //   O_i  = sum_j 2^(t_ij - m_i) v_j / l_i,   m_i a running maximum of t_ij
-//   l_i  = sum_j 2^(t_ij - m_i) (/ sv_j),    L_i = ln 2 (m_i + log2 l_i)
+//   l_i  = sum_j 2^(t_ij - log2 sv_j - m_i),  L_i = ln 2 (m_i + log2 l_i)
 //
 // A cached 8-bit row is code * scale.  A key's scale multiplies its finished
 // score; a value's scale sv_j is put into the exponent, so that the weights
 // 2^(t - m) <= 2^8 multiply the bare codes in fp16 (exact for both code types)
 // and are rounded relative to the row's largest contribution; the softmax
-// sum takes the scale out again in fp32.
+// sum takes the scale out again in fp32 (attn_cache.cuh).
 //
 // Query rows.  The G query heads that share a key head and the sequence's new
 // tokens make up to G * q_len rows, taken 16 MT at a time (MT m16n8k16 tiles:
@@ -50,7 +50,7 @@ struct Cfg {
   static constexpr int TK = KW * kWarps;                    // keys per tile
   static constexpr int CPR = RB / 16;                       // 16-byte chunks per row
   static constexpr int SLOT = 2 * KW * RB;                  // K and V of one warp and stage
-  static constexpr int SCALES = CT == kCache16 ? 0 : KW * 12;  // K scale, V scale (then its log2), 1 / V scale
+  static constexpr int SCALES = CT == kCache16 ? 0 : KW * 12;  // K scale, V scale (then its log2), sum's factor
   static constexpr int RING = STAGES * (SLOT + SCALES);    // one warp
   static_assert(SLOT >= 16 * D * 4, "a slot holds a row tile of a warp's accumulators");
   static constexpr int QBYTES = MT > 1 ? MT * D * 32 : 0;   // Q fragments (one row tile's stay in registers)
@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           }
         }
       } else {
-        // this lane's key: its value scale's log2 and 1 / scale take its place
+        // this lane's key: its value scale's log2 and the square root of 2^kSumUp /
+        // scale take its place
         {
           float vscale;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vscale) : "r"(sc_a + KW * 4 + lane * 4) : "memory");
@@ -365,11 +366,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           }
           // no scale (a row past the end, or of a page that the cache does not
           // have) stands for a value of zero whatever its codes; a NaN row's
-          // scores are NaN, its 1 / scale must not reach other rows' sums
+          // scores are NaN, its factor must not reach other rows' sums
           if (vscale < kMinScale) vscale = kMinScale;
-          const float inv = vscale == vscale ? __fdividef(1.f, vscale) : 0.f;
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(lg2(vscale)) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 8 + lane * 4), "f"(inv) : "memory");
+          const float lsv = lg2(vscale);
+          const float root = vscale == vscale ? ex2(0.5f * (kSumUp - lsv)) : 0.f;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(lsv) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 8 + lane * 4), "f"(root) : "memory");
           __syncwarp();
         }
         constexpr int PB = D / 4;  // bytes of a key's row per lane
@@ -465,8 +467,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
           for (int e = 0; e < 2; ++e) {
             const float mn = fmaxf(m[mt][e], mx[e]);
             al[e] = mn == -INFINITY ? 1.f : ex2(m[mt][e] - mn);
+            if constexpr (CT == kCache16) l[mt][e] *= al[e];
+            else l[mt][e] = mn == -INFINITY ? l[mt][e] : lower_sum(l[mt][e], m[mt][e] - mn);
             m[mt][e] = mn;
-            l[mt][e] *= al[e];
             al[e] = keep_infinite(al[e]);
           }
 #pragma unroll
@@ -485,12 +488,18 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float2 t = make_float2(s[mt][j][2 * e], s[mt][j][2 * e + 1]);
-            if constexpr (CT == kCache16) t = ffma2(t, sc2, ref2);
-            else t = fadd2(t, ref2);
-            t = make_float2(ex2(t.x), ex2(t.y));
+            if constexpr (CT == kCache16) {
+              t = ffma2(t, sc2, ref2);
+              t = make_float2(ex2(t.x), ex2(t.y));
+              sum = fadd2(sum, t);
+            } else {
+              t = ffma2(t, make_float2(0.5f, 0.5f), make_float2(0.5f * ref, 0.5f * ref));
+              t = make_float2(ex2(t.x), ex2(t.y));
+              const float2 x = fmul2(t, lds_f2(sc_a + KW * 8 + (j * 8 + 2 * cq) * 4));
+              sum = ffma2(x, x, sum);
+              t = fmul2(t, t);
+            }
             s[mt][j][2 * e] = t.x, s[mt][j][2 * e + 1] = t.y;
-            if constexpr (CT == kCache16) sum = fadd2(sum, t);
-            else sum = ffma2(t, lds_f2(sc_a + KW * 8 + (j * 8 + 2 * cq) * 4), sum);
           }
           l[mt][e] += sum.x + sum.y;
         }
@@ -661,15 +670,17 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           f[w] = mm == -INFINITY ? 0.f : ex2(ml[(w * ROWS + ur) * 2] - mm);
+          const float wl = ml[(w * ROWS + ur) * 2 + 1];
           // a NaN sum stays one where no score was a number
-          ll += (mm == -INFINITY ? 1.f : f[w]) * ml[(w * ROWS + ur) * 2 + 1];
+          if constexpr (CT == kCache16) ll += (mm == -INFINITY ? 1.f : f[w]) * wl;
+          else ll += mm == -INFINITY ? wl : lower_sum(wl, ml[(w * ROWS + ur) * 2] - mm);
           f[w] = keep_infinite(f[w]);
         }
         const int qr = cc.rt * ROWS + ur;
         const int t = static_cast<int>(a.g_div.div(qr)), hq = cc.h * a.G + (qr - t * a.G);
         const bool real = t < cc.s.q;
         float norm = 1.f;
-        if (whole) norm = ll == 0.f ? 0.f : 1.f / ll;
+        if (whole) norm = sum_norm<CT>(ll);
         T* const out = static_cast<T*>(a.o) + cc.b * a.os[0] + hq * a.os[1] + t * a.os[2];
 #pragma unroll
         for (int i = 0; i < (D / 4 + 7) / 8; ++i) {
@@ -702,8 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             part[ROWS * D + 2 * ur] = mm;
             part[ROWS * D + 2 * ur + 1] = ll;
           } else if (real) {
-            a.lse[(static_cast<long long>(cc.b) * a.Hq + hq) * c.T + t] =
-                ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
+            a.lse[(static_cast<long long>(cc.b) * a.Hq + hq) * c.T + t] = row_lse<CT>(mm, ll);
           }
         }
         __syncthreads();
@@ -756,21 +766,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
 #pragma unroll
       for (int p = 0; p < kCluster; ++p) {
         float f = pm[p] == -INFINITY ? 0.f : ex2(pm[p] - mm);
-        ll += mm == -INFINITY ? pl[p] : pl[p] * f;  // a NaN sum stays one where no score was a number
+        // a NaN sum stays one where no score was a number
+        ll += mm == -INFINITY ? pl[p] : CT == kCache16 ? pl[p] * f : lower_sum(pl[p], pm[p] - mm);
         f = keep_infinite(f);
         v[0] = fmaf(y[p].x, f, v[0]);
         v[1] = fmaf(y[p].y, f, v[1]);
         v[2] = fmaf(y[p].z, f, v[2]);
         v[3] = fmaf(y[p].w, f, v[3]);
       }
-      const float norm = ll == 0.f ? 0.f : 1.f / ll;
+      const float norm = sum_norm<CT>(ll);
       uint2 o;
       o.x = pack2<BF>(v[0] * norm, v[1] * norm);
       o.y = pack2<BF>(v[2] * norm, v[3] * norm);
       *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + cc.b * a.os[0] + hq * a.os[1] + t * a.os[2] + ch * 4) = o;
-      if (ch == 0)
-        a.lse[(static_cast<long long>(cc.b) * a.Hq + hq) * c.T + t] =
-            ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
+      if (ch == 0) a.lse[(static_cast<long long>(cc.b) * a.Hq + hq) * c.T + t] = row_lse<CT>(mm, ll);
     }
     cluster_sync_all();  // the peers have read this block's state
   }
@@ -841,7 +850,8 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   for (int i = lane; i < parts; i += 32) {
     const float2 v = mls[i];
     const float f = v.x == -INFINITY ? 0.f : ex2(v.x - mm);
-    ll += mm == -INFINITY ? v.y : v.y * f;  // a NaN sum stays one where no score was a number
+    // a NaN sum stays one where no score was a number
+    ll += mm == -INFINITY ? v.y : CT == kCache16 ? v.y * f : lower_sum(v.y, v.x - mm);
     mls[i].x = keep_infinite(f);
   }
 #pragma unroll
@@ -877,7 +887,7 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
   const int qr = u.rt * ROWS + r;
   const int t = static_cast<int>(a.g_div.div(qr)), hq = u.h * a.G + (qr - t * a.G);
   if (t >= u.q) return;
-  const float norm = ll == 0.f ? 0.f : 1.f / ll;
+  const float norm = sum_norm<CT>(ll);
   if (lane_on) {
     T* out = static_cast<T*>(a.o) + u.b * a.os[0] + hq * a.os[1] + t * a.os[2] + lane * VEC;
 #pragma unroll
@@ -894,9 +904,7 @@ __global__ void __launch_bounds__(512) attn_cache_join_kernel(CacheArgs c, Cache
       *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(w);
     }
   }
-  if (lane == 0)
-    a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + t] =
-        ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
+  if (lane == 0) a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + t] = row_lse<CT>(mm, ll);
 }
 
 // Whether each unit gets a cluster: few units, of sequences that cannot be long
