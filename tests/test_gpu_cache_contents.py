@@ -171,3 +171,19 @@ def test_rows_of_zeros_beside_large_values(gpu_lib, cache, Hkv, G, T, size, orde
     o, lse = attend(ta, st, q)
     assert ta.sync_status() == "TA_OK"
     compare(st, q, o, lse, heads=sorted({0, Hkv // 2, Hkv - 1}))
+
+
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (40, 4), (70, 2)])
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_one_large_query_beside_ordinary_ones(gpu_lib, cache, T, G, size):
+    ta = gpu_lib
+    D, n = 128, 300
+    st = blank(ta, n, 1, D, "bf16", cache)
+    put(ta, st, 0, values(11, (1, n, D), "bf16"), values(12, (1, n, D), "bf16"))
+    q = values(3, (1, G, T, D), "bf16")
+    q[0, 1, T // 2] *= size
+    q[0, 0, 0] *= 1 / size
+    o, lse = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    compare(st, q, o, lse)

@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   __shared__ int abort_flag;
   __shared__ int odd[4];  // piece + 1 (mod 4 slots) whose draft holds non-finite values
   __shared__ float xm[kBM], xl[kBM];
-  __shared__ __align__(8) uint64_t bar_qtop;
-  __shared__ uint32_t qtop[2][4];  // largest query magnitudes, of even and odd pieces
+  __shared__ float qfac[F::Q8 && BF ? kBM : 1];  // 8 bits: the rows' factors of the scores
   // 8 bits, per tile: biased exponent taken out of its values (0: all of them
   // are zero so far)
   __shared__ int tile_e[F::SCS];
@@ -239,7 +238,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     mbar_init(&bar_ofinal, 1);
     mbar_init(&bar_xfull, 4);
     mbar_init(&bar_xempty, 4);
-    mbar_init(&bar_qtop, 4);
     for (int i = 0; i < 4; ++i) odd[i] = 0;
     fence_mbar_init();
   }
@@ -293,7 +291,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     bool ok = true;
     long long x = x0;
     [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
-    [[maybe_unused]] float kfac = 0.f;       // 8-bit: factor of the keys' scales in this piece
     [[maybe_unused]] int vexp = 0;           // 8-bit: exponent taken out of the piece's values (tile_e)
     for (int piece = 0; ok && x < x1; ++piece) {
       const int nt = piece_tiles(u, x);
@@ -361,13 +358,12 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           long long off = 0;
           const bool has = q_row(u, 0, tid, &off);
           const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + off);
-          // bf16 rows: the tile's largest finite magnitude to [1, 2) by a power of
-          // two.  An element is then off by at most 2^-25 of that, so a score
-          // by 2^-25 of what the largest query could give with the same key:
-          // one factor for all rows costs the scores of smaller ones nothing
-          // that the softmax could see, and goes into the keys' scales.
+          // bf16 rows: the row's largest magnitude to [1, 2) by a power of two, so
+          // that an element is off by at most 2^-25 of that; the scores of the row
+          // get the power back.  (Its exponent, biased, is kept finite for rows of
+          // zeros and of infinities.)
           float up = 1.f;
-          kfac = a.scale_log2;
+          [[maybe_unused]] float back = 1.f;
           if constexpr (BF) {
             uint32_t top = 0;
 #pragma unroll 8
@@ -375,27 +371,17 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
               const uint4 v = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-                top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-              }
+              for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
             }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) {
-              qtop[piece & 1][pw] = top;
-              mbar_arrive(&bar_qtop);
-            }
-            if (!(ok = warp_wait(&bar_qtop, piece & 1, ctl, kErrTimeoutOther))) break;
-            const uint32_t* t = qtop[piece & 1];
-            int ex = static_cast<int>(max(max(t[0], t[1]), max(t[2], t[3])) >> 7);  // biased exponent
-            ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
-            up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            kfac *= __uint_as_float(static_cast<uint32_t>(ex) << 23);
+            const uint32_t ex = min(max(top >> 7, 1u), 253u);
+            up = __uint_as_float((254u - ex) << 23);
+            back = a.scale_log2 * __uint_as_float(ex << 23);
           }
           uint4 first[8];  // half of the row (D = 128) is here before its place is free
 #pragma unroll
           for (int j = 0; j < 8; ++j) first[j] = has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
           if (piece > 0 && !(ok = warp_wait(&bar_qfree, (piece - 1) & 1, ctl, kErrTimeoutMma))) break;
+          if constexpr (BF) qfac[tid] = back;
 #pragma unroll
           for (int j = 0; j < DP / 8; ++j) {
             const uint4 v = j < 8 ? first[j & 7] : has && j < dg / 8 ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u);
@@ -444,7 +430,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + key * 4) : "memory");
               // A row whose values are not numbers: through its scores it makes
               // the rows that see it NaN, and does not reach the others.
-              m = number ? m * kfac : __uint_as_float(0x7fc00000u);
+              if (!number) m = __uint_as_float(0x7fc00000u);
               if (key >= end) m = 0.f;  // whatever the memory holds there
               sts_f32(sMul + 1024 + ((n >> 1) % F::SCS) * 512 + key * 4, m);
               if (tid == 0) tile_e[(n >> 1) % F::SCS] = vexp;
@@ -773,6 +759,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
       int vis_t = max(0, past / kBN - u.t);
       if (!two) vis_t = vis_t <= w ? 0 : (vis_t - w + 1) >> 1;
       float m_ref = -INFINITY, l = 0.f;
+      [[maybe_unused]] float row_f = a.scale_log2;  // 8 bits: the row's factor of the scores
       [[maybe_unused]] int o_exp = 0;  // exponent taken out of the values that O has summed
       for (int t = 0; t < n; ++t, ++ns) {
         const int ti = two ? t : 2 * t + w;       // tile of the piece
@@ -782,7 +769,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           see_keys(t == 0 ? (u.t + (two ? vis_t : 2 * vis_t + w)) * kBN : k0, vis);
         if (!(ok = warp_wait(&bar_s[w], ns & 1, ctl, kErrTimeoutMma))) break;
         tc_fence_after();
-        const float f = F::Q8 ? 1.f : a.scale_log2;  // of the scores (8 bits: in the keys' scales)
+        if constexpr (F::Q8 && BF) {
+          if (t == 0) row_f = const_cast<volatile float*>(qfac)[r];
+        }
+        const float f = F::Q8 ? 1.f : a.scale_log2;  // of the scores (8 bits: row_f, in them already)
         int e = 0;
         if constexpr (F::Q8) e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
         [[maybe_unused]] const uint32_t key_scales = sMul + 1024 + ((kt0 + ti) % F::SCS) * 512;
@@ -809,8 +799,9 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < XC; j += 4) {
               const float4 kx = lds_f4(key_scales + (c0 + j) * 4);
-              const float2 p = fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y));
-              const float2 q = fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w));
+              const float2 f2 = make_float2(row_f, row_f);
+              const float2 p = fmul2(fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y)), f2);
+              const float2 q = fmul2(fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w)), f2);
               y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
             }
           }
