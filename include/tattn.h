@@ -327,10 +327,11 @@ size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, t
  * not be initialised; calls that may run at the same time need one each.
  * Scores, softmax sums and accumulators are fp32.  16-bit caches: weights are
  * rounded to dt for the product with V.  8-bit caches: products in fp16 on the
- * bare codes (exact), the scales applied in fp32; beyond 32 to 64 query rows
- * (Hq / Hkv * T) per key head the values are multiplied out and rounded to fp16;
- * bf16 queries are scaled by a power of two into fp16's range.  A row that sees a
- * value with a NaN scale gets NaN in O and L. */
+ * bare codes (exact), the keys' scales applied to the scores in fp32, the values' in
+ * the weights' exponents, so that the fp16 weights are rounded relative to the
+ * row's largest contribution; each bf16 query row is scaled by a power of two
+ * into fp16's range.  A row that sees a value with a NaN scale gets NaN in O and
+ * L. */
 ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_cache* cache, const int* pages,
                          int max_pages, const int* kv_lens, const int* q_lens, const uint8_t* tree,
                          const int64_t* tree_strides, void* o, const int64_t* o_strides, float* lse, void* ws,

@@ -173,6 +173,30 @@ def test_rows_of_zeros_beside_large_values(gpu_lib, cache, Hkv, G, T, size, orde
     compare(st, q, o, lse, heads=sorted({0, Hkv // 2, Hkv - 1}))
 
 
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 30, 2.0 ** 100])
+@pytest.mark.parametrize("T,G", [(3, 4), (40, 4), (70, 2)])
+@pytest.mark.parametrize("cache,dtype", [("e4m3", "bf16"), ("int8", "bf16")])
+def test_large_values_that_rows_do_not_use(gpu_lib, cache, dtype, T, G, size):
+    """A large value that the draft's tree hides from all rows but its own, and one
+    of an older token whose weight is far below all others: the other rows'
+    results are as exact as without them."""
+    ta = gpu_lib
+    D, n = 64, 300
+    st = blank(ta, n, 1, D, dtype, cache)
+    k, v = values(11, (1, n, D), dtype), values(12, (1, n, D), dtype)
+    hidden = 1
+    v[:, n - T + hidden] *= size
+    k[:, 40], v[:, 40] = -30.0, v[:, 40] * size  # scores about -480 below
+    put(ta, st, 0, k, v)
+    tree = np.tril(np.ones((T, T), dtype=bool))
+    tree[:, hidden] = False
+    tree[hidden, hidden] = True
+    q = values(3, (1, G, T, D), dtype, 0.1) + 2.0
+    o, lse = attend(ta, st, q, None, tree[None])
+    assert ta.sync_status() == "TA_OK"
+    compare(st, q, o, lse, tree)
+
+
 @pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40, 2.0 ** 100])
 @pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (40, 4), (70, 2)])
 @pytest.mark.parametrize("cache", ["e4m3", "int8"])

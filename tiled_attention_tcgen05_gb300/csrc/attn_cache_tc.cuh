@@ -7,7 +7,7 @@
 //                   tokens; 8 bits: turn the keys' codes into fp16, and four
 //                   warps more the values';
 //   a warp          issues the MMAs: S = Q K^T, O += P V with P in TMEM;
-//   two warps       fetch keys and values by TMA (8 bits: one fetches both);
+//   two warps       fetch keys and values by TMA;
 // and the registers handed to the softmax groups (setmaxnreg).  The groups
 // alternate on the tensor core:  S0 S1 | PV0 S0' | PV1 S1' | ...  Units of more
 // than 128 rows give each group a row tile of its own and both the same keys;
@@ -19,18 +19,19 @@
 // divides a page), a lane per box.  Boxes behind the sequence's end or of pages
 // that do not exist are fetched from outside the map and so read as zeros.
 // 16-bit rows go straight into the 128-byte-swizzled layout that the MMA
-// descriptors read.  8-bit codes and their scales go into staging rings, one of
-// keys and one of values; the eight helpers turn them into fp16: the keys' codes as
-// they are (exact; a key's scale multiplies its finished scores in fp32), the
-// values' rows multiplied out, with a power of two taken out that all values of
-// the piece so far share.  (A value's scale in the exponent, as in
-// attn_cache_rows.cuh, would have every row read two more numbers per key from
-// shared memory.)  That rounding, of a row to 11 bits, adds 2^-11 P |V| to the
-// result at most.  16 sequences of 8192, 8 key heads of 128, 64 rows, e4m3: 132 us,
-// 31 % of the copy rate.  Most of that is hand-overs between the roles: over int8
-// (138 us) the conversions' arithmetic and the first pass of the softmax are 8 to 10 us
-// each, the exponentials and the fetched bytes 5 more, and 108 are left without
-// all of them.
+// descriptors read.  8-bit codes go into staging rings, one of keys (with the
+// scales) and one of values, and the eight helpers turn them into fp16 as they
+// are, which is exact.  As in attn_cache_rows.cuh a key's scale multiplies its
+// finished scores, a value's is part of the weight's exponent, and the sum takes
+// it out again: whatever the scales' range, weights are rounded relative to the
+// row's largest contribution, and a value that a row does not see cannot cost
+// it anything.  (Values multiplied out to fp16 by one power of two for all of
+// them lost the small ones beside a large one that no row used, and took 124 us
+// where this takes 119: 16 sequences of 8192, 8 key heads of 128, 64 rows, e4m3.  That is
+// 34 % of the copy rate; over int8 122 us.  What bounds it are the hand-overs between the
+// roles: of the 138 us it took over int8 when conversions still multiplied,
+// 108 were left without the conversions' arithmetic, the softmax's first pass, the
+// exponentials and the fetches.)
 //
 // A box may bring rows behind the sequence's end, whose memory may hold
 // anything, and a draft's values may hold infinities and NaN that some rows
@@ -60,9 +61,9 @@ struct TcCfg {
   static constexpr int VST = Q8 ? KST : (DP == 128 ? 2 : 4);
   static constexpr int OPB = Q8 ? 64 * DP : 0;           // codes of half a tile
   static constexpr int SR = Q8 ? (DP == 128 ? 3 : 6) : 0;  // staging rings, of keys and of values
-  static constexpr int SSLOT = OPB + 1024;               // and the whole tile's scales (keys': both)
+  static constexpr int SSLOT = OPB + 1024;               // keys': and both scales of the whole tile's keys
   static constexpr int SCS = KST + 2;                    // tiles whose scales the softmax may need
-  static constexpr int MUL = Q8 ? 1024 + SCS * 512 : 0;  // values' multipliers; ring of keys' scales
+  static constexpr int SCALES = Q8 ? SCS * 1536 : 0;     // their ring: keys' scales, values' log2, sum's factors
   static constexpr int HELPERS = Q8 ? 8 : 4;             // warps 8 .. 8 + HELPERS - 1
   static constexpr int MMA = 8 + HELPERS;                // warp; the fetching warps follow it
   static constexpr int THREADS = 32 * (MMA + 4);         // whole register groups of four warps
@@ -75,7 +76,7 @@ struct TcCfg {
   // is free for the next piece only after that.
   static constexpr bool XOWN = DP == 64, XQ = DP == 128 && Q8;
   static constexpr int XCH = DP == 64 ? 16 : TILE / 2048;  // float4 columns of 128 rows a round
-  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? 2 * SR * SSLOT + MUL : 0) + (XOWN ? 32768 : 0);
+  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE + (Q8 ? SR * (SSLOT + OPB) + SCALES : 0) + (XOWN ? 32768 : 0);
   static_assert(SMEM + 2048 <= kSmemMax, "tiles do not fit in shared memory");
 };
 template <int CT, int DP>
@@ -178,9 +179,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   __shared__ int odd[4];  // piece + 1 (mod 4 slots) whose draft holds non-finite values
   __shared__ float xm[kBM], xl[kBM];
   __shared__ float qfac[F::Q8 && BF ? kBM : 1];  // 8 bits: the rows' factors of the scores
-  // 8 bits, per tile: biased exponent taken out of its values (0: all of them
-  // are zero so far)
-  __shared__ int tile_e[F::SCS];
   __shared__ __align__(8) uint64_t bar_scan[VST];  // values that have to be looked through have landed
   __shared__ __align__(8) uint64_t bar_stage[2][F::Q8 ? F::SR : 1], bar_sempty[2][F::Q8 ? F::SR : 1];  // 8 bits: keys', values'
 
@@ -207,8 +205,8 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
   auto sK = [&](int st) { return sQ + (F::QT + st) * F::TILE; };
   auto sV = [&](int st) { return sQ + (F::QT + KST + st) * F::TILE; };
   const uint32_t sStage = sQ + (F::QT + KST + VST) * F::TILE;
-  const uint32_t sMul = sStage + 2 * F::SR * F::SSLOT;
-  const uint32_t sX = F::XOWN ? sMul + F::MUL : F::XQ ? sQ : sQ + F::TILE;
+  const uint32_t sScale = sStage + F::SR * (F::SSLOT + F::OPB);
+  const uint32_t sX = F::XOWN ? sScale + F::SCALES : F::XQ ? sQ : sQ + F::TILE;
 
   WaitCtl ctl{c.err, a.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     }
     if constexpr (F::Q8) {
       for (int s = 0; s < 2 * F::SR; ++s) {
-        mbar_init(&bar_stage[0][0] + s, 1 + 32);  // the codes' fetch, a warp's copies of scales
+        mbar_init(&bar_stage[0][0] + s, s < F::SR ? 1 + 32 : 1);  // the codes' fetch; keys': a warp's copies of scales
         mbar_init(&bar_sempty[0][0] + s, 4);
       }
     }
@@ -291,7 +289,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
     bool ok = true;
     long long x = x0;
     [[maybe_unused]] uint32_t scan_par = 0;  // phase of each stage's bar_scan
-    [[maybe_unused]] int vexp = 0;           // 8-bit: exponent taken out of the piece's values (tile_e)
     for (int piece = 0; ok && x < x1; ++piece) {
       const int nt = piece_tiles(u, x);
       if constexpr (!F::Q8) {
@@ -353,7 +350,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         }
       } else {
         constexpr int CH = DP / 16;  // 16-byte chunks per row of codes
-        vexp = 0;
         if (keys) {  // the piece's queries, a row per thread, in fp16
           long long off = 0;
           const bool has = q_row(u, 0, tid, &off);
@@ -403,47 +399,26 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         // A tile's codes, of its half n & 1 -> fp16 in the tile; rows at and
         // behind `end` are zeros.  A warp converts rows pw * 16 .. + 15 of a half.
         const uint32_t ring = sStage + (keys ? 0 : F::SR * F::SSLOT);
+        const int pitch = keys ? F::SSLOT : F::OPB;
         auto convert = [&](int n, uint32_t tile, int end) -> bool {
           const int slot = n % F::SR;
-          const uint32_t st = ring + slot * F::SSLOT;
+          const uint32_t st = ring + slot * pitch;
           if (!warp_wait(&bar_stage[keys ? 0 : 1][slot], (n / F::SR) & 1, ctl, kErrTimeoutTma)) return false;
-          if (!(n & 1)) {  // the whole tile's scales have come with its first half
-            // The largest scale of the values, of four keys a lane; every warp, of
-            // keys too, for itself.
-            const uint32_t sc = st + F::OPB;
-            const float4 v4 = lds_f4(sc + 512 + lane * 16);
-            const float f4[4] = {v4.x, v4.y, v4.z, v4.w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b = __float_as_uint(f4[e]);
-              if (b < 0x7f800000u && lane * 4 + e < end) top = max(top, b);
-            }
-            const int ve = min(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23), 253);  // biased exponent
-            // |code| 2^7 < 65504: values up to 2^7 times the power's size fit
-            if (vexp == 0 || ve > vexp + 6) vexp = ve;
-            const int key = (lane >> 4) * 64 + pw * 16 + (lane & 15);  // this lane's row of the warp's
-            float m;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + 512 + key * 4) : "memory");
-            const bool number = m < INFINITY;
-            if (keys) {
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m) : "r"(sc + key * 4) : "memory");
-              // A row whose values are not numbers: through its scores it makes
-              // the rows that see it NaN, and does not reach the others.
-              if (!number) m = __uint_as_float(0x7fc00000u);
-              if (key >= end) m = 0.f;  // whatever the memory holds there
-              sts_f32(sMul + 1024 + ((n >> 1) % F::SCS) * 512 + key * 4, m);
-              if (tid == 0) tile_e[(n >> 1) % F::SCS] = vexp;
-            } else {
-              m = number && key < end ? m * __uint_as_float(static_cast<uint32_t>(254 - max(vexp, 1)) << 23) : 0.f;
-              // as the sum of two fp16, 22 bits
-              const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
-              const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sMul + key * 8),
-                           "r"(reinterpret_cast<const uint32_t&>(h2)), "r"(reinterpret_cast<const uint32_t&>(l2))
-                           : "memory");
-              __syncwarp();  // (the multipliers of the rows that this warp converts)
-            }
+          if (keys && !(n & 1)) {  // the whole tile's scales have come with its first half
+            const uint32_t sc = st + F::OPB, to = sScale + ((n >> 1) % F::SCS) * 1536;
+            const int key = (lane >> 4) * 64 + pw * 16 + (lane & 15);  // this lane's of the warp's
+            float kx, vscale;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kx) : "r"(sc + key * 4) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vscale) : "r"(sc + 512 + key * 4) : "memory");
+            // A row whose values are not numbers: through its scores it makes the
+            // rows that see it NaN, and does not reach the others.  No scale
+            // stands for a value of zero.
+            if (!(vscale < INFINITY)) kx = __uint_as_float(0x7fc00000u), vscale = 1.f;
+            if (key >= end) kx = 0.f, vscale = 1.f;  // whatever the memory holds there
+            const float lsv = lg2(fmaxf(vscale, kMinScale));
+            sts_f32(to + key * 4, kx);
+            sts_f32(to + 512 + key * 4, lsv);
+            sts_f32(to + 1024 + key * 4, ex2(0.5f * (kSumUp - lsv)));
           }
           // Chunk of 16 codes -> two of 8 fp16.  Eight neighbouring lanes take
           // four chunks of a row and the other four of the next one (D = 128),
@@ -461,17 +436,11 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           };
           // (all loads first: a load must not wait for the stores before it)
           uint4 codes[CH / 2];
-          uint32_t m[CH / 2][2] = {};
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) {
             int r, j;
             place(i, &r, &j);
             codes[i] = lds_u4(st + r * DP + j * 16);
-            if (!keys)
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                           : "=r"(m[i][0]), "=r"(m[i][1])
-                           : "r"(sMul + (row0 + r) * 8)
-                           : "memory");
           }
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) {
@@ -485,15 +454,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             code4_to_f16<CT>(v.y, h[2], h[3]);
             code4_to_f16<CT>(v.z, h[4], h[5]);
             code4_to_f16<CT>(v.w, h[6], h[7]);
-            if (!keys) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {  // code * scale, rounded once
-                const __half2 x = reinterpret_cast<const __half2&>(h[e]);
-                const __half2 y = __hfma2(x, reinterpret_cast<const __half2&>(m[i][0]),
-                                          __hmul2(x, reinterpret_cast<const __half2&>(m[i][1])));
-                h[e] = reinterpret_cast<const uint32_t&>(y);
-              }
-            }
             sts_v4(tile_at(tile, r, 2 * j), h[0], h[1], h[2], h[3]);
             sts_v4(tile_at(tile, r, 2 * j + 1), h[4], h[5], h[6], h[7]);
           }
@@ -654,6 +614,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         // A warp and a ring each for keys and values, in halves of a tile: the
         // rings are short beside a fetch's 1.2 us.
         const uint32_t ring = sStage + (is_k ? 0 : F::SR * F::SSLOT);
+        const int pitch = is_k ? F::SSLOT : F::OPB;
         uint64_t* const full = bar_stage[is_k ? 0 : 1];
         uint64_t* const empty = bar_sempty[is_k ? 0 : 1];
         int n = 0;
@@ -667,21 +628,20 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           for (int half = 0; half < 2; ++half, ++n) {
             const int slot = n % F::SR;
             if (n >= F::SR && !(ok = warp_wait(&empty[slot], (n / F::SR - 1) & 1, ctl, kErrTimeoutMma))) break;
-            const uint32_t st = ring + slot * F::SSLOT;
+            const uint32_t st = ring + slot * pitch;
             if (lane == 0) mbar_expect_tx(&full[slot], F::OPB);
             __syncwarp();
             const int first = half * (nbox >> 1);
             if (lane >= first && lane < first + (nbox >> 1))
               tma_load_rows(base + (st - sQ) + (lane - first) * box * DP, is_k ? &tm_k : &tm_v, &full[slot], row,
                             page >= 0 ? page * c.Hkv + h : outside);
-            if (half == 0) {
-              // The tile's scales, four keys' a lane, zeros for none: with the
-              // keys both, with the values theirs again.
+            if (!is_k) continue;
+            if (half == 0) {  // both scales of the tile's keys, four keys' a lane, zeros for none
               const int b = lane * 4 / box;
               const int pg = __shfl_sync(0xffffffffu, page, b);
               const int rw = __shfl_sync(0xffffffffu, row, b) + lane * 4 % box;
               const size_t at = pg < 0 ? 0 : static_cast<size_t>((pg * c.Hkv + h) * static_cast<int>(c.page.d) + rw);
-              if (is_k) cp_async16(st + F::OPB + lane * 16, c.ks + at, pg >= 0);
+              cp_async16(st + F::OPB + lane * 16, c.ks + at, pg >= 0);
               cp_async16(st + F::OPB + 512 + lane * 16, c.vs + at, pg >= 0);
             }
             cp_async_signal(&full[slot]);
@@ -760,7 +720,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
       if (!two) vis_t = vis_t <= w ? 0 : (vis_t - w + 1) >> 1;
       float m_ref = -INFINITY, l = 0.f;
       [[maybe_unused]] float row_f = a.scale_log2;  // 8 bits: the row's factor of the scores
-      [[maybe_unused]] int o_exp = 0;  // exponent taken out of the values that O has summed
       for (int t = 0; t < n; ++t, ++ns) {
         const int ti = two ? t : 2 * t + w;       // tile of the piece
         const int k0 = (u.t + ti) * kBN;
@@ -773,9 +732,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           if (t == 0) row_f = const_cast<volatile float*>(qfac)[r];
         }
         const float f = F::Q8 ? 1.f : a.scale_log2;  // of the scores (8 bits: row_f, in them already)
-        int e = 0;
-        if constexpr (F::Q8) e = const_cast<volatile int*>(tile_e)[(kt0 + ti) % F::SCS];
-        [[maybe_unused]] const uint32_t key_scales = sMul + 1024 + ((kt0 + ti) % F::SCS) * 512;
+        [[maybe_unused]] const uint32_t scales = sScale + ((kt0 + ti) % F::SCS) * 1536;
         // 16 bits: the row's 128 scores in registers.  8 bits: two passes over S
         // in tensor memory, XC columns at a time (scales, mask and maximum;
         // weights): the loops of the softmax, the conversions and the MMA warp
@@ -798,10 +755,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             if (!first) return;
 #pragma unroll
             for (int j = 0; j < XC; j += 4) {
-              const float4 kx = lds_f4(key_scales + (c0 + j) * 4);
+              const float4 kx = lds_f4(scales + (c0 + j) * 4), vx = lds_f4(scales + 512 + (c0 + j) * 4);
               const float2 f2 = make_float2(row_f, row_f);
-              const float2 p = fmul2(fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y)), f2);
-              const float2 q = fmul2(fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w)), f2);
+              const float2 p = ffma2(fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y)), f2, make_float2(vx.x, vx.y));
+              const float2 q = ffma2(fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w)), f2, make_float2(vx.z, vx.w));
               y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
             }
           }
@@ -850,19 +807,13 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
         } else if (m_new > m_ref + kRescaleThreshold) {
           resc = true;
           alpha = ex2(m_ref - m_new);
+          if constexpr (F::Q8) l = lower_sum(l, m_ref - m_new);
           m_ref = m_new;
-        }
-        float o_alpha = keep_infinite(alpha);
-        if constexpr (F::Q8) {  // values of a larger power of two from here on
-          if (t > 0 && e != o_exp) {
-            resc = true;
-            o_alpha *= o_exp ? ex2(static_cast<float>(o_exp - e)) : 0.f;
-          }
-          o_exp = e;
         }
         const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const float2 sc2 = make_float2(f, f);
         const float2 nm2 = make_float2(neg_m, neg_m);
+        const float2 half2 = make_float2(0.5f, 0.5f), nmh2 = make_float2(0.5f * neg_m, 0.5f * neg_m);
         float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += XC) {
@@ -870,22 +821,31 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < XC / 16; ++k) {
             uint32_t pk[8];
+            [[maybe_unused]] float4 root;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float2 y2 = make_float2(y[16 * k + 2 * e], y[16 * k + 2 * e + 1]);
-              const float2 t2 = F::Q8 ? fadd2(y2, nm2) : ffma2(y2, sc2, nm2);
-              const float2 p2 = make_float2(ex2(t2.x), ex2(t2.y));
-              rs2[e & 3] = fadd2(rs2[e & 3], p2);
+              const float2 t2 = F::Q8 ? ffma2(y2, half2, nmh2) : ffma2(y2, sc2, nm2);
+              float2 p2 = make_float2(ex2(t2.x), ex2(t2.y));
+              if constexpr (F::Q8) {  // the weight's root (attn_cache.cuh)
+                if (e % 2 == 0) root = lds_f4(scales + 1024 + (c0 + 16 * k + 2 * e) * 4);
+                const float2 x = fmul2(p2, e % 2 ? make_float2(root.z, root.w) : make_float2(root.x, root.y));
+                rs2[e & 3] = ffma2(x, x, rs2[e & 3]);
+                p2 = fmul2(p2, p2);
+              } else {
+                rs2[e & 3] = fadd2(rs2[e & 3], p2);
+              }
               pk[e] = pack2<MBF>(p2.x, p2.y);
             }
             tmem_st_x8(s_addr + c0 / 2 + 8 * k, pk);  // over columns that are read
           }
         }
         const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
-        l = l * alpha + (rsa.x + rsa.y);
+        l = (F::Q8 ? l : l * alpha) + (rsa.x + rsa.y);
         if (t > 0 && __any_sync(0xffffffffu, resc)) {
           if (!(ok = warp_wait(&bar_o[w], (ns - 1) & 1, ctl, kErrTimeoutMma))) break;
           tc_fence_after();
+          const float o_alpha = keep_infinite(alpha);
 #pragma unroll
           for (int k = 0; k < DP / 32; ++k) {
             uint32_t ov[32];
@@ -916,9 +876,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
       // one row tile: group 1 hands its state over in rounds of XCH columns
       constexpr int NCH = DP / 4;                                  // float4 columns
       constexpr int XCH = F::XCH, XR = NCH / XCH;
-      // O's power of two
-      const float o_pow = !F::Q8 ? 1.f : o_exp ? __uint_as_float(static_cast<uint32_t>(o_exp) << 23) : 0.f;
-      float f0 = o_pow, f1 = 0.f;
+      float f0 = 1.f, f1 = 0.f;
       const bool whole = u.t == 0 && nt == u.ntiles;
       float* const part = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (x > x0 ? 1 : 0)) * tc_part_floats<CT, DP>();
       const int prow = (two ? w * kBM : 0) + r;
@@ -939,10 +897,6 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             if (n > 0) {
               tmem_ld_x32(o_addr + (round * XCH + k) * 4, ov);
               tmem_ld_wait(ov);
-              if constexpr (F::Q8) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * o_pow);
-              }
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) ov[j] = 0u;
@@ -964,12 +918,14 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             const float mm = fmaxf(m_ref, m1);
             f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - mm);
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
-            l = mm == -INFINITY ? l + l1 : l * f0 + l1 * f1;  // NaN stays
-            f0 = keep_infinite(f0) * o_pow, f1 = keep_infinite(f1);
+            l = mm == -INFINITY ? l + l1  // NaN stays
+                : F::Q8         ? lower_sum(l, m_ref - mm) + lower_sum(l1, m1 - mm)
+                                : l * f0 + l1 * f1;
+            f0 = keep_infinite(f0), f1 = keep_infinite(f1);
             m_ref = mm;
           }
         }
-        const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const float norm = whole ? sum_norm<CT>(l) : 1.f;
 #pragma unroll 1
         for (int k = 0; k < XCH; k += 8) {
           const int ch0 = round * XCH + k;
@@ -1021,8 +977,7 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
           part[F::ROWS * DP + prow] = m_ref;
           part[F::ROWS * (DP + 1) + prow] = l;
         } else if (tok >= 0) {
-          a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + tok] =
-              l == 0.f ? -INFINITY : (m_ref == -INFINITY ? l : (m_ref + lg2(l)) * kLn2);
+          a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + tok] = row_lse<CT>(m_ref, l);
         }
         if constexpr (!F::Q8) {
           if (odd_values && tok >= 0)
@@ -1083,7 +1038,8 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
     if (slots[i] >= 0) {
       const float pm = __ldcg(part(i) + F::ROWS * DP + prow), pl = __ldcg(part(i) + F::ROWS * (DP + 1) + prow);
       f = pm == -INFINITY ? 0.f : ex2(pm - mm);
-      ll += mm == -INFINITY ? pl : pl * f;  // a NaN sum stays one where no score was a number
+      // a NaN sum stays one where no score was a number
+      ll += mm == -INFINITY ? pl : F::Q8 ? lower_sum(pl, pm - mm) : pl * f;
     }
     fs[i][lane] = keep_infinite(f);
   }
@@ -1112,7 +1068,7 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
   }
   if (rr >= rows) return;
   const int t = static_cast<int>(a.g_div.div(rr)), hq = u.h * a.G + (rr - t * a.G);
-  const float norm = ll == 0.f ? 0.f : 1.f / ll;
+  const float norm = sum_norm<CT>(ll);
   T* const out = static_cast<T*>(a.o) + u.b * a.os[0] + hq * a.os[1] + t * a.os[2];
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
@@ -1124,9 +1080,7 @@ __global__ void __launch_bounds__(256) attn_cache_tc_join_kernel(CacheArgs c, Ca
       *reinterpret_cast<uint2*>(out + ch * 4) = o;
     }
   }
-  if (warp == 0)
-    a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + t] =
-        ll == 0.f ? -INFINITY : (mm == -INFINITY ? ll : (mm + lg2(ll)) * kLn2);
+  if (warp == 0) a.lse[(static_cast<long long>(u.b) * a.Hq + hq) * c.T + t] = row_lse<CT>(mm, ll);
 }
 
 template <typename T, int CT, int DP>
