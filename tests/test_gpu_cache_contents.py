@@ -211,3 +211,25 @@ def test_one_large_query_beside_ordinary_ones(gpu_lib, cache, T, G, size):
     o, lse = attend(ta, st, q)
     assert ta.sync_status() == "TA_OK"
     compare(st, q, o, lse)
+
+
+@pytest.mark.parametrize("T,G", [(4, 4), (40, 4)])
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_negative_value_scales_are_no_numbers(gpu_lib, cache, T, G):
+    """A row that sees a value with a negative scale gets NaN; others keep
+    every bit."""
+    ta = gpu_lib
+    D, n = 64, 150
+    st = Setup(ta, [n], 1, 16, D, "bf16", cache, 6)
+    tree = np.tril(np.ones((T, T), dtype=bool))
+    tree[2:, 1] = False
+    q = values(3, (1, G, T, D), "bf16")
+    o, lse = attend(ta, st, q, None, tree[None])
+    pg, r = place(st, 0, n - T + 1)
+    for x in (-1.0, -2.0 ** -70, -INF):
+        st.cache.v_scale[pg, 0, r] = x
+        o2, lse2 = attend(ta, st, q, None, tree[None])
+        assert ta.sync_status() == "TA_OK"
+        own = torch.arange(T) == 1
+        assert torch.isnan(o2[:, :, own].float()).all() and torch.isnan(lse2[:, :, own]).all(), x
+        assert torch.equal(o2[:, :, ~own], o[:, :, ~own]) and torch.equal(lse2[:, :, ~own], lse[:, :, ~own]), x

@@ -337,7 +337,8 @@ class KVCache:
     """A key/value cache in pages: k, v contiguous CUDA tensors [num_pages,
     Hkv, page_size, D] of float16, bfloat16, float8_e4m3fn or int8; the 8-bit
     types with k_scale, v_scale float32 [num_pages, Hkv, page_size] (a row stands
-    for code * scale).  Holds the tensors; any page_size, D in {16, 32, 64, 128}.
+    for code * scale; scales are 2^-60 or more, or NaN, as cache_append writes them:
+    attention takes a v_scale from 0 to 2^-60 as 2^-60, a negative one as NaN).  Holds the tensors; any page_size, D in {16, 32, 64, 128}.
 
     Every call on it takes the sequences' page table and lengths, int32 CUDA
     tensors: pages [B, max_pages] (position n of sequence b is row n % page_size

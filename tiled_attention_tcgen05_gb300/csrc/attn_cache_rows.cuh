@@ -365,9 +365,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<CT, D, MT>::BPS) attn_cache_k
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + lane * 4), "f"(kscale * a.scale_log2) : "memory");
           }
           // no scale (a row past the end, or of a page that the cache does not
-          // have) stands for a value of zero whatever its codes; a NaN row's
-          // scores are NaN, its factor must not reach other rows' sums
-          if (vscale < kMinScale) vscale = kMinScale;
+          // have) stands for a value of zero; the scores of a key whose value's
+          // scale is NaN, or negative, are NaN, and its factor must not reach other
+          // rows' sums
+          vscale = vscale >= 0.f ? fmaxf(vscale, kMinScale) : __uint_as_float(0x7fc00000u);
           const float lsv = lg2(vscale);
           const float root = vscale == vscale ? ex2(0.5f * (kSumUp - lsv)) : 0.f;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc_a + KW * 4 + lane * 4), "f"(lsv) : "memory");

@@ -410,10 +410,10 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             float kx, vscale;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kx) : "r"(sc + key * 4) : "memory");
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vscale) : "r"(sc + 512 + key * 4) : "memory");
-            // A row whose values are not numbers: through its scores it makes the
-            // rows that see it NaN, and does not reach the others.  No scale
-            // stands for a value of zero.
-            if (!(vscale < INFINITY)) kx = __uint_as_float(0x7fc00000u), vscale = 1.f;
+            // A value whose scale is not a number, or negative: through its key's
+            // scores it makes the rows that see it NaN, and does not reach the
+            // others.  No scale stands for a value of zero.
+            if (!(vscale >= 0.f && vscale < INFINITY)) kx = __uint_as_float(0x7fc00000u), vscale = 1.f;
             if (key >= end) kx = 0.f, vscale = 1.f;  // whatever the memory holds there
             const float lsv = lg2(fmaxf(vscale, kMinScale));
             sts_f32(to + key * 4, kx);
