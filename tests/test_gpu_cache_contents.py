@@ -233,3 +233,32 @@ def test_negative_value_scales_are_no_numbers(gpu_lib, cache, T, G):
         own = torch.arange(T) == 1
         assert torch.isnan(o2[:, :, own].float()).all() and torch.isnan(lse2[:, :, own]).all(), x
         assert torch.equal(o2[:, :, ~own], o[:, :, ~own]) and torch.equal(lse2[:, :, ~own], lse[:, :, ~own]), x
+
+
+def test_outputs_made_for_another_stream(gpu_lib):
+    """A call on another stream makes its outputs and workspace out of that
+    stream's memory: memory that the current stream has freed may still be
+    written to by what runs there."""
+    ta = gpu_lib
+    st = Setup(ta, [64, 40], 2, 16, 64, "bf16", "int8", 3)
+    q = values(3, (2, 8, 3, 64), "bf16").cuda()
+    ql, keep, kl = int32([3, 3]), int32([0, 1, 2] * 2).view(2, 3), int32([2, 1])
+    calls = (lambda s: ta.cache_read(st.cache, st.pages, st.kv_lens, 64, stream=s),
+             lambda s: ta.attn_cache_fwd(q, st.cache, st.pages, st.kv_lens, stream=s),
+             lambda s: (ta.cache_keep(st.cache, st.pages, st.kv_lens, ql, keep, kl, stream=s),))
+    side = torch.cuda.Stream()
+    for call in calls:
+        ref = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        # what the call will allocate on the current stream, freed with writes pending
+        for _ in range(3):
+            pending = [torch.empty_like(t) for t in ref]
+            torch.cuda._sleep(200_000_000)
+            for t in pending:
+                t.fill_(77)
+            del pending, t
+            out = call(side)
+            side.synchronize()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert ta.sync_status() == "TA_OK"

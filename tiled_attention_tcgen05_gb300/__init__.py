@@ -345,7 +345,11 @@ class KVCache:
     of page pages[b, n // page_size]), kv_lens [B] (tokens, the new ones
     included) and q_lens [B] (new tokens, the last ones; None: T each).  Page ids
     and lengths outside the cache are skipped on the device and make the next
-    sync_status() return TA_ERR_INDEX."""
+    sync_status() return TA_ERR_INDEX.
+
+    A call runs on `stream` (None: the cache's device's current one); what it reads
+    has to be ready there, and what it returns is ready when that stream gets
+    there."""
 
     __slots__ = ("_t", "_c", "_ref", "_index", "dtype", "device", "shape")
 
@@ -437,19 +441,27 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _raw_stream(index, stream, *used):
-    """The handle of the stream a call runs on (None: the device's current one).
-    Tensors that the call allocates on the current stream and uses on another
-    are recorded there."""
-    current = _current_raw_stream(index)
+def _raw_stream(index, stream):
+    """The handle of the stream a call runs on (None: the device's current one)."""
     if stream is None:
-        return current
+        return _current_raw_stream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, index, stream, like=None):
+    """Memory for a call's output or workspace, out of the stream's that the call
+    runs on: what the current stream has freed may still be written to by what
+    runs there.  The current stream may use it too, once the call is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index) if like is None else torch.empty_like(like)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
-    if stream.cuda_stream != current:
-        for t in used:
-            t.record_stream(stream)
-    return stream.cuda_stream
+    current = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        t = _empty(shape, dtype, index, None, like)
+    if stream.cuda_stream != current.cuda_stream:
+        t.record_stream(current)
+    return t
 
 
 def _elsewhere(cache):
@@ -499,21 +511,18 @@ def cache_read(cache, pages, kv_lens, N, dtype=None, k=None, v=None, stream=None
         raise ValueError(f"unsupported dtype {dtype}")
     N = int(N)
     shape = (B, Hkv, N, D)
-    made = []
     for name, t in (("k", k), ("v", v)):
         if t is not None:
             _tokens(name, t, shape, dtype, cache._index)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        made.append(k)
+        k = _empty(shape, dtype, cache._index, stream)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
-        made.append(v)
+        v = _empty(shape, dtype, cache._index, stream)
     _check("attn_cache_read", lib.attn_cache_read(
         cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, _DT[dtype],
-        _raw_stream(cache._index, stream, *made)))
+        _raw_stream(cache._index, stream)))
     return k, v
 
 
@@ -532,10 +541,10 @@ def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
     T = keep.shape[1]
     _i32("keep", keep, (B, T), cache._index)
     _i32("keep_lens", keep_lens, (B,), cache._index)
-    new = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    new = _empty((B,), torch.int32, cache._index, stream)
     _check("attn_cache_keep", lib.attn_cache_keep(
         cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(),
-        keep.data_ptr(), keep_lens.data_ptr(), new.data_ptr(), B, T, _raw_stream(cache._index, stream, new)))
+        keep.data_ptr(), keep_lens.data_ptr(), new.data_ptr(), B, T, _raw_stream(cache._index, stream)))
     return new
 
 
@@ -573,31 +582,27 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
             raise ValueError(f"tree must be a bool [B or 1, {T}, {T}] tensor on CUDA device {index} with contiguous rows")
         ts = _TreeStrides(0 if tree.shape[0] == 1 else tree.stride(0), tree.stride(1))
         tp = tree.data_ptr()
-    made = []
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(shape, dtype, index, stream, like=q)
         if o.stride() != q.stride():  # an expanded q has rows in common, o has not
-            o = torch.empty(shape, dtype=dtype, device=cache.device)
-        made.append(o)
+            o = _empty(shape, dtype, index, stream)
     os_ = _tokens("o", o, shape, dtype, index, written=True)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
-        made.append(lse)
+        lse = _empty((B, Hq, T), torch.float32, index, stream)
     elif lse.dtype is not torch.float32 or lse.shape != (B, Hq, T) or lse.get_device() != index or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on CUDA device {index}")
     if ws is None:
         n = lib.attn_cache_workspace_bytes(B, Hq, Hkv, T, min(max_pages * page, 2 ** 31 - 1), D, _DT[dtype],
                                            _CT[cache.dtype])
-        ws = torch.empty(max(int(n), 16), dtype=torch.uint8, device=cache.device)
-        made.append(ws)
+        ws = _empty((max(int(n), 16),), torch.uint8, index, stream)
     elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on CUDA device {index}")
     _check("attn_cache_fwd", lib.attn_cache_fwd(
         q.data_ptr(), qs, cache._ref, pages.data_ptr(), max_pages, kv_lens.data_ptr(),
         None if q_lens is None else q_lens.data_ptr(), tp, ts, o.data_ptr(), os_, lse.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size(), B, Hq, T, _DT[dtype], -1.0 if sm_scale is None else float(sm_scale),
-        _raw_stream(cache._index, stream, *made)))
+        _raw_stream(index, stream)))
     return o, lse
 
 
