@@ -308,8 +308,9 @@ ta_status attn_cache_keep(const ta_kv_cache* cache, const int* pages, int max_pa
                           const int* q_lens, const int* keep, const int* keep_lens, int* new_lens, int B, int T,
                           void* stream);
 
-/* Bytes of workspace attn_cache_fwd needs.  N: the largest kv_lens (at most
- * max_pages * page_size). */
+/* Bytes of workspace attn_cache_fwd needs.  They follow from the rows per key
+ * head (Hq / Hkv * T), D and the types; N >= 0, the largest kv_lens (at most
+ * max_pages * page_size), does not change them now. */
 size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, ta_dtype dt, ta_dtype ct);
 
 /* Attention of the new tokens over the cache, which holds their own keys and

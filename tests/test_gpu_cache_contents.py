@@ -262,3 +262,20 @@ def test_outputs_made_for_another_stream(gpu_lib):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, ref))
     assert ta.sync_status() == "TA_OK"
+
+
+def test_page_tables_without_a_column(gpu_lib):
+    """Sequences that hold nothing, and so need no page."""
+    ta = gpu_lib
+    for cache in (torch.bfloat16, torch.int8):
+        c = ta.kv_cache(2, 2, 16, 64, cache)
+        pages, none = int32([]).view(2, 0), int32([0, 0])
+        for T in (1, 40):
+            q = torch.zeros(2, 8, T, 64, device="cuda", dtype=torch.bfloat16)
+            o = torch.full_like(q, 3.0)
+            ta.attn_cache_fwd(q, c, pages, none, none, o=o)
+            assert (o == 3).all()
+            ta.attn_cache_fwd(q, c, pages, none, int32([1, 1]), o=o)
+            assert ta.sync_status() == "TA_ERR_INDEX" and (o == 3).all()
+        k, _ = ta.cache_read(c, pages, none, 5)
+        assert (k == 0).all() and ta.sync_status() == "TA_OK"

@@ -550,7 +550,8 @@ def cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens, stream=None):
 
 def attn_cache_workspace_bytes(B, Hq, Hkv, T, N, D, dtype=torch.bfloat16, cache_dtype=None) -> int:
     """Bytes of workspace attn_cache_fwd needs for sequences of at most N
-    tokens (N = max_pages * page_size covers every length)."""
+    tokens (N = max_pages * page_size covers every length; N does not change
+    them now)."""
     ct = _CT[dtype if cache_dtype is None else cache_dtype]
     return int(load().attn_cache_workspace_bytes(B, Hq, Hkv, T, min(int(N), 2 ** 31 - 1), D, _DT[dtype], ct))
 

@@ -1101,7 +1101,7 @@ ta_status attn_cache_keep(const ta_kv_cache* cache, const int* pages, int max_pa
 }
 
 size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, ta_dtype dt, ta_dtype ct) {
-  if (B <= 0 || T <= 0 || N <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
+  if (B <= 0 || T <= 0 || N < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
       cache_dtype_status(dt, ct) != TA_OK)
     return 0;
   return attn_cache_bytes(Hq / Hkv, T, D, ct);
