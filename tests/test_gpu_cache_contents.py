@@ -235,6 +235,31 @@ def test_negative_value_scales_are_no_numbers(gpu_lib, cache, T, G):
         assert torch.equal(o2[:, :, ~own], o[:, :, ~own]) and torch.equal(lse2[:, :, ~own], lse[:, :, ~own]), x
 
 
+# ------------------------------------------------------------ batches, streams
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("e4m3", "bf16"), ("int8", "f16")])
+@pytest.mark.parametrize("T,G", [(1, 4), (5, 4), (40, 4)])
+def test_a_sequence_alone_and_in_a_batch(gpu_lib, cache, dtype, T, G):
+    """Other sequences beside it move a result by rounding only (its keys are
+    cut at other places, short tables go to another form of the kernel)."""
+    ta = gpu_lib
+    kv = [900, T + 20, 411, T] + [64 + 9 * i for i in range(40)]
+    st = Setup(ta, kv, 2, 16, 64, dtype, cache, 3)
+    q = values(3, (len(kv), 2 * G, T, 64), dtype)
+    o, lse = attend(ta, st, q)
+    for b in (0, 1, 2, 3, 43):
+        need = (kv[b] + 15) // 16
+        o1, l1 = ta.attn_cache_fwd(q[b:b + 1].cuda(), st.cache, st.pages[b:b + 1, :need].contiguous(), int32([kv[b]]))
+        assert ta.sync_status() == "TA_OK"
+        for h in range(2):
+            _, _, bO, bL = attention_reference(q[b, h * G:(h + 1) * G], st.rows["k"][b][h], st.rows["v"][b][h], None, cache,
+                                               dtype, None if st.scale["v"] is None else np.array(
+                                                   [st.scale["v"][pg, h, r] for pg, r in
+                                                    (place(st, b, i) for i in range(kv[b]))], dtype=np.float64), rows=1)
+            part = slice(h * G, (h + 1) * G)
+            assert (np.abs(to_np(o[b, part]) - to_np(o1[0, part])) <= 2 * bO).all()
+            assert (np.abs(to_np(lse[b, part]) - to_np(l1[0, part])) <= 2 * bL).all()
+
+
 def test_outputs_made_for_another_stream(gpu_lib):
     """A call on another stream makes its outputs and workspace out of that
     stream's memory: memory that the current stream has freed may still be
