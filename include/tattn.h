@@ -329,7 +329,8 @@ size_t attn_cache_workspace_bytes(int B, int Hq, int Hkv, int T, int N, int D, t
  * ws: >= attn_cache_workspace_bytes(...) bytes, 16-byte aligned, contents need
  * not be initialised; calls that may run at the same time need one each.
  * Scores, softmax sums and accumulators are fp32.  16-bit caches: weights are
- * rounded to dt for the product with V.  8-bit caches: products in fp16 on the
+ * rounded to dt for the product with V, and a row whose scores pass 2^31 (fp16:
+ * 2^27) in magnitude may not be finite, as in attn_fwd.  8-bit caches: products in fp16 on the
  * bare codes (exact), the keys' scales applied to the scores in fp32, the values' in
  * the weights' exponents, so that the fp16 weights are rounded relative to the
  * row's largest contribution; each bf16 query row is scaled by a power of two
