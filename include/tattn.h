@@ -249,8 +249,10 @@ ta_status attn_merge_bwd(const void* o1, const float* lse1, const void* o2, cons
  * type), TA_E4M3 or TA_I8.  The 8-bit types have k_scale and v_scale,
  * [num_pages, Hkv, page_size] fp32: a cached row stands for code * scale.  Scales
  * are as attn_cache_append writes them, 2^-60 or more, or NaN; of others
- * attn_cache_fwd takes a v_scale from 0 to 2^-60 as 2^-60 and a negative one as NaN.  All
- * four are 16-byte aligned.  Any page_size >= 1 (multiples of 8 are the fast ones); num_pages * Hkv * page_size < 2^31; D in {16, 32, 64, 128}.
+ * attn_cache_fwd takes a v_scale from 0 to 2^-60 as 2^-60 and a negative one as
+ * NaN.  All four are 16-byte aligned.  Any page_size >= 1 (where it is no multiple
+ * of 8, a prompt's chunk or a large tree takes several times as long);
+ * num_pages * Hkv * page_size < 2^31; D in {16, 32, 64, 128}.
  *
  * A sequence's tokens are found through three device arrays that every call
  * takes:

@@ -695,11 +695,14 @@ static int page_box_rows(int page) { return page % 32 == 0 ? 32 : page % 16 == 0
 
 // Query rows per key head up to which attn_cache (exact tiles of 16 rows) is
 // used; beyond, the tcgen05 kernel, whose tile has 128 rows.  Measured on 16
-// sequences of 8192 tokens, 8 key heads, pages of 32; attn_cache / tcgen05 us:
+// sequences of 8192 tokens, 8 key heads, pages of 32, replayed; attn_cache / tcgen05 us:
 //           bf16: 24 rows    32         48         64      int8: 32         48         64
-//   D 128:  110 / 116   110 / 116  188 / 116  190 / 116   106 / 138  171 / 139  173 / 138
-//   D  64:   65 / 73     67 / 73    79 / 74   108 / 75     61 / 108   81 / 108  118 / 108
-//   D  32:   44 / 69     46 / 69    60 / 71    71 / 69     52 / 104   65 / 104   77 / 104
+//   D 128:   97 / 106    97 / 107  175 / 107  177 / 107    85 / 122  150 / 122  152 / 122
+//   D  64:   54 / 63     55 / 63    66 / 64   109 / 63     56 / 100   72 / 101  123 / 101
+//   D  32:   38 / 57     40 / 58    48 / 58    57 / 58     43 / 96    53 / 97    64 / 96
+// Page sizes that are no multiple of 8 have no TMA box and go to attn_cache at
+// any number of rows: the bf16 chunk of 2048 over 16384, 32 / 8 heads of 128, takes 2409
+// us through pages of 20 and 375 through pages of 64.
 static bool attn_cache_few_rows(int D, bool bits8, long long rows) {
   if (D > 64) return rows <= 32;
   if (D > 32) return rows <= (bits8 ? 48 : 32);
