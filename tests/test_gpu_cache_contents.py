@@ -213,6 +213,21 @@ def test_one_large_query_beside_ordinary_ones(gpu_lib, cache, T, G, size):
     compare(st, q, o, lse)
 
 
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 118, 2.0 ** 124.5, 2.0 ** -40, 2.0 ** -50])
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (40, 4), (70, 2)])
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_large_keys_and_small_queries(gpu_lib, cache, T, G, size):
+    """Keys and queries far outside fp16's range whose scores are ordinary."""
+    ta = gpu_lib
+    D, n = 128, 300
+    st = blank(ta, n, 1, D, "bf16", cache)
+    put(ta, st, 0, values(11, (1, n, D), "bf16") * size, values(12, (1, n, D), "bf16"))
+    q = values(3, (1, G, T, D), "bf16") * (1 / size)
+    o, lse = attend(ta, st, q)
+    assert ta.sync_status() == "TA_OK"
+    compare(st, q, o, lse)
+
+
 @pytest.mark.parametrize("T,G", [(4, 4), (40, 4)])
 @pytest.mark.parametrize("cache", ["e4m3", "int8"])
 def test_negative_value_scales_are_no_numbers(gpu_lib, cache, T, G):

@@ -757,8 +757,9 @@ __global__ void __launch_bounds__(TcCfg<CT, DP>::THREADS, 1)
             for (int j = 0; j < XC; j += 4) {
               const float4 kx = lds_f4(scales + (c0 + j) * 4), vx = lds_f4(scales + 512 + (c0 + j) * 4);
               const float2 f2 = make_float2(row_f, row_f);
-              const float2 p = ffma2(fmul2(make_float2(y[j], y[j + 1]), make_float2(kx.x, kx.y)), f2, make_float2(vx.x, vx.y));
-              const float2 q = ffma2(fmul2(make_float2(y[j + 2], y[j + 3]), make_float2(kx.z, kx.w)), f2, make_float2(vx.z, vx.w));
+              // (the two factors first: a large key's with a small query's)
+              const float2 p = ffma2(make_float2(y[j], y[j + 1]), fmul2(make_float2(kx.x, kx.y), f2), make_float2(vx.x, vx.y));
+              const float2 q = ffma2(make_float2(y[j + 2], y[j + 3]), fmul2(make_float2(kx.z, kx.w), f2), make_float2(vx.z, vx.w));
               y[j] = p.x, y[j + 1] = p.y, y[j + 2] = q.x, y[j + 3] = q.y;
             }
           }
