@@ -343,6 +343,152 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
                          const int64_t* tree_strides, void* o, const int64_t* o_strides, float* lse, void* ws,
                          size_t ws_bytes, int B, int Hq, int T, ta_dtype dt, float sm_scale, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A step's pages and slots (no counterpart on the pages): from the requests'
+ * lengths, on the device, what the step's other calls take.
+ *
+ * Request b holds kv_lens[b] tokens in the pages of its row of `pages` [B, max_pages]
+ * and gets new_lens[b] more (0: none; -1: it has ended, and its pages become
+ * free).  free_ids [num_pages] is a stack of free page ids with *free_count
+ * entries; the pages are 0 .. num_pages - 1.
+ *  - Ended requests' pages go on top of the stack, in the order of b and of
+ *    their positions.
+ *  - Requests in the order of b ask for the pages that their new tokens need beyond
+ *    those they hold, and for rows of the step's `total` tokens.  A request is
+ *    served if both fit behind what every request before it asked for (one
+ *    that needs no new page is not held up by the pages).  A served request's
+ *    pages are popped one by one and written to its row; others' rows stay.
+ *  - kv_out[b]: the tokens it holds then (0 for an ended one); q_lens[b]: new tokens,
+ *    0 where it is not served; cu_seqlens [B + 1]: their exclusive sums;
+ *    *count_out: entries of the stack that are left.
+ *  - Row i of the step's tokens, [cu_seqlens[b], cu_seqlens[b + 1]): positions[i]
+ *    in its request, slots[i] = page * page_size + row in the page.  Rows behind the last
+ *    one get position 0 and slot -1.
+ * Inputs but pages and free_ids are only read: calls repeated on them give the same.
+ * Lengths that cannot be (negative, past the page table) make a request idle, page
+ * ids outside the cache give slot -1, a count outside [0, num_pages] is 0: each makes
+ * the next ta_sync_status return TA_ERR_INDEX.  A page that several rows hold
+ * must not be in the row of a request that ends.  Arrays that are written must
+ * not overlap others (TA_ERR_INVALID_ARG).  num_pages * page_size < 2^31. */
+ta_status attn_cache_assign(int* pages, int max_pages, const int* kv_lens, const int* new_lens, int* free_ids,
+                            int num_pages, const int* free_count, int page_size, int* kv_out, int* q_lens,
+                            int* cu_seqlens, int* positions, int* slots, int* count_out, int B, int total, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions (no counterpart on the pages).  Of a row x of D elements the first
+ * `dim` (even) are rotated, the rest passes through: with a_i the position times
+ * the angle of pair i < dim / 2 and elements j, l of the pair (i and i + dim / 2;
+ * interleaved: 2 i and 2 i + 1),
+ *   y_j = scale (x_j cos a_i - x_l sin a_i),  y_l = scale (x_l cos a_i + x_j sin a_i).
+ * turns[i] (device) is that angle as a fraction of a whole turn in units of 2^-64,
+ * rounded: the fraction of a turn that position * angle leaves is exact in them, so far
+ * positions lose nothing.
+ *
+ * ta_rows: rows [B, heads, T, D] of 16-bit elements with element strides (b, head,
+ * t); D contiguous, rows 16-byte aligned.  positions[b * pos_b + t * pos_t] int32.
+ * Computed in fp32, rounded once.  dt TA_F16 or TA_BF16; D in {16, 32, 64, 128};
+ * Hq or Hkv may be 0.  An output may be its input (same strides), and overlaps
+ * nothing else.  Calls allocate nothing and may be captured. */
+typedef struct {
+  void* p;
+  int64_t sb, sh, st;
+} ta_rows;
+
+typedef struct {
+  ta_rows q, k, v;      /* inputs: Hq, Hkv, Hkv heads (v: attn_rotary_append) */
+  ta_rows dq, dk;       /* attn_qk_norm_rotary_bwd: gradients of the outputs */
+  ta_rows q_out, k_out; /* outputs (k_out: not attn_rotary_append) */
+  const int* positions;
+  int64_t pos_b, pos_t;
+  const int* slots; /* attn_rotary_append: [B, T] */
+  const uint64_t* turns;
+  const void *q_weight, *k_weight; /* [D] of type wt: dt or TA_F32 */
+  float *dq_weight, *dk_weight;    /* attn_qk_norm_rotary_bwd: [D] */
+  void* ws;
+  size_t ws_bytes;
+  int dim, interleaved;
+  float scale, eps;
+  int B, T, Hq, Hkv, D;
+  ta_dtype dt, wt;
+} ta_rotary_call;
+
+/* q_out, k_out = the rows of q, k rotated.  Of the backward, q and k are the
+ * gradients of the outputs and q_out, k_out those of the inputs (the rotation by the
+ * negative angle, times scale). */
+ta_status attn_rotary_fwd(const ta_rotary_call* call, void* stream);
+ta_status attn_rotary_bwd(const ta_rotary_call* call, void* stream);
+
+/* A norm of each row, then the rotation: x = u w / sqrt(mean u^2 + eps) elementwise,
+ * w = q_weight or k_weight, eps >= 0. */
+ta_status attn_qk_norm_rotary_fwd(const ta_rotary_call* call, void* stream);
+
+/* Its backward.  q, k: the forward's inputs; dq, dk: gradients of its outputs.  Out:
+ * q_out, k_out (gradients of the inputs) and dq_weight, dk_weight (fp32, summed
+ * over all rows in fp32, in an order that the sizes fix).  ws: >=
+ * attn_qk_norm_rotary_bwd_workspace_bytes(D) bytes, 16-byte aligned, contents need
+ * not be initialised; calls that may run at the same time need one each. */
+size_t attn_qk_norm_rotary_bwd_workspace_bytes(int D);
+ta_status attn_qk_norm_rotary_bwd(const ta_rotary_call* call, void* stream);
+
+/* A step's new tokens on their way into a cache: q_out = q rotated (and normed
+ * before, where the weights are given), and keys, rotated (and normed) likewise,
+ * and values v written to row slots[b * T + t] of the cache (page slot / page_size,
+ * row slot % page_size), as attn_cache_append writes rows; 8-bit codes and scales are made
+ * of the rotated keys before any rounding to 16 bits.  A negative slot writes
+ * nothing (q_out is written all the same); one past the cache does so too and
+ * makes the next ta_sync_status return TA_ERR_INDEX.  Two tokens of one call must
+ * not share a slot. */
+ta_status attn_rotary_append(const ta_kv_cache* cache, const ta_rotary_call* call, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of packed sequences with shared key heads (no counterpart on the
+ * pages; the definitions are those of attn_fwd).  Queries are rows of [total_q, Hq,
+ * D], keys and values of [total_k, Hkv, D] (ta_rows with sb unused; strides above
+ * zero); sequence b has query rows cu_q[b] .. cu_q[b + 1] - 1 and key rows cu_k[b] ..
+ * cu_k[b + 1] - 1 (device arrays [B + 1]; cu_k may be cu_q).  Query head h reads
+ * key head h / (Hq / Hkv), Hq / Hkv <= 128.  Causal: query i of a sequence sees its keys
+ * j <= i + n_k - n_q.  Rows that see nothing get O = 0, L = -inf; rows that belong to
+ * no sequence are not read, and not written in outputs.  lse is [total_q, Hq]
+ * fp32.  dt TA_F16 or TA_BF16; D in {16, 32, 64, 128}.  Nothing is allocated,
+ * and calls may be captured.
+ *
+ * A plan lists the tiles of the sequences; it serves every call on the
+ * same offsets, sizes and heads (every layer, forward and backward), and is
+ * made on the device (a captured plan follows new offsets at replay).  Offsets
+ * that decrease or leave the tensors give an empty plan, and a plan of other sizes
+ * stops a call; both make the next ta_sync_status return TA_ERR_INDEX. */
+size_t attn_packed_plan_bytes(int B, int total_q, int total_k, int Hq, int Hkv);
+ta_status attn_packed_plan(const int* cu_q, const int* cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int causal,
+                           void* plan, size_t plan_bytes, void* stream);
+
+typedef struct {
+  ta_rows q, k, v, o;      /* o: output of the forward, input of the backward */
+  ta_rows dO, dq, dk, dv;  /* backward: the gradient of o; outputs */
+  const void* plan;        /* 16-byte aligned */
+  size_t plan_bytes;
+  float* lse;              /* output of the forward, input of the backward */
+  void* ws;                /* backward */
+  size_t ws_bytes;
+  int B, total_q, total_k, Hq, Hkv, D;
+  ta_dtype dt;
+  float sm_scale;          /* <= 0 or not finite: 1 / sqrt(D) */
+} ta_packed_call;
+
+/* Scores, softmax sums and accumulators are fp32, weights rounded to dt for the
+ * product with V.  Infinities and NaN reach the rows of their own sequence that
+ * see them, and no other row (an infinite value as NaN where the row's weight
+ * for it rounds to zero). */
+ta_status attn_packed_fwd(const ta_packed_call* call, void* stream);
+
+/* Gradients of <dO, O>; dk, dv are summed over the query heads of a key head in
+ * fp32, in a fixed order.  Keys that no query sees get zeros.  Infinities or
+ * NaN among a sequence's rows make its gradients unspecified, and no other
+ * sequence's.  ws: >= attn_packed_bwd_workspace_bytes(...) bytes, 16-byte aligned,
+ * contents need not be initialised; calls that may run at the same time need one
+ * each. */
+size_t attn_packed_bwd_workspace_bytes(int total_q, int Hq);
+ta_status attn_packed_bwd(const ta_packed_call* call, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word that
  * the kernels set when a bounded wait runs out or an index leaves the cache.
  * TA_OK, TA_ERR_TIMEOUT, TA_ERR_INDEX or

@@ -66,6 +66,10 @@ Definitions, and the page passages they follow:
   ones, token i sees every position before them and new token j where
   ``tree[i, j]`` (without a tree ``j <= i``); query head h reads key head
   ``h // (Hq // Hkv)``; softmax, L and empty rows as above.
+* Rotary positions, head norms, a step's pages and packed sequences (no counterpart
+  on the pages): ``rotary``, ``head_norm``, ``head_norm_bwd``, ``assign_pages`` and
+  ``packed_attention`` (each sequence and head as above, dK and dV summed over the
+  query heads of a key head).
 
 Every function here is pinned by the ``-m "not gpu"`` oracle tests (finite
 differences, closed forms, invariants, special cases); none is unpinned.
@@ -82,6 +86,7 @@ __all__ = [
     "attention_jvp_tl", "attention_jvp_tl_bhsd", "attention_jvp_bwd", "attention_jvp_bwd_bhsd",
     "bwd_delta", "bwd_delta_bhsd",
     "e4m3_grid", "cache_quantise", "cache_slot", "cache_attention",
+    "rotary", "head_norm", "head_norm_bwd", "assign_pages", "packed_attention",
 ]
 
 
@@ -465,3 +470,93 @@ def cache_attention(q, k, v, tree=None, sm_scale=None):
         for i in range(T):
             O[g, i] = P[i, keep[i]] @ v[keep[i]]
     return O, L
+
+
+# ----------------------------------- rotary positions, head norms, a step's pages
+def rotary(x, positions, inv_freq, interleaved=False, scale=1.0, back=False):
+    """Rows x [T, ..., D] at positions [T] with the first 2 len(inv_freq) elements
+    rotated: as complex numbers, pair i times scale e^(+-i a), a = position inv_freq_i."""
+    (x,) = _f64(x)
+    f = np.asarray(inv_freq, dtype=np.float64)
+    n = len(f)
+    a = np.asarray(positions, dtype=np.float64).reshape(-1, *([1] * (x.ndim - 1))) * f
+    z = scale * np.exp((-1j if back else 1j) * a)
+    y = x.copy()
+    re, im = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    w = (x[..., re] + 1j * x[..., im]) * z
+    y[..., re], y[..., im] = w.real, w.imag
+    return y
+
+
+def head_norm(x, w, eps):
+    """Rows x [..., D] -> x w / sqrt(mean x^2 + eps)."""
+    x, w = _f64(x, w)
+    return x / np.sqrt((x * x).mean(axis=-1, keepdims=True) + eps) * w
+
+
+def head_norm_bwd(x, w, eps, g):
+    """Gradients (dx [..., D], dw [D]) of <g, head_norm(x, w, eps)>."""
+    x, w, g = _f64(x, w, g)
+    D = x.shape[-1]
+    z = np.sqrt((x * x).mean(axis=-1, keepdims=True) + eps)
+    gw = g * w
+    dx = gw / z - x * (gw * x).sum(axis=-1, keepdims=True) / (D * z ** 3)
+    return dx, (g * x / z).reshape(-1, D).sum(axis=0)
+
+
+def assign_pages(pages, kv_lens, new_lens, free, count, page, total):
+    """A step's pages request by request: ended ones (-1) give theirs back first;
+    then each in turn takes what it asks for if that and everything asked for
+    before it fits.  Lists in, (pages, free, kv, q, cu, positions, slots, count) out."""
+    pages, free = [list(r) for r in pages], list(free)
+    B, held = len(kv_lens), lambda n: -(-n // page)
+    stack = free[:count]
+    for b in range(B):
+        if new_lens[b] == -1:
+            stack += pages[b][:held(kv_lens[b])]
+    free[:len(stack)] = stack
+    size, want, rows = len(stack), 0, 0
+    kv, q, pos, slot = [], [], [], []
+    for b in range(B):
+        n = max(new_lens[b], 0)
+        need = held(kv_lens[b] + n) - held(kv_lens[b]) if n else 0
+        want, rows = want + need, rows + n
+        if (need and want > size) or (n and rows > total):
+            n = need = 0
+        for i in range(need):
+            pages[b][held(kv_lens[b]) + i] = stack.pop()
+        for i in range(kv_lens[b], kv_lens[b] + n):
+            pos.append(i)
+            slot.append(pages[b][i // page] * page + i % page)
+        kv.append(0 if new_lens[b] == -1 else kv_lens[b] + n)
+        q.append(n)
+    cu = [0]
+    for n in q:
+        cu.append(cu[-1] + n)
+    rest = total - cu[-1]
+    return pages, free, kv, q, cu, pos + [0] * rest, slot + [-1] * rest, len(stack)
+
+
+def packed_attention(q, k, v, cu_q, cu_k, causal=True, sm_scale=None, do=None):
+    """Sequences packed one behind the other: q [Tq, Hq, D], k, v [Tk, Hkv, D] ->
+    (O, L [Tq, Hq]) and with do also (dQ, dK, dV); rows of no sequence are zeros."""
+    q, k, v = _f64(q, k, v)
+    Hq, G = q.shape[1], q.shape[1] // k.shape[1]
+    O, L = np.zeros_like(q), np.zeros(q.shape[:2])
+    grads = (np.zeros_like(q), np.zeros_like(k), np.zeros_like(v))
+    for b in range(len(cu_q) - 1):
+        s, t = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        if s.start == s.stop:
+            continue
+        if t.start == t.stop:
+            L[s] = -np.inf
+            continue
+        for h in range(Hq):
+            x = (q[s, h], k[t, h // G], v[t, h // G])
+            O[s, h], L[s, h] = attention_fwd(*x, causal, sm_scale)
+            if do is not None:
+                dq, dk, dv = attention_bwd(*x, _f64(do)[0][s, h], causal, sm_scale)
+                grads[0][s, h] = dq
+                grads[1][t, h // G] += dk
+                grads[2][t, h // G] += dv
+    return (O, L) if do is None else (O, L, *grads)

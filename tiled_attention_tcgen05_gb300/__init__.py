@@ -19,20 +19,36 @@ Entry points (same names as the C ABI):
   cache_read(cache, pages, kv_lens, N)                -> (k, v)
   cache_keep(cache, pages, kv_lens, q_lens, keep, keep_lens) -> new kv_lens
   attn_cache_fwd(q, cache, pages, kv_lens, q_lens, tree, sm_scale) -> (o, lse)
-Except for the cache's calls (below), tensors are contiguous [B, H, S, D] float16/bfloat16 CUDA tensors; lse is
-float32 [B, H, M].  sm_scale None means 1/sqrt(D).
+  cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total)
+                                                     -> Assigned: lengths, offsets, positions, slots of a step
+  rotary_fwd(q, k, positions, rotary) / rotary_bwd   -> (q, k) rotated / their gradients
+  qk_norm_rotary_fwd(q, k, q_weight, k_weight, positions, rotary, eps) -> (q, k)
+  qk_norm_rotary_bwd(dq, dk, q, k, q_weight, k_weight, positions, rotary, eps)
+                                                     -> (dq, dk, dq_weight, dk_weight)
+  rotary_append(cache, q, k, v, positions, slots, rotary) -> q; keys and values into the cache
+  packed_plan(cu_seqlens, total, Hq, Hkv, causal)    -> PackedPlan of sequences packed one behind the other
+  attn_packed_fwd(q, k, v, plan, sm_scale)           -> (o, lse)
+  attn_packed_bwd(q, k, v, o, lse, do, plan, sm_scale) -> (dq, dk, dv)
+Except for the calls from cache_append on (below), tensors are contiguous [B, H, S, D] float16/bfloat16 CUDA tensors;
+lse is float32 [B, H, M].  sm_scale None means 1/sqrt(D).
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import decimal
+import math
 import os
+import struct
 
 import torch
 
 __all__ = ["load", "lib_path", "attn_fwd", "attn_bwd", "attn_bwd_fused", "attn_fwd_jvp", "attn_bwd_jvp", "piecewise_fwd", "piecewise_bwd", "merge_fwd", "merge_bwd", "attn_fwd_fp8",
            "attn_bwd_workspace_bytes", "attn_bwd_fused_workspace_bytes", "sync_status", "selftest_wait_timeout", "profile_enable",
            "profile_read", "set_wait_timeout_ms", "fwd_kv_split", "set_fwd_kv_split", "KVCache", "kv_cache", "cache_append", "cache_read", "cache_keep", "attn_cache_fwd",
-           "attn_cache_workspace_bytes", "TAError", "STATUS"]
+           "attn_cache_workspace_bytes", "Assigned", "cache_assign", "Rotary", "rotary_fwd", "rotary_bwd", "qk_norm_rotary_fwd", "qk_norm_rotary_bwd",
+           "rotary_append", "PackedPlan", "packed_plan", "attn_packed_fwd", "attn_packed_bwd", "attn_packed_bwd_workspace_bytes",
+           "TAError", "STATUS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libtattn.so")
@@ -67,6 +83,18 @@ _SIGS = {
     "attn_cache_keep": ([_vp] * 2 + [_i] + [_vp] * 5 + [_i] * 2 + [_vp], _i),
     "attn_cache_workspace_bytes": ([_i] * 8, _sz),
     "attn_cache_fwd": ([_vp] * 4 + [_i] + [_vp] * 8 + [_sz] + [_i] * 4 + [_f, _vp], _i),
+    "attn_cache_assign": ([_vp, _i] + [_vp] * 3 + [_i, _vp, _i] + [_vp] * 6 + [_i] * 2 + [_vp], _i),
+    "attn_rotary_fwd": ([_vp] * 2, _i),
+    "attn_rotary_bwd": ([_vp] * 2, _i),
+    "attn_qk_norm_rotary_fwd": ([_vp] * 2, _i),
+    "attn_qk_norm_rotary_bwd_workspace_bytes": ([_i], _sz),
+    "attn_qk_norm_rotary_bwd": ([_vp] * 2, _i),
+    "attn_rotary_append": ([_vp] * 3, _i),
+    "attn_packed_plan_bytes": ([_i] * 5, _sz),
+    "attn_packed_plan": ([_vp] * 2 + [_i] * 6 + [_vp, _sz, _vp], _i),
+    "attn_packed_fwd": ([_vp] * 2, _i),
+    "attn_packed_bwd_workspace_bytes": ([_i] * 2, _sz),
+    "attn_packed_bwd": ([_vp] * 2, _i),
     "ta_sync_status": ([_vp], _i),
     "ta_status_str": ([_i], ctypes.c_char_p),
     "ta_selftest_wait_timeout": ([_i, _vp], _i),
@@ -605,6 +633,432 @@ def attn_cache_fwd(q, cache, pages, kv_lens, q_lens=None, tree=None, sm_scale=No
         ws.numel() * ws.element_size(), B, Hq, T, _DT[dtype], -1.0 if sm_scale is None else float(sm_scale),
         _raw_stream(index, stream)))
     return o, lse
+
+
+# ------------------------------------------------- a step's pages and slots
+def _on(index):
+    """None, or a context that makes CUDA device `index` current."""
+    if index is None or index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+Assigned = collections.namedtuple("Assigned", "kv_lens q_lens cu_seqlens positions slots free_count")
+
+
+def cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, stream=None) -> Assigned:
+    """A step's pages, slots and positions from the requests' lengths, on the GPU.
+
+    pages int32 [B, max_pages]: the requests' page table, written to; kv_lens [B]:
+    tokens they hold; new_lens [B]: tokens to add, 0: none, -1: the request has
+    ended and its pages become free.  free int32 [num_pages]: a stack of free page
+    ids, written to, with free_count [1] entries; total: rows of the step's tokens.
+
+    Requests are served in order as long as pages and rows last (one that needs no
+    new page is not held up by the pages); the others get no token.  Returns, int32:
+    kv_lens [B] (then), q_lens [B] (new tokens), cu_seqlens [B + 1] (their exclusive
+    sums), positions [total] and slots [total] (page * page_size + row; -1 behind the
+    last token) and free_count [1].  Impossible lengths and page ids make the next
+    sync_status() return TA_ERR_INDEX."""
+    index = pages.get_device()
+    there = _on(index)
+    if there is not None:
+        with there:
+            return cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, stream)
+    lib = load()
+    if pages.dim() != 2 or free.dim() != 1:
+        raise ValueError("pages must be [B, max_pages] and free [num_pages]")
+    B, max_pages = pages.shape
+    total = int(total)
+    if total < 0:
+        raise ValueError("total must not be negative")
+    _i32("pages", pages, pages.shape, index)
+    _i32("kv_lens", kv_lens, (B,), index)
+    _i32("new_lens", new_lens, (B,), index)
+    _i32("free", free, free.shape, index)
+    _i32("free_count", free_count, (1,), index)
+    out = Assigned(*_empty((3 * B + 2 + 2 * total,), torch.int32, index, stream).split([B, B, B + 1, total, total, 1]))
+    kv, ql, cu, pos, slot, count = (x.data_ptr() for x in out)
+    _check("attn_cache_assign", lib.attn_cache_assign(
+        pages.data_ptr(), max_pages, kv_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), free.shape[0],
+        free_count.data_ptr(), int(page_size), kv, ql, cu, pos, slot, count, B, total, _raw_stream(index, stream)))
+    return out
+
+
+# --------------------------------------------------------- rotary positions
+_TWO_PI = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510")
+
+
+class Rotary:
+    """Rotary positions of the first `dim` elements of a head: pair i turns by
+    position * base ** (-2 i / dim).  Pairs are (i, i + dim / 2), or (2 i, 2 i + 1)
+    with interleaved=True.
+
+    scaling stretches them to longer contexts:
+      "linear": all angles / factor;
+      "ntk": base * factor ** (dim / (dim - 2));
+      "yarn": pairs that turn more than beta[0] times in the first first_len positions
+              keep their angle, those that turn less than beta[1] times get angle / factor,
+              a linear ramp between; rotated elements times 0.1 ln(factor) + 1.
+    inv_freq: the angles themselves instead (dim / 2 numbers); scale: the factor of the rotated
+    elements, instead of the scaling's.  Angles are held as 64-bit fractions of a turn, so that far
+    positions are as exact as near ones.  Holds a tensor on `device`."""
+
+    __slots__ = ("dim", "interleaved", "scale", "inv_freq", "turns", "device", "_index", "_ptr")
+
+    def __init__(self, dim, base=10000.0, interleaved=False, scaling=None, factor=1.0, first_len=None, beta=(32.0, 1.0),
+                 inv_freq=None, scale=None, device="cuda"):
+        dim = int(dim)
+        if dim < 0 or dim % 2 or dim > 128:
+            raise ValueError("dim must be even, 0 to 128")
+        if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+            raise ValueError("base and factor must be positive numbers")
+        base, factor, by = float(base), float(factor), 1.0
+        if inv_freq is not None:
+            f = [float(x) for x in inv_freq]
+            if scaling is not None or len(f) != dim // 2 or not all(math.isfinite(x) for x in f):
+                raise ValueError(f"inv_freq must be {dim // 2} finite numbers, without a scaling")
+        else:
+            b = base
+            if scaling == "ntk" and dim > 2:
+                b = base * factor ** (dim / (dim - 2.0))
+            f = [b ** (-i / dim) for i in range(0, dim, 2)]
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "yarn":
+            if not first_len or first_len <= 0 or base == 1.0:
+                raise ValueError("yarn scaling needs first_len, the length before scaling, and base != 1")
+            lo, hi = (dim * math.log(first_len / (x * 2 * math.pi)) / (2 * math.log(base)) for x in beta)
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), dim - 1)
+            ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(dim // 2)]
+            f = [x / factor * r + x * (1 - r) for x, r in zip(f, ramp)]
+            by = 0.1 * math.log(factor) + 1.0
+        elif scaling not in (None, "none", "ntk"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        self.dim, self.interleaved = dim, bool(interleaved)
+        self.scale = float(by if scale is None else scale)
+        if not math.isfinite(self.scale):
+            raise ValueError("scale must be finite")
+        self.inv_freq = tuple(f)
+        with decimal.localcontext() as c:
+            c.prec = 60
+            turns = [int((decimal.Decimal(x) / _TWO_PI * 2 ** 64).to_integral_value()) % 2 ** 64 for x in f]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns] or [0], dtype=torch.int64,
+                                  device=device)
+        self.device, self._index, self._ptr = self.turns.device, self.turns.get_device(), self.turns.data_ptr()
+
+
+# ta_rotary_call of include/tattn.h, in its order
+_ROT = struct.Struct("@28q3q2q2q2q2q2i2f7i0q")
+_NONE = (0, 0, 0, 0)
+
+
+def _rows_arg(t):
+    """(pointer, strides b, head, t) of checked rows [tokens, heads, D] or [B, heads, T, D]."""
+    st = t.stride()
+    return (t.data_ptr(), 0, st[1], st[0]) if len(st) == 3 else (t.data_ptr(), st[0], st[1], st[2])
+
+
+def _rot_rows(name, t, lead, dtype, index, written=False):
+    """Checks q, k or the like, whose tokens are those of `lead` (3-D or 4-D)."""
+    if t.dim() != lead.dim():
+        raise ValueError(f"{name} must have {lead.dim()} dimensions")
+    a, b = t.shape, lead.shape
+    if a[-1] != b[-1] or a[0] != b[0] or (len(a) == 4 and a[2] != b[2]):
+        raise ValueError(f"{name} has shape {tuple(a)}, tokens and D of {tuple(b)} expected")
+    _dense_rows(name, t, dtype, index, written)
+    return _rows_arg(t)
+
+
+def _dense_rows(name, t, dtype, index, written=False):
+    """Checks dtype, device and contiguous rows; outputs must not overlap themselves."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on CUDA device {index}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if written and not t.is_contiguous():
+        end = 1
+        for step, n in sorted((x, n) for x, n in zip(st, t.shape) if n > 1):
+            if step < end:
+                raise ValueError(f"{name} overlaps itself")
+            end = step * (n - 1) + end
+
+
+def _token_ints(name, t, lead, index):
+    """Checks positions or slots of the tokens of `lead`; returns strides (b, t)."""
+    if t.dtype is not torch.int32 or t.get_device() != index:
+        raise ValueError(f"{name} must be an int32 tensor on CUDA device {index}")
+    if lead.dim() == 3:
+        if t.shape != lead.shape[:1]:
+            raise ValueError(f"{name} must be [{lead.shape[0]}]")
+        return 0, t.stride(0)
+    B, T = lead.shape[0], lead.shape[2]
+    if t.shape == (B, T):
+        return t.stride()
+    if t.shape == (T,):
+        return 0, t.stride(0)
+    raise ValueError(f"{name} must be [{B}, {T}] or [{T}]")
+
+
+def _rot_call(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, eps, outs, stream):
+    """Checks and runs one of the rotary calls; q (or k, where there is no q)
+    says which tokens there are.  Returns the outputs."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("neither q nor k is given")
+    index, dtype = lead.get_device(), lead.dtype
+    lib = load()
+    if lead.dim() not in (3, 4) or dtype not in _T16:
+        raise ValueError("q and k must be [tokens, heads, D] or [B, heads, T, D] tensors of float16 or bfloat16")
+    if not isinstance(rotary, Rotary) or rotary._index != index:
+        raise ValueError(f"rotary must be a Rotary on CUDA device {index}")
+    four = lead.dim() == 4
+    B, T, D = (lead.shape[0], lead.shape[2], lead.shape[3]) if four else (1, lead.shape[0], lead.shape[2])
+    if rotary.dim > D:
+        raise ValueError(f"rotary turns {rotary.dim} elements of rows of {D}")
+    args, heads = [], []
+    for name, t in (("q", q), ("k", k)):
+        args.append(_NONE if t is None else _rot_rows(name, t, lead, dtype, index))
+        heads.append(0 if t is None else t.shape[1])
+    args.append(_NONE if v is None else _rot_rows("v", v, lead, dtype, index))
+    if v is not None and v.shape != k.shape:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+    for name, t, x in (("dq", dq, q), ("dk", dk, k)):
+        if (t is None) != (x is None) and fn == "attn_qk_norm_rotary_bwd":
+            raise ValueError(f"{name} and its input go together")
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+        args.append(_NONE if t is None else _rot_rows(name, t, lead, dtype, index))
+    res = []
+    for name, t, x in (("q_out", outs[0], q), ("k_out", outs[1], k)):
+        if x is None or (cache is not None and name == "k_out"):
+            args.append(_NONE)
+            res.append(None)
+            continue
+        if t is None:
+            t = _empty(x.shape, dtype, index, stream, like=x if four else None)
+        elif t.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+        args.append(_rot_rows(name, t, lead, dtype, index, written=True))
+        res.append(t)
+    pb, pt = _token_ints("positions", positions, lead, index)
+    sp = 0
+    if slots is not None:
+        _token_ints("slots", slots, lead, index)
+        if not slots.is_contiguous() or slots.numel() != B * T:
+            raise ValueError("slots must be contiguous, one for each token")
+        sp = slots.data_ptr()
+    wt, wp, dw, ws, nws = _DT[dtype], [0, 0], (0, 0), 0, 0
+    if weights is not None:
+        for i, (name, w, x) in enumerate((("q_weight", weights[0], q), ("k_weight", weights[1], k))):
+            if x is None:
+                continue
+            if w is None or w.get_device() != index or w.shape != (D,) or not w.is_contiguous() or \
+                    w.dtype not in (dtype, torch.float32):
+                raise ValueError(f"{name} must be a contiguous [{D}] tensor of {dtype} or float32 on CUDA device {index}")
+            if wp[0] and w.dtype != weights[0].dtype:
+                raise ValueError("the weights must have one dtype")
+            wp[i], wt = w.data_ptr(), _DT[w.dtype]
+        if fn == "attn_qk_norm_rotary_bwd":
+            sums = _empty((2, D), torch.float32, index, stream)
+            nws = int(lib.attn_qk_norm_rotary_bwd_workspace_bytes(D))
+            room = _empty((max(nws, 16),), torch.uint8, index, stream)
+            dw, ws = (sums.data_ptr(), sums.data_ptr() + 4 * D), room.data_ptr()
+            res += [sums[0] if q is not None else None, sums[1] if k is not None else None]
+    call = _ROT.pack(*args[0], *args[1], *args[2], *args[3], *args[4], *args[5], *args[6], positions.data_ptr(), pb, pt, sp,
+                     rotary._ptr, *wp, *dw, ws, nws, rotary.dim, rotary.interleaved, rotary.scale, eps, B, T, *heads, D,
+                     _DT[dtype], wt)
+    raw = _raw_stream(index, stream)
+    _check(fn, getattr(lib, fn)(call, raw) if cache is None else lib.attn_rotary_append(cache._ref, call, raw))
+    return res
+
+
+def _rotate(fn, q, k, *rest):
+    lead = q if q is not None else k
+    there = None if lead is None else _on(lead.get_device())
+    if there is not None:
+        with there:
+            return _rot_call(fn, None, q, k, *rest)
+    return _rot_call(fn, None, q, k, *rest)
+
+
+def rotary_fwd(q, k, positions, rotary, q_out=None, k_out=None, stream=None):
+    """Rotates queries and keys: q [tokens, Hq, D], k [tokens, Hkv, D], positions int32 [tokens], or [B, heads,
+    T, D] with positions [B, T] or [T]; any strides with contiguous rows; k (or q) may be None.  q_out, k_out:
+    where to write (the inputs themselves, for instance).  Returns (q, k)."""
+    return tuple(_rotate("attn_rotary_fwd", q, k, None, None, None, positions, None, rotary, None, 0.0, (q_out, k_out),
+                         stream))
+
+
+def rotary_bwd(dq, dk, positions, rotary, dq_out=None, dk_out=None, stream=None):
+    """Gradients of rotary_fwd's inputs from those of its outputs; arguments and layouts as there."""
+    return tuple(_rotate("attn_rotary_bwd", dq, dk, None, None, None, positions, None, rotary, None, 0.0,
+                         (dq_out, dk_out), stream))
+
+
+def qk_norm_rotary_fwd(q, k, q_weight, k_weight, positions, rotary, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """A norm of every head's row, x * weight / sqrt(mean(x ** 2) + eps), then the rotation; weights [D] of q's
+    dtype or float32, layouts as in rotary_fwd.  Returns (q, k)."""
+    return tuple(_rotate("attn_qk_norm_rotary_fwd", q, k, None, None, None, positions, None, rotary,
+                         (q_weight, k_weight), eps, (q_out, k_out), stream))
+
+
+def qk_norm_rotary_bwd(dq, dk, q, k, q_weight, k_weight, positions, rotary, eps=1e-6, dq_out=None, dk_out=None,
+                       stream=None):
+    """Backward of qk_norm_rotary_fwd: q, k are its inputs, dq, dk the gradients of its outputs.  Returns (dq, dk,
+    dq_weight, dk_weight), the weights' in float32."""
+    return tuple(_rotate("attn_qk_norm_rotary_bwd", q, k, None, dq, dk, positions, None, rotary, (q_weight, k_weight),
+                         eps, (dq_out, dk_out), stream))
+
+
+def rotary_append(cache, q, k, v, positions, slots, rotary, q_weight=None, k_weight=None, eps=1e-6, q_out=None,
+                  stream=None):
+    """A step's new tokens on their way into a KVCache: queries and keys normed (where the weights are given) and
+    rotated, keys and values written to the cache's rows `slots` (int32, one a token: page * page_size + row, as
+    cache_assign gives them; a negative one writes nothing).  Layouts as in rotary_fwd.  Returns the queries."""
+    there = _elsewhere(cache)
+    if there is not None:
+        with there:
+            return rotary_append(cache, q, k, v, positions, slots, rotary, q_weight, k_weight, eps, q_out, stream)
+    if q is None or k is None or v is None or slots is None:
+        raise ValueError("q, k, v and slots must be given")
+    if q.get_device() != cache._index:
+        raise ValueError(f"q must be a tensor on CUDA device {cache._index}")
+    weights = None if q_weight is None and k_weight is None else (q_weight, k_weight)
+    return _rot_call("attn_rotary_append", cache, q, k, v, None, None, positions, slots, rotary, weights, eps,
+                     (q_out, None), stream)[0]
+
+
+# ------------------------------------------------- attention of packed sequences
+# ta_packed_call of include/tattn.h, in its order
+_PACKED = struct.Struct("@32q5q7if")
+
+
+class PackedPlan:
+    """What attn_packed_fwd and attn_packed_bwd need to know of the sequences; made by packed_plan, good for every
+    call on the same offsets and heads (every layer, forward and backward)."""
+
+    __slots__ = ("B", "total", "total_k", "Hq", "Hkv", "causal", "device", "_index", "_t", "_ptr", "_bytes")
+
+
+def packed_plan(cu_seqlens, total, Hq, Hkv, causal=True, cu_seqlens_k=None, total_k=None, stream=None) -> PackedPlan:
+    """The plan of sequences packed one behind the other: sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+    (int32 [B + 1], on the GPU) of the `total` rows of q, and of k and v (cu_seqlens_k, total_k: rows of their
+    own).  causal: query i of a sequence sees its keys j <= i + n_k - n_q.  Offsets that decrease or pass total
+    give an empty plan and make the next sync_status() return TA_ERR_INDEX.  The offsets are read when the
+    stream gets there; a later change of theirs needs another plan."""
+    index = cu_seqlens.get_device()
+    there = _on(index)
+    if there is not None:
+        with there:
+            return packed_plan(cu_seqlens, total, Hq, Hkv, causal, cu_seqlens_k, total_k, stream)
+    lib = load()
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    if cu_seqlens_k is None:
+        if total_k is not None and int(total_k) != int(total):
+            raise ValueError("total_k differs from total: cu_seqlens_k is missing")
+        cu_seqlens_k, total_k = cu_seqlens, total
+    elif total_k is None:
+        raise ValueError("cu_seqlens_k needs total_k")
+    n = cu_seqlens.shape[0]
+    _i32("cu_seqlens", cu_seqlens, (n,), index)
+    _i32("cu_seqlens_k", cu_seqlens_k, (n,), index)
+    p = PackedPlan()
+    p.B, p.total, p.total_k, p.Hq, p.Hkv, p.causal = n - 1, int(total), int(total_k), int(Hq), int(Hkv), bool(causal)
+    sizes = (p.B, p.total, p.total_k, p.Hq, p.Hkv)
+    p._bytes = int(lib.attn_packed_plan_bytes(*sizes))
+    p._t = _empty((max(p._bytes, 16),), torch.uint8, index, stream)
+    p._ptr, p._index, p.device = p._t.data_ptr(), index, cu_seqlens.device
+    _check("attn_packed_plan", lib.attn_packed_plan(cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr(), *sizes, int(p.causal),
+                                                    p._ptr, p._bytes, _raw_stream(index, stream)))
+    return p
+
+
+def _packed_rows(name, t, shape, dtype, index, written=False):
+    """Checks a [tokens, heads, D] tensor; returns its ta_rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _dense_rows(name, t, dtype, index, written)
+    st = t.stride()
+    return t.data_ptr(), 0, st[1], st[0]
+
+
+def _packed_sides(q, k, v, plan):
+    """Shapes of the query and the key side."""
+    if not isinstance(plan, PackedPlan):
+        raise ValueError("plan must be a PackedPlan")
+    if q.dim() != 3 or q.dtype not in _T16:
+        raise ValueError("q must be a [tokens, Hq, D] tensor of float16 or bfloat16")
+    return (plan.total, plan.Hq, q.shape[2]), (plan.total_k, plan.Hkv, q.shape[2])
+
+
+def _packed_lse(lse, plan, index):
+    if lse.dtype is not torch.float32 or lse.shape != (plan.total, plan.Hq) or lse.get_device() != index or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 {[plan.total, plan.Hq]} tensor on CUDA device {index}")
+    return lse.data_ptr()
+
+
+def attn_packed_fwd(q, k, v, plan, sm_scale=None, o=None, lse=None, stream=None):
+    """Attention of packed sequences: q [total, Hq, D], k, v [total_k, Hkv, D] (any strides with contiguous rows);
+    query head h reads key head h // (Hq // Hkv).  Returns (o, lse), lse float32 [total, Hq]; rows of given o, lse
+    that belong to no sequence are left as they were."""
+    there = _on(q.get_device())
+    if there is not None:
+        with there:
+            return attn_packed_fwd(q, k, v, plan, sm_scale, o, lse, stream)
+    lib = load()
+    qs, ks = _packed_sides(q, k, v, plan)
+    index, dtype = plan._index, q.dtype
+    rows = _packed_rows("q", q, qs, dtype, index) + _packed_rows("k", k, ks, dtype, index) + \
+        _packed_rows("v", v, ks, dtype, index)
+    if o is None:
+        o = _empty(qs, dtype, index, stream)
+    if lse is None:
+        lse = _empty(qs[:2], torch.float32, index, stream)
+    call = _PACKED.pack(*rows, *_packed_rows("o", o, qs, dtype, index, written=True), *_NONE, *_NONE, *_NONE, *_NONE,
+                        plan._ptr, plan._bytes, _packed_lse(lse, plan, index), 0, 0, plan.B, plan.total, plan.total_k,
+                        plan.Hq, plan.Hkv, qs[2], _DT[dtype], _scale(sm_scale))
+    _check("attn_packed_fwd", lib.attn_packed_fwd(call, _raw_stream(index, stream)))
+    return o, lse
+
+
+def attn_packed_bwd_workspace_bytes(total, Hq) -> int:
+    """Bytes of workspace attn_packed_bwd needs."""
+    return int(load().attn_packed_bwd_workspace_bytes(int(total), int(Hq)))
+
+
+def attn_packed_bwd(q, k, v, o, lse, do, plan, sm_scale=None, dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Backward of attn_packed_fwd for the loss <do, o>: returns (dq, dk, dv) in q's dtype, dk and dv summed over the
+    query heads of a key head.  Rows of given dq, dk, dv that belong to no sequence are left as they were."""
+    there = _on(q.get_device())
+    if there is not None:
+        with there:
+            return attn_packed_bwd(q, k, v, o, lse, do, plan, sm_scale, dq, dk, dv, ws, stream)
+    lib = load()
+    qs, ks = _packed_sides(q, k, v, plan)
+    index, dtype = plan._index, q.dtype
+    rows = ()
+    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs), ("do", do, qs)):
+        rows += _packed_rows(name, t, shape, dtype, index)
+    dq = _empty(qs, dtype, index, stream) if dq is None else dq
+    dk = _empty(ks, dtype, index, stream) if dk is None else dk
+    dv = _empty(ks, dtype, index, stream) if dv is None else dv
+    for name, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
+        rows += _packed_rows(name, t, shape, dtype, index, written=True)
+    if ws is None:
+        ws = _empty((max(16, int(lib.attn_packed_bwd_workspace_bytes(plan.total, plan.Hq))),), torch.uint8, index, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on CUDA device {index}")
+    call = _PACKED.pack(*rows, plan._ptr, plan._bytes, _packed_lse(lse, plan, index), ws.data_ptr(),
+                        ws.numel() * ws.element_size(), plan.B, plan.total, plan.total_k, plan.Hq, plan.Hkv, qs[2],
+                        _DT[dtype], _scale(sm_scale))
+    _check("attn_packed_bwd", lib.attn_packed_bwd(call, _raw_stream(index, stream)))
+    return dq, dk, dv
 
 
 def sync_status(stream=None) -> str:

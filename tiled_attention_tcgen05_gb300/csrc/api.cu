@@ -13,8 +13,11 @@
 #include <vector>
 
 #include "tattn.h"
+#include "assign.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "packed.cuh"
+#include "rotary.cuh"
 
 namespace ta {
 
@@ -55,7 +58,10 @@ static ta_status guard_status() {
                                {"attn_cache_e4m3.cu", guard_take_attn_cache_e4m3},
                                {"attn_cache_i8.cu", guard_take_attn_cache_i8},
                                {"attn_cache_tc.cu", guard_take_attn_cache_tc},
-                               {"attn_cache_tc8.cu", guard_take_attn_cache_tc8}};
+                               {"attn_cache_tc8.cu", guard_take_attn_cache_tc8},
+                               {"rotary.cu", guard_take_rotary}, {"assign.cu", guard_take_assign},
+                               {"packed_plan.cu", guard_take_packed_plan}, {"packed_fwd.cu", guard_take_packed_fwd},
+                               {"packed_bwd.cu", guard_take_packed_bwd}};
   bool failed = false;
   for (const Unit& u : units) {
     uint32_t info[4] = {0u, 0u, 0u, 0u};  // line, rejected value, shared memory base, size
@@ -789,6 +795,255 @@ static bool row_count(int B, int H, int T, int* rows) {
   return true;
 }
 
+// ------------------------------------------- rotary positions, packed attention
+// Rows [B, heads, T, D] with 16-byte steps, of a call's ta_rows.
+static ta_status check_rows(const ta_rows& r, int B, int H, int T, RotRows* out) {
+  ta_status st = check_ptrs({r.p});
+  if (st != TA_OK) return st;
+  const int64_t s[3] = {r.sb, r.sh, r.st};
+  st = check_strides(s, B, H, T);
+  *out = RotRows{r.p, r.sb, r.sh, r.st};
+  return st;
+}
+
+// Warps that a call should have: 16 on each of 152 SMs hide the latency of a
+// row's loads; tokens are cut into slices of heads until there are as many.
+constexpr int kRotWarps = 152 * 16;
+
+static ta_status rotary_args(const ta_rotary_call* c, int mode, const ta_kv_cache* cache, RotArgs* a, CacheArgs* ca) {
+  if (!c || c->B < 0 || c->T < 0 || c->Hq < 0 || c->Hkv < 0) return TA_ERR_INVALID_ARG;
+  if (c->dt != TA_F16 && c->dt != TA_BF16) return TA_ERR_UNSUPPORTED;
+  if (!head_dim_ok(c->D)) return TA_ERR_UNSUPPORTED;
+  if (c->dim < 0 || c->dim > c->D || (c->dim & 1)) return TA_ERR_INVALID_ARG;
+  if (!std::isfinite(c->scale)) return TA_ERR_INVALID_ARG;
+  const bool norm = mode == kRotNorm || mode == kRotNormBwd || (mode == kRotAppend && (c->q_weight || c->k_weight));
+  *a = RotArgs{};
+  *ca = CacheArgs{};
+  if (mode == kRotAppend) {
+    ta_status st = check_cache(cache, c->B, c->T, c->dt, ca);
+    if (st != TA_OK) return st;
+    if (cache->Hkv != c->Hkv || cache->D != c->D) return TA_ERR_INVALID_ARG;
+  }
+  if (norm) {
+    if (!(c->eps >= 0.f) || !std::isfinite(c->eps)) return TA_ERR_INVALID_ARG;
+    if (c->wt != c->dt && c->wt != TA_F32) return TA_ERR_UNSUPPORTED;
+    if ((c->Hq > 0 && !c->q_weight) || (c->Hkv > 0 && !c->k_weight)) return TA_ERR_INVALID_ARG;
+    const uintptr_t mask = c->wt == TA_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(c->q_weight) | reinterpret_cast<uintptr_t>(c->k_weight)) & mask)
+      return TA_ERR_ALIGNMENT;
+  }
+  const __int128 tokens = static_cast<__int128>(c->B) * c->T;
+  const int heads = c->Hq + c->Hkv;
+  if (static_cast<long long>(c->Hq) + 2ll * c->Hkv > 65536 || tokens > 0x7fffffffll) return TA_ERR_UNSUPPORTED;
+  if (tokens == 0 || heads == 0) return TA_OK;  // nothing to do: a->units stays 0
+  ta_status st = check_ints({c->positions});
+  if (st == TA_OK && mode == kRotAppend) st = check_ints({c->slots});
+  if (st == TA_OK && c->dim > 0 && !c->turns) st = TA_ERR_INVALID_ARG;
+  if (st == TA_OK && (reinterpret_cast<uintptr_t>(c->turns) & 7u)) st = TA_ERR_ALIGNMENT;
+  auto rows = [&](const ta_rows& r, int H, RotRows* out) {
+    if (st == TA_OK && H > 0) st = check_rows(r, c->B, H, c->T, out);
+  };
+  rows(c->q, c->Hq, &a->q);
+  rows(c->k, c->Hkv, &a->k);
+  rows(c->q_out, c->Hq, &a->qo);
+  if (mode != kRotAppend) rows(c->k_out, c->Hkv, &a->ko);
+  else rows(c->v, c->Hkv, &a->v);
+  if (mode == kRotNormBwd) {
+    rows(c->dq, c->Hq, &a->dq);
+    rows(c->dk, c->Hkv, &a->dk);
+  }
+  if (st != TA_OK) return st;
+  a->pos = c->positions;
+  a->pos_b = c->pos_b;
+  a->pos_t = c->pos_t;
+  a->slots = c->slots;
+  a->turns = c->turns;
+  a->rot = c->dim;
+  a->pairs = c->dim / 2;
+  a->interleaved = c->interleaved != 0;
+  a->scale = c->scale;
+  a->sign = 1.f;
+  if (norm) {
+    a->wq = c->q_weight;
+    a->wk = c->k_weight;
+    a->w32 = c->wt == TA_F32;
+    a->eps = c->eps;
+  }
+  a->T = c->T;
+  a->Hq = c->Hq;
+  a->Hkv = c->Hkv;
+  a->t_div = fast_div(c->T);
+  const int per_warp = 256 / c->D;  // rows a warp holds at once
+  const int all = mode == kRotAppend ? c->Hq + 2 * c->Hkv : heads;
+  const int groups = (all + per_warp - 1) / per_warp;
+  const long long n = static_cast<long long>(tokens);
+  const int slices = static_cast<int>(std::min<long long>(groups, std::max<long long>(1, (kRotWarps + n - 1) / n)));
+  a->slice_rows = (groups + slices - 1) / slices * per_warp;
+  const int cut = (all + a->slice_rows - 1) / a->slice_rows;
+  if (n * cut > 0x7fffffffll - 65536) return TA_ERR_UNSUPPORTED;
+  a->units = static_cast<int>(n * cut);
+  a->slice_div = fast_div(cut);
+  a->blocks = std::min((a->units + 7) / 8, kRotBwdBlocks);
+  return TA_OK;
+}
+
+static ta_status run_rotary(const ta_rotary_call* c, int mode, float sign, const ta_kv_cache* cache, const char* name,
+                            void* stream) {
+  RotArgs a;
+  CacheArgs ca;
+  ta_status st = rotary_args(c, mode, cache, &a, &ca);
+  if (st != TA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (mode == kRotNormBwd) {
+    if ((c->Hq > 0 && !c->dq_weight) || (c->Hkv > 0 && !c->dk_weight)) return TA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(c->dq_weight) | reinterpret_cast<uintptr_t>(c->dk_weight)) & 3u)
+      return TA_ERR_ALIGNMENT;
+    if (a.units == 0) {  // sums of no rows
+      cudaError_t e = cudaSuccess;
+      if (c->Hq > 0) e = cudaMemsetAsync(c->dq_weight, 0, sizeof(float) * c->D, s);
+      if (e == cudaSuccess && c->Hkv > 0) e = cudaMemsetAsync(c->dk_weight, 0, sizeof(float) * c->D, s);
+      return cuda_status(e);
+    }
+    st = check_ptrs({c->ws});
+    if (st != TA_OK) return st;
+    if (c->ws_bytes < attn_qk_norm_rotary_bwd_workspace_bytes(c->D)) return TA_ERR_INVALID_ARG;
+    a.part = static_cast<float*>(c->ws);
+    a.dwq = c->Hq > 0 ? c->dq_weight : nullptr;
+    a.dwk = c->Hkv > 0 ? c->dk_weight : nullptr;
+  }
+  if (a.units == 0) return TA_OK;
+  a.sign = sign;
+  if (!(ca.err = error_word_ptr())) return TA_ERR_CUDA;
+  prof_begin(name, s);
+  cudaError_t e = launch_rotary(mode, c->dt == TA_BF16, cache ? cache_type(cache->ct) : kCache16, c->D, a, ca, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+static bool packed_shape(int B, int total_q, int total_k, int Hq, int Hkv, PackedShape* p, ta_status* st) {
+  *st = TA_ERR_INVALID_ARG;
+  if (B < 0 || total_q < 0 || total_k < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return false;
+  *st = TA_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  // a token's heads fit a tile, and a last tile's rows stay below 2^31
+  if (G > kBM || total_q > 0x7fffffff - 4096 || total_k > 0x7fffffff - 4096) return false;
+  *p = PackedShape{B, total_q, total_k, Hq, Hkv, G, kBM / G, 0};
+  for (int kind = 0; kind < kPackedKinds; ++kind)
+    if (p->bound(kind) * Hkv > 0x7fffffffll - 65536) return false;
+  *st = TA_OK;
+  return true;
+}
+
+// [total, heads, D] with element strides (token, head) as a map whose boxes hold 64
+// columns x box_heads heads x box_tokens tokens (box_heads 0: tokens of one head).
+static bool make_packed_map(CUtensorMap* map, const ta_rows& r, long long total, int heads, int D, bool bf16, int box_heads,
+                            int box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || !ensure_context()) return false;
+  const cuuint64_t dense = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t sh = heads > 1 ? static_cast<cuuint64_t>(r.sh) * 2 : dense;
+  const cuuint64_t st = total > 1 ? static_cast<cuuint64_t>(r.st) * 2 : dense;
+  const bool by_head = box_heads == 0;  // key side: (D, token, head); query side: (D, head, token)
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(by_head ? total : heads),
+                        static_cast<cuuint64_t>(by_head ? heads : total)};
+  cuuint64_t strides[2] = {by_head ? st : sh, by_head ? sh : st};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(by_head ? box_tokens : box_heads),
+                       static_cast<cuuint32_t>(by_head ? 1 : box_tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, r.p, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows that a TMA map takes: 16-byte steps above zero, below 2^40 bytes.
+static ta_status check_packed_rows(const ta_rows& r, int total, int heads) {
+  ta_status st = check_ptrs({r.p});
+  if (st != TA_OK) return st;
+  const int64_t s[3] = {0, r.sh, r.st};
+  st = check_strides(s, 1, heads, total);
+  if (st != TA_OK) return st;
+  auto ok = [](int64_t x) { return x > 0 && x < (int64_t{1} << 39); };
+  if ((heads > 1 && !ok(r.sh)) || (total > 1 && !ok(r.st))) return TA_ERR_UNSUPPORTED;
+  return TA_OK;
+}
+
+// Checks shared by the forward and the backward; *none: no unit can exist.
+static ta_status packed_args(const ta_packed_call* c, bool bwd, PackedArgs* a, PackedMaps* m, bool* none) {
+  *none = false;
+  if (!c) return TA_ERR_INVALID_ARG;
+  PackedShape p;
+  ta_status st;
+  if (!packed_shape(c->B, c->total_q, c->total_k, c->Hq, c->Hkv, &p, &st)) return st;
+  if (c->dt != TA_F16 && c->dt != TA_BF16) return TA_ERR_UNSUPPORTED;
+  if (!head_dim_ok(c->D)) return TA_ERR_UNSUPPORTED;
+  const bool has_q = c->total_q > 0, has_k = c->total_k > 0;
+  if (c->B == 0 || (!has_q && !(bwd && has_k))) {
+    *none = true;
+    return TA_OK;
+  }
+  st = check_ptrs({c->plan});
+  if (st != TA_OK) return st;
+  if (c->plan_bytes < attn_packed_plan_bytes(c->B, c->total_q, c->total_k, c->Hq, c->Hkv)) return TA_ERR_INVALID_ARG;
+  auto rows = [&](const ta_rows& r, bool query) {
+    if (st == TA_OK && (query ? has_q : has_k))
+      st = check_packed_rows(r, query ? c->total_q : c->total_k, query ? c->Hq : c->Hkv);
+  };
+  rows(c->q, true);
+  rows(c->k, false);
+  rows(c->v, false);
+  rows(c->o, true);
+  if (bwd) {
+    rows(c->dO, true);
+    rows(c->dq, true);
+    rows(c->dk, false);
+    rows(c->dv, false);
+  }
+  if (st == TA_OK && has_q) st = check_ints({c->lse});
+  if (st != TA_OK) return st;
+  *a = PackedArgs{};
+  a->plan = static_cast<const uint8_t*>(c->plan);
+  a->shape = p;
+  a->hkv_div = fast_div(c->Hkv);
+  a->g_div = fast_div(p.G);
+  a->v = c->v.p;
+  a->vt = c->v.st;
+  a->vh = c->v.sh;
+  a->o = c->o.p;
+  a->o_t = c->o.st;
+  a->o_h = c->o.sh;
+  a->lse = c->lse;
+  a->sm_scale = (std::isfinite(c->sm_scale) && c->sm_scale > 0.f) ? c->sm_scale
+                                                                  : 1.0f / std::sqrt(static_cast<float>(c->D));
+  a->scale_log2 = a->sm_scale * kLog2e;
+  a->dg = c->D;
+  a->timeout_ns = g_timeout_ns;
+  if (!(a->err = error_word_ptr())) return TA_ERR_CUDA;
+  const bool bf16 = c->dt == TA_BF16;
+  // sides without rows have no tiles; their maps are stand-ins that no block uses
+  auto qmap = [&](CUtensorMap* map, const ta_rows& r) {
+    return has_q ? make_packed_map(map, r, c->total_q, c->Hq, c->D, bf16, p.G, p.TB)
+                 : make_packed_map(map, c->k, c->total_k, c->Hkv, c->D, bf16, 0, kBN);
+  };
+  auto kmap = [&](CUtensorMap* map, const ta_rows& r) {
+    return has_k ? make_packed_map(map, r, c->total_k, c->Hkv, c->D, bf16, 0, kBN)
+                 : make_packed_map(map, c->q, c->total_q, c->Hq, c->D, bf16, p.G, p.TB);
+  };
+  bool made = qmap(&m->q, c->q) && kmap(&m->k, c->k) && kmap(&m->v, c->v) && qmap(&m->o, c->o);
+  if (bwd) {
+    a->dq = c->dq.p;
+    a->dq_t = c->dq.st;
+    a->dq_h = c->dq.sh;
+    a->dk = c->dk.p;
+    a->dk_t = c->dk.st;
+    a->dk_h = c->dk.sh;
+    a->dv = c->dv.p;
+    a->dv_t = c->dv.st;
+    a->dv_h = c->dv.sh;
+    made = made && qmap(&m->dO, c->dO) && qmap(&m->dq, c->dq) && kmap(&m->dk, c->dk) && kmap(&m->dv, c->dv);
+  }
+  return made ? TA_OK : TA_ERR_CUDA;
+}
+
 }  // namespace ta
 
 using namespace ta;
@@ -1162,6 +1417,164 @@ ta_status attn_cache_fwd(const void* q, const int64_t* q_strides, const ta_kv_ca
     return TA_ERR_CUDA;
   return cuda_status(ct == kCache16 ? launch_attn_cache_tc16(bf16, cache->D, m, c, a, s)
                                     : launch_attn_cache_tc8(bf16, ct, cache->D, m, c, a, s));
+}
+
+ta_status attn_cache_assign(int* pages, int max_pages, const int* kv_lens, const int* new_lens, int* free_ids,
+                            int num_pages, const int* free_count, int page_size, int* kv_out, int* q_lens,
+                            int* cu_seqlens, int* positions, int* slots, int* count_out, int B, int total, void* stream) {
+  if (B < 0 || total < 0 || max_pages < 0 || num_pages < 0 || page_size < 1) return TA_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_pages) * page_size > 0x7fffffffll || total > 0x7fffffff - 65536 ||
+      B > 0x7fffffff - 65536)
+    return TA_ERR_UNSUPPORTED;
+  ta_status st = check_ints({free_count, cu_seqlens, count_out});
+  if (st == TA_OK && B > 0) st = check_ints({kv_lens, new_lens, kv_out, q_lens});
+  if (st == TA_OK && B > 0 && max_pages > 0) st = check_ints({pages});
+  if (st == TA_OK && num_pages > 0) st = check_ints({free_ids});
+  if (st == TA_OK && total > 0) st = check_ints({positions, slots});
+  if (st != TA_OK) return st;
+  // what the call writes must not lie on what it reads or on another output
+  struct Span {
+    const int* p;
+    size_t n;
+  };
+  const size_t table = static_cast<size_t>(B) * max_pages;
+  const Span in[] = {{kv_lens, static_cast<size_t>(B)}, {new_lens, static_cast<size_t>(B)}, {free_count, 1}};
+  const Span out[] = {{pages, table},
+                      {free_ids, static_cast<size_t>(num_pages)},
+                      {kv_out, static_cast<size_t>(B)},
+                      {q_lens, static_cast<size_t>(B)},
+                      {cu_seqlens, static_cast<size_t>(B) + 1},
+                      {positions, static_cast<size_t>(total)},
+                      {slots, static_cast<size_t>(total)},
+                      {count_out, 1}};
+  auto overlap = [](const Span& a, const Span& b) {
+    return a.p && b.p && a.n && b.n && a.p < b.p + b.n && b.p < a.p + a.n;
+  };
+  for (size_t i = 0; i < sizeof(out) / sizeof(out[0]); ++i) {
+    for (const Span& x : in)
+      if (overlap(out[i], x)) return TA_ERR_INVALID_ARG;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return TA_ERR_INVALID_ARG;
+  }
+  AssignArgs a;
+  a.pages = pages;
+  a.kv_lens = kv_lens;
+  a.new_lens = new_lens;
+  a.free_ids = free_ids;
+  a.free_count = free_count;
+  a.kv_out = kv_out;
+  a.q_lens = q_lens;
+  a.cu = cu_seqlens;
+  a.positions = positions;
+  a.slots = slots;
+  a.count_out = count_out;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.total = total;
+  a.capacity = static_cast<int>(std::min<long long>(static_cast<long long>(max_pages) * page_size, 0x7fffffffll - 4096));
+  a.page = fast_div(page_size);
+  if (!(a.err = error_word_ptr())) return TA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_cache_assign", s);
+  cudaError_t e = launch_cache_assign(a, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+ta_status attn_rotary_fwd(const ta_rotary_call* c, void* stream) {
+  return run_rotary(c, kRotPlain, 1.f, nullptr, "attn_rotary_fwd", stream);
+}
+
+ta_status attn_rotary_bwd(const ta_rotary_call* c, void* stream) {
+  return run_rotary(c, kRotPlain, -1.f, nullptr, "attn_rotary_bwd", stream);
+}
+
+ta_status attn_qk_norm_rotary_fwd(const ta_rotary_call* c, void* stream) {
+  return run_rotary(c, kRotNorm, 1.f, nullptr, "attn_qk_norm_rotary_fwd", stream);
+}
+
+size_t attn_qk_norm_rotary_bwd_workspace_bytes(int D) {
+  return head_dim_ok(D) ? static_cast<size_t>(kRotBwdBlocks) * 2 * D * sizeof(float) : 0;
+}
+
+ta_status attn_qk_norm_rotary_bwd(const ta_rotary_call* c, void* stream) {
+  return run_rotary(c, kRotNormBwd, -1.f, nullptr, "attn_qk_norm_rotary_bwd", stream);
+}
+
+ta_status attn_rotary_append(const ta_kv_cache* cache, const ta_rotary_call* c, void* stream) {
+  return run_rotary(c, kRotAppend, 1.f, cache, "attn_rotary_append", stream);
+}
+
+size_t attn_packed_plan_bytes(int B, int total_q, int total_k, int Hq, int Hkv) {
+  PackedShape p;
+  ta_status st;
+  return packed_shape(B, total_q, total_k, Hq, Hkv, &p, &st) ? p.first(kPackedKinds) : 0;
+}
+
+ta_status attn_packed_plan(const int* cu_q, const int* cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int causal,
+                           void* plan, size_t plan_bytes, void* stream) {
+  PackedShape p;
+  ta_status st;
+  if (!packed_shape(B, total_q, total_k, Hq, Hkv, &p, &st)) return st;
+  if (B == 0) return TA_OK;
+  p.causal = causal ? 1 : 0;
+  st = check_ints({cu_q, cu_k});
+  if (st == TA_OK) st = check_ptrs({plan});
+  if (st != TA_OK) return st;
+  if (plan_bytes < p.first(kPackedKinds)) return TA_ERR_INVALID_ARG;
+  uint32_t* err = error_word_ptr();
+  if (!err) return TA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_packed_plan", s);
+  cudaError_t e = launch_packed_plan(p, cu_q, cu_k, plan, err, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+ta_status attn_packed_fwd(const ta_packed_call* c, void* stream) {
+  PackedArgs a;
+  PackedMaps m;
+  bool none;
+  ta_status st = packed_args(c, false, &a, &m, &none);
+  if (st != TA_OK || none) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin("attn_packed_fwd", s);
+  cudaError_t e = launch_packed_fwd(c->dt == TA_BF16, kernel_d(c->D), m, a, s);
+  prof_end(s);
+  return cuda_status(e);
+}
+
+size_t attn_packed_bwd_workspace_bytes(int total_q, int Hq) {
+  if (total_q < 0 || Hq < 1) return 0;
+  return (static_cast<size_t>(total_q) * Hq * sizeof(float) + 255) & ~size_t{255};
+}
+
+ta_status attn_packed_bwd(const ta_packed_call* c, void* stream) {
+  PackedArgs a;
+  PackedMaps m;
+  bool none;
+  ta_status st = packed_args(c, true, &a, &m, &none);
+  if (st != TA_OK || none) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = c->dt == TA_BF16;
+  if (c->total_q > 0) {
+    st = check_ptrs({c->ws});
+    if (st != TA_OK) return st;
+    if (c->ws_bytes < attn_packed_bwd_workspace_bytes(c->total_q, c->Hq)) return TA_ERR_INVALID_ARG;
+    a.delta = static_cast<float*>(c->ws);
+    prof_begin("attn_packed_bwd_dq", s);
+    cudaError_t e = launch_packed_dq(bf16, kernel_d(c->D), m, a, s);
+    prof_end(s);
+    if (e != cudaSuccess) return TA_ERR_CUDA;
+  }
+  if (c->total_k > 0) {
+    prof_begin("attn_packed_bwd_dkdv", s);
+    cudaError_t e = launch_packed_dkdv(bf16, kernel_d(c->D), m, a, s);
+    prof_end(s);
+    if (e != cudaSuccess) return TA_ERR_CUDA;
+  }
+  return TA_OK;
 }
 
 ta_status ta_sync_status(void* stream) {

@@ -51,6 +51,11 @@ uint32_t guard_take_attn_cache_e4m3(uint32_t* info);
 uint32_t guard_take_attn_cache_i8(uint32_t* info);
 uint32_t guard_take_attn_cache_tc(uint32_t* info);
 uint32_t guard_take_attn_cache_tc8(uint32_t* info);
+uint32_t guard_take_rotary(uint32_t* info);
+uint32_t guard_take_assign(uint32_t* info);
+uint32_t guard_take_packed_plan(uint32_t* info);
+uint32_t guard_take_packed_fwd(uint32_t* info);
+uint32_t guard_take_packed_bwd(uint32_t* info);
 #endif
 cudaError_t launch_fwd(int mode, bool bf16, int D, const FwdMaps& maps, const FwdArgs& a, bool split,
                        cudaStream_t s);

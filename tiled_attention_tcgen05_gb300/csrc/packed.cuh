@@ -1,0 +1,151 @@
+// Attention of sequences packed one behind the other, with shared key heads:
+// the plan (which tiles there are), the geometry of a tile, and the helpers of
+// the kernels in packed_fwd.cu and packed_bwd.cu.
+//
+// A tile of 128 query rows holds TB = 128 / G consecutive tokens (rounded down) with
+// the G query heads of one key head, token by token: row r is token r / G, head
+// r % G.  All of its rows read the same keys, so a short sequence fills a tile
+// G times better than with a tile per head, and the key side of the backward
+// sums over the heads by walking rows.  TMA loads such a tile as a box of
+// 64 columns x G heads x TB tokens.
+#pragma once
+#include <atomic>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bwd_common.cuh"
+#include "cache.cuh"
+#include "common.cuh"
+
+namespace ta {
+
+// One CTA's work for one key head.  Query side (forward: two tiles, dQ: one):
+// row, left: first token's row and the tokens from it to the sequence's end;
+// krow, n: first key's row and the number of keys; off: last key the first
+// token sees (causal).  Key side: krow, n: first key of the tile and the keys from it
+// on; row, left: first token that sees any of it and the tokens from there
+// on; off: such token (counted from it) from which the tile's first key is seen.
+struct PackedUnit {
+  int row, left, krow, n, off, pad[3];
+};
+static_assert(sizeof(PackedUnit) == 32, "two 16-byte loads");
+
+enum PackedKind : int { kPackedFwd = 0, kPackedDq = 1, kPackedDkdv = 2, kPackedKinds = 3 };
+
+constexpr int kPackedMagic = 0x70a7c4ed;
+
+// Start of the plan's memory; the lists of units follow, kind by kind.
+struct PackedHeader {
+  int magic, B, total_q, total_k, Hq, Hkv, causal;
+  int count[kPackedKinds];
+  int pad[6];
+};
+static_assert(sizeof(PackedHeader) == 64, "units start on a 64-byte boundary");
+
+struct PackedShape {
+  int B, total_q, total_k, Hq, Hkv, G, TB, causal;
+  // units of a kind at most: sum of ceil(len / size) <= total / size + B
+  __host__ __device__ long long bound(int kind) const {
+    if (kind == kPackedFwd) return total_q / (2 * TB) + B;
+    return kind == kPackedDq ? total_q / TB + B : total_k / kBN + B;
+  }
+  __host__ __device__ size_t first(int kind) const {  // byte offset of a kind's list
+    size_t at = sizeof(PackedHeader);
+    for (int i = 0; i < kind; ++i) at += static_cast<size_t>(bound(i)) * sizeof(PackedUnit);
+    return at;
+  }
+};
+
+struct PackedArgs {
+  const uint8_t* plan;
+  PackedShape shape;
+  FastDiv hkv_div, g_div;
+  const void* v;        // forward: [total_k, Hkv, D], element strides vt, vh
+  long long vt, vh;
+  void *o, *dq, *dk, *dv;  // element strides (token, head)
+  long long o_t, o_h, dq_t, dq_h, dk_t, dk_h, dv_t, dv_h;
+  float* lse;           // [total_q, Hq]
+  float* delta;         // [total_q, Hq]
+  float scale_log2, sm_scale;
+  int dg;               // head dimension of the tensors in memory
+  uint32_t* err;
+  uint64_t timeout_ns;
+};
+
+// q, o, dO, dq: boxes of TB tokens x G heads; k, v, dk, dv: 128 rows of a head.
+struct PackedMaps {
+  CUtensorMap q, k, v, o, dO, dq, dk, dv;
+};
+
+cudaError_t launch_packed_plan(const PackedShape& p, const int* cu_q, const int* cu_k, void* plan, uint32_t* err,
+                               cudaStream_t s);
+cudaError_t launch_packed_fwd(bool bf16, int D, const PackedMaps& m, const PackedArgs& a, cudaStream_t s);
+cudaError_t launch_packed_dq(bool bf16, int D, const PackedMaps& m, const PackedArgs& a, cudaStream_t s);
+cudaError_t launch_packed_dkdv(bool bf16, int D, const PackedMaps& m, const PackedArgs& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The block's unit and key head; false: nothing to do.  A plan that was
+// not made for these sizes is recorded in the error word.
+__device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, PackedUnit* u, int* head) {
+  const PackedHeader* h = reinterpret_cast<const PackedHeader*>(a.plan);
+  const uint32_t i = a.hkv_div.div(blockIdx.x);
+  *head = static_cast<int>(blockIdx.x - i * a.hkv_div.d);
+  const int4 h0 = __ldg(reinterpret_cast<const int4*>(h));
+  const int4 h1 = __ldg(reinterpret_cast<const int4*>(h) + 1);
+  const int4 h2 = __ldg(reinterpret_cast<const int4*>(h) + 2);
+  // (the unit is inside the plan's memory whatever the header says)
+  const int4* list = reinterpret_cast<const int4*>(a.plan + a.shape.first(kind)) + 2 * static_cast<size_t>(i);
+  const int4 x = __ldg(list), y = __ldg(list + 1);
+  if (h0.x != kPackedMagic || h0.y != a.shape.B || h0.z != a.shape.total_q || h0.w != a.shape.total_k ||
+      h1.x != a.shape.Hq || h1.y != a.shape.Hkv) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) cache_error(a.err);
+    return false;
+  }
+  const int count = kind == kPackedFwd ? h1.w : kind == kPackedDq ? h2.x : h2.y;
+  if (i >= static_cast<uint32_t>(count)) return false;
+  u->row = x.x;
+  u->left = x.y;
+  u->krow = x.z;
+  u->n = x.w;
+  u->off = y.x;
+  u->pad[0] = h1.z;  // causal, of the plan
+  return true;
+}
+
+// Key tiles that a tile of `tokens` tokens visits, the first of which sees keys up to off.
+__host__ __device__ inline int packed_key_tiles(int tokens, int off, int n, int causal) {
+  if (tokens <= 0) return 0;
+  const int all = (n + kBN - 1) / kBN;
+  if (!causal) return all;
+  const long long last = static_cast<long long>(off) + tokens - 1;
+  if (last < 0) return 0;
+  const long long t = last / kBN + 1;
+  return t < all ? static_cast<int>(t) : all;
+}
+
+// Rows [first, 128) of a 128-row tile of NB 64-column blocks set to zero by one
+// warp, then made visible to the MMAs (whoever waits for the barrier the warp
+// arrives on next).
+template <int NB>
+__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int first, int lane) {
+  for (int kb = 0; kb < NB; ++kb)
+    for (int i = first * 8 + lane; i < kBM * 8; i += 32)
+      *reinterpret_cast<uint4*>(tile + kb * (kBM * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Rows of a staged output tile (stage_row_chunk_sw128's layout) to memory, 16
+// bytes a thread and a row's pieces side by side; row(r) is where row r goes,
+// or null.  `n` threads, tid among them.
+template <typename F>
+__device__ __forceinline__ void copy_tile_rows(const uint8_t* tile, int dg, int tid, int n, F row) {
+  const int c = dg >> 3;  // 16-byte pieces of a row: 2, 4, 8 or 16
+  const int sh = __ffs(c) - 1;
+  for (int i = tid; i < (kBM << sh); i += n) {
+    const int r = i >> sh, j = i & (c - 1);
+    uint4* p = static_cast<uint4*>(row(r));
+    if (p) p[j] = *reinterpret_cast<const uint4*>(tile + (j >> 3) * (kBM * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4));
+  }
+}
+#endif
+
+}  // namespace ta
