@@ -59,7 +59,8 @@ static ta_status guard_status() {
                                {"attn_cache_i8.cu", guard_take_attn_cache_i8},
                                {"attn_cache_tc.cu", guard_take_attn_cache_tc},
                                {"attn_cache_tc8.cu", guard_take_attn_cache_tc8},
-                               {"rotary.cu", guard_take_rotary}, {"assign.cu", guard_take_assign},
+                               {"rotary_bf16.cu", guard_take_rotary_bf16}, {"rotary_f16.cu", guard_take_rotary_f16},
+                               {"assign.cu", guard_take_assign},
                                {"packed_plan.cu", guard_take_packed_plan}, {"packed_fwd.cu", guard_take_packed_fwd},
                                {"packed_bwd.cu", guard_take_packed_bwd}};
   bool failed = false;
@@ -873,13 +874,15 @@ static ta_status rotary_args(const ta_rotary_call* c, int mode, const ta_kv_cach
   a->Hq = c->Hq;
   a->Hkv = c->Hkv;
   a->t_div = fast_div(c->T);
-  const int per_warp = 256 / c->D;  // rows a warp holds at once
-  const int all = mode == kRotAppend ? c->Hq + 2 * c->Hkv : heads;
-  const int groups = (all + per_warp - 1) / per_warp;
+  const int per_group = 512 / c->D;  // rows of a group: a warp's lanes hold 16 elements each
+  auto groups_of = [&](int h) { return (h + per_group - 1) / per_group; };
+  const int groups = groups_of(c->Hq) + groups_of(c->Hkv) * (mode == kRotAppend ? 2 : 1);
+  const int most = mode == kRotNormBwd ? kRotBwdGroups : kRotGroups;
   const long long n = static_cast<long long>(tokens);
-  const int slices = static_cast<int>(std::min<long long>(groups, std::max<long long>(1, (kRotWarps + n - 1) / n)));
-  a->slice_rows = (groups + slices - 1) / slices * per_warp;
-  const int cut = (all + a->slice_rows - 1) / a->slice_rows;
+  const int slices = static_cast<int>(
+      std::min<long long>(groups, std::max<long long>((groups + most - 1) / most, (kRotWarps + n - 1) / n)));
+  a->slice_groups = (groups + slices - 1) / slices;
+  const int cut = (groups + a->slice_groups - 1) / a->slice_groups;
   if (n * cut > 0x7fffffffll - 65536) return TA_ERR_UNSUPPORTED;
   a->units = static_cast<int>(n * cut);
   a->slice_div = fast_div(cut);
@@ -915,7 +918,8 @@ static ta_status run_rotary(const ta_rotary_call* c, int mode, float sign, const
   a.sign = sign;
   if (!(ca.err = error_word_ptr())) return TA_ERR_CUDA;
   prof_begin(name, s);
-  cudaError_t e = launch_rotary(mode, c->dt == TA_BF16, cache ? cache_type(cache->ct) : kCache16, c->D, a, ca, s);
+  const int ct = cache ? cache_type(cache->ct) : kCache16;
+  cudaError_t e = c->dt == TA_BF16 ? launch_rotary_bf16(mode, ct, c->D, a, ca, s) : launch_rotary_f16(mode, ct, c->D, a, ca, s);
   prof_end(s);
   return cuda_status(e);
 }

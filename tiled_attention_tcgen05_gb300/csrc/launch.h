@@ -51,7 +51,8 @@ uint32_t guard_take_attn_cache_e4m3(uint32_t* info);
 uint32_t guard_take_attn_cache_i8(uint32_t* info);
 uint32_t guard_take_attn_cache_tc(uint32_t* info);
 uint32_t guard_take_attn_cache_tc8(uint32_t* info);
-uint32_t guard_take_rotary(uint32_t* info);
+uint32_t guard_take_rotary_bf16(uint32_t* info);
+uint32_t guard_take_rotary_f16(uint32_t* info);
 uint32_t guard_take_assign(uint32_t* info);
 uint32_t guard_take_packed_plan(uint32_t* info);
 uint32_t guard_take_packed_fwd(uint32_t* info);

@@ -1,4 +1,4 @@
-// Arguments of the rotary position kernels (rotary.cu).
+// Arguments of the rotary position kernels (rotary_kernels.cuh).
 #pragma once
 #include <cuda_runtime.h>
 
@@ -35,13 +35,18 @@ struct RotArgs {
   int T, Hq, Hkv;
   FastDiv t_div;       // by T
   FastDiv slice_div;   // by the slices of a token
-  int slice_rows;      // rows of a slice
+  int slice_groups;    // groups of rows of a slice
   int units;           // tokens * slices
 };
 
-// Blocks of the backward of the norm at most: its partial sums take that many rows.
-constexpr int kRotBwdBlocks = 152 * 4;
+// Groups of rows of a slice at most: a warp copies all of a slice's to shared memory
+// before it works on them (1 KB a group, 2 KB in the backward of the norm).
+constexpr int kRotGroups = 12, kRotBwdGroups = 5;
 
-cudaError_t launch_rotary(int mode, bool bf16, int ct, int D, const RotArgs& a, const CacheArgs& c, cudaStream_t s);
+// Blocks of the backward of the norm at most, two a SM: its partial sums take that many rows.
+constexpr int kRotBwdBlocks = 152 * 2;
+
+cudaError_t launch_rotary_bf16(int mode, int ct, int D, const RotArgs& a, const CacheArgs& c, cudaStream_t s);
+cudaError_t launch_rotary_f16(int mode, int ct, int D, const RotArgs& a, const CacheArgs& c, cudaStream_t s);
 
 }  // namespace ta
