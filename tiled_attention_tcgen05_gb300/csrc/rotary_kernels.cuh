@@ -196,39 +196,50 @@ __device__ __forceinline__ void coefs(const RotArgs& a, const Place& w, const fl
     }
 }
 
-// 1 / sqrt(mean f^2 + eps) over the row; where the squares pass fp32's range
-// f and xp are scaled by *down first (the result is that of the scaled row).
+// r = 1 / sqrt(mean f^2 + eps) of U rows side by side; where a row's squares pass
+// fp32's range, f is scaled by down first (and r is that of the scaled row).
 // Warp-collective.
-template <int D>
-__device__ __forceinline__ float row_norm(float2 (&f)[2][4], float2 (&xp)[2][4], float eps, float* down) {
+template <int D, int U>
+__device__ __forceinline__ void row_norm(float2 (&f)[U][2][4], float eps, float (&r)[U], float (&down)[U]) {
   constexpr int L = D / 16;
+  float ss[U];
   auto squares = [&] {
-    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s0 = ffma2(f[0][e], f[0][e], s0);
-      s1 = ffma2(f[1][e], f[1][e], s1);
-    }
-    s0 = fadd2(s0, s1);
-    return row_sum<L>(s0.x + s0.y);
-  };
-  float ss = squares();
-  const bool big = !(ss < INFINITY);
-  float tiny = 1.f;
-  if (__any_sync(0xffffffffu, big)) {
-    tiny = big ? 5.421010862427522e-20f : 1.f;  // 2^-64
-    const float2 t2 = make_float2(tiny, tiny);
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int u = 0; u < U; ++u) {
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[c][e] = fmul2(f[c][e], t2);
-        xp[c][e] = fmul2(xp[c][e], t2);
+        s0 = ffma2(f[u][0][e], f[u][0][e], s0);
+        s1 = ffma2(f[u][1][e], f[u][1][e], s1);
       }
-    ss = squares();
+      s0 = fadd2(s0, s1);
+      ss[u] = s0.x + s0.y;
+    }
+#pragma unroll
+    for (int s = L / 2; s > 0; s >>= 1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], s);
+  };
+  squares();
+  bool big = false;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    down[u] = ss[u] < INFINITY ? 1.f : 5.421010862427522e-20f;  // 2^-64
+    big |= !(ss[u] < INFINITY);
   }
-  *down = tiny;
-  return rsqrtf(fmaf(ss, 1.f / D, eps * tiny * tiny));
+  if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float2 t2 = make_float2(down[u], down[u]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[u][c][e] = fmul2(f[u][c][e], t2);
+    }
+    squares();
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) r[u] = rsqrtf(fmaf(ss[u], 1.f / D, eps * down[u] * down[u]));
 }
 
 // A row's sixteen fp32 elements a lane -> codes of a cache type, and the scale.
@@ -381,33 +392,53 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_kernel(const 
     T* dst = rows(out);
     Coef k;
     coefs<PATH>(a, w, cs, sn, norm ? weights[key] : nullptr, k);
-#pragma unroll 1
-    for (int g = n0; g < n1; ++g) {
-      wait_copies(g1 - 1 - g);
-      const uint8_t* from = mine + (g - g0) * 1024;
-      const int h = (g - base) * RPW + sub;
-      const bool act = h < heads;
-      float2 f[2][4], xp[2][4], y[2][4];
-      unpack8<T>(staged(from, 0), f[0]);
-      unpack8<T>(staged(from, 1), f[1]);
-      partners<T, PATH>(a, w, f, rows(in) + h * in.sh, act, xp);
-      float r = 1.f, down;
-      if (norm) r = row_norm<D>(f, xp, a.eps, &down);
-      const float2 r2 = make_float2(r, r);
+    auto some = [&](auto count, int g) {  // groups g .. g + U - 1 side by side
+      constexpr int U = decltype(count)::value;
+      wait_copies(g1 - U - g);
+      float2 f[U][2][4];
+      float r[U], down[U];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[i][e] = ffma2(f[i][e], k.ca[i][e], fmul2(xp[i][e], k.cb[i][e]));
-          if (norm) y[i][e] = fmul2(y[i][e], r2);
-        }
-      if (cached) {
-        to_cache(0, h, act, y);
-      } else if (act) {
-        *reinterpret_cast<uint4*>(dst + h * out.sh + w.at[0]) = pack8<T>(y[0]);
-        *reinterpret_cast<uint4*>(dst + h * out.sh + w.at[1]) = pack8<T>(y[1]);
+      for (int u = 0; u < U; ++u) {
+        const uint8_t* from = mine + (g + u - g0) * 1024;
+        unpack8<T>(staged(from, 0), f[u][0]);
+        unpack8<T>(staged(from, 1), f[u][1]);
+        r[u] = down[u] = 1.f;
       }
+      if (norm) row_norm<D, U>(f, a.eps, r, down);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = (g + u - base) * RPW + sub;
+        const bool act = h < heads;
+        float2 xp[2][4], y[2][4];
+        partners<T, PATH>(a, w, f[u], rows(in) + h * in.sh, act, xp);
+        if (norm && PATH == kAny && w.reload) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xp[i][e] = fmul2(xp[i][e], make_float2(down[u], down[u]));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[i][e] = ffma2(f[u][i][e], k.ca[i][e], fmul2(xp[i][e], k.cb[i][e]));
+            if (norm) y[i][e] = fmul2(y[i][e], make_float2(r[u], r[u]));
+          }
+        if (cached) {
+          to_cache(0, h, act, y);
+        } else if (act) {
+          *reinterpret_cast<uint4*>(dst + h * out.sh + w.at[0]) = pack8<T>(y[0]);
+          *reinterpret_cast<uint4*>(dst + h * out.sh + w.at[1]) = pack8<T>(y[1]);
+        }
+      }
+    };
+    int g = n0;
+    if constexpr (!ANY) {
+#pragma unroll 1
+      for (; g + 1 < n1; g += 2) some(std::integral_constant<int, 2>{}, g);
     }
+#pragma unroll 1
+    for (; g < n1; ++g) some(std::integral_constant<int, 1>{}, g);
   };
   auto both = [&](auto path_tag) {
     turn(path_tag, 0, a.q, a.qo, a.Hq, 0, g0, min(g1, nq));
@@ -493,15 +524,17 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
           const uint8_t* from = mine + (gr - g0) * 2048;
           const int h = (gr - base) * RPW + sub;
           const bool act = h < heads;
-          float2 f[2][4], g[2][4], gp[2][4], none[2][4] = {};
+          float2 fr[1][2][4], g[2][4], gp[2][4];
+          float2(&f)[2][4] = fr[0];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             unpack8<T>(staged(from, i), f[i]);
             unpack8<T>(staged(from + 1024, i), g[i]);
           }
           partners<T, PATH>(a, w, g, rows(grad) + h * grad.sh, act, gp);
-          float down;
-          const float r = row_norm<D>(f, none, a.eps, &down);
+          float r1[1], down[1];
+          row_norm<D, 1>(fr, a.eps, r1, down);
+          const float r = r1[0];
           const float2 r2 = make_float2(r, r);
           float2 dot2 = make_float2(0.f, 0.f), wv[2][4];
           load_weights(w, wt, wv);
@@ -517,7 +550,7 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
               dot2 = ffma2(y[i][e], f[i][e], dot2);
             }
           const float dot = row_sum<L>(dot2.x + dot2.y) * (-1.f / D);
-          const float2 d2 = make_float2(dot, dot), rd = make_float2(r * down, r * down);
+          const float2 d2 = make_float2(dot, dot), rd = make_float2(r * down[0], r * down[0]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
