@@ -84,12 +84,12 @@ cudaError_t launch_packed_dq(bool bf16, int D, const PackedMaps& m, const Packed
 cudaError_t launch_packed_dkdv(bool bf16, int D, const PackedMaps& m, const PackedArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
-// The block's unit and key head; false: nothing to do.  A plan that was
-// not made for these sizes is recorded in the error word.
-__device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, PackedUnit* u, int* head) {
+// A block's first unit and its key head (PackedUnit::pad[0]: causal, pad[1]: the
+// head); false: nothing to do.  A plan that was not made for these sizes is
+// recorded in the error word.
+__device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, uint32_t block, PackedUnit* u) {
   const PackedHeader* h = reinterpret_cast<const PackedHeader*>(a.plan);
-  const uint32_t i = a.hkv_div.div(blockIdx.x);
-  *head = static_cast<int>(blockIdx.x - i * a.hkv_div.d);
+  const uint32_t i = a.hkv_div.div(block);
   const int4 h0 = __ldg(reinterpret_cast<const int4*>(h));
   const int4 h1 = __ldg(reinterpret_cast<const int4*>(h) + 1);
   const int4 h2 = __ldg(reinterpret_cast<const int4*>(h) + 2);
@@ -98,7 +98,7 @@ __device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, Packe
   const int4 x = __ldg(list), y = __ldg(list + 1);
   if (h0.x != kPackedMagic || h0.y != a.shape.B || h0.z != a.shape.total_q || h0.w != a.shape.total_k ||
       h1.x != a.shape.Hq || h1.y != a.shape.Hkv) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) cache_error(a.err);
+    if (threadIdx.x == 0 && block == 0) cache_error(a.err);
     return false;
   }
   const int count = kind == kPackedFwd ? h1.w : kind == kPackedDq ? h2.x : h2.y;
@@ -109,7 +109,110 @@ __device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, Packe
   u->n = x.w;
   u->off = y.x;
   u->pad[0] = h1.z;  // causal, of the plan
+  u->pad[1] = static_cast<int>(block - i * a.hkv_div.d);
   return true;
+}
+
+// ------------------------------------------------------- one block, many units
+// A block that has finished its unit takes over that of a block that has not
+// been launched yet (cluster launch control: the launch is cancelled and its block
+// index handed over), so that its shared memory, tensor memory and rings stay set
+// up and the next unit's tiles arrive while it works on the last one's.
+// One warp asks for units ahead and passes them to the others through two slots;
+// unit i is in slot i % 2, and is passed on only once every other role has
+// left unit i - 2, so that no role is ever two units ahead of another.
+struct UnitRing {
+  uint64_t full[2], left[2], answered;
+  uint4 answer;       // of the cancellation asked for
+  int4 unit[2][2];    // row, left, krow, n | off, causal, head, 1: there is one
+};
+
+__device__ __forceinline__ void ring_init(UnitRing* r, int roles, const PackedUnit& u) {
+  r->unit[0][0] = make_int4(u.row, u.left, u.krow, u.n);
+  r->unit[0][1] = make_int4(u.off, u.pad[0], u.pad[1], 1);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&r->full[i], 1);
+    mbar_init(&r->left[i], roles);
+  }
+  mbar_init(&r->answered, 1);
+}
+
+// Asks for the next block index (one thread; the one before must have been answered).
+__device__ __forceinline__ void ring_ask(UnitRing* r) {
+  // the last answer has been read before the next is written
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  mbar_expect_tx(&r->answered, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(&r->answer)),
+               "r"(smem_u32(&r->answered))
+               : "memory");
+}
+// The block index handed over; false: there is none left, and no more may be asked for.
+__device__ __forceinline__ bool ring_answer(const UnitRing* r, uint32_t* block) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .b128 a;\n .reg .pred p;\n ld.shared.b128 a, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(&r->answer))
+      : "memory");
+  *block = x;
+  return got != 0;
+}
+
+// The asking thread's side: requests made, and whether the last is unanswered.
+struct RingAsker {
+  int asks = 0;
+  bool open = false;
+  __device__ __forceinline__ void ask(UnitRing* r) {
+    ring_ask(r);
+    ++asks;
+    open = true;
+  }
+  __device__ __forceinline__ bool wait(UnitRing* r, const WaitCtl& ctl) {
+    if (!mbar_wait(&r->answered, (asks - 1) & 1, ctl, kErrTimeoutOther)) return false;
+    open = false;
+    return true;
+  }
+  // Before it (as a role) starts on unit i: passes unit i + 1 on.  False: a wait ran out.
+  __device__ __forceinline__ bool pass(UnitRing* r, const PackedArgs& a, int kind, int i, const WaitCtl& ctl) {
+    const int next = i + 1, s = next & 1;
+    PackedUnit u{};
+    bool there = false;
+    if (open) {
+      if (!wait(r, ctl)) return false;
+      uint32_t block;
+      there = ring_answer(r, &block) && packed_unit(a, kind, block, &u);
+      if (there) ask(r);
+    }
+    if (next >= 2 && !mbar_wait(&r->left[s], ((next >> 1) - 1) & 1, ctl, kErrTimeoutOther)) return false;
+    r->unit[s][0] = make_int4(u.row, u.left, u.krow, u.n);
+    r->unit[s][1] = make_int4(u.off, u.pad[0], u.pad[1], there ? 1 : 0);
+    mbar_arrive(&r->full[s]);
+    return true;
+  }
+  // An answer under way must land before the block's shared memory goes.
+  __device__ __forceinline__ void drain(UnitRing* r, const WaitCtl& ctl) {
+    if (open) wait(r, ctl);
+  }
+};
+
+// Whether the block has a unit i (false, too, where a wait ran out).  Whoever was
+// told so arrives on left[i % 2] when done with it.
+__device__ __forceinline__ bool ring_take(UnitRing* r, int i, const WaitCtl& ctl) {
+  if (i == 0) return true;
+  const int s = i & 1;
+  if (!mbar_wait(&r->full[s], ((i - 1) >> 1) & 1, ctl, kErrTimeoutOther)) return false;
+  return r->unit[s][1].w != 0;
+}
+// Unit i, until the role has left it.
+__device__ __forceinline__ PackedUnit ring_unit(const UnitRing* r, int i) {
+  int4 x, y;
+  const uint32_t at = smem_u32(&r->unit[i & 1][0]);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at + 16));
+  return PackedUnit{x.x, x.y, x.z, x.w, y.x, {y.y, y.z, 0}};
 }
 
 // Key tiles that a tile of `tokens` tokens visits, the first of which sees keys up to off.

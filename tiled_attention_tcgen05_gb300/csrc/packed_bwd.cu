@@ -123,9 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   PackedUnit unit;
-  int head;
-  if (!packed_unit(args, kPackedDq, &unit, &head)) return;
-  const int causal = unit.pad[0];
+  if (!packed_unit(args, kPackedDq, blockIdx.x, &unit)) return;
+  const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
   const int nkv = packed_key_tiles(min(unit.left, TB), unit.off, unit.n, causal);
   const bool ragged = nkv * kBN > unit.n;  // the last tile ends behind the keys
@@ -446,9 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   PackedUnit unit;
-  int head;
-  if (!packed_unit(args, kPackedDkdv, &unit, &head)) return;
-  const int causal = unit.pad[0];
+  if (!packed_unit(args, kPackedDkdv, blockIdx.x, &unit)) return;
+  const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
   const int nq = (unit.left + TB - 1) / TB;
   const int box = (D / 64) * TB * G * 128;
