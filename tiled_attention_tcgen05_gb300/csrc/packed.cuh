@@ -84,52 +84,61 @@ cudaError_t launch_packed_dq(bool bf16, int D, const PackedMaps& m, const Packed
 cudaError_t launch_packed_dkdv(bool bf16, int D, const PackedMaps& m, const PackedArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
-// A block's first unit and its key head (PackedUnit::pad[0]: causal, pad[1]: the
-// head); false: nothing to do.  A plan that was not made for these sizes is
-// recorded in the error word.
-__device__ __forceinline__ bool packed_unit(const PackedArgs& a, int kind, uint32_t block, PackedUnit* u) {
-  const PackedHeader* h = reinterpret_cast<const PackedHeader*>(a.plan);
-  const uint32_t i = a.hkv_div.div(block);
-  const int4 h0 = __ldg(reinterpret_cast<const int4*>(h));
-  const int4 h1 = __ldg(reinterpret_cast<const int4*>(h) + 1);
-  const int4 h2 = __ldg(reinterpret_cast<const int4*>(h) + 2);
-  // (the unit is inside the plan's memory whatever the header says)
-  const int4* list = reinterpret_cast<const int4*>(a.plan + a.shape.first(kind)) + 2 * static_cast<size_t>(i);
-  const int4 x = __ldg(list), y = __ldg(list + 1);
+// What a block reads of the plan's header.  A plan that was not made for these
+// sizes is recorded in the error word and has no units.
+struct PackedList {
+  const int4* units;
+  uint32_t items;  // units x key heads; item i is unit i / Hkv, head i % Hkv
+  int causal;
+};
+__device__ __forceinline__ PackedList packed_list(const PackedArgs& a, int kind) {
+  const int4* h = reinterpret_cast<const int4*>(a.plan);
+  const int4 h0 = __ldg(h), h1 = __ldg(h + 1), h2 = __ldg(h + 2);
+  PackedList l;
+  l.units = reinterpret_cast<const int4*>(a.plan + a.shape.first(kind));
+  l.causal = h1.z;
+  l.items = static_cast<uint32_t>(kind == kPackedFwd ? h1.w : kind == kPackedDq ? h2.x : h2.y) * a.shape.Hkv;
   if (h0.x != kPackedMagic || h0.y != a.shape.B || h0.z != a.shape.total_q || h0.w != a.shape.total_k ||
       h1.x != a.shape.Hq || h1.y != a.shape.Hkv) {
-    if (threadIdx.x == 0 && block == 0) cache_error(a.err);
-    return false;
+    if (threadIdx.x == 0 && blockIdx.x == 0) cache_error(a.err);
+    l.items = 0;
   }
-  const int count = kind == kPackedFwd ? h1.w : kind == kPackedDq ? h2.x : h2.y;
-  if (i >= static_cast<uint32_t>(count)) return false;
-  u->row = x.x;
-  u->left = x.y;
-  u->krow = x.z;
-  u->n = x.w;
-  u->off = y.x;
-  u->pad[0] = h1.z;  // causal, of the plan
-  u->pad[1] = static_cast<int>(block - i * a.hkv_div.d);
-  return true;
+  return l;
+}
+// An item's unit (PackedUnit::pad[0]: causal, pad[1]: the key head).
+__device__ __forceinline__ PackedUnit packed_item(const PackedArgs& a, const PackedList& l, uint32_t item) {
+  const uint32_t i = a.hkv_div.div(item);
+  const int4 x = __ldg(l.units + 2 * static_cast<size_t>(i)), y = __ldg(l.units + 2 * static_cast<size_t>(i) + 1);
+  return PackedUnit{x.x, x.y, x.z, x.w, y.x, {l.causal, static_cast<int>(item - i * a.hkv_div.d), 0}};
+}
+
+// Key tiles that a tile of `tokens` tokens visits, the first of which sees keys up to off.
+__host__ __device__ inline int packed_key_tiles(int tokens, int off, int n, int causal) {
+  if (tokens <= 0) return 0;
+  const int all = (n + kBN - 1) / kBN;
+  if (!causal) return all;
+  const long long last = static_cast<long long>(off) + tokens - 1;
+  if (last < 0) return 0;
+  const long long t = last / kBN + 1;
+  return t < all ? static_cast<int>(t) : all;
 }
 
 // ------------------------------------------------------- one block, many units
-// A block that has finished its unit takes over that of a block that has not
-// been launched yet (cluster launch control: the launch is cancelled and its block
-// index handed over), so that its shared memory, tensor memory and rings stay set
-// up and the next unit's tiles arrive while it works on the last one's.
+// Shared memory, tensor memory and the rings stay set up from unit to unit, and the
+// next unit's tiles arrive while a block works on the last one's: a block that has
+// done its unit takes over that of a block that has not been launched yet
+// (cluster launch control: the launch is cancelled and its block index handed
+// over), so units go out one by one, the longest first.
 // One warp asks for units ahead and passes them to the others through two slots;
 // unit i is in slot i % 2, and is passed on only once every other role has
 // left unit i - 2, so that no role is ever two units ahead of another.
 struct UnitRing {
   uint64_t full[2], left[2], answered;
   uint4 answer;       // of the cancellation asked for
-  int4 unit[2][2];    // row, left, krow, n | off, causal, head, 1: there is one
+  int4 unit[2][4];    // words of the kernel's own, made by pass()'s `fill`; [3].w: 1: there is one
 };
 
-__device__ __forceinline__ void ring_init(UnitRing* r, int roles, const PackedUnit& u) {
-  r->unit[0][0] = make_int4(u.row, u.left, u.krow, u.n);
-  r->unit[0][1] = make_int4(u.off, u.pad[0], u.pad[1], 1);
+__device__ __forceinline__ void ring_init(UnitRing* r, int roles) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&r->full[i], 1);
     mbar_init(&r->left[i], roles);
@@ -161,10 +170,10 @@ __device__ __forceinline__ bool ring_answer(const UnitRing* r, uint32_t* block) 
   return got != 0;
 }
 
-// The asking thread's side: requests made, and whether the last is unanswered.
+// The asking thread's side.
 struct RingAsker {
-  int asks = 0;
-  bool open = false;
+  int asks = 0;       // requests made
+  bool open = false;  // the last is unanswered
   __device__ __forceinline__ void ask(UnitRing* r) {
     ring_ask(r);
     ++asks;
@@ -175,20 +184,25 @@ struct RingAsker {
     open = false;
     return true;
   }
-  // Before it (as a role) starts on unit i: passes unit i + 1 on.  False: a wait ran out.
-  __device__ __forceinline__ bool pass(UnitRing* r, const PackedArgs& a, int kind, int i, const WaitCtl& ctl) {
+  // Once in unit i: passes unit i + 1 on; fill(u, words) makes the slot's words of it.
+  // False: a wait ran out.
+  template <typename F>
+  __device__ __forceinline__ bool pass(UnitRing* r, const PackedArgs& a, const PackedList& l, int i, const WaitCtl& ctl,
+                                       F fill) {
     const int next = i + 1, s = next & 1;
-    PackedUnit u{};
-    bool there = false;
+    int4 words[4] = {};
     if (open) {
       if (!wait(r, ctl)) return false;
       uint32_t block;
-      there = ring_answer(r, &block) && packed_unit(a, kind, block, &u);
-      if (there) ask(r);
+      if (ring_answer(r, &block) && block < l.items) {
+        ask(r);
+        fill(packed_item(a, l, block), words);
+        words[3].w = 1;
+      }
     }
     if (next >= 2 && !mbar_wait(&r->left[s], ((next >> 1) - 1) & 1, ctl, kErrTimeoutOther)) return false;
-    r->unit[s][0] = make_int4(u.row, u.left, u.krow, u.n);
-    r->unit[s][1] = make_int4(u.off, u.pad[0], u.pad[1], there ? 1 : 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r->unit[s][k] = words[k];
     mbar_arrive(&r->full[s]);
     return true;
   }
@@ -204,26 +218,15 @@ __device__ __forceinline__ bool ring_take(UnitRing* r, int i, const WaitCtl& ctl
   if (i == 0) return true;
   const int s = i & 1;
   if (!mbar_wait(&r->full[s], ((i - 1) >> 1) & 1, ctl, kErrTimeoutOther)) return false;
-  return r->unit[s][1].w != 0;
+  return r->unit[s][3].w != 0;
 }
-// Unit i, until the role has left it.
-__device__ __forceinline__ PackedUnit ring_unit(const UnitRing* r, int i) {
-  int4 x, y;
-  const uint32_t at = smem_u32(&r->unit[i & 1][0]);
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at + 16));
-  return PackedUnit{x.x, x.y, x.z, x.w, y.x, {y.y, y.z, 0}};
-}
-
-// Key tiles that a tile of `tokens` tokens visits, the first of which sees keys up to off.
-__host__ __device__ inline int packed_key_tiles(int tokens, int off, int n, int causal) {
-  if (tokens <= 0) return 0;
-  const int all = (n + kBN - 1) / kBN;
-  if (!causal) return all;
-  const long long last = static_cast<long long>(off) + tokens - 1;
-  if (last < 0) return 0;
-  const long long t = last / kBN + 1;
-  return t < all ? static_cast<int>(t) : all;
+// Words k of unit i, until the role has left it.
+__device__ __forceinline__ int4 ring_words(const UnitRing* r, int i, int k) {
+  int4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(smem_u32(&r->unit[i & 1][k])));
+  return x;
 }
 
 // Rows [first, 128) of a 128-row tile of NB 64-column blocks set to zero by one

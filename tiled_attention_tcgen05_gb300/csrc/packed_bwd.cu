@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  PackedUnit unit;
-  if (!packed_unit(args, kPackedDq, blockIdx.x, &unit)) return;
+  const PackedList list = packed_list(args, kPackedDq);
+  if (blockIdx.x >= list.items) return;
+  const PackedUnit unit = packed_item(args, list, blockIdx.x);
   const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
   const int nkv = packed_key_tiles(min(unit.left, TB), unit.off, unit.n, causal);
@@ -444,8 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  PackedUnit unit;
-  if (!packed_unit(args, kPackedDkdv, blockIdx.x, &unit)) return;
+  const PackedList list = packed_list(args, kPackedDkdv);
+  if (blockIdx.x >= list.items) return;
+  const PackedUnit unit = packed_item(args, list, blockIdx.x);
   const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
   const int nq = (unit.left + TB - 1) / TB;

@@ -6,18 +6,19 @@
 //
 // A CTA works on two 128-row query tiles of one key head (packed.cuh: TB tokens x G
 // heads each) that share every K/V tile: warps 0-3 and 4-7 run their softmax, one
-// thread a row, warp 8 feeds Q and the K and V rings by TMA, warp 9 issues the
-// MMAs, alternating between the tiles so that one's softmax runs beside the other's
-// products, and warps 10 and 11 look after the key tiles that some row sees only in part:
+// thread a row (and each group's first thread loads its Q and stores its O), warp 8
+// feeds the K and V rings by TMA, warp 9 issues the MMAs, alternating between the
+// tiles so that one's softmax runs beside the other's products, and warps 10 and 11
+// look after the key tiles that some row sees only in part:
 //   * the rows behind the sequence's keys belong to another sequence or to
 //     nobody, and a weight of zero times an infinity there would be NaN:
 //     they become zeros;
 //   * so would an infinity or a NaN in the value of a key that only some rows
 //     see: such elements become zeros for the product, and the rows that see them
 //     get them back from memory at the end.
-// They follow every V tile between its arrival and its product.  A CTA takes
-// over the units of CTAs that have not started (UnitRing); the rings run on
-// from one unit to the next.
+// Such tiles are the last ones of a unit, three at most; they come in through
+// barriers of their own.  The rings run on from one unit to the next (UnitRing);
+// warp 11 asks for the units.
 #include <cstdio>
 
 #include "launch.h"
@@ -29,12 +30,15 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kCare = 10;  // warps; kCare and the one behind it
+// registers: 384 x 168 at launch = 256 x 200 (softmax) + 128 x 104
+constexpr int kPart = 3;  // tiles that some row sees in part: its tokens' last keys lie within 256 of each other
+
 template <int D>
 struct PfCfg {
   static constexpr int TILE = (D / 64) * kBM * 128;
   static constexpr int KST = D == 128 ? 3 : 4;  // K ring depth
   static constexpr int VST = D == 128 ? 2 : 4;  // V ring depth
-  static constexpr int QB = D == 128 ? 1 : 2;   // pairs of Q tiles (their memory takes O on its way out)
+  static constexpr int QB = D == 128 ? 1 : 2;   // Q tiles of each group (their memory takes O on its way out)
   static constexpr int SMEM = (2 * QB + KST + VST) * TILE + 1024;
   static_assert(SMEM + 2048 <= kSmemMax, "tiles do not fit in shared memory");
 };
@@ -65,28 +69,54 @@ __device__ __forceinline__ uint32_t non_finite2(uint32_t w) {
   constexpr uint32_t E = BF ? 0x7f807f80u : 0x7c007c00u;
   return __vcmpeq2(w & E, E);
 }
+// Bit 15 of a half is set where it is one: an exponent of ones carries into it.
+template <bool BF>
+__device__ __forceinline__ uint32_t non_finite_bits(uint32_t w) {
+  constexpr uint32_t E = BF ? 0x7f807f80u : 0x7c007c00u, ONE = BF ? 0x00800080u : 0x04000400u;
+  return (w & E) + ONE;
+}
 
-// What the roles derive from a unit.
+// What the roles need of a unit, made by the asking thread.
 struct Pair {
-  int head, row, krow, n;   // key head, first token's row, first key's row, keys
-  int left[2], n_t[2];      // of each tile: tokens from its first to the sequence's end, key tiles
-  int off;                  // last key that the first token sees
-  int causal, nt, t_part;   // key tiles; from t_part on some row sees a tile in part, or it ends behind the keys
-  __device__ __forceinline__ Pair(const PackedUnit& u, int TB) {
-    head = u.pad[1];
-    causal = u.pad[0];
-    row = u.row;
-    krow = u.krow;
-    n = u.n;
-    off = u.off;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      left[w] = u.left - w * TB;
-      n_t[w] = packed_key_tiles(min(left[w], TB), off + w * TB, n, causal);
+  int row, krow, n, off;            // first token's row, first key's row, keys, last key the first token sees
+  int left, n0, n1, head;           // tokens to the sequence's end, key tiles of the two tiles, key head
+  int t_part, causal;               // from t_part on some row sees a tile in part, or it ends behind the keys
+  __device__ __forceinline__ Pair(const UnitRing* r, int i) {
+    const int4 a = ring_words(r, i, 0), b = ring_words(r, i, 1), c = ring_words(r, i, 2);
+    row = a.x;
+    krow = a.y;
+    n = a.z;
+    off = a.w;
+    left = b.x;
+    n0 = b.y;
+    n1 = b.z;
+    head = b.w;
+    t_part = c.x;
+    causal = c.y;
+  }
+  __device__ __forceinline__ int nt() const { return max(n0, n1); }
+  __device__ __forceinline__ int n_t(int w) const { return w ? n1 : n0; }
+};
+__device__ __forceinline__ void make_pair(const PackedUnit& u, int TB, int4 (&words)[4]) {
+  const int causal = u.pad[0];
+  const int n0 = packed_key_tiles(min(u.left, TB), u.off, u.n, causal);
+  const int n1 = packed_key_tiles(min(u.left - TB, TB), u.off + TB, u.n, causal);
+  int t_part = u.n / kBN;
+  if (causal) t_part = min(t_part, u.off < 0 ? 0 : (u.off + 1) / kBN);
+  words[0] = make_int4(u.row, u.krow, u.n, u.off);
+  words[1] = make_int4(u.left, n0, n1, u.pad[1]);
+  words[2] = make_int4(t_part, causal, 0, 0);
+}
+// A ring's next slot and the parity of its phase.
+template <int N>
+struct RingAt {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1u;
     }
-    nt = max(n_t[0], n_t[1]);
-    t_part = n / kBN;
-    if (causal) t_part = min(t_part, off < 0 ? 0 : (off + 1) / kBN);
   }
 };
 
@@ -101,34 +131,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) UnitRing ring;
-  __shared__ __align__(8) uint64_t bar_q[QB], bar_qfree[QB], bar_ofinal[QB];
-  __shared__ __align__(8) uint64_t bar_k[KST], bar_kempty[KST], bar_v[VST], bar_vempty[VST], bar_care[VST];
-  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2], bar_o[2];
+  __shared__ __align__(8) uint64_t bar_k[KST], bar_kempty[KST], bar_v[VST], bar_vempty[VST];
+  __shared__ __align__(8) uint64_t bar_part[2][kPart], bar_care[2][kPart];  // [unit % 2]: such a tile is in, is seen to
+  __shared__ __align__(8) uint64_t bar_q[2][QB], bar_s[2], bar_p[2], bar_o[2], bar_ofinal[2];  // [group]
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ int care_odd[VST][2];  // a V tile held non-finite values that only some rows see (by caring warp)
-  __shared__ int unit_odd[2];       // any of unit i's did, at i % 2
+  __shared__ int care_odd[2][kPart][2];  // the tile held non-finite values that only some rows see (by caring warp)
+  __shared__ int unit_odd[2];            // [group]: any of its last unit's did
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  PackedUnit first;
-  if (!packed_unit(args, kPackedFwd, blockIdx.x, &first)) return;
+  const PackedList list = packed_list(args, kPackedFwd);
+  if (blockIdx.x >= list.items) return;
   const int G = args.shape.G, TB = args.shape.TB;
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  auto sQ = [&](int qb, int w) { return base + (2 * qb + w) * C::TILE; };
+  auto sQ = [&](int w, int qb) { return base + (w * QB + qb) * C::TILE; };
   auto sK = [&](int st) { return base + (2 * QB + st) * C::TILE; };
   auto sV = [&](int st) { return base + (2 * QB + KST + st) * C::TILE; };
 
+  const bool asks = threadIdx.x == (kCare + 1) * 32;
+  if (asks) {
+    make_pair(packed_item(args, list, blockIdx.x), TB, ring.unit[0]);
+    ring.unit[0][3].w = 1;
+  }
   WaitCtl ctl{args.err, args.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    ring_init(&ring, 8 + 1 + 3 + 1, first);  // softmax warps, MMA, three producing lanes, warp 10
-    for (int q = 0; q < QB; ++q) {
-      mbar_init(&bar_q[q], 1);
-      mbar_init(&bar_qfree[q], 8);
-      mbar_init(&bar_ofinal[q], 2);
-    }
+    ring_init(&ring, 8 + 1 + 2 + 1);  // softmax warps, MMA, two producing lanes, warp 10
     for (int s = 0; s < KST; ++s) {
       mbar_init(&bar_k[s], 1);
       mbar_init(&bar_kempty[s], 1);
@@ -136,12 +166,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < VST; ++s) {
       mbar_init(&bar_v[s], 1);
       mbar_init(&bar_vempty[s], 1);
-      mbar_init(&bar_care[s], 2);
     }
     for (int w = 0; w < 2; ++w) {
+      for (int j = 0; j < kPart; ++j) {
+        mbar_init(&bar_part[w][j], 1);
+        mbar_init(&bar_care[w][j], 2);
+      }
+      for (int q = 0; q < QB; ++q) mbar_init(&bar_q[w][q], 1);
       mbar_init(&bar_s[w], 1);
       mbar_init(&bar_p[w], 4);
       mbar_init(&bar_o[w], 1);
+      mbar_init(&bar_ofinal[w], 2);
     }
     fence_mbar_init();
   }
@@ -153,121 +188,154 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const uint32_t col_s[2] = {0u, 128u};
-  const uint32_t col_o[2] = {256u, 256u + D};
+  constexpr uint32_t kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
 
-  // registers: 384 x 168 at launch = 256 x 200 (softmax) + 128 x 104
+  int zero = 0;  // (an exit waits for its own copies whatever the abort flag says)
+  const WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
   if (warp == kProducer) {
-    // ---------------- TMA producer: lane 0 the K ring, lane 1 the V ring, lane 2 Q
+    // ------------------------ TMA producer: lane 0 the K ring, lane 1 the V ring
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (lane < 3) {
-      int issued = 0;  // tiles of the ring, or pairs of Q tiles, so far
+    if (lane < 2) {
+      const bool is_k = lane == 0;
+      const int depth = is_k ? KST : VST;
+      uint64_t* full = is_k ? bar_k : bar_v;
+      uint64_t* empty = is_k ? bar_kempty : bar_vempty;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      int e = 0;             // tiles so far
+      uint32_t own = 0;      // V slots whose last tile came through bar_part
+      uint32_t part_ph = 0;  // parities of bar_part's phases (those armed so far are odd in number)
       bool ok = true;
-      const int depth = lane == 0 ? KST : VST;
-      uint64_t* full = lane == 0 ? bar_k : bar_v;
-      uint64_t* empty = lane == 0 ? bar_kempty : bar_vempty;
-      const CUtensorMap* map = lane == 0 ? &tm_k : &tm_v;
-      for (int i = 0;; ++i) {
-        if (!ring_take(&ring, i, ctl)) break;
-        const Pair p(ring_unit(&ring, i), TB);
-        if (lane < 2) {
-          for (int t = 0; t < p.nt; ++t, ++issued) {
-            const int st = issued % depth;
-            if (issued >= depth && !(ok = mbar_wait(&empty[st], ((issued / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
-            mbar_expect_tx(&full[st], C::TILE);
-            load_rows<D>(lane == 0 ? sK(st) : sV(st), map, &full[st], p.krow + t * kBN, p.head);
+      for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
+        const Pair p(&ring, i);
+        const int nt = p.nt();
+        for (int t = 0; t < nt; ++t, ++e) {
+          const int st = e % depth;
+          if (e >= depth && !(ok = mbar_wait(&empty[st], ((e / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
+          uint64_t* bar = &full[st];
+          if (!is_k && t >= p.t_part) {
+            const int j = t - p.t_part;
+            mbar_arrive(bar);  // (the ring's own phase passes on)
+            bar = &bar_part[i & 1][j];
+            part_ph ^= 1u << ((i & 1) * kPart + j);
+            own |= 1u << st;
+          } else {
+            own &= ~(1u << st);
           }
-        } else if (p.nt > 0) {
-          const int qb = issued % QB;
-          ok = issued < QB || mbar_wait(&bar_qfree[qb], ((issued / QB) - 1) & 1, ctl, kErrTimeoutSoftmax);
-          if (ok) {
-            const int tiles = p.left[1] > 0 ? 2 : 1;
-            mbar_expect_tx(&bar_q[qb], tiles * (D / 64) * TB * G * 128);  // rows past a tile's TB x G are not loaded
-            for (int w = 0; w < tiles; ++w) load_rows<D>(sQ(qb, w), &tm_q, &bar_q[qb], p.head * G, p.row + w * TB);
-            ++issued;
-          }
+          mbar_expect_tx(bar, C::TILE);
+          load_rows<D>(is_k ? sK(st) : sV(st), map, bar, p.krow + t * kBN, p.head);
         }
-        if (!ok) break;
-        mbar_arrive(&ring.left[i & 1]);
+        if (ok) mbar_arrive(&ring.left[i & 1]);
       }
-      // never leave a TMA write in flight behind an exit
-      int zero = 0;
-      WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
-      if (lane == 2) {
-        for (int u = issued - QB > 0 ? issued - QB : 0; u < issued; ++u)
-          mbar_wait(&bar_q[u % QB], (u / QB) & 1, drain, kErrTimeoutTma);
-      } else {
-        for (int t = issued - depth > 0 ? issued - depth : 0; t < issued; ++t)
-          mbar_wait(&full[t % depth], (t / depth) & 1, drain, kErrTimeoutTma);
-      }
+      for (int t = e - depth > 0 ? e - depth : 0; t < e; ++t)
+        if (!(own >> (t % depth) & 1u)) mbar_wait(&full[t % depth], (t / depth) & 1, drain, kErrTimeoutTma);
+      if (!is_k)  // (a phase that was never armed: the parity of the one before it, which has passed)
+        for (int j = 0; j < 2 * kPart; ++j)
+          mbar_wait(&bar_part[j / kPart][j % kPart], (part_ph >> j & 1u) ^ 1u, drain, kErrTimeoutTma);
     }
   } else if (warp == kMma) {
     // --------------------------------------------------------- MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr uint32_t idesc_qk = idesc_f16(kBM, kBN, BF, false, false);
     constexpr uint32_t idesc_pv = idesc_f16(kBM, D, BF, false, true);
-    int ik = 0, iv = 0, uq = 0;  // K tiles, V tiles and units with keys so far
-    int np[2] = {0, 0};          // tiles of each group so far
+    RingAt<KST> k;
+    RingAt<VST> v;
+    RingAt<QB> q[2];
+    uint32_t np0 = 0, np1 = 0;  // parities of the groups' tiles
+    uint32_t part_ph = 0;
     bool ok = true;
-    for (int i = 0;; ++i) {
+    for (int i = 0; ok; ++i) {
       if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
-      const Pair p(ring_unit(&ring, i), TB);
-      if (p.nt > 0) {
-        const int qb = uq % QB;
-        const uint32_t aQ[2] = {smem_u32(sQ(qb, 0)), smem_u32(sQ(qb, 1))};
+      int n0, n1, t_part;
+      {
+        const Pair p(&ring, i);
+        n0 = p.n0;
+        n1 = p.n1;
+        t_part = p.t_part;
+      }
+      const int nt = max(n0, n1);
+      if (nt > 0) {
+        const uint32_t aQ0 = smem_u32(sQ(0, q[0].st)), aQ1 = smem_u32(sQ(1, q[1].st));
         int odd = 0;
-        ok = warp_wait(&bar_q[qb], (uq / QB) & 1, ctl, kErrTimeoutTma) &&
-             warp_wait(&bar_k[ik % KST], (ik / KST) & 1, ctl, kErrTimeoutTma);
-        if (ok) {
-          tc_fence_after();
-          const int sk = ik % KST;
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            if (p.n_t[w] > 0) {
-              mma_abT<D>(tmem + col_s[w], aQ[w], smem_u32(sK(sk)), idesc_qk);
-              commit_el(&bar_s[w]);
-            }
-          commit_el(&bar_kempty[sk]);
-          ++ik;
-        }
-        for (int t = 0; ok && t < p.nt; ++t, ++iv) {
-          const int sv = iv % VST;
-          const int sk1 = ik % KST;
-          if (!(ok = warp_wait(&bar_care[sv], (iv / VST) & 1, ctl, kErrTimeoutTma))) break;
-          if (t >= p.t_part) odd |= care_odd[sv][0] | care_odd[sv][1];
-          const bool next = t + 1 < p.nt;
-          if (next && !(ok = warp_wait(&bar_k[sk1], (ik / KST) & 1, ctl, kErrTimeoutTma))) break;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (t < p.n_t[w]) {
-              if (!(ok = warp_wait(&bar_p[w], np[w] & 1, ctl, kErrTimeoutSoftmax))) break;
-              ++np[w];
-              tc_fence_after();
-              mma_pv<D>(tmem + col_o[w], tmem + col_s[w], smem_u32(sV(sv)), idesc_pv, t > 0);
-              commit_el(&bar_o[w]);
-            }
-            if (next && t + 1 < p.n_t[w]) {
-              mma_abT<D>(tmem + col_s[w], aQ[w], smem_u32(sK(sk1)), idesc_qk);
-              commit_el(&bar_s[w]);
-            }
+        ok = warp_wait(&bar_k[k.st], k.ph, ctl, kErrTimeoutTma);
+        if (ok && n0 > 0) {
+          ok = warp_wait(&bar_q[0][q[0].st], q[0].ph, ctl, kErrTimeoutTma);
+          if (ok) {
+            q[0].step();
+            tc_fence_after();
+            mma_abT<D>(tmem, aQ0, smem_u32(sK(k.st)), idesc_qk);
+            commit_el(&bar_s[0]);
           }
-          if (!ok) break;
-          commit_el(&bar_vempty[sv]);
-          if (next) {
-            commit_el(&bar_kempty[sk1]);
-            ++ik;
+        }
+        if (ok && n1 > 0) {
+          ok = warp_wait(&bar_q[1][q[1].st], q[1].ph, ctl, kErrTimeoutTma);
+          if (ok) {
+            q[1].step();
+            tc_fence_after();
+            mma_abT<D>(tmem + kColS1, aQ1, smem_u32(sK(k.st)), idesc_qk);
+            commit_el(&bar_s[1]);
           }
         }
         if (!ok) break;
-        commit_el(&bar_ofinal[qb]);
-        if (lane == 0) {
-          unit_odd[i & 1] = odd;
-          mbar_arrive(&bar_ofinal[qb]);  // (with the flag behind it)
+        commit_el(&bar_kempty[k.st]);
+        k.step();
+        for (int t = 0; t < nt; ++t) {
+          if (t < t_part) {
+            ok = warp_wait(&bar_v[v.st], v.ph, ctl, kErrTimeoutTma);
+          } else {
+            const int j = t - t_part, bit = (i & 1) * kPart + j;
+            ok = warp_wait(&bar_care[i & 1][j], part_ph >> bit & 1u, ctl, kErrTimeoutOther);
+            part_ph ^= 1u << bit;
+            if (ok) odd |= care_odd[i & 1][j][0] | care_odd[i & 1][j][1];
+          }
+          if (!ok) break;
+          const bool next = t + 1 < nt;
+          if (next && !(ok = warp_wait(&bar_k[k.st], k.ph, ctl, kErrTimeoutTma))) break;
+          if (t < n0) {
+            if (!(ok = warp_wait(&bar_p[0], np0, ctl, kErrTimeoutSoftmax))) break;
+            np0 ^= 1u;
+            tc_fence_after();
+            mma_pv<D>(tmem + kColO0, tmem, smem_u32(sV(v.st)), idesc_pv, t > 0);
+            commit_el(&bar_o[0]);
+            if (t + 1 < n0) {
+              mma_abT<D>(tmem, aQ0, smem_u32(sK(k.st)), idesc_qk);
+              commit_el(&bar_s[0]);
+            } else {
+              commit_el(&bar_ofinal[0]);
+              if (lane == 0) {
+                unit_odd[0] = odd;
+                mbar_arrive(&bar_ofinal[0]);  // (with the flag behind it)
+              }
+              __syncwarp();
+            }
+          }
+          if (t < n1) {
+            if (!(ok = warp_wait(&bar_p[1], np1, ctl, kErrTimeoutSoftmax))) break;
+            np1 ^= 1u;
+            tc_fence_after();
+            mma_pv<D>(tmem + kColO1, tmem + kColS1, smem_u32(sV(v.st)), idesc_pv, t > 0);
+            commit_el(&bar_o[1]);
+            if (t + 1 < n1) {
+              mma_abT<D>(tmem + kColS1, aQ1, smem_u32(sK(k.st)), idesc_qk);
+              commit_el(&bar_s[1]);
+            } else {
+              commit_el(&bar_ofinal[1]);
+              if (lane == 0) {
+                unit_odd[1] = odd;
+                mbar_arrive(&bar_ofinal[1]);
+              }
+              __syncwarp();
+            }
+          }
+          commit_el(&bar_vempty[v.st]);
+          v.step();
+          if (next) {
+            commit_el(&bar_kempty[k.st]);
+            k.step();
+          }
         }
-        ++uq;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
+      if (ok && lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
   } else if (warp >= kCare) {
     // ------------------ value tiles that some row sees in part; warp 11: units ahead
@@ -275,56 +343,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp - kCare;
     const int r0 = half * 64;  // each warp's half of the tile's rows
     RingAsker asker;
-    if (half == 1 && lane == 0) asker.ask(&ring);
-    int iv = 0;
+    if (asks) asker.ask(&ring);
+    int vst = 0;  // V slot of the unit's first tile
+    uint32_t part_ph = 0;
     bool ok = true;
-    for (int i = 0;; ++i) {
+    for (int i = 0; ok; ++i) {
       if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
       if (half == 1) {
-        if (lane == 0) ok = asker.pass(&ring, args, kPackedFwd, i, ctl);
+        if (asks)
+          ok = asker.pass(&ring, args, list, i, ctl,
+                          [&](const PackedUnit& u, int4(&words)[4]) { make_pair(u, TB, words); });
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-      const Pair p(ring_unit(&ring, i), TB);
-      for (int t = 0; t < p.nt; ++t, ++iv) {
-        const int sv = iv % VST;
-        if (!(ok = warp_wait(&bar_v[sv], (iv / VST) & 1, ctl, kErrTimeoutTma))) break;
-        if (t >= p.t_part) {
-          const int valid = min(kBN, p.n - t * kBN);  // rows of the tile that are keys
-          bool odd = false;
+      const Pair p(&ring, i);
+      const int nt = p.nt();
+      for (int t = p.t_part; t < nt; ++t) {
+        const int j = t - p.t_part, bit = (i & 1) * kPart + j;
+        if (!(ok = warp_wait(&bar_part[i & 1][j], part_ph >> bit & 1u, ctl, kErrTimeoutTma))) break;
+        part_ph ^= 1u << bit;
+        const int valid = min(kBN, p.n - t * kBN);  // rows of the tile that are keys
+        const int keys = min(max(valid - r0, 0), 64) * 8;  // 16-byte pieces
+        uint4* rows = reinterpret_cast<uint4*>(sV((vst + t) % VST) + r0 * 128);
+        uint32_t bits = 0;
 #pragma unroll
-          for (int kb = 0; kb < D / 64; ++kb) {
-            uint4* rows = reinterpret_cast<uint4*>(sV(sv) + kb * (kBM * 128) + r0 * 128);
-            const int keys = min(max(valid - r0, 0), 64) * 8;  // 16-byte pieces
-            for (int j = keys + lane; j < 64 * 8; j += 32) rows[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.causal) {
-#pragma unroll 4
-              for (int j = lane; j < keys; j += 32) {
-                uint4 x = rows[j];
-                const uint4 m = make_uint4(non_finite2<BF>(x.x), non_finite2<BF>(x.y), non_finite2<BF>(x.z),
-                                           non_finite2<BF>(x.w));
-                if (m.x | m.y | m.z | m.w) {
-                  odd = true;
-                  rows[j] = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
-                }
-              }
+        for (int kb = 0; kb < D / 64; ++kb) {
+          uint4* blk = rows + kb * (kBM * 8);
+          for (int x = keys + lane; x < 64 * 8; x += 32) blk[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.causal) {
+#pragma unroll 8
+            for (int x = lane; x < keys; x += 32) {
+              const uint4 y = blk[x];
+              bits |= non_finite_bits<BF>(y.x) | non_finite_bits<BF>(y.y) | non_finite_bits<BF>(y.z) |
+                      non_finite_bits<BF>(y.w);
             }
           }
-          odd = __any_sync(0xffffffffu, odd);
-          if (lane == 0) care_odd[sv][half] = odd;
-          fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&bar_care[sv]);
+        const bool odd = __any_sync(0xffffffffu, (bits & 0x80008000u) != 0u);
+        if (odd) {
+          for (int kb = 0; kb < D / 64; ++kb)
+            for (int x = lane; x < keys; x += 32) {
+              uint4 y = rows[kb * (kBM * 8) + x];
+              y.x &= ~non_finite2<BF>(y.x);
+              y.y &= ~non_finite2<BF>(y.y);
+              y.z &= ~non_finite2<BF>(y.z);
+              y.w &= ~non_finite2<BF>(y.w);
+              rows[kb * (kBM * 8) + x] = y;
+            }
+        }
+        if (lane == 0) care_odd[i & 1][j][half] = odd;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_care[i & 1][j]);
       }
-      if (!ok) break;
+      vst = (vst + nt) % VST;
       __syncwarp();
-      if (half == 0 && lane == 0) mbar_arrive(&ring.left[i & 1]);
+      if (ok && half == 0 && lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
-    if (half == 1 && lane == 0) {
-      int zero = 0;
-      WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
-      asker.drain(&ring, drain);
-    }
+    if (asks) asker.drain(&ring, drain);
   } else {
     // ------------------------------- softmax / correction / epilogue (tile w)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -332,21 +407,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const int tok = static_cast<int>(args.g_div.div(r)), g = r - tok * G;  // of the tile
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t scol = w ? col_s[1] : col_s[0], ocol = w ? col_o[1] : col_o[0];
-    int np = 0, uq = 0;  // tiles of this group, units with keys so far
+    const uint32_t scol = w ? kColS1 : 0u, ocol = w ? kColO1 : kColO0;
+    const bool serves = r == 0;  // the group's thread that loads Q and stores O
+    uint32_t np = 0, units = 0;  // parities of this group's tiles, and units with any
+    RingAt<QB> q;                // Q of the unit at hand
+    uint32_t q_armed = 0;        // (serving thread) Q tiles asked for
+    // Q of unit i's tile of this group into buffer st, which nothing reads any more
+    auto load_q = [&](int i, int st) {
+      const Pair p(&ring, i);
+      if (p.n_t(w) == 0) return;
+      mbar_expect_tx(&bar_q[w][st], (D / 64) * TB * G * 128);  // rows past a tile's TB x G are not loaded
+      load_rows<D>(sQ(w, st), &tm_q, &bar_q[w][st], p.head * G, p.row + w * TB);
+      ++q_armed;
+    };
+    // Q of the unit behind unit i, if there is one (this thread waits until it is known)
+    auto load_next_q = [&](int i, int st) {
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // O of the buffer's last unit is on its way
+      if (ring_take(&ring, i + 1, ctl)) load_q(i + 1, st);
+    };
+    if (serves) load_q(0, 0);
     bool ok = true;
     for (int i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
       int n, sees, t_part;  // key tiles, last key of this row (the rest of the unit is read again behind the loop)
       {
-        const Pair p(ring_unit(&ring, i), TB);
-        n = w ? p.n_t[1] : p.n_t[0];
+        const Pair p(&ring, i);
+        n = p.n_t(w);
         sees = p.causal ? min(p.n - 1, p.off + w * TB + tok) : p.n - 1;
         t_part = p.t_part;
       }
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = 0; t < n; ++t, ++np) {
-        if (!(ok = warp_wait(&bar_s[w], np & 1, ctl, kErrTimeoutMma))) break;
+      for (int t = 0; t < n; ++t, np ^= 1u) {
+        if (!(ok = warp_wait(&bar_s[w], np, ctl, kErrTimeoutMma))) break;
         tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -358,9 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 128; ++j) x[j] = __uint_as_float(s[j]);
         if (t >= t_part) {
           const int lim = sees - t * kBN;
+          const int near = __shfl_sync(0xffffffffu, lim, 0);  // (rows' tokens ascend)
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j > lim) x[j] = -INFINITY;
+          for (int c = 0; c < 4; ++c) {
+            if (32 * c + 31 > near) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * c + j > lim) x[32 * c + j] = -INFINITY;
+            }
+          }
         }
         float mx8[8];  // eight three-input max chains of 16 scores each
 #pragma unroll
@@ -400,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
         l = l * alpha + (rsa.x + rsa.y);
         if (t > 0 && __any_sync(0xffffffffu, resc)) {
-          if (!(ok = warp_wait(&bar_o[w], (np - 1) & 1, ctl, kErrTimeoutMma))) break;
+          if (!(ok = warp_wait(&bar_o[w], np ^ 1u, ctl, kErrTimeoutMma))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -416,50 +514,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_p[w]);
+        if (QB == 2 && t == 0 && serves) load_next_q(i, q.st ^ 1);
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      const Pair p(ring_unit(&ring, i), TB);
-      const int left = w ? p.left[1] : p.left[0];
-      const int qb = uq % QB;
-      if (p.nt > 0) {
-        if (!(ok = warp_wait(&bar_ofinal[qb], (uq / QB) & 1, ctl, kErrTimeoutMma))) break;
-        ++uq;
-      }
-      tc_fence_after();
+      const Pair p(&ring, i);
+      const int left = p.left - w * TB;
       const int tokens = min(left, TB);  // (none: the sequence ends before this tile)
-      if (tokens > 0) {
-        const size_t qrow = static_cast<size_t>(p.row) + w * TB;
+      const long long qrow = static_cast<long long>(p.row) + w * TB;
+      auto out_row = [&](int j) -> void* {
+        if (j >= tokens * G) return nullptr;
+        const int k = static_cast<int>(args.g_div.div(j));
+        return static_cast<T*>(args.o) + (qrow + k) * args.o_t + (p.head * G + j - k * G) * args.o_h;
+      };
+      if (n == 0) {  // rows that see nothing
+        if (serves) load_next_q(i, q.st);
+        if (tok < tokens) args.lse[(qrow + tok) * args.shape.Hq + p.head * G + g] = -INFINITY;
+        const int c = args.dg >> 3;
+        for (int j = r; j < tokens * G * c; j += 128) {
+          const int row = j / c;
+          static_cast<uint4*>(out_row(row))[j - row * c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      } else {
+        if (!(ok = warp_wait(&bar_ofinal[w], units, ctl, kErrTimeoutMma))) break;
+        units ^= 1u;
+        tc_fence_after();
         if (tok < tokens)
-          args.lse[(qrow + tok) * args.shape.Hq + p.head * G + g] =
-              (n > 0 && l != 0.f) ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
-        T* const out = static_cast<T*>(args.o) + static_cast<long long>(qrow) * args.o_t + p.head * G * args.o_h;
-        auto out_row = [&](int j) -> void* {
-          if (j >= tokens * G) return nullptr;
-          const int k = static_cast<int>(args.g_div.div(j));
-          return out + k * args.o_t + (j - k * G) * args.o_h;
-        };
-        if (n == 0) {  // rows that see nothing
-          const int c = args.dg >> 3;
-          for (int j = r; j < tokens * G * c; j += 128) {
-            const int row = j / c;
-            static_cast<uint4*>(out_row(row))[j - row * c] = make_uint4(0u, 0u, 0u, 0u);
-          }
-        } else {
-          const float inv_l = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-          // non-finite values that were taken out of this unit's tiles: this row's are added to O here
-          const bool odd = p.causal && *reinterpret_cast<volatile int*>(&unit_odd[i & 1]) != 0;
-          const uint32_t stage = smem_u32(sQ(qb, w));
+          args.lse[(qrow + tok) * args.shape.Hq + p.head * G + g] = l != 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
+        const float inv_l = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+        const uint32_t stage = smem_u32(sQ(w, q.st));  // (its products are done)
+        // non-finite values that were taken out of this unit's tiles: this row's are added to O here
+        if (p.causal && *reinterpret_cast<volatile int*>(&unit_odd[w]) != 0) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
             tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
             tmem_ld_wait(ov);
-            float scale = inv_l;
-            if (odd && tok < tokens && l > 0.f) {
-              const int ng = chunk_groups(args.dg, 32 * c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * inv_l);
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * inv_l);
+            if (tok < tokens && l > 0.f) {
+              const int ng = chunk_groups(args.dg, 32 * c);
               for (int k = t_part * kBN; k <= min(sees, n * kBN - 1); ++k) {
                 const T* vrow = static_cast<const T*>(args.v) + (static_cast<long long>(p.krow) + k) * args.vt +
                                 p.head * args.vh + 32 * c;
@@ -469,43 +563,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint4 xv = __ldg(reinterpret_cast<const uint4*>(vrow) + q);
                   const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const uint32_t m = non_finite2<BF>(xs[e]);
+                  for (int k2 = 0; k2 < 4; ++k2) {
+                    const uint32_t m = non_finite2<BF>(xs[k2]);
                     if (!m) continue;
-                    const uint32_t y = xs[e] & m;
+                    const uint32_t y = xs[k2] & m;
                     const T* h = reinterpret_cast<const T*>(&y);
-                    if (m & 0xffffu)
-                      ov[8 * q + 2 * e] = __float_as_uint(__uint_as_float(ov[8 * q + 2 * e]) + static_cast<float>(h[0]));
-                    if (m >> 16)
-                      ov[8 * q + 2 * e + 1] =
-                          __float_as_uint(__uint_as_float(ov[8 * q + 2 * e + 1]) + static_cast<float>(h[1]));
+                    float *lo = reinterpret_cast<float*>(&ov[8 * q + 2 * k2]), *hi = lo + 1;
+                    if (m & 0xffffu) *lo += static_cast<float>(h[0]);
+                    if (m >> 16) *hi += static_cast<float>(h[1]);
                   }
                 }
               }
-              scale = 1.f;
             }
-            stage_row_chunk_sw128<BF>(stage, r, c, ov, scale);
+            stage_row_chunk_sw128<BF>(stage, r, c, ov, 1.f);
           }
-          tc_fence_before();  // O's columns are free for the next unit
-          fence_proxy_async_smem();
-          named_bar_sync(1 + w, 4 * 32);  // the tile's four warps have staged their rows
-          if (left >= TB) {  // whole: a box
-            if ((warp & 3) == 0 && lane == 0) {
+        } else {
 #pragma unroll
-              for (int kb = 0; kb < D / 64; ++kb)
-                tma_store_3d(&tm_o, sQ(qb, w) + kb * (kBM * 128), kb * 64, p.head * G, p.row + w * TB);
-              tma_store_commit_and_wait_read();
-            }
-          } else {  // the rows behind it are another sequence's
-            copy_tile_rows(sQ(qb, w), args.dg, r, 128, out_row);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
+            tmem_ld_wait(ov);
+            stage_row_chunk_sw128<BF>(stage, r, c, ov, inv_l);
           }
         }
+        tc_fence_before();  // O's columns are free for the next unit
+        fence_proxy_async_smem();
+        named_bar_sync(1 + w, 4 * 32);  // the tile's four warps have staged their rows
+        if (left >= TB) {  // whole: a box
+          if (serves) {
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_store_3d(&tm_o, sQ(w, q.st) + kb * (kBM * 128), kb * 64, p.head * G, p.row + w * TB);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {  // the rows behind it are another sequence's
+          copy_tile_rows(sQ(w, q.st), args.dg, r, 128, out_row);
+          named_bar_sync(1 + w, 4 * 32);
+        }
+        if (QB == 1 && serves) load_next_q(i, 0);
+        q.step();
       }
       __syncwarp();
-      if (lane == 0) {
-        if (p.nt > 0) mbar_arrive(&bar_qfree[qb]);
-        mbar_arrive(&ring.left[i & 1]);
-      }
+      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
+    }
+    if (serves) {
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      for (uint32_t a = q_armed > QB ? q_armed - QB : 0; a < q_armed; ++a)
+        mbar_wait(&bar_q[w][a % QB], (a / QB) & 1, drain, kErrTimeoutTma);
     }
   }
 
