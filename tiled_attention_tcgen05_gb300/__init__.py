@@ -643,6 +643,23 @@ def _on(index):
     return None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
+# Layouts that have passed a call's checks, with what the call needs of them: the
+# same call on other memory is spared the checks, which cost as much as
+# a small call's launch.
+_passed = {}
+
+
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _remember(key, what):
+    if len(_passed) >= 1024:
+        _passed.clear()
+    _passed[key] = what
+    return what
+
+
 Assigned = collections.namedtuple("Assigned", "kv_lens q_lens cu_seqlens positions slots free_count")
 
 
@@ -666,23 +683,30 @@ def cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, s
         with there:
             return cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, stream)
     lib = load()
-    if pages.dim() != 2 or free.dim() != 1:
-        raise ValueError("pages must be [B, max_pages] and free [num_pages]")
-    B, max_pages = pages.shape
-    total = int(total)
-    if total < 0:
-        raise ValueError("total must not be negative")
-    _i32("pages", pages, pages.shape, index)
-    _i32("kv_lens", kv_lens, (B,), index)
-    _i32("new_lens", new_lens, (B,), index)
-    _i32("free", free, free.shape, index)
-    _i32("free_count", free_count, (1,), index)
-    out = Assigned(*_empty((3 * B + 2 + 2 * total,), torch.int32, index, stream).split([B, B, B + 1, total, total, 1]))
-    kv, ql, cu, pos, slot, count = (x.data_ptr() for x in out)
+    key = ("cache_assign", _layout(pages), _layout(kv_lens), _layout(new_lens), _layout(free), _layout(free_count), total)
+    sizes = _passed.get(key)
+    if sizes is None:
+        if pages.dim() != 2 or free.dim() != 1:
+            raise ValueError("pages must be [B, max_pages] and free [num_pages]")
+        if int(total) < 0:
+            raise ValueError("total must not be negative")
+        B = pages.shape[0]
+        _i32("pages", pages, pages.shape, index)
+        _i32("kv_lens", kv_lens, (B,), index)
+        _i32("new_lens", new_lens, (B,), index)
+        _i32("free", free, free.shape, index)
+        _i32("free_count", free_count, (1,), index)
+        sizes = _remember(key, (B, B, B + 1, int(total), int(total), 1))
+    B, total = sizes[0], sizes[3]
+    out = _empty((3 * B + 2 + 2 * total,), torch.int32, index, stream)
+    kv = out.data_ptr()
+    ql, cu, pos = kv + 4 * B, kv + 8 * B, kv + 12 * B + 4
+    slot = pos + 4 * total
     _check("attn_cache_assign", lib.attn_cache_assign(
-        pages.data_ptr(), max_pages, kv_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), free.shape[0],
-        free_count.data_ptr(), int(page_size), kv, ql, cu, pos, slot, count, B, total, _raw_stream(index, stream)))
-    return out
+        pages.data_ptr(), pages.shape[1], kv_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), free.shape[0],
+        free_count.data_ptr(), int(page_size), kv, ql, cu, pos, slot, slot + 4 * total, B, total,
+        _raw_stream(index, stream)))
+    return Assigned(*torch.split_with_sizes(out, sizes))
 
 
 # --------------------------------------------------------- rotary positions
@@ -803,14 +827,14 @@ def _token_ints(name, t, lead, index):
     raise ValueError(f"{name} must be [{B}, {T}] or [{T}]")
 
 
-def _rot_call(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, eps, outs, stream):
-    """Checks and runs one of the rotary calls; q (or k, where there is no q)
-    says which tokens there are.  Returns the outputs."""
+def _rot_checks(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, outs, index):
+    """The checks of a rotary call; q (or k, where there is no q) says which tokens there are.  Returns the strides
+    of the seven row tensors (outputs not given: None), the positions' strides, (B, T, Hq, Hkv, D) and the two
+    dtypes' codes."""
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("neither q nor k is given")
-    index, dtype = lead.get_device(), lead.dtype
-    lib = load()
+    dtype = lead.dtype
     if lead.dim() not in (3, 4) or dtype not in _T16:
         raise ValueError("q and k must be [tokens, heads, D] or [B, heads, T, D] tensors of float16 or bfloat16")
     if not isinstance(rotary, Rotary) or rotary._index != index:
@@ -819,11 +843,9 @@ def _rot_call(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, eps
     B, T, D = (lead.shape[0], lead.shape[2], lead.shape[3]) if four else (1, lead.shape[0], lead.shape[2])
     if rotary.dim > D:
         raise ValueError(f"rotary turns {rotary.dim} elements of rows of {D}")
-    args, heads = [], []
-    for name, t in (("q", q), ("k", k)):
-        args.append(_NONE if t is None else _rot_rows(name, t, lead, dtype, index))
-        heads.append(0 if t is None else t.shape[1])
-    args.append(_NONE if v is None else _rot_rows("v", v, lead, dtype, index))
+    strides = []
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        strides.append(_NONE[1:] if t is None else _rot_rows(name, t, lead, dtype, index)[1:])
     if v is not None and v.shape != k.shape:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
     for name, t, x in (("dq", dq, q), ("dk", dk, k)):
@@ -831,49 +853,76 @@ def _rot_call(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, eps
             raise ValueError(f"{name} and its input go together")
         if t is not None and t.shape != x.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
-        args.append(_NONE if t is None else _rot_rows(name, t, lead, dtype, index))
-    res = []
+        strides.append(_NONE[1:] if t is None else _rot_rows(name, t, lead, dtype, index)[1:])
     for name, t, x in (("q_out", outs[0], q), ("k_out", outs[1], k)):
         if x is None or (cache is not None and name == "k_out"):
-            args.append(_NONE)
-            res.append(None)
-            continue
-        if t is None:
-            t = _empty(x.shape, dtype, index, stream, like=x if four else None)
-        elif t.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
-        args.append(_rot_rows(name, t, lead, dtype, index, written=True))
-        res.append(t)
-    pb, pt = _token_ints("positions", positions, lead, index)
-    sp = 0
+            strides.append(_NONE[1:])
+        elif t is None:
+            strides.append(None)
+        else:
+            if t.shape != x.shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+            strides.append(_rot_rows(name, t, lead, dtype, index, written=True)[1:])
+    at = _token_ints("positions", positions, lead, index)
     if slots is not None:
         _token_ints("slots", slots, lead, index)
         if not slots.is_contiguous() or slots.numel() != B * T:
             raise ValueError("slots must be contiguous, one for each token")
-        sp = slots.data_ptr()
-    wt, wp, dw, ws, nws = _DT[dtype], [0, 0], (0, 0), 0, 0
+    wt = dtype
     if weights is not None:
-        for i, (name, w, x) in enumerate((("q_weight", weights[0], q), ("k_weight", weights[1], k))):
-            if x is None:
-                continue
-            if w is None or w.get_device() != index or w.shape != (D,) or not w.is_contiguous() or \
-                    w.dtype not in (dtype, torch.float32):
+        given = [w for w, x in zip(weights, (q, k)) if x is not None]
+        for name, w, x in (("q_weight", weights[0], q), ("k_weight", weights[1], k)):
+            if x is not None and (w is None or w.get_device() != index or w.shape != (D,) or not w.is_contiguous() or
+                                  w.dtype not in (dtype, torch.float32)):
                 raise ValueError(f"{name} must be a contiguous [{D}] tensor of {dtype} or float32 on CUDA device {index}")
-            if wp[0] and w.dtype != weights[0].dtype:
-                raise ValueError("the weights must have one dtype")
-            wp[i], wt = w.data_ptr(), _DT[w.dtype]
-        if fn == "attn_qk_norm_rotary_bwd":
-            sums = _empty((2, D), torch.float32, index, stream)
-            nws = int(lib.attn_qk_norm_rotary_bwd_workspace_bytes(D))
-            room = _empty((max(nws, 16),), torch.uint8, index, stream)
-            dw, ws = (sums.data_ptr(), sums.data_ptr() + 4 * D), room.data_ptr()
-            res += [sums[0] if q is not None else None, sums[1] if k is not None else None]
-    call = _ROT.pack(*args[0], *args[1], *args[2], *args[3], *args[4], *args[5], *args[6], positions.data_ptr(), pb, pt, sp,
-                     rotary._ptr, *wp, *dw, ws, nws, rotary.dim, rotary.interleaved, rotary.scale, eps, B, T, *heads, D,
-                     _DT[dtype], wt)
+        wt = given[0].dtype
+        if given[-1].dtype != wt:
+            raise ValueError("the weights must have one dtype")
+    heads = tuple(0 if t is None else t.shape[1] for t in (q, k))
+    return strides, tuple(at), (B, T) + heads + (D,), (_DT[dtype], _DT[wt])
+
+
+def _rot_call(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, eps, outs, stream):
+    """Checks and runs one of the rotary calls.  Returns the outputs."""
+    lib = load()
+    lead = q if q is not None else k
+    index = -1 if lead is None else lead.get_device()
+    wq, wk = (None, None) if weights is None else weights
+    qo, ko = outs
+    key = (fn, _layout(q), _layout(k), _layout(v), _layout(dq), _layout(dk), _layout(positions), _layout(slots),
+           _layout(wq), _layout(wk), _layout(qo), _layout(ko), rotary.dim if isinstance(rotary, Rotary) else None,
+           rotary._index if isinstance(rotary, Rotary) else None, weights is None)
+    got = _passed.get(key)
+    if got is None:
+        got = _remember(key, _rot_checks(fn, cache, q, k, v, dq, dk, positions, slots, rotary, weights, outs, index))
+    (sq, sk, sv, sdq, sdk, sqo, sko), at, sizes, types = got
+    like = q if q is not None and q.dim() == 4 else k if q is None and k.dim() == 4 else None
+    if sqo is None:
+        qo = _empty(q.shape, q.dtype, index, stream, like=q if like is not None else None)
+        sqo = _rows_arg(qo)[1:]
+    if sko is None:
+        ko = _empty(k.shape, k.dtype, index, stream, like=k if like is not None else None)
+        sko = _rows_arg(ko)[1:]
+    res = [qo if q is not None else None, ko if k is not None else None]
+    dw, ws, nws = (0, 0), 0, 0
+    if fn == "attn_qk_norm_rotary_bwd":
+        D = sizes[4]
+        sums = _empty((2, D), torch.float32, index, stream)
+        nws = int(lib.attn_qk_norm_rotary_bwd_workspace_bytes(D))
+        room = _empty((max(nws, 16),), torch.uint8, index, stream)
+        dw, ws = (sums.data_ptr(), sums.data_ptr() + 4 * D), room.data_ptr()
+        res += [sums[0] if q is not None else None, sums[1] if k is not None else None]
+    p = _pointer
+    call = _ROT.pack(p(q), *sq, p(k), *sk, p(v), *sv, p(dq), *sdq, p(dk), *sdk, p(qo if q is not None else None), *sqo,
+                     p(ko if k is not None else None), *sko, positions.data_ptr(), *at, p(slots), rotary._ptr, p(wq), p(wk),
+                     *dw, ws, nws, rotary.dim, rotary.interleaved, rotary.scale, eps, *sizes, *types)
     raw = _raw_stream(index, stream)
     _check(fn, getattr(lib, fn)(call, raw) if cache is None else lib.attn_rotary_append(cache._ref, call, raw))
     return res
+
+
+def _pointer(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _rotate(fn, q, k, *rest):
