@@ -10,9 +10,14 @@
 //
 // Warps: 0-7 the element-wise part (warp % 4 selects the 32 TMEM lanes, warp / 4
 // the half of a tile's 128 columns), 8 the TMA producer, 9 the MMA issuer, 10
-// zeroes the rows of the last streamed tile that belong to no token of the
-// sequence: their P and dS are zero, and a neighbour's infinity in a product with
-// zero would be NaN.
+// asks for units ahead (UnitRing) and zeroes the rows of a unit's last streamed tile
+// that belong to no token of the sequence: their P and dS are zero, and a
+// neighbour's infinity in a product with zero would be NaN.  Such tiles come in
+// through barriers of their own.
+//
+// The rings run on from one unit to the next.  What leaves a block goes
+// through a ring's slot, too: an entry behind the unit's tiles, which the storing
+// thread hands back.
 #include "launch.h"
 #include "packed.cuh"
 
@@ -23,6 +28,28 @@ namespace {
 constexpr int kThreads = 352;
 constexpr int kProducer = 8, kMma = 9, kCare = 10;
 constexpr int kRowWarps = 8;
+
+// A ring's next slot and the parity of its phase.
+template <int N>
+struct RingAt {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+// The row threads' (256) zeros into rows of an output.
+template <typename F>
+__device__ __forceinline__ void zero_rows(int rows, int dg, F row) {
+  const int c = dg >> 3;
+  for (int j = threadIdx.x; j < rows * c; j += kRowWarps * 32) {
+    const int k = j / c;
+    static_cast<uint4*>(row(k))[j - k * c] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
 
 template <int D>
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2) {
@@ -88,21 +115,43 @@ __device__ __forceinline__ float half_dot(uint32_t a_tmem, const uint8_t* b, int
 //                         dQ (query-stationary)
 // ======================================================================
 // Q and dO are the A operands of every score product and live in TMEM; they
-// come through the last slot of the K/V ring.  O arrives behind the first K/V
-// tile, and delta is formed while the first products run.
+// come through the ring as the entry in front of a unit's K/V tiles.  O has a tile
+// of its own, and delta is formed while the first products run.  dQ leaves
+// through the entry behind the tiles.
 template <int D>
 struct PdqCfg {
   static constexpr int TILE = (D / 64) * kBM * 128;
   static constexpr int STAGE = 2 * TILE;  // K, V
   static constexpr int ST_FIT = (kSmemMax - 2048 - TILE) / STAGE;
   static constexpr int STAGES = ST_FIT > 4 ? 4 : ST_FIT;
-  static constexpr int OFF_O = STAGES * STAGE;
+  static constexpr int OFF_O = STAGES * STAGE;  // O, then the halves of delta
   static constexpr int SMEM = OFF_O + TILE + 1024;
   static constexpr uint32_t COL_A = 0, COL_B = 128, COL_DQ = 256;
   static constexpr uint32_t COL_QT = 256 + D, COL_DOT = 256 + D + D / 2;
   static_assert(STAGES >= 3 && SMEM + 2048 <= kSmemMax, "shared memory");
   static_assert(COL_DOT + D / 2 <= 512, "TMEM");
 };
+
+struct DqUnit {
+  int row, krow, n, off;         // first token's row, first key's row, keys, last key the first token sees
+  int left, nkv, head, causal;   // tokens to the sequence's end, key tiles, key head
+  __device__ __forceinline__ DqUnit(const UnitRing* r, int i) {
+    const int4 a = ring_words(r, i, 0), b = ring_words(r, i, 1);
+    row = a.x;
+    krow = a.y;
+    n = a.z;
+    off = a.w;
+    left = b.x;
+    nkv = b.y;
+    head = b.z;
+    causal = b.w;
+  }
+  __device__ __forceinline__ bool ragged() const { return nkv * kBN > n; }  // the last tile ends behind the keys
+};
+__device__ __forceinline__ void make_dq_unit(const PackedUnit& u, int TB, int4 (&words)[4]) {
+  words[0] = make_int4(u.row, u.krow, u.n, u.off);
+  words[1] = make_int4(u.left, packed_key_tiles(min(u.left, TB), u.off, u.n, u.pad[0]), u.pad[1], u.pad[0]);
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -115,8 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int STAGES = C::STAGES;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q, bar_qfree, bar_kv[STAGES], bar_kvempty[STAGES];
-  __shared__ __align__(8) uint64_t bar_s, bar_consumed, bar_dp, bar_ds[2], bar_done, bar_o, bar_last, bar_care;
+  __shared__ __align__(16) UnitRing ring;
+  __shared__ __align__(8) uint64_t bar_qfree, bar_kv[STAGES], bar_kvempty[STAGES];
+  __shared__ __align__(8) uint64_t bar_s, bar_consumed, bar_dp, bar_ds[2], bar_done, bar_o;
+  __shared__ __align__(8) uint64_t bar_last[2], bar_care[2];  // [unit % 2]: a ragged last tile is in, is seen to
+  __shared__ __align__(8) uint64_t bar_out[2];                // [live units so far % 2]: dQ's slot is free to write
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -124,24 +176,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const PackedList list = packed_list(args, kPackedDq);
   if (blockIdx.x >= list.items) return;
-  const PackedUnit unit = packed_item(args, list, blockIdx.x);
-  const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
-  const int nkv = packed_key_tiles(min(unit.left, TB), unit.off, unit.n, causal);
-  const bool ragged = nkv * kBN > unit.n;  // the last tile ends behind the keys
   const int box = (D / 64) * TB * G * 128;  // bytes of a query tile
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  auto sK = [&](int st) { return base + st * C::STAGE; };
-  auto sV = [&](int st) { return base + st * C::STAGE + C::TILE; };
-  uint8_t* sQ = sK(STAGES - 1);
-  uint8_t* sDO = sV(STAGES - 1);
+  auto sK = [&](int st) { return base + st * C::STAGE; };           // K | Q | dQ
+  auto sV = [&](int st) { return base + st * C::STAGE + C::TILE; };  // V | dO
   uint8_t* sO = base + C::OFF_O;
+  float* halves = reinterpret_cast<float*>(sO);
 
+  const bool asks = threadIdx.x == kCare * 32;
+  if (asks) {
+    make_dq_unit(packed_item(args, list, blockIdx.x), TB, ring.unit[0]);
+    ring.unit[0][3].w = 1;
+  }
   WaitCtl ctl{args.err, args.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    mbar_init(&bar_q, 1);
+    ring_init(&ring, kRowWarps + 2);  // row warps, MMA, producer
     mbar_init(&bar_qfree, kRowWarps);
     for (int st = 0; st < STAGES; ++st) {
       mbar_init(&bar_kv[st], 1);
@@ -150,12 +202,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_s, 1);
     mbar_init(&bar_consumed, kRowWarps);
     mbar_init(&bar_dp, 1);
-    mbar_init(&bar_ds[0], kRowWarps);
-    mbar_init(&bar_ds[1], kRowWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_ds[i], kRowWarps);
+      mbar_init(&bar_last[i], 1);
+      mbar_init(&bar_care[i], 1);
+      mbar_init(&bar_out[i], 1);
+    }
     mbar_init(&bar_done, 1);
     mbar_init(&bar_o, 1);
-    mbar_init(&bar_last, 1);
-    mbar_init(&bar_care, 1);
     fence_mbar_init();
   }
   if (warp == kMma) {
@@ -166,95 +220,156 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  int zero = 0;  // (an exit waits for its own copies whatever the abort flag says)
+  const WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
 
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
-    if (lane == 0 && nkv > 0) {
-      mbar_expect_tx(&bar_q, 2 * box);
-      load_rows<D>(sQ, &tm_q, &bar_q, head * G, unit.row);
-      load_rows<D>(sDO, &tm_do, &bar_q, head * G, unit.row);
-      int issued = 0;
-      bool o_issued = false;
-      for (int t = 0; t < nkv; ++t) {
-        const int st = t % STAGES;
-        if (t >= STAGES) {
-          if (!mbar_wait(&bar_kvempty[st], ((t / STAGES) - 1) & 1, ctl, kErrTimeoutMma)) break;
-        } else if (st == STAGES - 1) {  // the slot still holds Q and dO until they are in TMEM
-          if (!mbar_wait(&bar_qfree, 0, ctl, kErrTimeoutSoftmax)) break;
+    if (lane == 0) {
+      RingAt<STAGES> k;
+      int e = 0;              // entries so far
+      uint32_t own = 0;       // slots whose last entry did not come through bar_kv
+      uint32_t last_ph = 0;   // bit i: bar_last[i] has been armed an odd number of times
+      uint32_t outs = 0;
+      bool ok = true;
+      auto slot = [&] { return e < STAGES || mbar_wait(&bar_kvempty[k.st], k.ph ^ 1u, ctl, kErrTimeoutMma); };
+      for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
+        const DqUnit p(&ring, i);
+        for (int t = -1; p.nkv > 0 && t <= p.nkv; ++t, ++e) {
+          if (!(ok = slot())) break;
+          own &= ~(1u << k.st);
+          if (t < 0) {
+            mbar_expect_tx(&bar_kv[k.st], 2 * box);
+            load_rows<D>(sK(k.st), &tm_q, &bar_kv[k.st], p.head * G, p.row);
+            load_rows<D>(sV(k.st), &tm_do, &bar_kv[k.st], p.head * G, p.row);
+          } else if (t < p.nkv) {
+            uint64_t* bar = &bar_kv[k.st];
+            if (t == p.nkv - 1 && p.ragged()) {
+              mbar_arrive(bar);  // (the ring's own phase passes on)
+              bar = &bar_last[i & 1];
+              last_ph ^= 1u << (i & 1);
+              own |= 1u << k.st;
+            }
+            mbar_expect_tx(bar, 2 * C::TILE);
+            load_rows<D>(sK(k.st), &tm_k, bar, p.krow + t * kBN, p.head);
+            load_rows<D>(sV(k.st), &tm_v, bar, p.krow + t * kBN, p.head);
+          } else {
+            mbar_arrive(&bar_kv[k.st]);
+            mbar_arrive(&bar_out[outs & 1]);
+            ++outs;
+            own |= 1u << k.st;
+          }
+          k.step();
         }
-        uint64_t* bar = ragged && t == nkv - 1 ? &bar_last : &bar_kv[st];
-        mbar_expect_tx(bar, 2 * C::TILE);
-        load_rows<D>(sK(st), &tm_k, bar, unit.krow + t * kBN, head);
-        load_rows<D>(sV(st), &tm_v, bar, unit.krow + t * kBN, head);
-        issued = t + 1;
-        if (t == 0) {  // O for delta
-          mbar_expect_tx(&bar_o, box);
-          load_rows<D>(sO, &tm_o, &bar_o, head * G, unit.row);
-          o_issued = true;
-        }
+        if (ok) mbar_arrive(&ring.left[i & 1]);
       }
-      int zero = 0;
-      WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
-      mbar_wait(&bar_q, 0, drain, kErrTimeoutTma);
-      if (o_issued) mbar_wait(&bar_o, 0, drain, kErrTimeoutTma);
-      for (int t = issued - STAGES > 0 ? issued - STAGES : 0; t < issued; ++t) {
-        if (ragged && t == nkv - 1) mbar_wait(&bar_last, 0, drain, kErrTimeoutTma);
-        else mbar_wait(&bar_kv[t % STAGES], (t / STAGES) & 1, drain, kErrTimeoutTma);
-      }
+      for (int t = e - STAGES > 0 ? e - STAGES : 0; t < e; ++t)
+        if (!(own >> (t % STAGES) & 1u)) mbar_wait(&bar_kv[t % STAGES], (t / STAGES) & 1, drain, kErrTimeoutTma);
+      for (int j = 0; j < 2; ++j) mbar_wait(&bar_last[j], (last_ph >> j & 1u) ^ 1u, drain, kErrTimeoutTma);
     }
   } else if (warp == kMma) {
     // ----------------------------------------------------------------- MMA
-    if (nkv > 0) {
-      constexpr uint32_t idesc_s = idesc_f16(kBM, kBN, BF, false, false);
-      constexpr uint32_t idesc_g = idesc_f16(kBM, D, BF, false, true);
-      auto kv_ready = [&](int t) {
-        if (ragged && t == nkv - 1) return warp_wait(&bar_care, 0, ctl, kErrTimeoutOther);
-        return warp_wait(&bar_kv[t % STAGES], (t / STAGES) & 1, ctl, kErrTimeoutTma);
-      };
-      bool ok = warp_wait(&bar_qfree, 0, ctl, kErrTimeoutSoftmax) && kv_ready(0);
-      if (ok) {
+    constexpr uint32_t idesc_s = idesc_f16(kBM, kBN, BF, false, false);
+    constexpr uint32_t idesc_g = idesc_f16(kBM, D, BF, false, true);
+    RingAt<STAGES> k;
+    uint32_t units = 0, tiles = 0, nc = 0, care_ph = 0;  // parities
+    bool any = false, ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      int nkv;
+      bool ragged;
+      {
+        const DqUnit p(&ring, i);
+        nkv = p.nkv;
+        ragged = p.ragged();
+      }
+      if (nkv > 0) {
+        auto kv_ready = [&](int t) {
+          if (ragged && t == nkv - 1) {
+            const uint32_t ph = care_ph >> (i & 1) & 1u;
+            care_ph ^= 1u << (i & 1);
+            return warp_wait(&bar_care[i & 1], ph, ctl, kErrTimeoutOther);
+          }
+          return warp_wait(&bar_kv[k.st], k.ph, ctl, kErrTimeoutTma);
+        };
+        // Q and dO are in TMEM: their slot is free, and the last unit's S has been read
+        ok = warp_wait(&bar_qfree, units, ctl, kErrTimeoutSoftmax);
+        units ^= 1u;
+        if (ok && any) {
+          ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax);
+          nc ^= 1u;
+        }
+        any = true;
+        if (!ok) break;
+        commit_el(&bar_kvempty[k.st]);
+        k.step();
+        if (!(ok = kv_ready(0))) break;
         tc_fence_after();
-        mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(0)), idesc_s);
+        mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(k.st)), idesc_s);
         commit_el(&bar_s);
-        mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(0)), idesc_s);  // dP = dO V^T
+        mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(k.st)), idesc_s);  // dP = dO V^T
         commit_el(&bar_dp);
-      }
-      for (int t = 0; ok && t < nkv; ++t) {
-        const int st = t % STAGES;
-        const int st1 = (t + 1) % STAGES;
-        const bool next = t + 1 < nkv;
-        if (next) {
-          if (!(ok = warp_wait(&bar_consumed, t & 1, ctl, kErrTimeoutSoftmax))) break;
-          if (!(ok = kv_ready(t + 1))) break;
+        for (int t = 0; t < nkv; ++t) {
+          const int st = k.st;
+          const bool next = t + 1 < nkv;
+          k.step();
+          if (next) {
+            if (!(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
+            nc ^= 1u;
+            if (!(ok = kv_ready(t + 1))) break;
+            tc_fence_after();
+            mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(k.st)), idesc_s);
+            commit_el(&bar_s);
+          }
+          if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
           tc_fence_after();
-          mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(st1)), idesc_s);
-          commit_el(&bar_s);
+          mma_half_y<0>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, t > 0);
+          if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
+          tiles ^= 1u;
+          tc_fence_after();
+          mma_half_y<1>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, true);
+          commit_el(&bar_kvempty[st]);
+          if (next) {
+            mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(k.st)), idesc_s);
+            commit_el(&bar_dp);
+          }
         }
-        if (!(ok = warp_wait(&bar_ds[0], t & 1, ctl, kErrTimeoutSoftmax))) break;
-        tc_fence_after();
-        mma_half_y<0>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, t > 0);
-        if (!(ok = warp_wait(&bar_ds[1], t & 1, ctl, kErrTimeoutSoftmax))) break;
-        tc_fence_after();
-        mma_half_y<1>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, true);
-        commit_el(&bar_kvempty[st]);
-        if (next) {
-          mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(st1)), idesc_s);
-          commit_el(&bar_dp);
-        }
+        if (!ok) break;
+        commit_el(&bar_done);
+        k.step();  // dQ's entry
       }
-      if (ok) commit_el(&bar_done);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
   } else if (warp == kCare) {
-    if (nkv > 0 && ragged) {
-      const int t = nkv - 1, st = t % STAGES;
-      if (warp_wait(&bar_last, 0, ctl, kErrTimeoutTma)) {
-        zero_tile_rows<D / 64>(sK(st), unit.n - t * kBN, lane);
-        zero_tile_rows<D / 64>(sV(st), unit.n - t * kBN, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_care);
+    // --------------------------------- units ahead; rows behind the keys
+    RingAsker asker;
+    if (asks) asker.ask(&ring);
+    int st = 0;  // slot of the unit's first entry
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      if (asks)
+        ok = asker.pass(&ring, args, list, i, ctl,
+                        [&](const PackedUnit& u, int4(&words)[4]) { make_dq_unit(u, TB, words); });
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const DqUnit p(&ring, i);
+      if (p.nkv > 0) {
+        if (p.ragged()) {
+          if (!(ok = warp_wait(&bar_last[i & 1], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma))) break;
+          ph ^= 1u << (i & 1);
+          const int at = (st + p.nkv) % STAGES, first = p.n - (p.nkv - 1) * kBN;
+          zero_tile_rows<D / 64>(sK(at), first, lane);
+          zero_tile_rows<D / 64>(sV(at), first, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_care[i & 1]);
+        }
+        st = (st + p.nkv + 2) % STAGES;
       }
     }
+    if (asks) asker.drain(&ring, drain);
   } else {
     // --------------------------------------------- query-row softmax gradient
     const int hc = warp >> 2;  // key half of the tile: columns [64 hc, 64 hc + 64)
@@ -262,120 +377,166 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const int tok = static_cast<int>(args.g_div.div(r)), hq = r - tok * G;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const bool in = tok < min(unit.left, TB);
-    const size_t g = (static_cast<size_t>(unit.row) + (in ? tok : 0)) * args.shape.Hq + head * G + (in ? hq : 0);
-    const float neg_L2 = in ? -args.lse[g] * kLog2e : -INFINITY;
-    const int sees = causal ? min(unit.n - 1, unit.off + tok) : unit.n - 1;
-    const int t_part = causal ? min(unit.n / kBN, unit.off < 0 ? 0 : (unit.off + 1) / kBN) : unit.n / kBN;
+    const bool serves = threadIdx.x == 0;  // loads O, stores dQ
+    RingAt<STAGES> k;
+    uint32_t units = 0, tiles = 0, outs = 0, os = 0;  // os: (serving thread) O tiles asked for
+    int lent = -1;                                    // slot that a store still reads
+    auto load_o = [&](int i) {
+      const DqUnit p(&ring, i);
+      if (p.nkv == 0) return;
+      mbar_expect_tx(&bar_o, box);
+      load_rows<D>(sO, &tm_o, &bar_o, p.head * G, p.row);
+      ++os;
+    };
+    auto give_back = [&] {
+      if (lent >= 0) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive(&bar_kvempty[lent]);
+        lent = -1;
+      }
+    };
+    if (serves) load_o(0);
     bool ok = true;
-    if (nkv > 0) {  // group 0 copies Q, group 1 dO into TMEM
-      ok = warp_wait(&bar_q, 0, ctl, kErrTimeoutTma);
-      if (ok) {
-        tile_row_to_tmem<D>(hc == 0 ? sQ : sDO, r, lane_addr + (hc == 0 ? C::COL_QT : C::COL_DOT));
-        tmem_st_wait();
-        tc_fence_before();
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      const DqUnit p(&ring, i);
+      const int nkv = p.nkv;
+      const bool in = tok < min(p.left, TB);
+      const size_t g = (static_cast<size_t>(p.row) + (in ? tok : 0)) * args.shape.Hq + p.head * G + (in ? hq : 0);
+      T* const dq = static_cast<T*>(args.dq) + static_cast<long long>(p.row) * args.dq_t + p.head * G * args.dq_h;
+      auto out_row = [&](int j) -> void* {
+        const int tk = static_cast<int>(args.g_div.div(j));
+        return dq + tk * args.dq_t + (j - tk * G) * args.dq_h;
+      };
+      if (nkv == 0) {  // rows that see nothing: O = 0
+        if (hc == 0 && in) args.delta[g] = 0.f;
+        zero_rows(min(p.left, TB) * G, args.dg, out_row);
+        if (serves) {
+          give_back();
+          if (ring_take(&ring, i + 1, ctl)) load_o(i + 1);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_qfree);
+        if (lane == 0) mbar_arrive(&ring.left[i & 1]);
+        continue;
       }
-    }
-    // delta: each group half of every row's columns; a tile that sees no key has O = 0
-    float dlt = 0.f;
-    if (nkv > 0 && ok) {
-      ok = warp_wait(&bar_qfree, 0, ctl, kErrTimeoutSoftmax) && warp_wait(&bar_o, 0, ctl, kErrTimeoutTma);
-      if (ok) {
-        tc_fence_after();
-        dlt = half_dot<T, D>(lane_addr + C::COL_DOT, sO, r, hc);
-      }
-    }
-    float* halves = reinterpret_cast<float*>(sO);
-    named_bar_sync(1, kRowWarps * 32);
-    halves[hc * kBM + r] = dlt;
-    named_bar_sync(1, kRowWarps * 32);
-    dlt = halves[r] + halves[kBM + r];
-    if (hc == 0 && in) args.delta[g] = dlt;
-    for (int t = 0; ok && t < nkv; ++t) {
-      const int k0 = t * kBN;
-      if (!(ok = warp_wait(&bar_s, t & 1, ctl, kErrTimeoutMma))) break;
-      tc_fence_after();
-      uint32_t sv[64];
-      tmem_ld_x32(lane_addr + C::COL_A + cb, TB_CHUNK(sv, 0));
-      tmem_ld_x32(lane_addr + C::COL_A + cb + 32, TB_CHUNK(sv, 1));
-      tmem_ld_wait(TB_CHUNK(sv, 0));
-      tmem_ld_wait(TB_CHUNK(sv, 1));
+      const float neg_L2 = in ? -args.lse[g] * kLog2e : -INFINITY;
+      const int sees = p.causal ? min(p.n - 1, p.off + tok) : p.n - 1;
+      const int t_part = p.causal ? min(p.n / kBN, p.off < 0 ? 0 : (p.off + 1) / kBN) : p.n / kBN;
+      // group 0 copies Q, group 1 dO into TMEM (the last unit's products are done)
+      if (!(ok = warp_wait(&bar_kv[k.st], k.ph, ctl, kErrTimeoutTma))) break;
+      tile_row_to_tmem<D>(hc == 0 ? sK(k.st) : sV(k.st), r, lane_addr + (hc == 0 ? C::COL_QT : C::COL_DOT));
+      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_consumed);  // S buffer free for S(t + 1)
-      float p[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float2 y = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
-                               make_float2(args.scale_log2, args.scale_log2), make_float2(neg_L2, neg_L2));
-        p[c] = ex2(y.x);
-        p[c + 1] = ex2(y.y);
-      }
-      if (t >= t_part) {
-        const int lim = sees - k0 - cb;
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c > lim) p[c] = 0.f;
-      }
-      if (!(ok = warp_wait(&bar_dp, t & 1, ctl, kErrTimeoutMma))) break;
+      if (lane == 0) mbar_arrive(&bar_qfree);
+      k.step();
+      if (serves) give_back();
+      // delta: each group half of every row's columns
+      if (!(ok = warp_wait(&bar_qfree, units, ctl, kErrTimeoutSoftmax) && warp_wait(&bar_o, units, ctl, kErrTimeoutTma)))
+        break;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t dp[32];
-        tmem_ld_x32(lane_addr + C::COL_B + cb + 32 * c, dp);
-        tmem_ld_wait(dp);
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c0 = 32 * c + 2 * e;
-          const float2 ds = fmul2(make_float2(p[c0], p[c0 + 1]),
-                                  fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])),
-                                        make_float2(-dlt, -dlt)));
-          pk[e] = pack2<BF>(ds.x, ds.y);
-        }
-        tmem_st_x16(lane_addr + C::COL_B + cb + 16 * c, pk);  // dS (16-bit) over dP
-        tmem_st_wait();
+      float dlt = half_dot<T, D>(lane_addr + C::COL_DOT, sO, r, hc);
+      named_bar_sync(1, kRowWarps * 32);  // the halves go over O
+      halves[hc * kBM + r] = dlt;
+      named_bar_sync(1, kRowWarps * 32);
+      dlt = halves[r] + halves[kBM + r];
+      fence_proxy_async_smem();
+      if (hc == 0 && in) args.delta[g] = dlt;
+      for (int t = 0; t < nkv; ++t, tiles ^= 1u) {
+        const int k0 = t * kBN;
+        if (!(ok = warp_wait(&bar_s, tiles, ctl, kErrTimeoutMma))) break;
+        tc_fence_after();
+        uint32_t sv[64];
+        tmem_ld_x32(lane_addr + C::COL_A + cb, TB_CHUNK(sv, 0));
+        tmem_ld_x32(lane_addr + C::COL_A + cb + 32, TB_CHUNK(sv, 1));
+        tmem_ld_wait(TB_CHUNK(sv, 0));
+        tmem_ld_wait(TB_CHUNK(sv, 1));
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_ds[c]);
-      }
-    }
-    if (nkv > 0 && ok) ok = warp_wait(&bar_done, 0, ctl, kErrTimeoutMma);
-    tc_fence_after();
-    // dQ (x sm_scale) staged over the ring's first K slot (every MMA has finished)
-    const bool live = ok && nkv > 0;
+        if (lane == 0) mbar_arrive(&bar_consumed);  // S buffer free for S(t + 1)
+        float pr[64];
 #pragma unroll
-    for (int cc = 0; cc < D / 64; ++cc) {
-      const int c = hc * (D / 64) + cc;
-      uint32_t v[32];
-      if (live) {
+        for (int c = 0; c < 64; c += 2) {
+          const float2 y = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                                 make_float2(args.scale_log2, args.scale_log2), make_float2(neg_L2, neg_L2));
+          pr[c] = ex2(y.x);
+          pr[c + 1] = ex2(y.y);
+        }
+        if (t >= t_part) {
+          const int lim = sees - k0 - cb;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c > lim) pr[c] = 0.f;
+        }
+        if (!(ok = warp_wait(&bar_dp, tiles, ctl, kErrTimeoutMma))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[32];
+          tmem_ld_x32(lane_addr + C::COL_B + cb + 32 * c, dp);
+          tmem_ld_wait(dp);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c0 = 32 * c + 2 * e;
+            const float2 ds = fmul2(make_float2(pr[c0], pr[c0 + 1]),
+                                    fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])),
+                                          make_float2(-dlt, -dlt)));
+            pk[e] = pack2<BF>(ds.x, ds.y);
+          }
+          tmem_st_x16(lane_addr + C::COL_B + cb + 16 * c, pk);  // dS (16-bit) over dP
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_ds[c]);
+        }
+        k.step();
+      }
+      if (!ok) break;
+      if (!(ok = warp_wait(&bar_done, units, ctl, kErrTimeoutMma) &&
+                 warp_wait(&bar_out[outs & 1], (outs >> 1) & 1, ctl, kErrTimeoutMma)))
+        break;
+      units ^= 1u;
+      ++outs;
+      tc_fence_after();
+      // (every warp has handed in its last dS, and so has read O and delta)
+      if (serves && ring_take(&ring, i + 1, ctl)) load_o(i + 1);
+      __syncwarp();
+      // dQ (x sm_scale) staged in its slot
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        const int c = hc * (D / 64) + cc;
+        uint32_t v[32];
         tmem_ld_x32(lane_addr + C::COL_DQ + 32 * c, v);
         tmem_ld_wait(v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0u;
+        stage_row_chunk_sw128<BF>(smem_u32(sK(k.st)), r, c, v, args.sm_scale);
       }
-      stage_row_chunk_sw128<BF>(smem_u32(sK(0)), r, c, v, args.sm_scale);
+      tc_fence_before();
+      fence_proxy_async_smem();
+      named_bar_sync(1, kRowWarps * 32);
+      if (p.left >= TB) {
+        if (serves) {
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_store_3d(&tm_dq, sK(k.st) + kb * (kBM * 128), kb * 64, p.head * G, p.row);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          lent = k.st;
+        }
+      } else {  // the rows behind it are another sequence's
+        const int rows = p.left * G;
+        copy_tile_rows(sK(k.st), args.dg, threadIdx.x, kRowWarps * 32,
+                       [&](int j) -> void* { return j < rows ? out_row(j) : nullptr; });
+        named_bar_sync(1, kRowWarps * 32);
+        if (serves) mbar_arrive(&bar_kvempty[k.st]);
+      }
+      k.step();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kRowWarps * 32);
-    if (unit.left >= TB) {
-      if (warp == 0 && lane == 0) {
-#pragma unroll
-        for (int kb = 0; kb < D / 64; ++kb)
-          tma_store_3d(&tm_dq, sK(0) + kb * (kBM * 128), kb * 64, head * G, unit.row);
-        tma_store_commit_and_wait_read();
-      }
-    } else {
-      T* dq = static_cast<T*>(args.dq);
-      const int rows = unit.left * G;
-      copy_tile_rows(sK(0), args.dg, threadIdx.x, kRowWarps * 32, [&](int i) -> void* {
-        if (i >= rows) return nullptr;
-        const int k = static_cast<int>(args.g_div.div(i));
-        return dq + (static_cast<long long>(unit.row) + k) * args.dq_t + (head * G + i - k * G) * args.dq_h;
-      });
+    if (serves) {
+      give_back();
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      if (os > 0) mbar_wait(&bar_o, (os - 1) & 1, drain, kErrTimeoutTma);
     }
   }
 
@@ -391,8 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Per query tile u:  S^T(u + 1) | dV(u) dK(u) | dP^T(u + 1), with P^T and dS^T
 // (16 + 16 packed columns per 32-column chunk) written over dP^T.  Q has a ring
 // of its own, a tile ahead of dO's; L and delta of a tile are fetched a tile
-// ahead into a double buffer.  All shared memory is in the dynamic region (K, V,
-// the Q and dO rings, L and delta, barriers).
+// ahead into a double buffer.  K and V are free for the next unit's once the last
+// S^T and dP^T are done; dK leaves through the Q ring, dV through dO's.  All
+// shared memory is in the dynamic region (K, V, the rings, L and delta, barriers).
 template <int D>
 struct PkvCfg {
   static constexpr int TILE = (D / 64) * kBM * 128;
@@ -400,14 +562,38 @@ struct PkvCfg {
   static constexpr int OST = D == 128 ? 2 : 4;
   static constexpr int LD_OFF = (2 + QST + OST) * TILE;  // [buffer][half][L, delta][64] floats
   static constexpr int BAR_OFF = LD_OFF + 2 * 2 * 2 * 64 * 4;
-  static constexpr int BAR_BYTES = 256;
+  static constexpr int BAR_BYTES = 576;
   static constexpr int USED = BAR_OFF + BAR_BYTES;
   static constexpr int PAD = (kSmemMax - USED) < 1023 ? (kSmemMax - USED) : 1023;
   static constexpr int SMEM = USED + PAD;
   static constexpr uint32_t COL_A = 0, COL_B = 128, COL_DV = 256, COL_DK = 256 + D;
   static_assert(PAD >= 0 && SMEM <= kSmemMax, "tiles do not fit in shared memory");
-  static_assert(BAR_BYTES >= 8 * (1 + 2 * QST + 2 * OST + 6 + 4 + 4) + 8, "barrier area too small");
+  static_assert(BAR_BYTES >= static_cast<int>(sizeof(UnitRing)) + 8 * (2 + 2 * QST + 2 * OST + 6 + 4 + 8 + 4) + 8, "barrier area too small");
 };
+
+struct KvUnit {
+  int krow, n, row, left, off;  // first key's row, keys from it on, first token that sees any, tokens from it on; see PackedUnit
+  int nq, head, causal;         // query tiles, key head
+  int ragged;                   // the last tile ends behind the tokens
+  __device__ __forceinline__ KvUnit(const UnitRing* r, int i) {
+    const int4 a = ring_words(r, i, 0), b = ring_words(r, i, 1), c = ring_words(r, i, 2);
+    krow = a.x;
+    n = a.y;
+    row = a.z;
+    left = a.w;
+    off = b.x;
+    nq = b.y;
+    head = b.z;
+    causal = b.w;
+    ragged = c.x;
+  }
+};
+__device__ __forceinline__ void make_kv_unit(const PackedUnit& u, int TB, int4 (&words)[4]) {
+  const int nq = (u.left + TB - 1) / TB;
+  words[0] = make_int4(u.krow, u.n, u.row, u.left);
+  words[1] = make_int4(u.off, nq, u.pad[1], u.pad[0]);
+  words[2] = make_int4(nq * TB > u.left, 0, 0, 0);
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -425,9 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && args.err) atomicOr(args.err, kErrSmemLayout);
     return;
   }
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::BAR_OFF);
+  UnitRing& ring = *reinterpret_cast<UnitRing*>(base + C::BAR_OFF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(&ring + 1);
   uint64_t& bar_kv = bars[0];
-  uint64_t* bar_qf = bars + 1;
+  uint64_t& bar_kvfree = bars[1];
+  uint64_t* bar_qf = bars + 2;
   uint64_t* bar_qe = bar_qf + QST;
   uint64_t* bar_of = bar_qe + QST;
   uint64_t* bar_oe = bar_of + OST;
@@ -437,32 +625,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_ds = bar_oe + OST + 3;  // [chunk group]
   uint64_t& bar_done = bar_oe[OST + 5];
   uint64_t* bar_pub = bar_oe + OST + 6;  // [buffer * 2 + half]: L / delta of a tile stored
-  uint64_t* bar_care = bar_pub + 4;      // [0]: the last Q tile's rows zeroed, [1]: dO's
-  uint64_t* bar_last = bar_care + 2;     // the last Q and dO tile, where they end behind the tokens
-  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bar_last + 2);
-  int& abort_flag = *(reinterpret_cast<int*>(bar_last + 2) + 1);
+  uint64_t* bar_care = bar_pub + 4;      // [unit % 2 * 2 + (0: Q, 1: dO)]: a ragged last tile's rows zeroed
+  uint64_t* bar_last = bar_care + 4;     // the same: it is in
+  uint64_t* bar_out = bar_last + 4;      // [live units % 2 * 2 + (0: Q ring, 1: dO ring)]: a slot is free to write
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bar_out + 4);
+  int& abort_flag = *(reinterpret_cast<int*>(bar_out + 4) + 1);
   float* sLD = reinterpret_cast<float*>(base + C::LD_OFF);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const PackedList list = packed_list(args, kPackedDkdv);
   if (blockIdx.x >= list.items) return;
-  const PackedUnit unit = packed_item(args, list, blockIdx.x);
-  const int causal = unit.pad[0], head = unit.pad[1];
   const int G = args.shape.G, TB = args.shape.TB;
-  const int nq = (unit.left + TB - 1) / TB;
   const int box = (D / 64) * TB * G * 128;
-  const bool ragged = nq * TB > unit.left;
 
   uint8_t* sK = base;
   uint8_t* sV = base + C::TILE;
   auto sQ = [&](int i) { return base + (2 + i) * C::TILE; };
   auto sDO = [&](int i) { return base + (2 + QST + i) * C::TILE; };
 
+  const bool asks = threadIdx.x == kCare * 32;
+  if (asks) {
+    make_kv_unit(packed_item(args, list, blockIdx.x), TB, ring.unit[0]);
+    ring.unit[0][3].w = 1;
+  }
   WaitCtl ctl{args.err, args.timeout_ns, &abort_flag};
   if (threadIdx.x == 0) {
     abort_flag = 0;
+    ring_init(&ring, kRowWarps + 3);  // row warps, MMA, two producing lanes
     mbar_init(&bar_kv, 1);
+    mbar_init(&bar_kvfree, 1);
     for (int i = 0; i < QST; ++i) {
       mbar_init(&bar_qf[i], 1);
       mbar_init(&bar_qe[i], 1);
@@ -477,11 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_ds[0], kRowWarps);
     mbar_init(&bar_ds[1], kRowWarps);
     mbar_init(&bar_done, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&bar_pub[i], kRowWarps / 2);
-    mbar_init(&bar_care[0], 1);
-    mbar_init(&bar_care[1], 1);
-    mbar_init(&bar_last[0], 1);
-    mbar_init(&bar_last[1], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_pub[i], kRowWarps / 2);
+      mbar_init(&bar_care[i], 1);
+      mbar_init(&bar_last[i], 1);
+      mbar_init(&bar_out[i], 1);
+    }
     fence_mbar_init();
   }
   if (TB * G < kBM) {  // rows that no box ever fills, in every slot
@@ -496,269 +689,387 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  int zero = 0;  // (an exit waits for its own copies whatever the abort flag says)
+  const WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
 
   if (warp == kProducer) {
     // ---------------------- producer: lane 0 K, V and the Q ring; lane 1 the dO ring
-    if (lane < 2 && nq > 0) {
-      const bool is_q = (lane == 0);
+    if (lane < 2) {
+      const bool is_q = lane == 0;
       const int depth = is_q ? QST : OST;
       uint64_t* full = is_q ? bar_qf : bar_of;
       uint64_t* empty = is_q ? bar_qe : bar_oe;
       const CUtensorMap* map = is_q ? &tm_q : &tm_do;
-      if (is_q) {
-        mbar_expect_tx(&bar_kv, 2 * C::TILE);
-        load_rows<D>(sK, &tm_k, &bar_kv, unit.krow, head);
-        load_rows<D>(sV, &tm_v, &bar_kv, unit.krow, head);
+      int e = 0;                     // entries so far
+      uint32_t own = 0, last_ph = 0, units = 0;
+      bool ok = true;
+      for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
+        const KvUnit p(&ring, i);
+        if (p.nq > 0 && is_q) {
+          if (units > 0 && !(ok = mbar_wait(&bar_kvfree, (units - 1) & 1, ctl, kErrTimeoutMma))) break;
+          mbar_expect_tx(&bar_kv, 2 * C::TILE);
+          load_rows<D>(sK, &tm_k, &bar_kv, p.krow, p.head);
+          load_rows<D>(sV, &tm_v, &bar_kv, p.krow, p.head);
+        }
+        for (int u = 0; p.nq > 0 && u <= p.nq; ++u, ++e) {
+          const int st = e % depth;
+          if (e >= depth && !(ok = mbar_wait(&empty[st], ((e / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
+          own &= ~(1u << st);
+          if (u == p.nq) {  // the way out
+            mbar_arrive(&full[st]);
+            mbar_arrive(&bar_out[(units & 1) * 2 + lane]);
+            own |= 1u << st;
+            continue;
+          }
+          uint64_t* bar = &full[st];
+          if (p.ragged && u == p.nq - 1) {
+            mbar_arrive(bar);  // (the ring's own phase passes on)
+            bar = &bar_last[(i & 1) * 2 + lane];
+            last_ph ^= 1u << (i & 1);
+            own |= 1u << st;
+          }
+          mbar_expect_tx(bar, box);
+          load_rows<D>(is_q ? sQ(st) : sDO(st), map, bar, p.head * G, p.row + u * TB);
+        }
+        if (p.nq > 0) ++units;
+        if (ok) mbar_arrive(&ring.left[i & 1]);
       }
-      int issued = 0;
-      for (int u = 0; u < nq; ++u) {
-        const int st = u % depth;
-        if (u >= depth && !mbar_wait(&empty[st], ((u / depth) - 1) & 1, ctl, kErrTimeoutMma)) break;
-        uint64_t* bar = ragged && u == nq - 1 ? &bar_last[lane] : &full[st];
-        mbar_expect_tx(bar, box);
-        load_rows<D>(is_q ? sQ(st) : sDO(st), map, bar, head * G, unit.row + u * TB);
-        issued = u + 1;
-      }
-      int zero = 0;
-      WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
-      if (is_q) mbar_wait(&bar_kv, 0, drain, kErrTimeoutTma);
-      for (int u = issued - depth > 0 ? issued - depth : 0; u < issued; ++u) {
-        if (ragged && u == nq - 1) mbar_wait(&bar_last[lane], 0, drain, kErrTimeoutTma);
-        else mbar_wait(&full[u % depth], (u / depth) & 1, drain, kErrTimeoutTma);
-      }
+      if (is_q && units > 0) mbar_wait(&bar_kv, (units - 1) & 1, drain, kErrTimeoutTma);
+      for (int u = e - depth > 0 ? e - depth : 0; u < e; ++u)
+        if (!(own >> (u % depth) & 1u)) mbar_wait(&full[u % depth], (u / depth) & 1, drain, kErrTimeoutTma);
+      for (int j = 0; j < 2; ++j) mbar_wait(&bar_last[j * 2 + lane], (last_ph >> j & 1u) ^ 1u, drain, kErrTimeoutTma);
     }
   } else if (warp == kMma) {
     // ----------------------------------------------------------------- MMA
-    if (nq > 0) {
-      constexpr uint32_t idesc_s = idesc_f16(kBN, kBM, BF, false, false);  // M = keys, N = query rows
-      constexpr uint32_t idesc_g = idesc_f16(kBN, D, BF, false, true);     // M = keys, N = D
-      auto q_ready = [&](int u) {
-        if (ragged && u == nq - 1) return warp_wait(&bar_care[0], 0, ctl, kErrTimeoutOther);
-        return warp_wait(&bar_qf[u % QST], (u / QST) & 1, ctl, kErrTimeoutTma);
-      };
-      auto o_ready = [&](int u) {
-        if (ragged && u == nq - 1) return warp_wait(&bar_care[1], 0, ctl, kErrTimeoutOther);
-        return warp_wait(&bar_of[u % OST], (u / OST) & 1, ctl, kErrTimeoutTma);
-      };
-      bool ok = warp_wait(&bar_kv, 0, ctl, kErrTimeoutTma) && q_ready(0) && o_ready(0);
-      if (ok) {
+    constexpr uint32_t idesc_s = idesc_f16(kBN, kBM, BF, false, false);  // M = keys, N = query rows
+    constexpr uint32_t idesc_g = idesc_f16(kBN, D, BF, false, true);     // M = keys, N = D
+    RingAt<QST> q;  // the entry of S^T and dK to come
+    RingAt<OST> o;
+    uint32_t units = 0, tiles = 0, nc = 0, care_ph = 0;  // parities
+    bool any = false, ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      int nq, ragged;
+      {
+        const KvUnit p(&ring, i);
+        nq = p.nq;
+        ragged = p.ragged;
+      }
+      if (nq > 0) {
+        const uint32_t ph = care_ph >> (i & 1) & 1u;
+        if (ragged) care_ph ^= 1u << (i & 1);
+        auto q_ready = [&](int u) {
+          return ragged && u == nq - 1 ? warp_wait(&bar_care[(i & 1) * 2], ph, ctl, kErrTimeoutOther)
+                                       : warp_wait(&bar_qf[q.st], q.ph, ctl, kErrTimeoutTma);
+        };
+        auto o_ready = [&](int u) {
+          return ragged && u == nq - 1 ? warp_wait(&bar_care[(i & 1) * 2 + 1], ph, ctl, kErrTimeoutOther)
+                                       : warp_wait(&bar_of[o.st], o.ph, ctl, kErrTimeoutTma);
+        };
+        ok = warp_wait(&bar_kv, units, ctl, kErrTimeoutTma) && q_ready(0) && o_ready(0);
+        units ^= 1u;
+        if (ok && any) {  // the last unit's S^T has been read
+          ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax);
+          nc ^= 1u;
+        }
+        any = true;
+        if (!ok) break;
         tc_fence_after();
-        mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(0)), idesc_s);  // S^T = K Q^T
+        mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(q.st)), idesc_s);  // S^T = K Q^T
         commit_el(&bar_s);
-        mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(0)), idesc_s);  // dP^T = V dO^T
+        mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(o.st)), idesc_s);  // dP^T = V dO^T
         commit_el(&bar_dp);
-      }
-      for (int u = 0; ok && u < nq; ++u) {
-        const int sq = u % QST, so = u % OST;
-        const int sq1 = (u + 1) % QST, so1 = (u + 1) % OST;
-        const bool next = u + 1 < nq;
-        if (next) {
-          if (!(ok = warp_wait(&bar_consumed, u & 1, ctl, kErrTimeoutSoftmax))) break;
-          if (!(ok = q_ready(u + 1))) break;
+        if (nq == 1) commit_el(&bar_kvfree);
+        for (int u = 0; u < nq; ++u) {
+          const int sq = q.st, so = o.st;
+          const bool next = u + 1 < nq;
+          q.step();
+          o.step();
+          if (next) {
+            if (!(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
+            nc ^= 1u;
+            if (!(ok = q_ready(u + 1))) break;
+            tc_fence_after();
+            mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(q.st)), idesc_s);
+            commit_el(&bar_s);
+          }
+          if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
           tc_fence_after();
-          mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(sq1)), idesc_s);
-          commit_el(&bar_s);
-        }
-        if (!(ok = warp_wait(&bar_ds[0], u & 1, ctl, kErrTimeoutSoftmax))) break;
-        tc_fence_after();
-        mma_tY_il_g<0>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, u > 0);
-        mma_tY_il_g<0>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, u > 0);
-        if (!(ok = warp_wait(&bar_ds[1], u & 1, ctl, kErrTimeoutSoftmax))) break;
-        tc_fence_after();
-        mma_tY_il_g<1>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, true);
-        commit_el(&bar_oe[so]);
-        mma_tY_il_g<1>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, true);
-        commit_el(&bar_qe[sq]);
-        if (next) {
-          if (!(ok = o_ready(u + 1))) break;
+          mma_tY_il_g<0>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, u > 0);
+          mma_tY_il_g<0>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, u > 0);
+          if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
+          tiles ^= 1u;
           tc_fence_after();
-          mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(so1)), idesc_s);
-          commit_el(&bar_dp);
+          mma_tY_il_g<1>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, true);
+          commit_el(&bar_oe[so]);
+          mma_tY_il_g<1>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, true);
+          commit_el(&bar_qe[sq]);
+          if (next) {
+            if (!(ok = o_ready(u + 1))) break;
+            tc_fence_after();
+            mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(o.st)), idesc_s);
+            commit_el(&bar_dp);
+            if (u + 2 == nq) commit_el(&bar_kvfree);  // nothing reads K and V any more
+          }
         }
+        if (!ok) break;
+        commit_el(&bar_done);
+        q.step();  // the entries of dK and dV
+        o.step();
       }
-      if (ok) commit_el(&bar_done);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
   } else if (warp == kCare) {
-    if (nq > 0 && ragged) {
-      const int u = nq - 1, rows = (unit.left - u * TB) * G;
-      bool ok = warp_wait(&bar_last[0], 0, ctl, kErrTimeoutTma);
-      if (ok) {
-        zero_tile_rows<D / 64>(sQ(u % QST), rows, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_care[0]);
-        ok = warp_wait(&bar_last[1], 0, ctl, kErrTimeoutTma);
-      }
-      if (ok) {
-        zero_tile_rows<D / 64>(sDO(u % OST), rows, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_care[1]);
+    // ------------------------------ units ahead; rows behind the tokens
+    RingAsker asker;
+    if (asks) asker.ask(&ring);
+    int qs = 0, os = 0;  // slots of the unit's first entries
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      if (asks)
+        ok = asker.pass(&ring, args, list, i, ctl,
+                        [&](const PackedUnit& u, int4(&words)[4]) { make_kv_unit(u, TB, words); });
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const KvUnit p(&ring, i);
+      if (p.nq > 0) {
+        if (p.ragged) {
+          const int rows = (p.left - (p.nq - 1) * TB) * G;
+          for (int x = 0; x < 2; ++x) {
+            if (!(ok = warp_wait(&bar_last[(i & 1) * 2 + x], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma))) break;
+            zero_tile_rows<D / 64>(x ? sDO((os + p.nq - 1) % OST) : sQ((qs + p.nq - 1) % QST), rows, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_care[(i & 1) * 2 + x]);
+          }
+          ph ^= 1u << (i & 1);
+        }
+        qs = (qs + p.nq + 1) % QST;
+        os = (os + p.nq + 1) % OST;
       }
     }
+    if (asks) asker.drain(&ring, drain);
   } else {
     // ------------------------------------------- key-row softmax gradient
     const int hc = warp >> 2;  // half of the query tile's rows: columns [64 hc, 64 hc + 64)
     const int cb = 64 * hc;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const bool serves = threadIdx.x == 0;  // stores dK and dV
     // L and delta of the half's 64 rows, one value a thread; rows of no token read
     // L = +inf (P = 0) and delta = 0
     const int ld_arr = (threadIdx.x & 127) >> 6;  // 0: L, 1: delta
     const int ld_col = threadIdx.x & 63;
     const int ld_tok = static_cast<int>(args.g_div.div(cb + ld_col)), ld_head = cb + ld_col - ld_tok * G;
-    auto ld_fetch = [&](int u) -> float {
-      if (ld_tok >= TB || u * TB + ld_tok >= unit.left) return ld_arr ? 0.f : INFINITY;
-      const size_t row = static_cast<size_t>(unit.row) + u * TB + ld_tok;
-      return __ldg((ld_arr ? args.delta : args.lse) + row * args.shape.Hq + head * G + ld_head);
-    };
-    auto ld_slot = [&](int u) { return sLD + ((u & 1) * 2 + hc) * 128; };
-    if (nq > 0) {
-      ld_slot(0)[ld_arr * 64 + ld_col] = ld_fetch(0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_pub[hc]);
-    }
     const int m = lane & 3;
     const int kl = 32 * (warp & 3) + (lane >> 2);  // the thread's first key of the tile (then + 8, + 16, + 24)
+    const int r = threadIdx.x & 127;
+    uint32_t tiles = 0, units = 0;  // so far (tiles with any tokens' units)
+    RingAt<QST> q;
+    RingAt<OST> o;
+    int lent_q = -1, lent_o = -1;  // slots that stores still read
+    auto give_back = [&] {
+      if (lent_q >= 0) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive(&bar_qe[lent_q]);
+        mbar_arrive(&bar_oe[lent_o]);
+        lent_q = -1;
+      }
+    };
     bool ok = true;
-    for (int u = 0; u < nq; ++u) {
-      const float pre = (u + 1 < nq) ? ld_fetch(u + 1) : 0.f;
-      if (!(ok = warp_wait(&bar_s, u & 1, ctl, kErrTimeoutMma))) break;
-      tc_fence_after();
-      // 16-lane shapes: sv[32 g + 4 jj + e], e = {(k, q), (k, q + 1), (k + 8, q), (k + 8, q + 1)} with
-      // k = kl + 16 g and q = cb + 8 jj + 2 m
-      uint32_t sv[64];
-      tmem_ld_16x256b_x8(lane_addr + C::COL_A + cb, TB_CHUNK(sv, 0));
-      tmem_ld_16x256b_x8(lane_addr + (16u << 16) + C::COL_A + cb, TB_CHUNK(sv, 1));
-      tmem_ld_wait(TB_CHUNK(sv, 0));
-      tmem_ld_wait(TB_CHUNK(sv, 1));
-      tc_fence_before();
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+      const KvUnit p(&ring, i);
+      const int nq = p.nq;
+      auto grad = [&](void* to, long long st, long long sh) {
+        return static_cast<T*>(to) + p.head * sh + static_cast<long long>(p.krow) * st;
+      };
+      if (nq == 0) {  // keys that no query sees
+        T *dk = grad(args.dk, args.dk_t, args.dk_h), *dv = grad(args.dv, args.dv_t, args.dv_h);
+        zero_rows(min(p.n, kBN), args.dg, [&](int j) -> void* { return dk + j * args.dk_t; });
+        zero_rows(min(p.n, kBN), args.dg, [&](int j) -> void* { return dv + j * args.dv_t; });
+        if (serves) give_back();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.left[i & 1]);
+        continue;
+      }
+      const float* ld_base = (ld_arr ? args.delta : args.lse) +
+                             (static_cast<size_t>(p.row) + ld_tok) * args.shape.Hq + p.head * G + ld_head;
+      auto ld_fetch = [&](int u) -> float {
+        if (ld_tok >= TB || u * TB + ld_tok >= p.left) return ld_arr ? 0.f : INFINITY;
+        return __ldg(ld_base + static_cast<size_t>(u) * TB * args.shape.Hq);
+      };
+      auto ld_slot = [&](uint32_t c) { return sLD + ((c & 1) * 2 + hc) * 128; };
+      // (every warp is past the unit before: its last barrier)
+      ld_slot(tiles)[ld_arr * 64 + ld_col] = ld_fetch(0);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_consumed);  // score buffer free for S^T(u + 1)
-      if (!(ok = warp_wait(&bar_pub[(u & 1) * 2 + hc], (u >> 1) & 1, ctl, kErrTimeoutSoftmax))) break;
-      const float* sL = ld_slot(u) + 2 * m;
-      const float* sD = sL + 64;
-      const float2 sc2 = make_float2(args.scale_log2, args.scale_log2);
-      float p[64];
-#pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        const float2 l2 = *reinterpret_cast<const float2*>(sL + 8 * jj);
-        const float2 nl = fmul2(l2, make_float2(-kLog2e, -kLog2e));
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int i = 32 * g + 4 * jj;
-          const float2 y0 = ffma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), sc2, nl);
-          const float2 y1 = ffma2(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), sc2, nl);
-          p[i + 0] = ex2(y0.x);
-          p[i + 1] = ex2(y0.y);
-          p[i + 2] = ex2(y1.x);
-          p[i + 3] = ex2(y1.y);
-        }
-      }
-      // key k of the tile is seen from token off + k on: column q (token u TB + q / G)
-      // is masked iff q < (off + k - u TB) G
-      if (causal && unit.off + kBN - 1 > u * TB) {
-        int lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = unit.off + kl + 8 * i - u * TB;
-          lo[i] = min(max(x, 0), kBM) * G - cb - 2 * m;  // (past the tile's end: everything)
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int jj = 0; jj < 8; ++jj)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (8 * jj + (e & 1) < lo[2 * g + (e >> 1)]) p[32 * g + 4 * jj + e] = 0.f;
-      }
-      if (!(ok = warp_wait(&bar_dp, u & 1, ctl, kErrTimeoutMma))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        // chunk c (32 rows): read dP^T, write P^T and dS^T back into the same 32 columns
-        uint32_t dp[32];  // [g][16]
-        tmem_ld_16x256b_x4(lane_addr + C::COL_B + cb + 32 * c, TB_CHUNK16(dp, 0));
-        tmem_ld_16x256b_x4(lane_addr + (16u << 16) + C::COL_B + cb + 32 * c, TB_CHUNK16(dp, 1));
-        tmem_ld_wait(TB_CHUNK16(dp, 0));
-        tmem_ld_wait(TB_CHUNK16(dp, 1));
-        float2 nd2[4];  // -delta of the thread's query pairs
-#pragma unroll
-        for (int jq = 0; jq < 4; ++jq) {
-          const float2 d2 = *reinterpret_cast<const float2*>(sD + 8 * (4 * c + jq));
-          nd2[jq] = make_float2(-d2.x, -d2.y);
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t pp[8], pd[8];
-#pragma unroll
-          for (int jq = 0; jq < 4; ++jq) {
-            const int i = 32 * g + 4 * (4 * c + jq);
-            const int di = 16 * g + 4 * jq;
-            pp[2 * jq] = pack2<BF>(p[i], p[i + 1]);
-            pp[2 * jq + 1] = pack2<BF>(p[i + 2], p[i + 3]);
-            const float2 s0 = fmul2(make_float2(p[i], p[i + 1]),
-                                    fadd2(make_float2(__uint_as_float(dp[di]), __uint_as_float(dp[di + 1])), nd2[jq]));
-            const float2 s1 = fmul2(make_float2(p[i + 2], p[i + 3]),
-                                    fadd2(make_float2(__uint_as_float(dp[di + 2]), __uint_as_float(dp[di + 3])), nd2[jq]));
-            pd[2 * jq] = pack2<BF>(s0.x, s0.y);
-            pd[2 * jq + 1] = pack2<BF>(s1.x, s1.y);
-          }
-          const uint32_t ga = lane_addr + (static_cast<uint32_t>(16 * g) << 16) + C::COL_B + cb + 32 * c;
-          tmem_st_16x128b_x4(ga, pp);
-          tmem_st_16x128b_x4(ga + 16, pd);
-        }
-        tmem_st_wait();
+      if (lane == 0) mbar_arrive(&bar_pub[(tiles & 1) * 2 + hc]);
+      for (int u = 0; u < nq; ++u, ++tiles) {
+        const float pre = (u + 1 < nq) ? ld_fetch(u + 1) : 0.f;
+        if (!(ok = warp_wait(&bar_s, tiles & 1, ctl, kErrTimeoutMma))) break;
+        tc_fence_after();
+        // 16-lane shapes: sv[32 g + 4 jj + e], e = {(k, q), (k, q + 1), (k + 8, q), (k + 8, q + 1)} with
+        // k = kl + 16 g and q = cb + 8 jj + 2 m
+        uint32_t sv[64];
+        tmem_ld_16x256b_x8(lane_addr + C::COL_A + cb, TB_CHUNK(sv, 0));
+        tmem_ld_16x256b_x8(lane_addr + (16u << 16) + C::COL_A + cb, TB_CHUNK(sv, 1));
+        tmem_ld_wait(TB_CHUNK(sv, 0));
+        tmem_ld_wait(TB_CHUNK(sv, 1));
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_ds[c]);
-      }
-      if (u + 1 < nq) {  // every warp of the half is past tile u - 1, the buffer's previous tile
-        ld_slot(u + 1)[ld_arr * 64 + ld_col] = pre;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_pub[((u + 1) & 1) * 2 + hc]);
-      }
-    }
-    // ------------------------------------------------------------ epilogue
-    if (nq > 0 && ok) ok = warp_wait(&bar_done, 0, ctl, kErrTimeoutMma);
-    tc_fence_after();
-    // dV staged over K, dK (x sm_scale) over V (every MMA has finished)
-    const int r = threadIdx.x & 127;
-    const bool live = ok && nq > 0;
+        if (lane == 0) mbar_arrive(&bar_consumed);  // score buffer free for S^T(u + 1)
+        if (!(ok = warp_wait(&bar_pub[(tiles & 1) * 2 + hc], (tiles >> 1) & 1, ctl, kErrTimeoutSoftmax))) break;
+        const float* sL = ld_slot(tiles) + 2 * m;
+        const float* sD = sL + 64;
+        const float2 sc2 = make_float2(args.scale_log2, args.scale_log2);
+        float pr[64];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+        for (int jj = 0; jj < 8; ++jj) {
+          const float2 l2 = *reinterpret_cast<const float2*>(sL + 8 * jj);
+          const float2 nl = fmul2(l2, make_float2(-kLog2e, -kLog2e));
 #pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc) {
-        const int c = hc * (D / 64) + cc;
-        uint32_t v[32];
-        if (live) {
+          for (int g = 0; g < 2; ++g) {
+            const int x = 32 * g + 4 * jj;
+            const float2 y0 = ffma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), sc2, nl);
+            const float2 y1 = ffma2(make_float2(__uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3])), sc2, nl);
+            pr[x + 0] = ex2(y0.x);
+            pr[x + 1] = ex2(y0.y);
+            pr[x + 2] = ex2(y1.x);
+            pr[x + 3] = ex2(y1.y);
+          }
+        }
+        // key k of the tile is seen from token off + k on: column q (token u TB + q / G)
+        // is masked iff q < (off + k - u TB) G
+        if (p.causal && p.off + kBN - 1 > u * TB) {
+          int lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            lo[x] = min(max(p.off + kl + 8 * x - u * TB, 0), kBM) * G - cb - 2 * m;  // (past the tile's end: everything)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (8 * jj + (e & 1) < lo[2 * g + (e >> 1)]) pr[32 * g + 4 * jj + e] = 0.f;
+        }
+        if (!(ok = warp_wait(&bar_dp, tiles & 1, ctl, kErrTimeoutMma))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // chunk c (32 rows): read dP^T, write P^T and dS^T back into the same 32 columns
+          uint32_t dp[32];  // [g][16]
+          tmem_ld_16x256b_x4(lane_addr + C::COL_B + cb + 32 * c, TB_CHUNK16(dp, 0));
+          tmem_ld_16x256b_x4(lane_addr + (16u << 16) + C::COL_B + cb + 32 * c, TB_CHUNK16(dp, 1));
+          tmem_ld_wait(TB_CHUNK16(dp, 0));
+          tmem_ld_wait(TB_CHUNK16(dp, 1));
+          float2 nd2[4];  // -delta of the thread's query pairs
+#pragma unroll
+          for (int jq = 0; jq < 4; ++jq) {
+            const float2 d2 = *reinterpret_cast<const float2*>(sD + 8 * (4 * c + jq));
+            nd2[jq] = make_float2(-d2.x, -d2.y);
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t pp[8], pd[8];
+#pragma unroll
+            for (int jq = 0; jq < 4; ++jq) {
+              const int x = 32 * g + 4 * (4 * c + jq);
+              const int di = 16 * g + 4 * jq;
+              pp[2 * jq] = pack2<BF>(pr[x], pr[x + 1]);
+              pp[2 * jq + 1] = pack2<BF>(pr[x + 2], pr[x + 3]);
+              const float2 s0 = fmul2(make_float2(pr[x], pr[x + 1]),
+                                      fadd2(make_float2(__uint_as_float(dp[di]), __uint_as_float(dp[di + 1])), nd2[jq]));
+              const float2 s1 =
+                  fmul2(make_float2(pr[x + 2], pr[x + 3]),
+                        fadd2(make_float2(__uint_as_float(dp[di + 2]), __uint_as_float(dp[di + 3])), nd2[jq]));
+              pd[2 * jq] = pack2<BF>(s0.x, s0.y);
+              pd[2 * jq + 1] = pack2<BF>(s1.x, s1.y);
+            }
+            const uint32_t ga = lane_addr + (static_cast<uint32_t>(16 * g) << 16) + C::COL_B + cb + 32 * c;
+            tmem_st_16x128b_x4(ga, pp);
+            tmem_st_16x128b_x4(ga + 16, pd);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_ds[c]);
+        }
+        if (u == 0 && serves) give_back();
+        if (u + 1 < nq) {  // every warp of the half is past tile u - 1, the buffer's previous tile
+          ld_slot(tiles + 1)[ld_arr * 64 + ld_col] = pre;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_pub[((tiles + 1) & 1) * 2 + hc]);
+        }
+        q.step();
+        o.step();
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      if (!(ok = warp_wait(&bar_done, units & 1, ctl, kErrTimeoutMma) &&
+                 warp_wait(&bar_out[(units & 1) * 2], (units >> 1) & 1, ctl, kErrTimeoutMma) &&
+                 warp_wait(&bar_out[(units & 1) * 2 + 1], (units >> 1) & 1, ctl, kErrTimeoutMma)))
+        break;
+      ++units;
+      tc_fence_after();
+      // dV staged in dO's ring, dK (x sm_scale) in Q's
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+#pragma unroll
+        for (int cc = 0; cc < D / 64; ++cc) {
+          const int c = hc * (D / 64) + cc;
+          uint32_t v[32];
           tmem_ld_x32(lane_addr + (a == 0 ? C::COL_DV : C::COL_DK) + 32 * c, v);
           tmem_ld_wait(v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
+          stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sDO(o.st) : sQ(q.st)), r, c, v, a ? args.sm_scale : 1.f);
         }
-        stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sK : sV), r, c, v, a ? args.sm_scale : 1.f);
       }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      named_bar_sync(1, kRowWarps * 32);
+      const bool whole = p.n >= kBN, refill = TB * G < kBM;
+      if (whole) {
+        if (serves) {
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb) {
+            tma_store_3d(&tm_dv, sDO(o.st) + kb * (kBM * 128), kb * 64, p.krow, p.head);
+            tma_store_3d(&tm_dk, sQ(q.st) + kb * (kBM * 128), kb * 64, p.krow, p.head);
+          }
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          lent_q = q.st;
+          lent_o = o.st;
+        }
+      } else {  // the rows behind the keys are another sequence's
+        T *dk = grad(args.dk, args.dk_t, args.dk_h), *dv = grad(args.dv, args.dv_t, args.dv_h);
+        copy_tile_rows(sDO(o.st), args.dg, threadIdx.x, kRowWarps * 32,
+                       [&](int j) -> void* { return j < p.n ? dv + j * args.dv_t : nullptr; });
+        copy_tile_rows(sQ(q.st), args.dg, threadIdx.x, kRowWarps * 32,
+                       [&](int j) -> void* { return j < p.n ? dk + j * args.dk_t : nullptr; });
+      }
+      if (!whole || refill) {
+        // the slots go back at once; rows that no box fills are zeros again
+        if (whole && serves) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        named_bar_sync(1, kRowWarps * 32);
+        if (refill) {
+          if (warp < 2) zero_tile_rows<D / 64>(warp ? sDO(o.st) : sQ(q.st), TB * G, lane);
+          fence_proxy_async_smem();
+          named_bar_sync(1, kRowWarps * 32);
+        }
+        if (serves) {
+          mbar_arrive(&bar_qe[q.st]);
+          mbar_arrive(&bar_oe[o.st]);
+          lent_q = -1;
+        }
+      }
+      q.step();
+      o.step();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kRowWarps * 32);
-    if (unit.n >= kBN) {
-      if (warp == 0 && lane == 0) {
-#pragma unroll
-        for (int kb = 0; kb < D / 64; ++kb) {
-          tma_store_3d(&tm_dv, sK + kb * (kBM * 128), kb * 64, unit.krow, head);
-          tma_store_3d(&tm_dk, sV + kb * (kBM * 128), kb * 64, unit.krow, head);
-        }
-        tma_store_commit_and_wait_read();
-      }
-    } else {  // the rows behind the keys are another sequence's
-      auto copy = [&](const uint8_t* tile, void* to, long long st, long long sh) {
-        T* p = static_cast<T*>(to) + head * sh + static_cast<long long>(unit.krow) * st;
-        copy_tile_rows(tile, args.dg, threadIdx.x, kRowWarps * 32,
-                       [&](int i) -> void* { return i < unit.n ? p + i * st : nullptr; });
-      };
-      copy(sK, args.dv, args.dv_t, args.dv_h);
-      copy(sV, args.dk, args.dk_t, args.dk_h);
+    if (serves) {
+      give_back();
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
   }
 
