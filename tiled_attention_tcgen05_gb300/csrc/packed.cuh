@@ -129,11 +129,13 @@ __host__ __device__ inline int packed_key_tiles(int tokens, int off, int n, int 
 // done its unit takes over that of a block that has not been launched yet
 // (cluster launch control: the launch is cancelled and its block index handed
 // over), so units go out one by one, the longest first.
-// One warp asks for units ahead and passes them to the others through two slots;
-// unit i is in slot i % 2, and is passed on only once every other role has
-// left unit i - 2, so that no role is ever two units ahead of another.
+// One warp asks for the next unit once a producer has asked for the last tile of this
+// one (earlier, and a block would sit on a unit that another could start on), and
+// passes it to the others through two slots; unit i is in slot i % 2, and is
+// passed on only once every other role has left unit i - 2, so that no role is
+// ever two units ahead of another.
 struct UnitRing {
-  uint64_t full[2], left[2], answered;
+  uint64_t full[2], left[2], near, answered;
   uint4 answer;       // of the cancellation asked for
   int4 unit[2][4];    // words of the kernel's own, made by pass()'s `fill`; [3].w: 1: there is one
 };
@@ -143,6 +145,7 @@ __device__ __forceinline__ void ring_init(UnitRing* r, int roles) {
     mbar_init(&r->full[i], 1);
     mbar_init(&r->left[i], roles);
   }
+  mbar_init(&r->near, 1);
   mbar_init(&r->answered, 1);
 }
 
@@ -172,30 +175,29 @@ __device__ __forceinline__ bool ring_answer(const UnitRing* r, uint32_t* block) 
 
 // The asking thread's side.
 struct RingAsker {
-  int asks = 0;       // requests made
-  bool open = false;  // the last is unanswered
-  __device__ __forceinline__ void ask(UnitRing* r) {
-    ring_ask(r);
-    ++asks;
-    open = true;
-  }
+  uint32_t asks = 0;  // requests made
+  bool more = true, open = false;  // there may be another unit; a request is unanswered
   __device__ __forceinline__ bool wait(UnitRing* r, const WaitCtl& ctl) {
     if (!mbar_wait(&r->answered, (asks - 1) & 1, ctl, kErrTimeoutOther)) return false;
     open = false;
     return true;
   }
-  // Once in unit i: passes unit i + 1 on; fill(u, words) makes the slot's words of it.
+  // In unit i: passes unit i + 1 on; fill(u, words) makes the slot's words of it.
   // False: a wait ran out.
   template <typename F>
   __device__ __forceinline__ bool pass(UnitRing* r, const PackedArgs& a, const PackedList& l, int i, const WaitCtl& ctl,
                                        F fill) {
     const int next = i + 1, s = next & 1;
     int4 words[4] = {};
-    if (open) {
+    if (!mbar_wait(&r->near, i & 1, ctl, kErrTimeoutOther)) return false;
+    if (more) {
+      ring_ask(r);
+      ++asks;
+      open = true;
       if (!wait(r, ctl)) return false;
       uint32_t block;
-      if (ring_answer(r, &block) && block < l.items) {
-        ask(r);
+      more = ring_answer(r, &block) && block < l.items;
+      if (more) {
         fill(packed_item(a, l, block), words);
         words[3].w = 1;
       }

@@ -25,7 +25,10 @@ namespace ta {
 
 namespace {
 
-constexpr int kThreads = 352;
+// Registers: 384 x 168 at launch = 256 x 200 (row warps) + 128 x 104; warp 11 only makes up the
+// warpgroup.  With 168 a thread for all and units asked for one ahead, three documents of
+// up to 16384 tokens, 32 / 8 heads of 128 took 2185 us, so 2024 us.
+constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kCare = 10;
 constexpr int kRowWarps = 8;
 
@@ -225,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (lane == 0) {
       RingAt<STAGES> k;
       int e = 0;              // entries so far
@@ -235,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto slot = [&] { return e < STAGES || mbar_wait(&bar_kvempty[k.st], k.ph ^ 1u, ctl, kErrTimeoutMma); };
       for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
         const DqUnit p(&ring, i);
+        if (p.nkv == 0) mbar_arrive(&ring.near);
         for (int t = -1; p.nkv > 0 && t <= p.nkv; ++t, ++e) {
+          if (t == p.nkv) mbar_arrive(&ring.near);
           if (!(ok = slot())) break;
           own &= ~(1u << k.st);
           if (t < 0) {
@@ -269,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMma) {
     // ----------------------------------------------------------------- MMA
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr uint32_t idesc_s = idesc_f16(kBM, kBN, BF, false, false);
     constexpr uint32_t idesc_g = idesc_f16(kBM, D, BF, false, true);
     RingAt<STAGES> k;
@@ -341,37 +348,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
-  } else if (warp == kCare) {
+  } else if (warp >= kCare) {
     // --------------------------------- units ahead; rows behind the keys
-    RingAsker asker;
-    if (asks) asker.ask(&ring);
-    int st = 0;  // slot of the unit's first entry
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
-      if (asks)
-        ok = asker.pass(&ring, args, list, i, ctl,
-                        [&](const PackedUnit& u, int4(&words)[4]) { make_dq_unit(u, TB, words); });
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const DqUnit p(&ring, i);
-      if (p.nkv > 0) {
-        if (p.ragged()) {
-          if (!(ok = warp_wait(&bar_last[i & 1], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma))) break;
-          ph ^= 1u << (i & 1);
-          const int at = (st + p.nkv) % STAGES, first = p.n - (p.nkv - 1) * kBN;
-          zero_tile_rows<D / 64>(sK(at), first, lane);
-          zero_tile_rows<D / 64>(sV(at), first, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_care[i & 1]);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kCare) {
+      RingAsker asker;
+      int st = 0;  // slot of the unit's first entry
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+        const DqUnit p(&ring, i);
+        if (p.nkv > 0) {
+          if (p.ragged()) {
+            if (!(ok = warp_wait(&bar_last[i & 1], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma))) break;
+            ph ^= 1u << (i & 1);
+            const int at = (st + p.nkv) % STAGES, first = p.n - (p.nkv - 1) * kBN;
+            zero_tile_rows<D / 64>(sK(at), first, lane);
+            zero_tile_rows<D / 64>(sV(at), first, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_care[i & 1]);
+          }
+          st = (st + p.nkv + 2) % STAGES;
         }
-        st = (st + p.nkv + 2) % STAGES;
+        if (asks)
+          ok = asker.pass(&ring, args, list, i, ctl,
+                          [&](const PackedUnit& u, int4(&words)[4]) { make_dq_unit(u, TB, words); });
+        ok = __all_sync(0xffffffffu, ok);
       }
+      if (asks) asker.drain(&ring, drain);
     }
-    if (asks) asker.drain(&ring, drain);
   } else {
     // --------------------------------------------- query-row softmax gradient
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int hc = warp >> 2;  // key half of the tile: columns [64 hc, 64 hc + 64)
     const int cb = 64 * hc;
     const int r = threadIdx.x & 127;
@@ -694,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducer) {
     // ---------------------- producer: lane 0 K, V and the Q ring; lane 1 the dO ring
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (lane < 2) {
       const bool is_q = lane == 0;
       const int depth = is_q ? QST : OST;
@@ -711,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_rows<D>(sK, &tm_k, &bar_kv, p.krow, p.head);
           load_rows<D>(sV, &tm_v, &bar_kv, p.krow, p.head);
         }
+        if (p.nq == 0 && is_q) mbar_arrive(&ring.near);
         for (int u = 0; p.nq > 0 && u <= p.nq; ++u, ++e) {
+          if (u == p.nq && is_q) mbar_arrive(&ring.near);
           const int st = e % depth;
           if (e >= depth && !(ok = mbar_wait(&empty[st], ((e / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
           own &= ~(1u << st);
@@ -741,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMma) {
     // ----------------------------------------------------------------- MMA
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr uint32_t idesc_s = idesc_f16(kBN, kBM, BF, false, false);  // M = keys, N = query rows
     constexpr uint32_t idesc_g = idesc_f16(kBN, D, BF, false, true);     // M = keys, N = D
     RingAt<QST> q;  // the entry of S^T and dK to come
@@ -758,13 +772,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nq > 0) {
         const uint32_t ph = care_ph >> (i & 1) & 1u;
         if (ragged) care_ph ^= 1u << (i & 1);
+        const int care_u = ragged ? nq - 1 : -1;
         auto q_ready = [&](int u) {
-          return ragged && u == nq - 1 ? warp_wait(&bar_care[(i & 1) * 2], ph, ctl, kErrTimeoutOther)
-                                       : warp_wait(&bar_qf[q.st], q.ph, ctl, kErrTimeoutTma);
+          const bool c = u == care_u;
+          return warp_wait(c ? &bar_care[(i & 1) * 2] : &bar_qf[q.st], c ? ph : q.ph, ctl, kErrTimeoutTma);
         };
         auto o_ready = [&](int u) {
-          return ragged && u == nq - 1 ? warp_wait(&bar_care[(i & 1) * 2 + 1], ph, ctl, kErrTimeoutOther)
-                                       : warp_wait(&bar_of[o.st], o.ph, ctl, kErrTimeoutTma);
+          const bool c = u == care_u;
+          return warp_wait(c ? &bar_care[(i & 1) * 2 + 1] : &bar_of[o.st], c ? ph : o.ph, ctl, kErrTimeoutTma);
         };
         ok = warp_wait(&bar_kv, units, ctl, kErrTimeoutTma) && q_ready(0) && o_ready(0);
         units ^= 1u;
@@ -820,39 +835,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.left[i & 1]);
     }
-  } else if (warp == kCare) {
+  } else if (warp >= kCare) {
     // ------------------------------ units ahead; rows behind the tokens
-    RingAsker asker;
-    if (asks) asker.ask(&ring);
-    int qs = 0, os = 0;  // slots of the unit's first entries
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
-      if (asks)
-        ok = asker.pass(&ring, args, list, i, ctl,
-                        [&](const PackedUnit& u, int4(&words)[4]) { make_kv_unit(u, TB, words); });
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const KvUnit p(&ring, i);
-      if (p.nq > 0) {
-        if (p.ragged) {
-          const int rows = (p.left - (p.nq - 1) * TB) * G;
-          for (int x = 0; x < 2; ++x) {
-            if (!(ok = warp_wait(&bar_last[(i & 1) * 2 + x], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma))) break;
-            zero_tile_rows<D / 64>(x ? sDO((os + p.nq - 1) % OST) : sQ((qs + p.nq - 1) % QST), rows, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_care[(i & 1) * 2 + x]);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kCare) {
+      RingAsker asker;
+      int qs = 0, os = 0;  // slots of the unit's first entries
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
+        const KvUnit p(&ring, i);
+        if (p.nq > 0) {
+          if (p.ragged) {
+            const int rows = (p.left - (p.nq - 1) * TB) * G;
+            for (int x = 0; x < 2; ++x) {
+              ok = warp_wait(&bar_last[(i & 1) * 2 + x], ph >> (i & 1) & 1u, ctl, kErrTimeoutTma);
+              if (!ok) break;
+              zero_tile_rows<D / 64>(x ? sDO((os + p.nq - 1) % OST) : sQ((qs + p.nq - 1) % QST), rows, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_care[(i & 1) * 2 + x]);
+            }
+            if (!ok) break;
+            ph ^= 1u << (i & 1);
           }
-          ph ^= 1u << (i & 1);
+          qs = (qs + p.nq + 1) % QST;
+          os = (os + p.nq + 1) % OST;
         }
-        qs = (qs + p.nq + 1) % QST;
-        os = (os + p.nq + 1) % OST;
+        if (asks)
+          ok = asker.pass(&ring, args, list, i, ctl,
+                          [&](const PackedUnit& u, int4(&words)[4]) { make_kv_unit(u, TB, words); });
+        ok = __all_sync(0xffffffffu, ok);
       }
+      if (asks) asker.drain(&ring, drain);
     }
-    if (asks) asker.drain(&ring, drain);
   } else {
     // ------------------------------------------- key-row softmax gradient
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int hc = warp >> 2;  // half of the query tile's rows: columns [64 hc, 64 hc + 64)
     const int cb = 64 * hc;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);

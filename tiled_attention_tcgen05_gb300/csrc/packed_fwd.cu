@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(bar, C::TILE);
           load_rows<D>(is_k ? sK(st) : sV(st), map, bar, p.krow + t * kBN, p.head);
         }
-        if (ok) mbar_arrive(&ring.left[i & 1]);
+        if (!ok) break;
+        if (is_k) mbar_arrive(&ring.near);
+        mbar_arrive(&ring.left[i & 1]);
       }
       for (int t = e - depth > 0 ? e - depth : 0; t < e; ++t)
         if (!(own >> (t % depth) & 1u)) mbar_wait(&full[t % depth], (t / depth) & 1, drain, kErrTimeoutTma);
@@ -343,18 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp - kCare;
     const int r0 = half * 64;  // each warp's half of the tile's rows
     RingAsker asker;
-    if (asks) asker.ask(&ring);
     int vst = 0;  // V slot of the unit's first tile
     uint32_t part_ph = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
-      if (half == 1) {
-        if (asks)
-          ok = asker.pass(&ring, args, list, i, ctl,
-                          [&](const PackedUnit& u, int4(&words)[4]) { make_pair(u, TB, words); });
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      }
       const Pair p(&ring, i);
       const int nt = p.nt();
       for (int t = p.t_part; t < nt; ++t) {
@@ -398,6 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       vst = (vst + nt) % VST;
       __syncwarp();
       if (ok && half == 0 && lane == 0) mbar_arrive(&ring.left[i & 1]);
+      if (ok && half == 1) {
+        if (asks)
+          ok = asker.pass(&ring, args, list, i, ctl,
+                          [&](const PackedUnit& u, int4(&words)[4]) { make_pair(u, TB, words); });
+        ok = __all_sync(0xffffffffu, ok);
+      }
     }
     if (asks) asker.drain(&ring, drain);
   } else {
@@ -420,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_rows<D>(sQ(w, st), &tm_q, &bar_q[w][st], p.head * G, p.row + w * TB);
       ++q_armed;
     };
-    // Q of the unit behind unit i, if there is one (this thread waits until it is known)
+    // Q of the unit behind unit i, if there is one: this thread waits until it is known, which
+    // needs nothing from this group any more but what it has given by then (its last P)
     auto load_next_q = [&](int i, int st) {
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // O of the buffer's last unit is on its way
       if (ring_take(&ring, i + 1, ctl)) load_q(i + 1, st);
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_p[w]);
-        if (QB == 2 && t == 0 && serves) load_next_q(i, q.st ^ 1);
+        if (QB == 2 && t + 1 == n && serves) load_next_q(i, q.st ^ 1);
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
