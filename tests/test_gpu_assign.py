@@ -44,6 +44,7 @@ def compare(got, want, B, width):
     (1, 0, 1, 1, 0, 0), (1, 30, 1, 16, 1, 0), (3, 50, 1, 7, 0, 0), (64, 300, 1, 16, 4, 0), (64, 100, 90, 8, 5, 0),
     (64, 100, 90, 8, 5, 0.5), (33, 40, 300, 64, 0, 0.3), (1023, 20, 9, 4, 3, 0), (1024, 20, 9, 4, 3, 0.6),
     (1025, 20, 9, 4, 3, 0), (2500, 12, 20, 5, 9, 0.7), (200, 64, 200, 24, 0, 0), (5, 3000, 4000, 32, 2, 0),
+    (300, 500, 700, 8, 0, 0.8), (8192, 6, 5, 4, 2, 0), (8193, 6, 5, 4, 2, 0), (9001, 6, 5, 4, 2, 0.8),
 ])
 @pytest.mark.parametrize("seed", [1, 2])
 def test_against_the_oracle(gpu_lib, B, kv, new, page, spare, short, seed):

@@ -706,7 +706,7 @@ def cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, s
         pages.data_ptr(), pages.shape[1], kv_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), free.shape[0],
         free_count.data_ptr(), int(page_size), kv, ql, cu, pos, slot, slot + 4 * total, B, total,
         _raw_stream(index, stream)))
-    return Assigned(*torch.split_with_sizes(out, sizes))
+    return Assigned(*torch.unsafe_split_with_sizes(out, sizes))
 
 
 # --------------------------------------------------------- rotary positions
