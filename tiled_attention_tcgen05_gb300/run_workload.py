@@ -7,10 +7,12 @@ Workloads (synth_inputs.WORKLOADS): 1 fwd+bwd fp16 B1 H2 S128 D64 non-causal;
 2 fwd+bwd bf16 causal B4 H16 S2048 D128; 3 fwd+bwd bf16 causal B1 H32 S8192
 D128; 4 JVP forward (with tL) and the backward of the JVP, fp16 B2 H8 S1024
 D64 (--causal 0/1); 5 piecewise fwd+bwd bf16 causal B2 H16 S4096 D64 w=512.
---shape B,H,S,D replaces the workload's sizes; --op merge / --op fp8 / --op cache
-runs the merge (forward and backward), the e5m2 forward or a generation step
+--shape B,H,S,D replaces the workload's sizes; --op merge / --op fp8 / --op cache /
+--op prompt / --op packed runs the merge (forward and backward), the e5m2 forward, a generation step
 over a key/value cache (append, attention; --cache its type, --tokens new
-tokens a sequence) instead; --kv-split sets
+tokens a sequence), a step of prompts on their way into one (pages assigned, queries
+and keys normed and rotated, packed attention) or a training step of packed documents
+(the same forward and backward, without a cache) instead; --kv-split sets
 the key split of the one-query-tile forward.  Prints the mean milliseconds per
 step.
 """
@@ -53,6 +55,44 @@ def make_cache_step(shape=None, cache="bf16", tokens=1):
     def step():
         ta.cache_append(c, k, v, pages, kv_lens)
         ta.attn_cache_fwd(q, c, pages, kv_lens, ws=ws)
+    return step
+
+
+def make_prompt_step(shape=None, cache="bf16", train=False):
+    """B prompts (or documents) of S / 4 to S tokens, packed, H query heads over H / 4 key heads.  A server's
+    step assigns pages of 16 and writes rotated keys and values there; a training step goes backward instead."""
+    B, H, S, D = shape if shape is not None else (3, 32, 16384, 128)
+    Hkv, page = max(1, H // 4), 16
+    lens = [S - (S * 3 // 4) * b // B for b in range(B)]
+    T = sum(lens)
+    q, do = (si.randn((T, H, D), "bf16", si.seed_for(9, i)).cuda() for i in (0, 1))
+    k, v = (si.randn((T, Hkv, D), "bf16", si.seed_for(9, i)).cuda() for i in (2, 3))
+    wq, wk = (1 + 0.1 * si.randn((D,), "bf16", si.seed_for(9, i)).cuda() for i in (4, 5))
+    rot = ta.Rotary(D)
+    if train:
+        cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
+        pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]).cuda()
+        plan = ta.packed_plan(cu, T, H, Hkv)
+
+        def train_step():
+            qr, kr = ta.qk_norm_rotary_fwd(q, k, wq, wk, pos, rot)
+            o, lse = ta.attn_packed_fwd(qr, kr, v, plan)
+            dq, dk, dv = ta.attn_packed_bwd(qr, kr, v, o, lse, do, plan)
+            return ta.qk_norm_rotary_bwd(dq, dk, q, k, wq, wk, pos, rot, dq_out=dq, dk_out=dk), dv
+        return train_step
+    need = (S + page - 1) // page
+    ct = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[cache]
+    c = ta.kv_cache(B * need, Hkv, page, D, ct)
+    pages = torch.full((B, need), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(B * need, dtype=torch.int32, device="cuda")
+    count = torch.full((1,), B * need, dtype=torch.int32, device="cuda")
+    none, new = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32).cuda()
+
+    def step():
+        a = ta.cache_assign(pages, none, new, free, count, page, T)
+        qr = ta.rotary_append(c, q, k, v, a.positions, a.slots, rot, wq, wk)
+        _, kr = ta.qk_norm_rotary_fwd(None, k, None, wk, a.positions, rot)
+        return ta.attn_packed_fwd(qr, kr, v, ta.packed_plan(a.cu_seqlens, T, H, Hkv))
     return step
 
 
@@ -116,9 +156,11 @@ def main():
     ap.add_argument("--warmup", type=int, default=1)
     ap.add_argument("--causal", type=int, default=None)
     ap.add_argument("--shape", type=str, default=None, help="B,H,S,D instead of the workload's own (M = N = S)")
-    ap.add_argument("--op", type=str, default=None, choices=["merge", "fp8", "cache"],
-                    help="time attn_merge_fwd/bwd, attn_fwd_fp8 or a step over a key/value cache instead of a workload")
-    ap.add_argument("--cache", type=str, default="bf16", choices=["bf16", "e4m3", "int8"], help="cache type of --op cache")
+    ap.add_argument("--op", type=str, default=None, choices=["merge", "fp8", "cache", "prompt", "packed"],
+                    help="time attn_merge_fwd/bwd, attn_fwd_fp8, a step over a key/value cache, a step of prompts or a "
+                         "training step of packed documents instead of a workload")
+    ap.add_argument("--cache", type=str, default="bf16", choices=["bf16", "e4m3", "int8"],
+                    help="cache type of --op cache and --op prompt")
     ap.add_argument("--tokens", type=int, default=1, help="new tokens a sequence of --op cache")
     ap.add_argument("--kv-split", type=str, default="auto", choices=["auto", "never", "always"],
                     help="key split of the one-query-tile forward (JVP, D = 128 piecewise)")
@@ -128,6 +170,8 @@ def main():
     shape = tuple(int(x) for x in a.shape.split(",")) if a.shape else None
     if a.op == "cache":
         step = make_cache_step(shape, a.cache, a.tokens)
+    elif a.op in ("prompt", "packed"):
+        step = make_prompt_step(shape, a.cache, a.op == "packed")
     else:
         step = make_op_step(a.op, shape) if a.op else make_step(a.workload, a.causal, shape)
     for _ in range(a.warmup):
