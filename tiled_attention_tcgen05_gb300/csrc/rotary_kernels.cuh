@@ -592,27 +592,33 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
   }
 }
 
-// dw[i] = sum of the blocks' partial sums, each of a block's 8 warps over every
-// eighth block, in a fixed order.
+// dw[i] = sum of the blocks' partial sums, each of a block's 32 warps over every
+// 32nd block, in a fixed order.  A warp's loads are under way together: with 8 warps and four
+// at a time the kernel was nine dependent trips to L2.
+constexpr int kDwWarps = 32;
 template <int D>
-__global__ void __launch_bounds__(256) rotary_dw_kernel(const float* part, int blocks, float* dwq, float* dwk) {
-  __shared__ float sums[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kDwWarps * 32) rotary_dw_kernel(const float* part, int blocks, float* dwq,
+                                                                  float* dwk) {
+  constexpr int kMost = (kRotBwdBlocks + kDwWarps - 1) / kDwWarps;
+  __shared__ float sums[kDwWarps][32];
+  const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane, warp = threadIdx.x >> 5;
   pdl_wait();
-  float v[4] = {};
-  int i = warp;
-  for (; i + 24 < blocks; i += 32)
+  float v[kMost];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] += part[static_cast<size_t>(i + 8 * u) * 2 * D + col];
-  for (; i < blocks; i += 8) v[0] += part[static_cast<size_t>(i) * 2 * D + col];
-  sums[warp][threadIdx.x & 31] = (v[0] + v[1]) + (v[2] + v[3]);
+  for (int u = 0; u < kMost; ++u) {
+    const int i = warp + kDwWarps * u;
+    v[u] = i < blocks ? part[static_cast<size_t>(i) * 2 * D + col] : 0.f;
+  }
+#pragma unroll
+  for (int u = 1; u < kMost; ++u) v[0] += v[u];
+  sums[warp][lane] = v[0];
   __syncthreads();
   if (warp == 0) {
-    float t = 0.f;
+    float t[4] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += sums[k][threadIdx.x];
+    for (int k = 0; k < kDwWarps; ++k) t[k & 3] += sums[k][lane];
     float* out = col < D ? dwq : dwk;
-    if (out) out[col % D] = t;
+    if (out) out[col % D] = (t[0] + t[1]) + (t[2] + t[3]);
   }
 }
 
@@ -643,7 +649,7 @@ static cudaError_t run_rotary_any(int mode, int ct, const RotArgs& a, const Cach
   kern<<<a.blocks, kWarps * 32, kWarps * a.slice_groups * 2048, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pdl_launch(rotary_dw_kernel<D>, dim3(2 * D / 32), 256, 0, s, static_cast<const float*>(a.part), a.blocks, a.dwq,
+  return pdl_launch(rotary_dw_kernel<D>, dim3(2 * D / 32), kDwWarps * 32, 0, s, static_cast<const float*>(a.part), a.blocks, a.dwq,
                     a.dwk);
 }
 
