@@ -387,8 +387,9 @@ ta_status attn_cache_assign(int* pages, int max_pages, const int* kv_lens, const
  * ta_rows: rows [B, heads, T, D] of 16-bit elements with element strides (b, head,
  * t); D contiguous, rows 16-byte aligned.  positions[b * pos_b + t * pos_t] int32.
  * Computed in fp32, rounded once.  dt TA_F16 or TA_BF16; D in {16, 32, 64, 128};
- * Hq or Hkv may be 0.  An output may be its input (same strides), and overlaps
- * nothing else.  Calls allocate nothing and may be captured. */
+ * Hq or Hkv may be 0.  An output may be the input of its kind (q_out q or dq, k_out
+ * k or dk; same strides), and overlaps nothing else (TA_ERR_INVALID_ARG where they
+ * start at one address).  Calls allocate nothing and may be captured. */
 typedef struct {
   void* p;
   int64_t sb, sh, st;
@@ -449,8 +450,9 @@ ta_status attn_rotary_append(const ta_kv_cache* cache, const ta_rotary_call* cal
  * key head h / (Hq / Hkv), Hq / Hkv <= 128.  Causal: query i of a sequence sees its keys
  * j <= i + n_k - n_q.  Rows that see nothing get O = 0, L = -inf; rows that belong to
  * no sequence are not read, and not written in outputs.  lse is [total_q, Hq]
- * fp32.  dt TA_F16 or TA_BF16; D in {16, 32, 64, 128}.  Nothing is allocated,
- * and calls may be captured.
+ * fp32.  dt TA_F16 or TA_BF16; D in {16, 32, 64, 128}.  Outputs overlap nothing
+ * (TA_ERR_INVALID_ARG where they start at another operand's address).  Nothing is
+ * allocated, and calls may be captured.
  *
  * A plan lists the tiles of the sequences; it serves every call on the
  * same offsets, sizes and heads (every layer, forward and backward), and is

@@ -94,6 +94,25 @@ def test_rotary_refusals(ta):
         assert call(fn, **kw) == want, kw
 
 
+def test_outputs_on_other_operands_are_refused(ta):
+    call = rotary(ta)
+    at = {r: 0x10000 * (i + 1) for i, r in enumerate(("q", "k", "v", "dq", "dk", "q_out", "k_out"))}
+    for fn in ROTARY:
+        bwd = fn == ROTARY[3]
+        for kw in [dict(q_out__p=at["k"]), dict(k_out__p=at["q"]), dict(k_out__p=at["q_out"]),
+                   dict(q_out__p=at["q"], q_out__st=1024), dict(k_out__p=at["k"], k_out__sh=128)] + \
+                [dict(q_out__p=at["dk"]), dict(k_out__p=at["dq"]), dict(q_out__p=at["dq"], q_out__sb=8192)] * bwd:
+            assert call(fn, **kw) == INVALID, (fn, kw)
+    call = packed(ta)
+    at = {r: 0x10000 * (i + 1) for i, r in enumerate(("q", "k", "v", "o", "dO", "dq", "dk", "dv"))}
+    for out, others in (("dq", ("q", "k", "v", "o", "dO", "dk", "dv")), ("dk", ("q", "k", "v", "o", "dO", "dv")),
+                        ("dv", ("q", "k", "v", "o", "dO"))):
+        for x in others:
+            assert call("attn_packed_bwd", **{out + "__p": at[x]}) == INVALID, (out, x)
+    for x in ("q", "k", "v"):
+        assert call("attn_packed_fwd", o__p=at[x]) == INVALID, x
+
+
 def test_append_refusals(ta):
     names = fields("ta_rotary_call")
     lib = ta.load()

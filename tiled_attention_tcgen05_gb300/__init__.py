@@ -988,9 +988,13 @@ _PACKED = struct.Struct("@32q5q7if")
 
 class PackedPlan:
     """What attn_packed_fwd and attn_packed_bwd need to know of the sequences; made by packed_plan, good for every
-    call on the same offsets and heads (every layer, forward and backward)."""
+    call on the same offsets and heads (every layer, forward and backward).  Its memory is that of a tensor of the
+    stream it was made on: where other streams use it, record_stream tells the allocator."""
 
     __slots__ = ("B", "total", "total_k", "Hq", "Hkv", "causal", "device", "_index", "_t", "_ptr", "_bytes")
+
+    def record_stream(self, stream):
+        self._t.record_stream(stream)
 
 
 def packed_plan(cu_seqlens, total, Hq, Hkv, causal=True, cu_seqlens_k=None, total_k=None, stream=None) -> PackedPlan:

@@ -834,9 +834,8 @@ static ta_status rotary_args(const ta_rotary_call* c, int mode, const ta_kv_cach
       return TA_ERR_ALIGNMENT;
   }
   const __int128 tokens = static_cast<__int128>(c->B) * c->T;
-  const int heads = c->Hq + c->Hkv;
   if (static_cast<long long>(c->Hq) + 2ll * c->Hkv > 65536 || tokens > 0x7fffffffll) return TA_ERR_UNSUPPORTED;
-  if (tokens == 0 || heads == 0) return TA_OK;  // nothing to do: a->units stays 0
+  if (tokens == 0 || c->Hq + c->Hkv == 0) return TA_OK;  // nothing to do: a->units stays 0
   ta_status st = check_ints({c->positions});
   if (st == TA_OK && mode == kRotAppend) st = check_ints({c->slots});
   if (st == TA_OK && c->dim > 0 && !c->turns) st = TA_ERR_INVALID_ARG;
@@ -854,6 +853,19 @@ static ta_status rotary_args(const ta_rotary_call* c, int mode, const ta_kv_cach
     rows(c->dk, c->Hkv, &a->dk);
   }
   if (st != TA_OK) return st;
+  // an output may be the input of its kind, row for row, and no other operand (unused ones are null here)
+  auto in_place = [&](const RotRows& out, const RotRows& in, int H) {
+    return out.p != in.p || ((c->B <= 1 || out.sb == in.sb) && (H <= 1 || out.sh == in.sh) && (c->T <= 1 || out.st == in.st));
+  };
+  auto apart = [](const RotRows& out, std::initializer_list<const void*> others) {
+    for (const void* p : others)
+      if (out.p && out.p == p) return false;
+    return true;
+  };
+  if (!in_place(a->qo, a->q, c->Hq) || !in_place(a->qo, a->dq, c->Hq) || !in_place(a->ko, a->k, c->Hkv) ||
+      !in_place(a->ko, a->dk, c->Hkv) || !apart(a->qo, {a->k.p, a->v.p, a->dk.p, a->ko.p}) ||
+      !apart(a->ko, {a->q.p, a->dq.p}))
+    return TA_ERR_INVALID_ARG;
   a->pos = c->positions;
   a->pos_b = c->pos_b;
   a->pos_t = c->pos_t;
@@ -1004,6 +1016,20 @@ static ta_status packed_args(const ta_packed_call* c, bool bwd, PackedArgs* a, P
   }
   if (st == TA_OK && has_q) st = check_ints({c->lse});
   if (st != TA_OK) return st;
+  {  // an output is no other operand
+    const void* q_side[] = {c->q.p, bwd ? c->dO.p : nullptr, c->o.p, bwd ? c->dq.p : nullptr};
+    const void* k_side[] = {c->k.p, c->v.p, bwd ? c->dk.p : nullptr, bwd ? c->dv.p : nullptr};
+    const void* at[8];
+    bool out[8];
+    int n = 0;
+    for (int i = 0; i < 4; ++i) {
+      if (has_q && q_side[i]) out[n] = i == (bwd ? 3 : 2), at[n++] = q_side[i];
+      if (has_k && k_side[i]) out[n] = i >= 2, at[n++] = k_side[i];
+    }
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < n; ++j)
+        if (i != j && out[i] && at[i] == at[j]) return TA_ERR_INVALID_ARG;
+  }
   *a = PackedArgs{};
   a->plan = static_cast<const uint8_t*>(c->plan);
   a->shape = p;
