@@ -807,9 +807,12 @@ static ta_status check_rows(const ta_rows& r, int B, int H, int T, RotRows* out)
   return st;
 }
 
-// Warps that a call should have: 16 on each of 152 SMs hide the latency of a
-// row's loads; tokens are cut into slices of heads until there are as many.
-constexpr int kRotWarps = 152 * 16;
+// Warps that a call should have: tokens are cut into slices of heads until there are
+// as many.  Few tokens would leave most of the GPU idle, and each slice makes the
+// token's cosines and sines anew.  32 / 8 heads of 128, us a call in a replayed row of calls, with
+// 1, 4, 16 and 48 warps for each of 152 SMs: 64 tokens 3.1, 2.5, 2.5, 2.5; 256 tokens
+// 4.7, 3.1, 3.8, 3.8; 1024 tokens 5.0, 5.0, 5.7, 6.2; from 4096 on all but 48 (13.1 against 11.6) the same.
+constexpr int kRotWarps = 152 * 4;
 
 static ta_status rotary_args(const ta_rotary_call* c, int mode, const ta_kv_cache* cache, RotArgs* a, CacheArgs* ca) {
   if (!c || c->B < 0 || c->T < 0 || c->Hq < 0 || c->Hkv < 0) return TA_ERR_INVALID_ARG;

@@ -18,6 +18,12 @@
 // The rings run on from one unit to the next.  What leaves a block goes
 // through a ring's slot, too: an entry behind the unit's tiles, which the storing
 // thread hands back.
+//
+// Bound, for long sequences, by the MMAs: S and dP are made in both passes, seven products where
+// five would do, and no dQ is summed in memory.  Three documents of up to 8192 tokens, 32 / 8 heads of
+// 128, bf16: 2.02 ms (0.89 + 1.28 apart); seven products at the measured peak take 1.81, five 1.30.
+// Short documents are bound by the way from one role to the next: 24 of up to 700 tokens, 16 heads
+// of 64, 95 us (45 + 53) where memory would need 19.
 #include "launch.h"
 #include "packed.cuh"
 
