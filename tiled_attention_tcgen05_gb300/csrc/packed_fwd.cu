@@ -6,8 +6,8 @@
 //
 // A CTA works on two 128-row query tiles of one key head (packed.cuh: TB tokens x G
 // heads each) that share every K/V tile: warps 0-3 and 4-7 run their softmax, one
-// thread a row (and each group's first thread loads its Q and stores its O), warp 8
-// feeds the K and V rings by TMA, warp 9 issues the MMAs, alternating between the
+// thread a row (and each group's first thread stores its O), warp 8
+// feeds the K and V rings and Q by TMA, warp 9 issues the MMAs, alternating between the
 // tiles so that one's softmax runs beside the other's products, and warps 10 and 11
 // look after the key tiles that some row sees only in part:
 //   * the rows behind the sequence's keys belong to another sequence or to
@@ -21,12 +21,14 @@
 // warp 11 asks for the units.
 //
 // Bound, for long sequences, by the MMAs: three prompts of up to 16384 tokens, 32 / 8 heads of 128, bf16,
-// take 2.05 ms, 1704 TFLOP/s, 0.91 of the measured peak.  Short ones are bound by
-// the way from one role to the next: 64 prompts of up to 250 tokens, 32 / 4 heads of 64, take 40 us, some 4.5 us
-// a unit of one or two key tiles, of which its memory and products need 1.3.  Measured and not
-// taken: scores of the tile after next before a tile's product with V (long 2.44 ms), two
-// more softmax groups (2.78 ms), a loop over 32 columns at a time in tiles seen in part, which skips those that
-// no row sees (short 40 us all the same, long 2.22 ms).
+// take 2.05 ms, 1704 TFLOP/s, 0.91 of the measured peak.  Short ones are bound by the way
+// from one role to the next and by fetching code that runs once a unit: 64 prompts of up to 250 tokens, 32 / 4
+// heads of 64, take 35 us, some 3.5 us a unit of one or two key tiles, of which its memory and products need 1.3.
+// For them there is an instance whose short units (kFewTiles) go through one copy of each
+// product and through loops over 32 columns; with the long units' straight-line code they took 40 us. The
+// other way round the loops cost long units 13 % (products) and 8 % (scores).
+// Measured and not taken: scores of the tile after next before a tile's product with V (long 2.44 ms), two
+// more softmax groups (2.78 ms).
 #include "launch.h"
 #include "packed.cuh"
 
@@ -37,6 +39,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kCare = 10;  // warps; kCare and the one behind it
 // registers: 384 x 168 at launch = 256 x 200 (softmax) + 128 x 104
+// Key tiles of a short unit.  3 and 5 instead of 2 gain up to 5 % (400 tokens, 16 / 16 heads of 128) and lose up to
+// 10 (400 tokens, 16 / 16 of 64); sequences of up to 256 take the same.
+constexpr int kFewTiles = 2;
 constexpr int kPart = 3;  // tiles that some row sees in part: its tokens' last keys lie within 256 of each other
 
 template <int D>
@@ -126,7 +131,7 @@ struct RingAt {
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -140,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_k[KST], bar_kempty[KST], bar_v[VST], bar_vempty[VST];
   __shared__ __align__(8) uint64_t bar_part[2][kPart], bar_care[2][kPart];  // [unit % 2]: such a tile is in, is seen to
   __shared__ __align__(8) uint64_t bar_q[2][QB], bar_s[2], bar_p[2], bar_o[2], bar_ofinal[2];  // [group]
+  __shared__ __align__(8) uint64_t bar_qfree[2];  // [group] (QB == 2) its other Q buffer can be loaded
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int care_odd[2][kPart][2];  // the tile held non-finite values that only some rows see (by caring warp)
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_p[w], 4);
       mbar_init(&bar_o[w], 1);
       mbar_init(&bar_ofinal[w], 2);
+      mbar_init(&bar_qfree[w], 1);
     }
     fence_mbar_init();
   }
@@ -198,8 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int zero = 0;  // (an exit waits for its own copies whatever the abort flag says)
   const WaitCtl drain{args.err, args.timeout_ns, reinterpret_cast<volatile int*>(&zero)};
+  const uint32_t qbytes = (D / 64) * TB * G * 128;  // of a Q tile: rows past its TB x G are not loaded
+  // (on the way out) waits for the Q tiles of group w that are still on their way
+  auto drain_q = [&](int w, uint32_t n) {
+    for (uint32_t a = n > QB ? n - QB : 0; a < n; ++a)
+      mbar_wait(&bar_q[w][a % QB], (a / QB) & 1, drain, kErrTimeoutTma);
+  };
   if (warp == kProducer) {
-    // ------------------------ TMA producer: lane 0 the K ring, lane 1 the V ring
+    // ------ TMA producer: lane 0 the K ring and, where it has two buffers, Q; lane 1 the V ring
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (lane < 2) {
       const bool is_k = lane == 0;
@@ -210,10 +223,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e = 0;             // tiles so far
       uint32_t own = 0;      // V slots whose last tile came through bar_part
       uint32_t part_ph = 0;  // parities of bar_part's phases (those armed so far are odd in number)
+      uint32_t qs[2] = {0, 0};  // (lane 0) Q tiles asked for, by group
       bool ok = true;
       for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
         const Pair p(&ring, i);
         const int nt = p.nt();
+        if (QB == 2 && is_k) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || p.n_t(w) == 0) continue;
+            if (qs[w] > 0 && !(ok = mbar_wait(&bar_qfree[w], (qs[w] - 1) & 1, ctl, kErrTimeoutSoftmax))) continue;
+            uint64_t* bar = &bar_q[w][qs[w] % QB];
+            mbar_expect_tx(bar, qbytes);
+            load_rows<D>(sQ(w, qs[w] % QB), &tm_q, bar, p.head * G, p.row + w * TB);
+            ++qs[w];
+          }
+          if (!ok) break;
+        }
         for (int t = 0; t < nt; ++t, ++e) {
           const int st = e % depth;
           if (e >= depth && !(ok = mbar_wait(&empty[st], ((e / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
@@ -234,6 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_k) mbar_arrive(&ring.near);
         mbar_arrive(&ring.left[i & 1]);
       }
+      if (QB == 2 && is_k) {
+        drain_q(0, qs[0]);
+        drain_q(1, qs[1]);
+      }
       for (int t = e - depth > 0 ? e - depth : 0; t < e; ++t)
         if (!(own >> (t % depth) & 1u)) mbar_wait(&full[t % depth], (t / depth) & 1, drain, kErrTimeoutTma);
       if (!is_k)  // (a phase that was never armed: the parity of the one before it, which has passed)
@@ -247,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_pv = idesc_f16(kBM, D, BF, false, true);
     RingAt<KST> k;
     RingAt<VST> v;
-    RingAt<QB> q[2];
+    uint32_t qs0 = 0, qs1 = 0;  // Q tiles of the groups so far
     uint32_t np0 = 0, np1 = 0;  // parities of the groups' tiles
     uint32_t part_ph = 0;
     bool ok = true;
@@ -261,23 +291,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         t_part = p.t_part;
       }
       const int nt = max(n0, n1);
-      if (nt > 0) {
-        const uint32_t aQ0 = smem_u32(sQ(0, q[0].st)), aQ1 = smem_u32(sQ(1, q[1].st));
-        int odd = 0;
+      int odd = 0;
+      if (SHORT && nt <= kFewTiles) {
+        // one copy of each product, for both groups and a unit's first tile, too: a short unit's
+        // time is that of fetching this code
+#pragma unroll 1
+        for (int t = -1; t < nt; ++t) {
+          const bool next = t + 1 < nt;
+          if (t >= 0) {
+            if (t < t_part) {
+              ok = warp_wait(&bar_v[v.st], v.ph, ctl, kErrTimeoutTma);
+            } else {
+              const int j = t - t_part, bit = (i & 1) * kPart + j;
+              ok = warp_wait(&bar_care[i & 1][j], part_ph >> bit & 1u, ctl, kErrTimeoutOther);
+              part_ph ^= 1u << bit;
+              if (ok) odd |= care_odd[i & 1][j][0] | care_odd[i & 1][j][1];
+            }
+            if (!ok) break;
+          }
+          if (next && !(ok = warp_wait(&bar_k[k.st], k.ph, ctl, kErrTimeoutTma))) break;
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            const int n = w ? n1 : n0;
+            if (t >= n) continue;
+            const bool more = t + 1 < n;
+            const uint32_t cs = tmem + (w ? kColS1 : 0u);
+            const uint32_t qs = w ? qs1 : qs0;
+            if (t < 0) {
+              if (!more) continue;
+              if (!(ok = warp_wait(&bar_q[w][qs % QB], (qs / QB) & 1u, ctl, kErrTimeoutTma))) break;
+            } else {
+              if (!(ok = warp_wait(&bar_p[w], w ? np1 : np0, ctl, kErrTimeoutSoftmax))) break;
+              np0 ^= w ? 0u : 1u;
+              np1 ^= w ? 1u : 0u;
+              tc_fence_after();
+              mma_pv<D>(tmem + (w ? kColO1 : kColO0), cs, smem_u32(sV(v.st)), idesc_pv, t > 0);
+              commit_el(&bar_o[w]);
+            }
+            if (more) {
+              tc_fence_after();
+              mma_abT<D>(cs, smem_u32(sQ(w, qs % QB)), smem_u32(sK(k.st)), idesc_qk);
+              commit_el(&bar_s[w]);
+            } else {
+              if (w) ++qs1;
+              else ++qs0;
+              commit_el(&bar_ofinal[w]);
+              if (lane == 0) {
+                unit_odd[w] = odd;
+                mbar_arrive(&bar_ofinal[w]);  // (with the flag behind it)
+              }
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          if (t >= 0) {
+            commit_el(&bar_vempty[v.st]);
+            v.step();
+          }
+          if (next) {
+            commit_el(&bar_kempty[k.st]);
+            k.step();
+          }
+        }
+      } else if (nt > 0) {
+        const uint32_t aQ0 = smem_u32(sQ(0, qs0 % QB)), aQ1 = smem_u32(sQ(1, qs1 % QB));
         ok = warp_wait(&bar_k[k.st], k.ph, ctl, kErrTimeoutTma);
         if (ok && n0 > 0) {
-          ok = warp_wait(&bar_q[0][q[0].st], q[0].ph, ctl, kErrTimeoutTma);
+          ok = warp_wait(&bar_q[0][qs0 % QB], (qs0 / QB) & 1u, ctl, kErrTimeoutTma);
           if (ok) {
-            q[0].step();
+            ++qs0;
             tc_fence_after();
             mma_abT<D>(tmem, aQ0, smem_u32(sK(k.st)), idesc_qk);
             commit_el(&bar_s[0]);
           }
         }
         if (ok && n1 > 0) {
-          ok = warp_wait(&bar_q[1][q[1].st], q[1].ph, ctl, kErrTimeoutTma);
+          ok = warp_wait(&bar_q[1][qs1 % QB], (qs1 / QB) & 1u, ctl, kErrTimeoutTma);
           if (ok) {
-            q[1].step();
+            ++qs1;
             tc_fence_after();
             mma_abT<D>(tmem + kColS1, aQ1, smem_u32(sK(k.st)), idesc_qk);
             commit_el(&bar_s[1]);
@@ -418,22 +509,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool serves = r == 0;  // the group's thread that loads Q and stores O
     uint32_t np = 0, units = 0;  // parities of this group's tiles, and units with any
     RingAt<QB> q;                // Q of the unit at hand
-    uint32_t q_armed = 0;        // (serving thread) Q tiles asked for
-    // Q of unit i's tile of this group into buffer st, which nothing reads any more
-    auto load_q = [&](int i, int st) {
+    // QB == 1: the serving thread loads Q, and waits until it knows of the unit behind unit i.  That
+    // needs nothing from this group any more.
+    uint32_t q_armed = 0;
+    auto load_q = [&](int i) {
       const Pair p(&ring, i);
       if (p.n_t(w) == 0) return;
-      mbar_expect_tx(&bar_q[w][st], (D / 64) * TB * G * 128);  // rows past a tile's TB x G are not loaded
-      load_rows<D>(sQ(w, st), &tm_q, &bar_q[w][st], p.head * G, p.row + w * TB);
+      mbar_expect_tx(&bar_q[w][0], qbytes);
+      load_rows<D>(sQ(w, 0), &tm_q, &bar_q[w][0], p.head * G, p.row + w * TB);
       ++q_armed;
     };
-    // Q of the unit behind unit i, if there is one: this thread waits until it is known, which
-    // needs nothing from this group any more but what it has given by then (its last P)
-    auto load_next_q = [&](int i, int st) {
+    auto load_next_q = [&](int i) {
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // O of the buffer's last unit is on its way
-      if (ring_take(&ring, i + 1, ctl)) load_q(i + 1, st);
+      if (ring_take(&ring, i + 1, ctl)) load_q(i + 1);
     };
-    if (serves) load_q(0, 0);
+    if (QB == 1 && serves) load_q(0);
     bool ok = true;
     for (int i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, ring_take(&ring, i, ctl))) break;
@@ -445,84 +535,188 @@ __global__ void __launch_bounds__(kThreads, 1)
         t_part = p.t_part;
       }
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = 0; t < n; ++t, np ^= 1u) {
-        if (!(ok = warp_wait(&bar_s[w], np, ctl, kErrTimeoutMma))) break;
-        tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(lane_addr + scol + 32 * c, TB_CHUNK(s, c));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(TB_CHUNK(s, c));
-        float x[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j) x[j] = __uint_as_float(s[j]);
-        if (t >= t_part) {
+      if (SHORT && n <= kFewTiles) {
+        // A short unit's time is that of fetching code that runs once in it: 32 columns at a time, as far as
+        // a row of the warp sees, and twice over the scores.
+#pragma unroll 1
+        for (int t = 0; t < n; ++t, np ^= 1u) {
+          if (!(ok = warp_wait(&bar_s[w], np, ctl, kErrTimeoutMma))) break;
+          tc_fence_after();
+          if (QB == 2 && t == 0 && serves) {  // O of the last unit has left the other buffer
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            mbar_arrive(&bar_qfree[w]);
+          }
           const int lim = sees - t * kBN;
-          const int near = __shfl_sync(0xffffffffu, lim, 0);  // (rows' tokens ascend)
+          // (rows' tokens ascend)
+          const int near = __shfl_sync(0xffffffffu, lim, 0), far = __shfl_sync(0xffffffffu, lim, 31);
+          const int chunks = min(max(far + 32, 0) >> 5, 4);
+          float x[32];
+          auto load = [&](int c) {
+            uint32_t s[32];
+            tmem_ld_x32(lane_addr + scol + 32 * c, s);
+            tmem_ld_wait(s);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(s[j]);
             if (32 * c + 31 > near) {
+              const int v = lim - 32 * c;
+              const uint32_t keep = v >= 31 ? 0xffffffffu : v < 0 ? 0u : (2u << v) - 1u;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (32 * c + j > lim) x[32 * c + j] = -INFINITY;
+                if (!(keep >> j & 1u)) x[j] = -INFINITY;
+            }
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            load(c);
+            float m4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              m4[k] = fmax3(x[k], x[4 + k], x[8 + k]);
+              m4[k] = fmax3(m4[k], x[12 + k], x[16 + k]);
+              m4[k] = fmax3(m4[k], x[20 + k], x[24 + k]);
+              m4[k] = fmaxf(m4[k], x[28 + k]);
+            }
+            mx = fmaxf(mx, fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]));
+          }
+          const float m_new = fmaxf(m_ref, mx * args.scale_log2);
+          float alpha = 1.f;
+          bool resc = false;
+          if (t == 0) {
+            m_ref = m_new;
+          } else if (m_new > m_ref + kRescaleThreshold) {
+            resc = true;
+            alpha = ex2(m_ref - m_new);
+            m_ref = m_new;
+          }
+          const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          const float2 sc2 = make_float2(args.scale_log2, args.scale_log2);
+          const float2 nm2 = make_float2(neg_m, neg_m);
+          float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            if (c < chunks) {
+              load(c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 y = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2);
+                const float2 pr = make_float2(ex2(y.x), ex2(y.y));
+                rs2[e & 3] = fadd2(rs2[e & 3], pr);
+                pk[e] = pack2<BF>(pr.x, pr.y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            }
+            tmem_st_x16(lane_addr + scol + 16 * c, pk);
+          }
+          const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
+          l = l * alpha + (rsa.x + rsa.y);
+          if (t > 0 && __any_sync(0xffffffffu, resc)) {
+            if (!(ok = warp_wait(&bar_o[w], np ^ 1u, ctl, kErrTimeoutMma))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
+              tmem_ld_wait(ov);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tmem_st_x32(lane_addr + ocol + 32 * c, ov);
             }
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_p[w]);
         }
-        float mx8[8];  // eight three-input max chains of 16 scores each
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          mx8[k] = fmax3(x[k], x[8 + k], x[16 + k]);
-#pragma unroll
-          for (int j = 24; j < 120; j += 16) mx8[k] = fmax3(mx8[k], x[j + k], x[j + 8 + k]);
-          mx8[k] = fmaxf(mx8[k], x[120 + k]);
-        }
-        const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-        const float m_new = fmaxf(m_ref, mx * args.scale_log2);
-        bool resc = false;
-        float alpha = 1.f;
-        if (t == 0) {
-          m_ref = m_new;
-        } else if (m_new > m_ref + kRescaleThreshold) {
-          resc = true;
-          alpha = ex2(m_ref - m_new);
-          m_ref = m_new;
-        }
-        const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-        const float2 sc2 = make_float2(args.scale_log2, args.scale_log2);
-        const float2 nm2 = make_float2(neg_m, neg_m);
-        float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 16 columns of S, 8 packed columns of P, at a time
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = ffma2(make_float2(x[16 * c + 2 * e], x[16 * c + 2 * e + 1]), sc2, nm2);
-            const float2 pr = make_float2(ex2(y.x), ex2(y.y));
-            rs2[e & 3] = fadd2(rs2[e & 3], pr);
-            pk[e] = pack2<BF>(pr.x, pr.y);
-          }
-          tmem_st_x8(lane_addr + scol + 8 * c, pk);
-        }
-        const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
-        l = l * alpha + (rsa.x + rsa.y);
-        if (t > 0 && __any_sync(0xffffffffu, resc)) {
-          if (!(ok = warp_wait(&bar_o[w], np ^ 1u, ctl, kErrTimeoutMma))) break;
+      } else {
+        for (int t = 0; t < n; ++t, np ^= 1u) {
+          if (!(ok = warp_wait(&bar_s[w], np, ctl, kErrTimeoutMma))) break;
           tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
-            tmem_ld_wait(ov);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-            tmem_st_x32(lane_addr + ocol + 32 * c, ov);
+          if (QB == 2 && t == 0 && serves) {  // O of the last unit has left the other buffer
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            mbar_arrive(&bar_qfree[w]);
           }
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_x32(lane_addr + scol + 32 * c, TB_CHUNK(s, c));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait(TB_CHUNK(s, c));
+          float x[128];
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] = __uint_as_float(s[j]);
+          if (t >= t_part) {
+            const int lim = sees - t * kBN;
+            // (rows' tokens ascend)
+            const int near = __shfl_sync(0xffffffffu, lim, 0), far = __shfl_sync(0xffffffffu, lim, 31);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (32 * c + 31 > near) {
+                const int v = lim - 32 * c;
+                const uint32_t keep = v >= 31 ? 0xffffffffu : v < 0 ? 0u : (2u << v) - 1u;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!(keep >> j & 1u)) x[32 * c + j] = -INFINITY;
+              }
+            }
+          }
+          float mx8[8];  // eight three-input max chains of 16 scores each
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            mx8[k] = fmax3(x[k], x[8 + k], x[16 + k]);
+#pragma unroll
+            for (int j = 24; j < 120; j += 16) mx8[k] = fmax3(mx8[k], x[j + k], x[j + 8 + k]);
+            mx8[k] = fmaxf(mx8[k], x[120 + k]);
+          }
+          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+          const float m_new = fmaxf(m_ref, mx * args.scale_log2);
+          bool resc = false;
+          float alpha = 1.f;
+          if (t == 0) {
+            m_ref = m_new;
+          } else if (m_new > m_ref + kRescaleThreshold) {
+            resc = true;
+            alpha = ex2(m_ref - m_new);
+            m_ref = m_new;
+          }
+          const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          const float2 sc2 = make_float2(args.scale_log2, args.scale_log2);
+          const float2 nm2 = make_float2(neg_m, neg_m);
+          float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {  // 16 columns of S, 8 packed columns of P, at a time
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = ffma2(make_float2(x[16 * c + 2 * e], x[16 * c + 2 * e + 1]), sc2, nm2);
+              const float2 pr = make_float2(ex2(y.x), ex2(y.y));
+              rs2[e & 3] = fadd2(rs2[e & 3], pr);
+              pk[e] = pack2<BF>(pr.x, pr.y);
+            }
+            tmem_st_x8(lane_addr + scol + 8 * c, pk);
+          }
+          const float2 rsa = fadd2(fadd2(rs2[0], rs2[1]), fadd2(rs2[2], rs2[3]));
+          l = l * alpha + (rsa.x + rsa.y);
+          if (t > 0 && __any_sync(0xffffffffu, resc)) {
+            if (!(ok = warp_wait(&bar_o[w], np ^ 1u, ctl, kErrTimeoutMma))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
+              tmem_ld_wait(ov);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tmem_st_x32(lane_addr + ocol + 32 * c, ov);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_p[w]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p[w]);
-        if (QB == 2 && t + 1 == n && serves) load_next_q(i, q.st ^ 1);
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
@@ -536,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<T*>(args.o) + (qrow + k) * args.o_t + (p.head * G + j - k * G) * args.o_h;
       };
       if (n == 0) {  // rows that see nothing
-        if (serves) load_next_q(i, q.st);
+        if (QB == 1 && serves) load_next_q(i);
         if (tok < tokens) args.lse[(qrow + tok) * args.shape.Hq + p.head * G + g] = -INFINITY;
         const int c = args.dg >> 3;
         for (int j = r; j < tokens * G * c; j += 128) {
@@ -586,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage_row_chunk_sw128<BF>(stage, r, c, ov, 1.f);
           }
         } else {
-#pragma unroll
+#pragma unroll(SHORT ? 1 : 4)
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
             tmem_ld_x32(lane_addr + ocol + 32 * c, ov);
@@ -608,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           copy_tile_rows(sQ(w, q.st), args.dg, r, 128, out_row);
           named_bar_sync(1 + w, 4 * 32);
         }
-        if (QB == 1 && serves) load_next_q(i, 0);
+        if (QB == 1 && serves) load_next_q(i);
         q.step();
       }
       __syncwarp();
@@ -616,8 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (serves) {
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      for (uint32_t a = q_armed > QB ? q_armed - QB : 0; a < q_armed; ++a)
-        mbar_wait(&bar_q[w][a % QB], (a / QB) & 1, drain, kErrTimeoutTma);
+      if (QB == 1) drain_q(w, q_armed);
     }
   }
 
@@ -627,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int D>
-cudaError_t run(const PackedMaps& m, const PackedArgs& a, cudaStream_t s) {
+template <typename T, int D, bool SHORT>
+cudaError_t run_kernel(const PackedMaps& m, const PackedArgs& a, cudaStream_t s) {
   using C = PfCfg<D>;
-  auto kern = packed_fwd_kernel<T, D>;
+  auto kern = packed_fwd_kernel<T, D, SHORT>;
   static std::atomic<bool> attr[kMaxDevices];
   cudaError_t e = smem_attr_once(kern, C::SMEM, attr);
   if (e != cudaSuccess) return e;
@@ -638,6 +831,15 @@ cudaError_t run(const PackedMaps& m, const PackedArgs& a, cudaStream_t s) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   kern<<<static_cast<unsigned>(blocks), kThreads, C::SMEM, s>>>(m.q, m.k, m.v, m.o, a);
   return cudaGetLastError();
+}
+
+// Sequences of up to 512 keys on average: most units have one or two key tiles.  With and without the instance for
+// them, us, 65536 / 4 tokens and fewer: 32 / 4 heads of 64, sequences of 100 tokens 121 / 153, 256 114 / 132, 400 137 / 147,
+// 512 78 / 81, 1024 109 / 108, 2048 173 / 167; 32 / 8 of 128: 100 179 / 194, 256 169 / 171, 400 233 / 230, 1024 159 / 155.
+template <typename T, int D>
+cudaError_t run(const PackedMaps& m, const PackedArgs& a, cudaStream_t s) {
+  const bool few = a.shape.total_k <= 512ll * a.shape.B;
+  return few ? run_kernel<T, D, true>(m, a, s) : run_kernel<T, D, false>(m, a, s);
 }
 
 }  // namespace
