@@ -76,3 +76,20 @@ def test_scores_far_apart(gpu_lib, D, pad):
     ref, bounds = packed_case(q, k, v, cu, cu, True, "bf16")
     within("O", o[:cu[-1]], ref[0][:cu[-1]], bounds[0][:cu[-1]])
     within("L", lse[:cu[-1]], ref[1][:cu[-1]], bounds[1][:cu[-1]])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 1)])
+def test_a_lone_key_has_no_gradient(gpu_lib, D, G, causal):
+    """P = 1 whatever the score: dQ and dK are zeros, dV is the sum of dO."""
+    lens, klens = [1, 5, 1, 130, 129], [1, 1, 1, 1, 129]
+    cu, ck = offsets(lens), offsets(klens)
+    q, k, v = make(6, cu[-1], ck[-1], 2 * G, 2, D, "bf16")
+    do = values(9, tuple(q.shape), "bf16")
+    got = run(gpu_lib, q, k, v, cu, ck, causal, do)
+    assert gpu_lib.sync_status() == "TA_OK"
+    ref, bounds = packed_case(q, k, v, cu, ck, causal, "bf16", do)
+    for name, g, r, b in zip(("O", "L", "dQ", "dK", "dV"), got, ref, bounds):
+        within(name, g, r, b)
+    assert (got[2][:cu[4]] == 0).all() and (got[3][:ck[4]] == 0).all()
+    assert (got[2][cu[4] + 1:] != 0).any() and (got[3][ck[4]:] != 0).any()

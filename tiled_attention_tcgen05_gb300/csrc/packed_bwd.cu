@@ -518,14 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (every warp has handed in its last dS, and so has read O and delta)
       if (serves && ring_take(&ring, i + 1, ctl)) load_o(i + 1);
       __syncwarp();
-      // dQ (x sm_scale) staged in its slot
+      // dQ (x sm_scale) staged in its slot.  A lone key has P = 1 whatever its score: dS is zero, and what the
+      // products leave of dP - delta is not.
+      const float by = p.n == 1 ? 0.f : args.sm_scale;
 #pragma unroll
       for (int cc = 0; cc < D / 64; ++cc) {
         const int c = hc * (D / 64) + cc;
         uint32_t v[32];
         tmem_ld_x32(lane_addr + C::COL_DQ + 32 * c, v);
         tmem_ld_wait(v);
-        stage_row_chunk_sw128<BF>(smem_u32(sK(k.st)), r, c, v, args.sm_scale);
+        stage_row_chunk_sw128<BF>(smem_u32(sK(k.st)), r, c, v, by);
       }
       tc_fence_before();
       fence_proxy_async_smem();
@@ -591,6 +593,7 @@ struct KvUnit {
   int krow, n, row, left, off;  // first key's row, keys from it on, first token that sees any, tokens from it on; see PackedUnit
   int nq, head, causal;         // query tiles, key head
   int ragged;                   // the last tile ends behind the tokens
+  int lone;                     // the sequence has one key
   __device__ __forceinline__ KvUnit(const UnitRing* r, int i) {
     const int4 a = ring_words(r, i, 0), b = ring_words(r, i, 1), c = ring_words(r, i, 2);
     krow = a.x;
@@ -602,13 +605,14 @@ struct KvUnit {
     head = b.z;
     causal = b.w;
     ragged = c.x;
+    lone = c.y;
   }
 };
 __device__ __forceinline__ void make_kv_unit(const PackedUnit& u, int TB, int4 (&words)[4]) {
   const int nq = (u.left + TB - 1) / TB;
   words[0] = make_int4(u.krow, u.n, u.row, u.left);
   words[1] = make_int4(u.off, nq, u.pad[1], u.pad[0]);
-  words[2] = make_int4(nq * TB > u.left, 0, 0, 0);
+  words[2] = make_int4(nq * TB > u.left, u.pad[2], 0, 0);
 }
 
 template <typename T, int D>
@@ -1039,7 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       ++units;
       tc_fence_after();
-      // dV staged in dO's ring, dK (x sm_scale) in Q's
+      // dV staged in dO's ring, dK (x sm_scale; a lone key's is zero) in Q's
+      const float by = p.lone ? 0.f : args.sm_scale;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
 #pragma unroll
@@ -1048,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld_x32(lane_addr + (a == 0 ? C::COL_DV : C::COL_DK) + 32 * c, v);
           tmem_ld_wait(v);
-          stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sDO(o.st) : sQ(q.st)), r, c, v, a ? args.sm_scale : 1.f);
+          stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sDO(o.st) : sQ(q.st)), r, c, v, a ? by : 1.f);
         }
       }
       tc_fence_before();
