@@ -541,9 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lent = k.st;
         }
       } else {  // the rows behind it are another sequence's
-        const int rows = p.left * G;
-        copy_tile_rows(sK(k.st), args.dg, threadIdx.x, kRowWarps * 32,
-                       [&](int j) -> void* { return j < rows ? out_row(j) : nullptr; });
+        copy_tile_rows(sK(k.st), args.dg, threadIdx.x, kRowWarps * 32, p.left * G, out_row);
         named_bar_sync(1, kRowWarps * 32);
         if (serves) mbar_arrive(&bar_kvempty[k.st]);
       }
@@ -1073,10 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {  // the rows behind the keys are another sequence's
         T *dk = grad(args.dk, args.dk_t, args.dk_h), *dv = grad(args.dv, args.dv_t, args.dv_h);
-        copy_tile_rows(sDO(o.st), args.dg, threadIdx.x, kRowWarps * 32,
-                       [&](int j) -> void* { return j < p.n ? dv + j * args.dv_t : nullptr; });
-        copy_tile_rows(sQ(q.st), args.dg, threadIdx.x, kRowWarps * 32,
-                       [&](int j) -> void* { return j < p.n ? dk + j * args.dk_t : nullptr; });
+        copy_tile_rows(sDO(o.st), args.dg, threadIdx.x, kRowWarps * 32, p.n,
+                       [&](int j) -> void* { return dv + j * args.dv_t; });
+        copy_tile_rows(sQ(q.st), args.dg, threadIdx.x, kRowWarps * 32, p.n,
+                       [&](int j) -> void* { return dk + j * args.dk_t; });
       }
       if (!whole || refill) {
         // the slots go back at once; rows that no box fills are zeros again

@@ -23,7 +23,7 @@
 // Bound, for long sequences, by the MMAs: three prompts of up to 16384 tokens, 32 / 8 heads of 128, bf16,
 // take 2.05 ms, 1704 TFLOP/s, 0.91 of the measured peak.  Short ones are bound by the way
 // from one role to the next and by fetching code that runs once a unit: 64 prompts of up to 250 tokens, 32 / 4
-// heads of 64, take 35 us, some 3.5 us a unit of one or two key tiles, of which its memory and products need 1.3.
+// heads of 64, take 34 us, some 3.4 us a unit of one or two key tiles, of which its memory and products need 1.3.
 // For them there is an instance whose short units (kFewTiles) go through one copy of each
 // product and through loops over 32 columns; with the long units' straight-line code they took 40 us. The
 // other way round the loops cost long units 13 % (products) and 8 % (scores).
@@ -228,18 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && ring_take(&ring, i, ctl); ++i) {
         const Pair p(&ring, i);
         const int nt = p.nt();
-        if (QB == 2 && is_k) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (!ok || p.n_t(w) == 0) continue;
-            if (qs[w] > 0 && !(ok = mbar_wait(&bar_qfree[w], (qs[w] - 1) & 1, ctl, kErrTimeoutSoftmax))) continue;
-            uint64_t* bar = &bar_q[w][qs[w] % QB];
-            mbar_expect_tx(bar, qbytes);
-            load_rows<D>(sQ(w, qs[w] % QB), &tm_q, bar, p.head * G, p.row + w * TB);
-            ++qs[w];
-          }
-          if (!ok) break;
-        }
         for (int t = 0; t < nt; ++t, ++e) {
           const int st = e % depth;
           if (e >= depth && !(ok = mbar_wait(&empty[st], ((e / depth) - 1) & 1, ctl, kErrTimeoutMma))) break;
@@ -255,6 +243,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_expect_tx(bar, C::TILE);
           load_rows<D>(is_k ? sK(st) : sV(st), map, bar, p.krow + t * kBN, p.head);
+          if (QB == 2 && is_k && t == 0) {  // (the first K tile waits for no group)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (!ok || p.n_t(w) == 0) continue;
+              if (qs[w] > 0 && !(ok = mbar_wait(&bar_qfree[w], (qs[w] - 1) & 1, ctl, kErrTimeoutSoftmax))) continue;
+              uint64_t* qbar = &bar_q[w][qs[w] % QB];
+              mbar_expect_tx(qbar, qbytes);
+              load_rows<D>(sQ(w, qs[w] % QB), &tm_q, qbar, p.head * G, p.row + w * TB);
+              ++qs[w];
+            }
+            if (!ok) {
+              ++e;
+              break;
+            }
+          }
         }
         if (!ok) break;
         if (is_k) mbar_arrive(&ring.near);
@@ -725,7 +728,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tokens = min(left, TB);  // (none: the sequence ends before this tile)
       const long long qrow = static_cast<long long>(p.row) + w * TB;
       auto out_row = [&](int j) -> void* {
-        if (j >= tokens * G) return nullptr;
         const int k = static_cast<int>(args.g_div.div(j));
         return static_cast<T*>(args.o) + (qrow + k) * args.o_t + (p.head * G + j - k * G) * args.o_h;
       };
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {  // the rows behind it are another sequence's
-          copy_tile_rows(sQ(w, q.st), args.dg, r, 128, out_row);
+          copy_tile_rows(sQ(w, q.st), args.dg, r, 128, tokens * G, out_row);
           named_bar_sync(1 + w, 4 * 32);
         }
         if (QB == 1 && serves) load_next_q(i);
@@ -834,8 +836,9 @@ cudaError_t run_kernel(const PackedMaps& m, const PackedArgs& a, cudaStream_t s)
 }
 
 // Sequences of up to 512 keys on average: most units have one or two key tiles.  With and without the instance for
-// them, us, 65536 / 4 tokens and fewer: 32 / 4 heads of 64, sequences of 100 tokens 121 / 153, 256 114 / 132, 400 137 / 147,
-// 512 78 / 81, 1024 109 / 108, 2048 173 / 167; 32 / 8 of 128: 100 179 / 194, 256 169 / 171, 400 233 / 230, 1024 159 / 155.
+// them, us, 32768 tokens (16384 from 512 on): 32 / 4 heads of 64, sequences of 100 tokens 114 / 153, 256 111 / 132,
+// 400 138 / 147, 512 78 / 81, 1024 109 / 108, 2048 173 / 167; 32 / 8 of 128: 100 171 / 194, 256 168 / 171, 400 227 / 230,
+// 1024 159 / 155.
 template <typename T, int D>
 cudaError_t run(const PackedMaps& m, const PackedArgs& a, cudaStream_t s) {
   const bool few = a.shape.total_k <= 512ll * a.shape.B;
