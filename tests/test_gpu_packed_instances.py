@@ -93,3 +93,23 @@ def test_a_lone_key_has_no_gradient(gpu_lib, D, G, causal):
         within(name, g, r, b)
     assert (got[2][:cu[4]] == 0).all() and (got[3][:ck[4]] == 0).all()
     assert (got[2][cu[4] + 1:] != 0).any() and (got[3][ck[4]:] != 0).any()
+
+
+def test_a_plan_used_on_another_stream(gpu_lib):
+    ta = gpu_lib
+    cu = offsets([200, 3, 90])
+    q, k, v = (x.cuda() for x in make(7, cu[-1], cu[-1], 4, 2, 64, "bf16"))
+    want = ta.attn_packed_fwd(q, k, v, ta.packed_plan(torch.tensor(cu, dtype=torch.int32).cuda(), cu[-1], 4, 2))
+    torch.cuda.synchronize()
+    makes, uses = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(makes):
+        plan = ta.packed_plan(torch.tensor(cu, dtype=torch.int32).cuda(), cu[-1], 4, 2)
+    uses.wait_stream(makes)
+    plan.record_stream(uses)
+    got = ta.attn_packed_fwd(q, k, v, plan, stream=uses)
+    del plan  # its memory may go to the stream it was made on, once `uses` is past the call
+    with torch.cuda.stream(makes):
+        torch.full((1 << 16,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert ta.sync_status() == "TA_OK"
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
