@@ -23,7 +23,8 @@
 // five would do, and no dQ is summed in memory.  Three documents of up to 8192 tokens, 32 / 8 heads of
 // 128, bf16: 2.02 ms (0.89 + 1.28 apart); seven products at the measured peak take 1.81, five 1.30.
 // Short documents are bound by the way from one role to the next: 24 of up to 700 tokens, 16 heads
-// of 64, 95 us (45 + 53) where memory would need 19.
+// of 64, 92 us (45 + 52) where memory would need 19.  The MMA warp's loops hold one copy of each product, a
+// unit's first scores too (95 us with a copy of their own; the long case takes the same).
 #include "launch.h"
 #include "packed.cuh"
 
@@ -308,42 +309,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q and dO are in TMEM: their slot is free, and the last unit's S has been read
         ok = warp_wait(&bar_qfree, units, ctl, kErrTimeoutSoftmax);
         units ^= 1u;
-        if (ok && any) {
-          ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax);
-          nc ^= 1u;
-        }
-        any = true;
         if (!ok) break;
         commit_el(&bar_kvempty[k.st]);
         k.step();
-        if (!(ok = kv_ready(0))) break;
-        tc_fence_after();
-        mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(k.st)), idesc_s);
-        commit_el(&bar_s);
-        mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(k.st)), idesc_s);  // dP = dO V^T
-        commit_el(&bar_dp);
-        for (int t = 0; t < nkv; ++t) {
+#pragma unroll 1
+        for (int t = -1; t < nkv; ++t) {
           const int st = k.st;
           const bool next = t + 1 < nkv;
-          k.step();
+          if (t >= 0) k.step();
           if (next) {
-            if (!(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
-            nc ^= 1u;
+            if (any && !(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
+            nc ^= any ? 1u : 0u;
+            any = true;
             if (!(ok = kv_ready(t + 1))) break;
             tc_fence_after();
             mma_tmem_abT<D>(tmem + C::COL_A, tmem + C::COL_QT, smem_u32(sK(k.st)), idesc_s);
             commit_el(&bar_s);
           }
-          if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
-          tc_fence_after();
-          mma_half_y<0>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, t > 0);
-          if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
-          tiles ^= 1u;
-          tc_fence_after();
-          mma_half_y<1>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, true);
-          commit_el(&bar_kvempty[st]);
+          if (t >= 0) {
+            if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
+            tc_fence_after();
+            mma_half_y<0>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, t > 0);
+            if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
+            tiles ^= 1u;
+            tc_fence_after();
+            mma_half_y<1>(tmem + C::COL_DQ, tmem + C::COL_B, smem_u32(sK(st)), idesc_g, true);
+            commit_el(&bar_kvempty[st]);
+          }
           if (next) {
-            mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(k.st)), idesc_s);
+            mma_tmem_abT<D>(tmem + C::COL_B, tmem + C::COL_DOT, smem_u32(sV(k.st)), idesc_s);  // dP = dO V^T
             commit_el(&bar_dp);
           }
         }
@@ -479,10 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           pr[c + 1] = ex2(y.y);
         }
         if (t >= t_part) {
-          const int lim = sees - k0 - cb;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c > lim) pr[c] = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int lim = sees - k0 - cb - 32 * h;
+            const uint32_t keep = lim >= 31 ? 0xffffffffu : lim < 0 ? 0u : (2u << lim) - 1u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(keep >> c & 1u)) pr[32 * h + c] = 0.f;
+          }
         }
         if (!(ok = warp_wait(&bar_dp, tiles, ctl, kErrTimeoutMma))) break;
         tc_fence_after();
@@ -789,48 +787,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool c = u == care_u;
           return warp_wait(c ? &bar_care[(i & 1) * 2 + 1] : &bar_of[o.st], c ? ph : o.ph, ctl, kErrTimeoutTma);
         };
-        ok = warp_wait(&bar_kv, units, ctl, kErrTimeoutTma) && q_ready(0) && o_ready(0);
+        if (!(ok = warp_wait(&bar_kv, units, ctl, kErrTimeoutTma))) break;
         units ^= 1u;
-        if (ok && any) {  // the last unit's S^T has been read
-          ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax);
-          nc ^= 1u;
-        }
-        any = true;
-        if (!ok) break;
-        tc_fence_after();
-        mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(q.st)), idesc_s);  // S^T = K Q^T
-        commit_el(&bar_s);
-        mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(o.st)), idesc_s);  // dP^T = V dO^T
-        commit_el(&bar_dp);
-        if (nq == 1) commit_el(&bar_kvfree);
-        for (int u = 0; u < nq; ++u) {
+#pragma unroll 1
+        for (int u = -1; u < nq; ++u) {
           const int sq = q.st, so = o.st;
           const bool next = u + 1 < nq;
-          q.step();
-          o.step();
+          if (u >= 0) {
+            q.step();
+            o.step();
+          }
           if (next) {
-            if (!(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
-            nc ^= 1u;
+            if (any && !(ok = warp_wait(&bar_consumed, nc, ctl, kErrTimeoutSoftmax))) break;
+            nc ^= any ? 1u : 0u;
+            any = true;
             if (!(ok = q_ready(u + 1))) break;
             tc_fence_after();
-            mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(q.st)), idesc_s);
+            mma_abT<D>(tmem + C::COL_A, smem_u32(sK), smem_u32(sQ(q.st)), idesc_s);  // S^T = K Q^T
             commit_el(&bar_s);
           }
-          if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
-          tc_fence_after();
-          mma_tY_il_g<0>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, u > 0);
-          mma_tY_il_g<0>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, u > 0);
-          if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
-          tiles ^= 1u;
-          tc_fence_after();
-          mma_tY_il_g<1>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, true);
-          commit_el(&bar_oe[so]);
-          mma_tY_il_g<1>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, true);
-          commit_el(&bar_qe[sq]);
+          if (u >= 0) {
+            if (!(ok = warp_wait(&bar_ds[0], tiles, ctl, kErrTimeoutSoftmax))) break;
+            tc_fence_after();
+            mma_tY_il_g<0>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, u > 0);
+            mma_tY_il_g<0>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, u > 0);
+            if (!(ok = warp_wait(&bar_ds[1], tiles, ctl, kErrTimeoutSoftmax))) break;
+            tiles ^= 1u;
+            tc_fence_after();
+            mma_tY_il_g<1>(tmem + C::COL_DV, tmem + C::COL_B, smem_u32(sDO(so)), idesc_g, true);
+            commit_el(&bar_oe[so]);
+            mma_tY_il_g<1>(tmem + C::COL_DK, tmem + C::COL_B + 16, smem_u32(sQ(sq)), idesc_g, true);
+            commit_el(&bar_qe[sq]);
+          }
           if (next) {
             if (!(ok = o_ready(u + 1))) break;
             tc_fence_after();
-            mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(o.st)), idesc_s);
+            mma_abT<D>(tmem + C::COL_B, smem_u32(sV), smem_u32(sDO(o.st)), idesc_s);  // dP^T = V dO^T
             commit_el(&bar_dp);
             if (u + 2 == nq) commit_el(&bar_kvfree);  // nothing reads K and V any more
           }
