@@ -20,8 +20,8 @@
 // thread hands back.
 //
 // Bound, for long sequences, by the MMAs: S and dP are made in both passes, seven products where
-// five would do, and no dQ is summed in memory.  Three documents of up to 8192 tokens, 32 / 8 heads of
-// 128, bf16: 2.02 ms (0.89 + 1.28 apart); seven products at the measured peak take 1.81, five 1.30.
+// five would do, and no dQ is summed in memory.  Three documents of 2000 to 8192 tokens, 32 / 8 heads of
+// 128, bf16: 2.02 ms (0.89 + 1.28 timed one by one); seven products at the measured peak take 1.81, five 1.30.
 // Short documents are bound by the way from one role to the next: 24 of up to 700 tokens, 16 heads
 // of 64, 92 us (45 + 52) where memory would need 19.  The MMA warp's loops hold one copy of each product, a
 // unit's first scores too (95 us with a copy of their own; the long case takes the same).
@@ -34,7 +34,7 @@ namespace {
 
 // Registers: 384 x 168 at launch = 256 x 200 (row warps) + 128 x 104; warp 11 only makes up the
 // warpgroup.  With 168 a thread for all and units asked for one ahead, three documents of
-// up to 16384 tokens, 32 / 8 heads of 128 took 2185 us, so 2024 us.
+// 2000 to 8192 tokens, 32 / 8 heads of 128, took 2185 us, so 2024 us.
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kCare = 10;
 constexpr int kRowWarps = 8;
