@@ -1,0 +1,56 @@
+"""Head norms with the rotation where a side has no heads."""
+import numpy as np
+import pytest
+import torch
+
+from _prompt import TORCH, ints, values
+from test_gpu_rotary import EPS, check_rows, weights
+
+pytestmark = pytest.mark.gpu
+
+
+def call_c(ta, fn, cache=None, **kw):
+    """A call of the C ABI on rows [tokens, heads, D] given by name, on the current stream."""
+    rows = [kw.get(n) for n in ("q", "k", "v", "dq", "dk", "q_out", "k_out")]
+    x = next(t for t in rows if t is not None)
+    heads = [0 if t is None else t.shape[1] for t in rows[:2]]
+    p = lambda n: 0 if kw.get(n) is None else kw[n].data_ptr()
+    ws = kw.get("ws")
+    rot, dt = kw["rotary"], 0 if x.dtype is torch.float16 else 1
+    wt = next((w.dtype for w in (kw.get("q_weight"), kw.get("k_weight")) if w is not None), x.dtype)
+    call = ta._ROT.pack(*[y for t in rows for y in ((0, 0, 0, 0) if t is None else ta._rows_arg(t))], p("positions"), 0, 1,
+                        p("slots"), rot.turns.data_ptr(), p("q_weight"), p("k_weight"), p("dq_weight"), p("dk_weight"),
+                        p("ws"), 0 if ws is None else ws.numel(), rot.dim, rot.interleaved, rot.scale, kw.get("eps", EPS), 1,
+                        x.shape[0], *heads, x.shape[2], dt, 2 if wt is torch.float32 else dt)
+    s = torch.cuda.current_stream().cuda_stream
+    lib = ta.load()
+    return getattr(lib, fn)(call, s) if cache is None else lib.attn_rotary_append(cache._ref, call, s)
+
+
+@pytest.mark.parametrize("dim", [64, 32, 24])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+def test_append_of_normed_keys_without_queries(gpu_lib, kind, dim):
+    """A call with no queries norms its keys by the keys' weight."""
+    ta = gpu_lib
+    T, H, D, page = 21, 3, 64, 8
+    rot = ta.Rotary(dim)
+    q, k, v = (values(i, (T, H, D), "bf16").cuda() for i in (1, 2, 3))
+    wq, wk = (w.cuda() for w in weights(D, "bf16"))
+    pos = ints(range(5, 5 + T))
+    slots = torch.from_numpy(np.random.default_rng(3).permutation(4 * page)[:T].astype(np.int32)).cuda()
+    caches = [ta.kv_cache(4, H, page, D, TORCH[kind]) for _ in range(2)]
+    for c in caches:
+        for t in (c.k, c.v):
+            t.view(torch.uint8).zero_()
+        for t in (c.k_scale, c.v_scale):
+            if t is not None:
+                t.zero_()
+    assert call_c(ta, "attn_rotary_append", caches[0], k=k, v=v, positions=pos, slots=slots, rotary=rot, k_weight=wk) == 0
+    ta.rotary_append(caches[1], q, k, v, pos, slots, rot, wq, wk, eps=EPS)
+    assert ta.sync_status() == "TA_OK"
+    for x, y in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v), (caches[0].k_scale, caches[1].k_scale),
+                 (caches[0].v_scale, caches[1].v_scale)):
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    if kind == "bf16":
+        i = slots.long()
+        check_rows("k", caches[0].k[i // page, :, i % page], k, pos, rot, "bf16", wk)

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_kernel(const 
     constexpr int PATH = decltype(path_tag)::value;
     const bool cached = MODE == kRotAppend && key;
     if (n0 >= n1 || (cached && slot_row < 0)) return;
-    const bool norm = MODE == kRotNorm || (MODE == kRotAppend && a.wq);
+    const bool norm = MODE == kRotNorm || (MODE == kRotAppend && (key ? a.wk : a.wq));
     T* dst = rows(out);
     Coef k;
     coefs<PATH>(a, w, cs, sn, norm ? weights[key] : nullptr, k);
