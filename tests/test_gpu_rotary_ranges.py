@@ -1,9 +1,12 @@
-"""Head norms with the rotation where a side has no heads."""
+"""Head norms with the rotation where a side has no heads, and where a row's squares leave
+fp32's range."""
 import numpy as np
 import pytest
 import torch
 
-from _prompt import TORCH, ints, values
+import oracle
+from _parity import ROUND_U, to_np
+from _prompt import TORCH, ints, partner, values, within
 from test_gpu_rotary import EPS, check_rows, weights
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +57,33 @@ def test_append_of_normed_keys_without_queries(gpu_lib, kind, dim):
     if kind == "bf16":
         i = slots.long()
         check_rows("k", caches[0].k[i // page, :, i % page], k, pos, rot, "bf16", wk)
+
+
+def norm_case(ta, x, g, w, rot, eps, dtype="bf16"):
+    """Forward and backward of rows x [tokens, heads, D] against the oracle."""
+    T, H, D = x.shape
+    pos = ints(range(T))
+    y, _ = ta.qk_norm_rotary_fwd(x.cuda(), None, w.cuda(), None, pos, rot, eps=eps)
+    check_rows("rows", y, x, pos, rot, dtype, w, eps)
+    dx, _, dw, _ = ta.qk_norm_rotary_bwd(g.cuda(), None, x.cuda(), None, w.cuda(), None, pos, rot, eps=eps)
+    assert ta.sync_status() == "TA_OK"
+    a, ga, wn = to_np(x), to_np(g), to_np(w)
+    back = oracle.rotary(ga, pos.cpu().numpy(), rot.inv_freq, rot.interleaved, rot.scale, back=True)
+    ref, rw = oracle.head_norm_bwd(a, wn, eps, back)
+    r = 1 / np.sqrt((a * a).mean(-1, keepdims=True) + eps)
+    h = a * r
+    # the rotated gradient as in rotary_bound, times w; h as a norm's row; their mean's D products
+    size = np.abs(ga) + partner(ga, rot.dim, rot.interleaved)
+    rel = 2.0 ** -21 + (2 * D + 64) * 2.0 ** -24
+    mean = (size * np.abs(wn * h)).mean(-1, keepdims=True)
+    # (a gradient below fp32's normal numbers may flush to zero)
+    within("dx", dx, ref, r * rel * (size * np.abs(wn) + 2 * np.abs(h) * mean) + ROUND_U[dtype] * np.abs(ref) + 2.0 ** -126)
+    within("dw", dw, rw, (rel + T * H * 2.0 ** -24) * (size * np.abs(h)).reshape(-1, D).sum(0))
+
+
+@pytest.mark.parametrize("D,dim", [(16, 16), (64, 64), (128, 128), (128, 64), (64, 24)])
+def test_norm_of_the_largest_rows(gpu_lib, D, dim):
+    """Rows whose every element is near the type's largest number (bf16: 2^128)."""
+    x = values(3, (6, 3, D), "bf16").sign() * 3.0e38
+    x[3:] = values(4, (3, 3, D), "bf16") * 2.0 ** 125
+    norm_case(gpu_lib, x.to(torch.bfloat16), values(5, (6, 3, D), "bf16"), weights(D, "f32")[0], gpu_lib.Rotary(dim), EPS)

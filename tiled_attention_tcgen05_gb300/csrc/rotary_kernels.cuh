@@ -204,7 +204,8 @@ __device__ __forceinline__ void coefs(const RotArgs& a, const Place& w, const fl
 }
 
 // r = 1 / sqrt(mean f^2 + eps) of U rows side by side; where a row's squares pass
-// fp32's range, f is scaled by down first (and r is that of the scaled row).
+// fp32's range, f is scaled by down first (and r is that of the scaled row): elements
+// below 2^128 become 2^48 at most, and one past 2^60, which such a row has, 2^-20.
 // Warp-collective.
 template <int D, int U>
 __device__ __forceinline__ void row_norm(float2 (&f)[U][2][4], float eps, float (&r)[U], float (&down)[U]) {
@@ -231,7 +232,7 @@ __device__ __forceinline__ void row_norm(float2 (&f)[U][2][4], float eps, float 
   bool big = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    down[u] = ss[u] < INFINITY ? 1.f : 5.421010862427522e-20f;  // 2^-64
+    down[u] = ss[u] < INFINITY ? 1.f : 8.271806125530277e-25f;  // 2^-80
     big |= !(ss[u] < INFINITY);
   }
   if (__any_sync(0xffffffffu, big)) {
