@@ -1,5 +1,5 @@
-"""Head norms with the rotation where a side has no heads, and where a row's squares leave
-fp32's range."""
+"""Head norms with the rotation where a side has no heads, where a row's squares leave
+fp32's range, and without eps."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +87,11 @@ def test_norm_of_the_largest_rows(gpu_lib, D, dim):
     x = values(3, (6, 3, D), "bf16").sign() * 3.0e38
     x[3:] = values(4, (3, 3, D), "bf16") * 2.0 ** 125
     norm_case(gpu_lib, x.to(torch.bfloat16), values(5, (6, 3, D), "bf16"), weights(D, "f32")[0], gpu_lib.Rotary(dim), EPS)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("H,D,dim", [(1, 16, 16), (5, 128, 128), (3, 64, 64), (7, 64, 24), (1, 32, 16)])
+def test_norm_without_eps_beside_rows_that_are_none(gpu_lib, H, D, dim, dtype):
+    """Heads that do not fill a group of rows: what stands in the others' place is in no sum."""
+    x, g = values(3, (9, H, D), dtype), values(5, (9, H, D), dtype)
+    norm_case(gpu_lib, x, g, weights(D, "f32")[0], gpu_lib.Rotary(dim), 0.0, dtype)

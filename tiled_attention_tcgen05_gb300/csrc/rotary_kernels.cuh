@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
           partners<T, PATH>(a, w, g, rows(grad) + h * grad.sh, act, gp);
           float r1[1], down[1];
           row_norm<D, 1>(fr, a.eps, r1, down);
-          const float r = r1[0];
+          const float r = act ? r1[0] : 0.f;  // (without eps a row of zeros has none: rows that are none must add zeros)
           const float2 r2 = make_float2(r, r);
           float2 dot2 = make_float2(0.f, 0.f), wv[2][4];
           load_weights(w, wt, wv);
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
             for (int e = 0; e < 4; ++e) {
               y[i][e] = ffma2(g[i][e], k.ca[i][e], fmul2(gp[i][e], k.cb[i][e]));
               f[i][e] = fmul2(f[i][e], r2);  // h = u r
-              acc[i][e] = ffma2(y[i][e], f[i][e], acc[i][e]);  // (rows that are none: zeros)
+              acc[i][e] = ffma2(y[i][e], f[i][e], acc[i][e]);
               y[i][e] = fmul2(y[i][e], wv[i][e]);
               dot2 = ffma2(y[i][e], f[i][e], dot2);
             }
