@@ -420,7 +420,7 @@ ta_status attn_rotary_fwd(const ta_rotary_call* call, void* stream);
 ta_status attn_rotary_bwd(const ta_rotary_call* call, void* stream);
 
 /* A norm of each row, then the rotation: x = u w / sqrt(mean u^2 + eps) elementwise,
- * w = q_weight or k_weight, eps >= 0. */
+ * w = q_weight or k_weight, eps >= 0 (with 0 a row of zeros gives NaN). */
 ta_status attn_qk_norm_rotary_fwd(const ta_rotary_call* call, void* stream);
 
 /* Its backward.  q, k: the forward's inputs; dq, dk: gradients of its outputs.  Out:

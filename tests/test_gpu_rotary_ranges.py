@@ -89,6 +89,17 @@ def test_norm_of_the_largest_rows(gpu_lib, D, dim):
     norm_case(gpu_lib, x.to(torch.bfloat16), values(5, (6, 3, D), "bf16"), weights(D, "f32")[0], gpu_lib.Rotary(dim), EPS)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38])
+@pytest.mark.parametrize("D,dim", [(16, 16), (64, 64), (128, 128), (128, 64), (64, 24)])
+def test_norm_of_tiny_rows_without_eps(gpu_lib, D, dim, eps):
+    """Rows whose squares fp32 does not hold, and an eps that does not outweigh them."""
+    sizes = torch.tensor([2.0 ** -40, 2.0 ** -50, 2.0 ** -63, 2.0 ** -70, 2.0 ** -75, 2.0 ** -100, 2.0 ** -120, 2.0 ** -129])
+    x = (values(3, (8, 4, D), "bf16").float() * sizes.view(-1, 1, 1)).to(torch.bfloat16)
+    eps = float(np.float32(eps))
+    # (gradients that leave the rows' ones below the type's largest number)
+    norm_case(gpu_lib, x, values(5, (8, 4, D), "bf16", 2.0 ** -10), weights(D, "f32")[0], gpu_lib.Rotary(dim), eps)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("H,D,dim", [(1, 16, 16), (5, 128, 128), (3, 64, 64), (7, 64, 24), (1, 32, 16)])
 def test_norm_without_eps_beside_rows_that_are_none(gpu_lib, H, D, dim, dtype):

@@ -203,12 +203,14 @@ __device__ __forceinline__ void coefs(const RotArgs& a, const Place& w, const fl
     }
 }
 
-// r = 1 / sqrt(mean f^2 + eps) of U rows side by side; where a row's squares pass
-// fp32's range, f is scaled by down first (and r is that of the scaled row): elements
-// below 2^128 become 2^48 at most, and one past 2^60, which such a row has, 2^-20.
-// Warp-collective.
+// r = 1 / sqrt(mean f^2 + eps) of U rows side by side.  Where a row's squares leave
+// fp32's range, f is scaled by by[] first, and r is that of the scaled row (true: some row of
+// the warp's is).  Squares past it: elements below 2^128 become 2^48 at most, and one past 2^60,
+// which such a row has, 2^-20.  Squares below it: where mean and eps together pass 2^-100, what
+// fp32 loses of the squares (2^-150 each) is nothing beside them; else elements of 2^-133 to 2^-46 become
+// 2^-53 to 2^34, and eps at most 2^60.  Warp-collective.
 template <int D, int U>
-__device__ __forceinline__ void row_norm(float2 (&f)[U][2][4], float eps, float (&r)[U], float (&down)[U]) {
+__device__ __forceinline__ bool row_norm(float2 (&f)[U][2][4], float eps, float (&r)[U], float (&by)[U]) {
   constexpr int L = D / 16;
   float ss[U];
   auto squares = [&] {
@@ -229,25 +231,33 @@ __device__ __forceinline__ void row_norm(float2 (&f)[U][2][4], float eps, float 
       for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], s);
   };
   squares();
-  bool big = false;
+  constexpr float LOW = 7.888609052210118e-31f;  // 2^-100
+  bool scaled = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    down[u] = ss[u] < INFINITY ? 1.f : 8.271806125530277e-25f;  // 2^-80
-    big |= !(ss[u] < INFINITY);
+    r[u] = fmaf(ss[u], 1.f / D, eps);
+    by[u] = 1.f;
+    // (not in [LOW, infinity): one comparison of the bits of a number that is not negative)
+    scaled |= __float_as_uint(r[u]) - __float_as_uint(LOW) >= 0x7f800000u - __float_as_uint(LOW);
   }
-  if (__any_sync(0xffffffffu, big)) {
+  scaled = __any_sync(0xffffffffu, scaled);
+  if (scaled) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float2 t2 = make_float2(down[u], down[u]);
+      by[u] = r[u] < LOW ? 1.2089258196146292e24f : r[u] < INFINITY ? 1.f : 8.271806125530277e-25f;  // 2^80, 2^-80
+      const float2 t2 = make_float2(by[u], by[u]);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[u][c][e] = fmul2(f[u][c][e], t2);
     }
     squares();
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = fmaf(ss[u], 1.f / D, eps * by[u] * by[u]);
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) r[u] = rsqrtf(fmaf(ss[u], 1.f / D, eps * down[u] * down[u]));
+  for (int u = 0; u < U; ++u) r[u] = rsqrtf(r[u]);
+  return scaled;
 }
 
 // A row's sixteen fp32 elements a lane -> codes of a cache type, and the scale.
@@ -404,15 +414,15 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_kernel(const 
       constexpr int U = decltype(count)::value;
       wait_copies(g1 - U - g);
       float2 f[U][2][4];
-      float r[U], down[U];
+      float r[U], by[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint8_t* from = mine + (g + u - g0) * 1024;
         unpack8<T>(staged(from, 0), f[u][0]);
         unpack8<T>(staged(from, 1), f[u][1]);
-        r[u] = down[u] = 1.f;
+        r[u] = by[u] = 1.f;
       }
-      if (norm) row_norm<D, U>(f, a.eps, r, down);
+      if (norm) row_norm<D, U>(f, a.eps, r, by);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = (g + u - base) * RPW + sub;
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_kernel(const 
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) xp[i][e] = fmul2(xp[i][e], make_float2(down[u], down[u]));
+            for (int e = 0; e < 4; ++e) xp[i][e] = fmul2(xp[i][e], make_float2(by[u], by[u]));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -540,8 +550,8 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
             unpack8<T>(staged(from + 1024, i), g[i]);
           }
           partners<T, PATH>(a, w, g, rows(grad) + h * grad.sh, act, gp);
-          float r1[1], down[1];
-          row_norm<D, 1>(fr, a.eps, r1, down);
+          float r1[1], by[1];
+          const bool scaled = row_norm<D, 1>(fr, a.eps, r1, by);
           const float r = act ? r1[0] : 0.f;  // (without eps a row of zeros has none: rows that are none must add zeros)
           const float2 r2 = make_float2(r, r);
           float2 dot2 = make_float2(0.f, 0.f), wv[2][4];
@@ -558,11 +568,14 @@ __global__ void __launch_bounds__(kWarps * 32, ANY ? 1 : 2) rotary_norm_bwd_kern
               dot2 = ffma2(y[i][e], f[i][e], dot2);
             }
           const float dot = row_sum<L>(dot2.x + dot2.y) * (-1.f / D);
-          const float2 d2 = make_float2(dot, dot), rd = make_float2(r * down[0], r * down[0]);
+          const float2 d2 = make_float2(dot, dot), by2 = make_float2(by[0], by[0]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[i][e] = fmul2(rd, ffma2(f[i][e], d2, y[i][e]));
+            for (int e = 0; e < 4; ++e) {
+              y[i][e] = fmul2(r2, ffma2(f[i][e], d2, y[i][e]));
+              if (scaled) y[i][e] = fmul2(y[i][e], by2);  // (r times by may be past fp32's range)
+            }
             if (act) *reinterpret_cast<uint4*>(po + h * out.sh + w.at[i]) = pack8<T>(y[i]);
           }
         }
