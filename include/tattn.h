@@ -425,7 +425,8 @@ ta_status attn_qk_norm_rotary_fwd(const ta_rotary_call* call, void* stream);
 
 /* Its backward.  q, k: the forward's inputs; dq, dk: gradients of its outputs.  Out:
  * q_out, k_out (gradients of the inputs) and dq_weight, dk_weight (fp32, summed
- * over all rows in fp32, in an order that the sizes fix).  ws: >=
+ * over all rows in fp32, in an order that the sizes fix; a side without heads: zeros, and
+ * its pointer may be NULL).  ws: >=
  * attn_qk_norm_rotary_bwd_workspace_bytes(D) bytes, 16-byte aligned, contents need
  * not be initialised; calls that may run at the same time need one each. */
 size_t attn_qk_norm_rotary_bwd_workspace_bytes(int D);

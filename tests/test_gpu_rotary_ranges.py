@@ -106,3 +106,28 @@ def test_norm_without_eps_beside_rows_that_are_none(gpu_lib, H, D, dim, dtype):
     """Heads that do not fill a group of rows: what stands in the others' place is in no sum."""
     x, g = values(3, (9, H, D), dtype), values(5, (9, H, D), dtype)
     norm_case(gpu_lib, x, g, weights(D, "f32")[0], gpu_lib.Rotary(dim), 0.0, dtype)
+
+
+@pytest.mark.parametrize("T", [0, 4])
+def test_weights_of_no_heads_have_no_gradient(gpu_lib, T):
+    ta = gpu_lib
+    D = 64
+    rot, pos = ta.Rotary(D), ints(range(T))
+    x, none = values(3, (T, 2, D), "bf16").cuda(), torch.empty(T, 0, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(D, device="cuda")
+    ws = torch.empty(max(1, ta.load().attn_qk_norm_rotary_bwd_workspace_bytes(D)), dtype=torch.uint8, device="cuda")
+    for side in (0, 1):
+        dw = torch.full((2, D), 7.0, device="cuda")
+        rows = dict(k=x, dk=x.clone(), k_out=x.clone()) if side == 0 else dict(q=x, dq=x.clone(), q_out=x.clone())
+        if T == 0:
+            rows = dict(q=none, k=none)
+        assert call_c(ta, "attn_qk_norm_rotary_bwd", positions=pos, rotary=rot, q_weight=w, k_weight=w, dq_weight=dw[0],
+                      dk_weight=dw[1], ws=ws, **rows) == 0
+        assert ta.sync_status() == "TA_OK"
+        assert not dw[side].any()
+    pair = lambda a: (x, none) if a else (none, x)
+    for side in (0, 1):
+        junk = [torch.full((2, D), float("nan"), device="cuda") for _ in range(8)]
+        del junk
+        got = ta.qk_norm_rotary_bwd(*pair(side), *pair(side), w, w, pos, rot)
+        assert not got[2 + side].any() and torch.isfinite(got[3 - side]).all()

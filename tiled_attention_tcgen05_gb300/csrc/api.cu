@@ -918,16 +918,16 @@ static ta_status run_rotary(const ta_rotary_call* c, int mode, float sign, const
       return TA_ERR_ALIGNMENT;
     if (a.units == 0) {  // sums of no rows
       cudaError_t e = cudaSuccess;
-      if (c->Hq > 0) e = cudaMemsetAsync(c->dq_weight, 0, sizeof(float) * c->D, s);
-      if (e == cudaSuccess && c->Hkv > 0) e = cudaMemsetAsync(c->dk_weight, 0, sizeof(float) * c->D, s);
+      if (c->dq_weight) e = cudaMemsetAsync(c->dq_weight, 0, sizeof(float) * c->D, s);
+      if (e == cudaSuccess && c->dk_weight) e = cudaMemsetAsync(c->dk_weight, 0, sizeof(float) * c->D, s);
       return cuda_status(e);
     }
     st = check_ptrs({c->ws});
     if (st != TA_OK) return st;
     if (c->ws_bytes < attn_qk_norm_rotary_bwd_workspace_bytes(c->D)) return TA_ERR_INVALID_ARG;
     a.part = static_cast<float*>(c->ws);
-    a.dwq = c->Hq > 0 ? c->dq_weight : nullptr;
-    a.dwk = c->Hkv > 0 ? c->dk_weight : nullptr;
+    a.dwq = c->dq_weight;  // (of no heads: zeros)
+    a.dwk = c->dk_weight;
   }
   if (a.units == 0) return TA_OK;
   a.sign = sign;
