@@ -484,7 +484,9 @@ typedef struct {
 ta_status attn_packed_fwd(const ta_packed_call* call, void* stream);
 
 /* Gradients of <dO, O>; dk, dv are summed over the query heads of a key head in
- * fp32, in a fixed order.  Keys that no query sees get zeros.  Infinities or
+ * fp32, in a fixed order.  Keys that no query sees get zeros.  o and lse may be those over
+ * more keys than the call's (attn_merge_fwd of several calls): dk, dv are then the
+ * gradients of its keys, and dq their part of the whole.  Infinities or
  * NaN among a sequence's rows make its gradients unspecified, and no other
  * sequence's.  ws: >= attn_packed_bwd_workspace_bytes(...) bytes, 16-byte aligned,
  * contents need not be initialised; calls that may run at the same time need one

@@ -1087,7 +1087,8 @@ def attn_packed_bwd_workspace_bytes(total, Hq) -> int:
 
 def attn_packed_bwd(q, k, v, o, lse, do, plan, sm_scale=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """Backward of attn_packed_fwd for the loss <do, o>: returns (dq, dk, dv) in q's dtype, dk and dv summed over the
-    query heads of a key head.  Rows of given dq, dk, dv that belong to no sequence are left as they were."""
+    query heads of a key head.  o and lse may be those of several key sets, joined by merge_fwd: the gradients are then
+    those of this call's keys.  Rows of given dq, dk, dv that belong to no sequence are left as they were."""
     there = _on(q.get_device())
     if there is not None:
         with there:

@@ -60,7 +60,7 @@ struct PackedArgs {
   const uint8_t* plan;
   PackedShape shape;
   FastDiv hkv_div, g_div;
-  const void* v;        // forward: [total_k, Hkv, D], element strides vt, vh
+  const void* v;        // [total_k, Hkv, D], element strides vt, vh
   long long vt, vh;
   void *o, *dq, *dk, *dv;  // element strides (token, head)
   long long o_t, o_h, dq_t, dq_h, dk_t, dk_h, dv_t, dv_h;
@@ -105,11 +105,11 @@ __device__ __forceinline__ PackedList packed_list(const PackedArgs& a, int kind)
   }
   return l;
 }
-// An item's unit (PackedUnit::pad[0]: causal, pad[1]: the key head, pad[2]: key side, the sequence has one key).
+// An item's unit (PackedUnit::pad[0]: causal, pad[1]: the key head).
 __device__ __forceinline__ PackedUnit packed_item(const PackedArgs& a, const PackedList& l, uint32_t item) {
   const uint32_t i = a.hkv_div.div(item);
   const int4 x = __ldg(l.units + 2 * static_cast<size_t>(i)), y = __ldg(l.units + 2 * static_cast<size_t>(i) + 1);
-  return PackedUnit{x.x, x.y, x.z, x.w, y.x, {l.causal, static_cast<int>(item - i * a.hkv_div.d), y.y}};
+  return PackedUnit{x.x, x.y, x.z, x.w, y.x, {l.causal, static_cast<int>(item - i * a.hkv_div.d), 0}};
 }
 
 // Key tiles that a tile of `tokens` tokens visits, the first of which sees keys up to off.

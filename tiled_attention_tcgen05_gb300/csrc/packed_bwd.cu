@@ -121,6 +121,34 @@ __device__ __forceinline__ float half_dot(uint32_t a_tmem, const uint8_t* b, int
   return acc;
 }
 
+// Whether half of row r of a swizzled tile holds the numbers of a value's row of `dg` elements (zeros
+// of either sign are one number).
+template <int D>
+__device__ __forceinline__ bool half_equal(const void* row, int dg, const uint8_t* b, int r, int half) {
+  uint32_t eq = 0xffffffffu;
+  auto both = [&](uint32_t u, uint32_t v) { eq &= __vcmpeq2(u, v) | __vcmpeq2((u | v) & 0x7fff7fffu, 0u); };
+#pragma unroll 1
+  for (int gc = half * (D / 16); gc < (half + 1) * (D / 16) && gc * 8 < dg; ++gc) {
+    const uint4 x = __ldg(static_cast<const uint4*>(row) + gc);
+    const uint4 y = *reinterpret_cast<const uint4*>(b + (gc >> 3) * (kBM * 128) + r * 128 + (((gc & 7) ^ (r & 7)) * 16));
+    both(x.x, y.x);
+    both(x.y, y.y);
+    both(x.z, y.z);
+    both(x.w, y.w);
+  }
+  return eq == 0xffffffffu;
+}
+// named_bar_sync that tells whether x held for all of its threads.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t count, bool x) {
+  uint32_t all = x;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "+r"(all)
+      : "r"(id), "r"(count)
+      : "memory");
+  return all != 0u;
+}
+
 // ======================================================================
 //                         dQ (query-stationary)
 // ======================================================================
@@ -128,6 +156,13 @@ __device__ __forceinline__ float half_dot(uint32_t a_tmem, const uint8_t* b, int
 // come through the ring as the entry in front of a unit's K/V tiles.  O has a tile
 // of its own, and delta is formed while the first products run.  dQ leaves
 // through the entry behind the tiles.
+//
+// A sequence's only key: where a row's O is that key's value, dS = P (<dO, V> - <dO, O>) = 0.  The
+// product's sum and delta's are of the same numbers in different orders and would leave their rounding, so
+// such rows' delta is the product's own dP, here and, through memory, in the other pass (whose product sums
+// the same terms in the same order).  With O and L over more keys than this call's, O is another, and dS what it is.
+// (The same for every row that sees one key, the first of each causal sequence among them, would cost
+// short documents 2 us of 92: the value's row is fetched in the first unit of each.)
 template <int D>
 struct PdqCfg {
   static constexpr int TILE = (D / 64) * kBM * 128;
@@ -446,12 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       tc_fence_after();
       float dlt = half_dot<T, D>(lane_addr + C::COL_DOT, sO, r, hc);
+      const bool lone = p.n == 1 && in && sees == 0;
+      const bool same = !lone || half_equal<D>(static_cast<const T*>(args.v) + static_cast<long long>(p.krow) * args.vt +
+                                                   p.head * args.vh,
+                                               args.dg, sO, r, hc);
       named_bar_sync(1, kRowWarps * 32);  // the halves go over O
       halves[hc * kBM + r] = dlt;
-      named_bar_sync(1, kRowWarps * 32);
+      // the tile in which delta becomes the lone key's dP (-1: none)
+      const int t_lone = named_bar_all(1, kRowWarps * 32, same) && lone && hc == 0 ? 0 : -1;
       dlt = halves[r] + halves[kBM + r];
       fence_proxy_async_smem();
-      if (hc == 0 && in) args.delta[g] = dlt;
       for (int t = 0; t < nkv; ++t, tiles ^= 1u) {
         const int k0 = t * kBN;
         if (!(ok = warp_wait(&bar_s, tiles, ctl, kErrTimeoutMma))) break;
@@ -489,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t dp[32];
           tmem_ld_x32(lane_addr + C::COL_B + cb + 32 * c, dp);
           tmem_ld_wait(dp);
+          if (c == 0 && t == t_lone) dlt = __uint_as_float(dp[0]);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -507,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         k.step();
       }
       if (!ok) break;
+      if (hc == 0 && in) args.delta[g] = dlt;
       if (!(ok = warp_wait(&bar_done, units, ctl, kErrTimeoutMma) &&
                  warp_wait(&bar_out[outs & 1], (outs >> 1) & 1, ctl, kErrTimeoutMma)))
         break;
@@ -516,16 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (every warp has handed in its last dS, and so has read O and delta)
       if (serves && ring_take(&ring, i + 1, ctl)) load_o(i + 1);
       __syncwarp();
-      // dQ (x sm_scale) staged in its slot.  A lone key has P = 1 whatever its score: dS is zero, and what the
-      // products leave of dP - delta is not.
-      const float by = p.n == 1 ? 0.f : args.sm_scale;
+      // dQ (x sm_scale) staged in its slot
 #pragma unroll
       for (int cc = 0; cc < D / 64; ++cc) {
         const int c = hc * (D / 64) + cc;
         uint32_t v[32];
         tmem_ld_x32(lane_addr + C::COL_DQ + 32 * c, v);
         tmem_ld_wait(v);
-        stage_row_chunk_sw128<BF>(smem_u32(sK(k.st)), r, c, v, by);
+        stage_row_chunk_sw128<BF>(smem_u32(sK(k.st)), r, c, v, args.sm_scale);
       }
       tc_fence_before();
       fence_proxy_async_smem();
@@ -589,7 +628,6 @@ struct KvUnit {
   int krow, n, row, left, off;  // first key's row, keys from it on, first token that sees any, tokens from it on; see PackedUnit
   int nq, head, causal;         // query tiles, key head
   int ragged;                   // the last tile ends behind the tokens
-  int lone;                     // the sequence has one key
   __device__ __forceinline__ KvUnit(const UnitRing* r, int i) {
     const int4 a = ring_words(r, i, 0), b = ring_words(r, i, 1), c = ring_words(r, i, 2);
     krow = a.x;
@@ -601,14 +639,13 @@ struct KvUnit {
     head = b.z;
     causal = b.w;
     ragged = c.x;
-    lone = c.y;
   }
 };
 __device__ __forceinline__ void make_kv_unit(const PackedUnit& u, int TB, int4 (&words)[4]) {
   const int nq = (u.left + TB - 1) / TB;
   words[0] = make_int4(u.krow, u.n, u.row, u.left);
   words[1] = make_int4(u.off, nq, u.pad[1], u.pad[0]);
-  words[2] = make_int4(nq * TB > u.left, u.pad[2], 0, 0);
+  words[2] = make_int4(nq * TB > u.left, 0, 0, 0);
 }
 
 template <typename T, int D>
@@ -1033,8 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       ++units;
       tc_fence_after();
-      // dV staged in dO's ring, dK (x sm_scale; a lone key's is zero) in Q's
-      const float by = p.lone ? 0.f : args.sm_scale;
+      // dV staged in dO's ring, dK (x sm_scale) in Q's
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
 #pragma unroll
@@ -1043,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld_x32(lane_addr + (a == 0 ? C::COL_DV : C::COL_DK) + 32 * c, v);
           tmem_ld_wait(v);
-          stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sDO(o.st) : sQ(q.st)), r, c, v, a ? by : 1.f);
+          stage_row_chunk_sw128<BF>(smem_u32(a == 0 ? sDO(o.st) : sQ(q.st)), r, c, v, a ? args.sm_scale : 1.f);
         }
       }
       tc_fence_before();

@@ -42,7 +42,6 @@ __device__ __forceinline__ int make_unit(const PackedShape& p, int kind, const S
     u->row = s.q0 + first;
     u->left = s.nq - first;
     u->off = k0 - P - first;
-    u->pad[2] = s.nk == 1;
     return (u->left + p.TB - 1) / p.TB;
   }
   const int per = kind == kPackedFwd ? 2 * p.TB : p.TB;
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedS
       if (!there) return;
       int4* dst = reinterpret_cast<int4*>(list + at);
       dst[0] = make_int4(w.row, w.left, w.krow, w.n);
-      dst[1] = make_int4(w.off, w.pad[2], 0, 0);
+      dst[1] = make_int4(w.off, 0, 0, 0);
     });
   }
   if (kind == 0 && tid == 0) {
