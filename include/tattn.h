@@ -479,8 +479,8 @@ typedef struct {
 
 /* Scores, softmax sums and accumulators are fp32, weights rounded to dt for the
  * product with V.  Infinities and NaN reach the rows of their own sequence that
- * see them, and no other row (an infinite value as NaN where the row's weight
- * for it rounds to zero). */
+ * see them, and no other row (an infinite value whose weight in the row rounds to
+ * zero as NaN, or, where a causal call's row sees the key among its last ones, as itself). */
 ta_status attn_packed_fwd(const ta_packed_call* call, void* stream);
 
 /* Gradients of <dO, O>; dk, dv are summed over the query heads of a key head in

@@ -1,5 +1,5 @@
 """Packed attention over one of several key sets, the backward with the O and L of all of
-them, and sequences with a single key."""
+them, sequences with a single key, and infinite values whose weight has vanished."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 import oracle
 from _parity import ROUND_U, to_np
 from _prompt import TINY, ints, offsets, packed_case, values, within
-from test_gpu_packed import make, run
+from test_gpu_packed import INF, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,27 @@ def test_scores_of_a_lone_key_have_no_gradient(gpu_lib, D, G, dtype, causal):
     dq, dk = got[2:4]
     assert not dq[cu[1]:].any() and not dk[ck[1]:].any()
     assert dq[1:cu[1]].any() and dk[:ck[1]].any()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("short", [True, False])
+@pytest.mark.parametrize("G,D", [(1, 64), (4, 128)])
+def test_infinite_values_of_vanished_weights(gpu_lib, G, D, short, causal):
+    """A row that sees an infinite value gets it, or NaN, whatever its weight; no other row knows of it."""
+    ta = gpu_lib
+    n = 300
+    cu = offsets([n] + [1] * 4 * short)
+    q, k, v = make(4, cu[-1], cu[-1], 2 * G, 2, D, "bf16", gain=0.1)
+    q += 4.0
+    k[0] = 40.0  # all other weights vanish
+    for at in (5, 130, n - 1):
+        x = v.clone()
+        x[at, 0, 3] = INF
+        o, _ = run(ta, q, k, x, cu, cu, causal)
+        assert ta.sync_status() == "TA_OK"
+        f = o.float().cpu()
+        bad = ~torch.isfinite(f)
+        want = torch.zeros_like(bad)
+        want[at if causal else 0:n, :G, 3] = True
+        assert torch.equal(bad, want)
+        assert not (f == -INF).any()
