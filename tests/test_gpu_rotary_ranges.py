@@ -1,5 +1,5 @@
 """Head norms with the rotation where a side has no heads, where a row's squares leave
-fp32's range, and without eps."""
+fp32's range, and without eps; angles on another stream than their own."""
 import numpy as np
 import pytest
 import torch
@@ -131,3 +131,27 @@ def test_weights_of_no_heads_have_no_gradient(gpu_lib, T):
         del junk
         got = ta.qk_norm_rotary_bwd(*pair(side), *pair(side), w, w, pos, rot)
         assert not got[2 + side].any() and torch.isfinite(got[3 - side]).all()
+
+
+def test_angles_used_on_another_stream(gpu_lib):
+    """The memory of a Rotary that is gone is given away only once the streams it was recorded on are done."""
+    ta = gpu_lib
+    T, H, D = 4096, 32, 128
+    q, pos = values(3, (T, H, D), "bf16").cuda(), ints(range(T))
+    want, _ = ta.rotary_fwd(q, None, pos, ta.Rotary(D))
+    outs = [torch.empty_like(q) for _ in range(40)]
+    torch.cuda.synchronize()
+    makes, uses = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(makes):
+        rot = ta.Rotary(D)
+    uses.wait_stream(makes)
+    rot.record_stream(uses)
+    for o in outs:  # some milliseconds of work on the stream
+        ta.rotary_fwd(q, None, pos, rot, q_out=o, stream=uses)
+    del rot
+    with torch.cuda.stream(makes):
+        for _ in range(8):
+            torch.zeros(D // 2, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    assert ta.sync_status() == "TA_OK"
+    assert all(torch.equal(o, want) for o in outs)

@@ -726,7 +726,8 @@ class Rotary:
               a linear ramp between; rotated elements times 0.1 ln(factor) + 1.
     inv_freq: the angles themselves instead (dim / 2 numbers); scale: the factor of the rotated
     elements, instead of the scaling's.  Angles are held as 64-bit fractions of a turn, so that far
-    positions are as exact as near ones.  Holds a tensor on `device`."""
+    positions are as exact as near ones.  Holds a tensor on `device`, of the stream that is current there; where other
+    streams use it, record_stream tells the allocator."""
 
     __slots__ = ("dim", "interleaved", "scale", "inv_freq", "turns", "device", "_index", "_ptr")
 
@@ -770,6 +771,9 @@ class Rotary:
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns] or [0], dtype=torch.int64,
                                   device=device)
         self.device, self._index, self._ptr = self.turns.device, self.turns.get_device(), self.turns.data_ptr()
+
+    def record_stream(self, stream):
+        self.turns.record_stream(stream)
 
 
 # ta_rotary_call of include/tattn.h, in its order
