@@ -675,8 +675,8 @@ def cache_assign(pages, kv_lens, new_lens, free, free_count, page_size, total, s
     new page is not held up by the pages); the others get no token.  Returns, int32:
     kv_lens [B] (then), q_lens [B] (new tokens), cu_seqlens [B + 1] (their exclusive
     sums), positions [total] and slots [total] (page * page_size + row; -1 behind the
-    last token) and free_count [1].  Impossible lengths and page ids make the next
-    sync_status() return TA_ERR_INDEX."""
+    last token) and free_count [1]: views of one buffer, which lives as long as any of them.  Impossible lengths and
+    page ids make the next sync_status() return TA_ERR_INDEX."""
     index = pages.get_device()
     there = _on(index)
     if there is not None:

@@ -21,10 +21,10 @@
 //
 // Bound, for long sequences, by the MMAs: S and dP are made in both passes, seven products where
 // five would do, and no dQ is summed in memory.  Three documents of 2000 to 8192 tokens, 32 / 8 heads of
-// 128, bf16: 2.02 ms (0.89 + 1.28 timed one by one); seven products at the measured peak take 1.81, five 1.30.
+// 128, bf16: 2.05 ms (0.84 + 1.20); seven products at the measured peak take 1.81, five 1.30.
 // Short documents are bound by the way from one role to the next: 24 of up to 700 tokens, 16 heads
-// of 64, 92 us (45 + 52) where memory would need 19.  The MMA warp's loops hold one copy of each product, a
-// unit's first scores too (95 us with a copy of their own; the long case takes the same).
+// of 64, 92 us (45 + 52 timed one by one) where memory would need 19.  The MMA warp's loops hold one copy of
+// each product, a unit's first scores too (95 us with a copy of their own; the long case takes the same).
 #include "launch.h"
 #include "packed.cuh"
 

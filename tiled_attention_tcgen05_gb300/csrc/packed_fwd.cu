@@ -21,7 +21,8 @@
 // warp 11 asks for the units.
 //
 // Bound, for long sequences, by the MMAs: three prompts of up to 16384 tokens, 32 / 8 heads of 128, bf16,
-// take 2.05 ms, 1704 TFLOP/s, 0.91 of the measured peak.  Short ones are bound by the way
+// take 2.06 ms, 1693 TFLOP/s, 0.90 of the measured peak, in short runs (in runs of seconds the power limit lowers
+// the clock, and they take 2.23).  Short ones are bound by the way
 // from one role to the next and by fetching code that runs once a unit: 64 prompts of up to 250 tokens, 32 / 4
 // heads of 64, take 34 us, some 3.4 us a unit of one or two key tiles, of which its memory and products need 1.3.
 // For them there is an instance whose short units (kFewTiles) go through one copy of each

@@ -25,7 +25,7 @@
 // were too few to fill the memory's latency.  Replayed calls:
 //   rotation of 8192 tokens, 32 / 8 heads of 128, bf16: 32 us, 5.3 TB/s (16384: 52 us, 6.4 TB/s);
 //   norm and rotation of 16383 tokens of these: 64 us, 5.3 TB/s, and of 64: 2.5 us in a row of calls;
-//   its backward for 8192 tokens, 32 / 4 heads of 64, fp16: 30 us, 3.8 TB/s (issue: half of all slots);
+//   its backward for 8192 tokens, 32 / 4 heads of 64, fp16: 31 us, 3.7 TB/s (issue: half of all slots);
 //   8191 tokens of the first kind into a cache: 41 us, 4.9 TB/s.
 // A plain copy reaches 6.8 TB/s; at these sizes launch, first loads and last stores are some 5 us.
 #pragma once
